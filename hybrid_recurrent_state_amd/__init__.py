@@ -23,7 +23,7 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libhrs.so")
 
 HRS_OK, HRS_EINVAL, HRS_EGEOMETRY, HRS_EALIGN, HRS_EDEVICE, HRS_EUNSUPPORTED = 0, -1, -2, -3, -4, -5
-HRS_F32, HRS_BF16 = 0, 1
+HRS_F32, HRS_BF16, HRS_F8E4M3 = 0, 1, 2
 HRS_CHAIN, HRS_TREE = 0, 1
 HRS_MAX_POS = 64
 GEOMETRY_CLASSES = {0: "OK", 1: "NULL", 2: "TRUNCATED", 3: "ROOT", 4: "RANGE", 5: "FORWARD", 6: "NOT_CHAIN"}
@@ -40,6 +40,7 @@ class HrsError(RuntimeError):
 
 # --- C structs (mirror include/hrs.h) -------------------------------------
 _i32 = ctypes.c_int32
+_i64 = ctypes.c_int64
 _p = ctypes.c_void_p
 
 
@@ -91,6 +92,34 @@ class RingDesc(ctypes.Structure):
                 ("n_packed_rows", _i32), ("n_runs", _i32), ("runs", ctypes.POINTER(RingRun))]
 
 
+class QkDesc(ctypes.Structure):
+    _fields_ = [("n_req", _i32), ("n_pos", _i32), ("n_heads", _i32), ("n_kvheads", _i32), ("d", _i32), ("rot", _i32),
+                ("dtype", _i32), ("q_stride", _i64), ("k_stride", _i64), ("eps", ctypes.c_float),
+                ("weight_offset", ctypes.c_float), ("interleaved", _i32), ("topo", _i32),
+                ("parent", ctypes.POINTER(_i32))]
+
+
+class CacheDesc(ctypes.Structure):
+    _fields_ = [("n_pages", _i32), ("page_size", _i32), ("table_len", _i32), ("dtype", _i32)]
+
+
+class AttnDesc(ctypes.Structure):
+    _fields_ = [("n_req", _i32), ("n_pos", _i32), ("n_heads", _i32), ("n_kvheads", _i32), ("d", _i32),
+                ("dtype", _i32), ("q_stride", _i64), ("k_stride", _i64), ("v_stride", _i64),
+                ("scale", ctypes.c_float), ("window", _i32), ("cache", CacheDesc), ("topo", _i32),
+                ("parent", ctypes.POINTER(_i32))]
+
+
+class AppendDesc(ctypes.Structure):
+    _fields_ = [("n_layers", _i32), ("n_req", _i32), ("n_pos", _i32), ("n_kvheads", _i32), ("d", _i32),
+                ("dtype", _i32), ("k_stride", _i64), ("v_stride", _i64), ("cache", CacheDesc)]
+
+
+class SampleDesc(ctypes.Structure):
+    _fields_ = [("n_req", _i32), ("n_pos", _i32), ("vocab", _i32), ("logit_dtype", _i32), ("draft_dtype", _i32),
+                ("topo", _i32), ("parent", ctypes.POINTER(_i32))]
+
+
 # Exported symbols and their signatures (every function of include/hrs.h).
 _SIGNATURES = {
     "hrs_validate_tree": (_i32, [ctypes.POINTER(_i32), _i32, _i32, ctypes.POINTER(_i32)]),
@@ -113,6 +142,12 @@ _SIGNATURES = {
     "rollback_restore": (_i32, [ctypes.POINTER(RollbackDesc), _p, _p, _p, _p, _p, _p, _p]),
     "ring_set_2d": (_i32, [ctypes.POINTER(RingDesc), _p, _p, _p]),
     "ring_get_2d": (_i32, [ctypes.POINTER(RingDesc), _p, _p, _p]),
+    "qk_norm_rope": (_i32, [ctypes.POINTER(QkDesc)] + [_p] * 9),
+    "attn_verify_span_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(AttnDesc)]),
+    "attn_verify_span": (_i32, [ctypes.POINTER(AttnDesc)] + [_p] * 12 + [ctypes.c_size_t, _p]),
+    "kv_cache_append": (_i32, [ctypes.POINTER(AppendDesc)] + [_p] * 13),
+    "accept_sample_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(SampleDesc)]),
+    "accept_sample": (_i32, [ctypes.POINTER(SampleDesc)] + [_p] * 12 + [ctypes.c_size_t, _p]),
     "hrs_strerror": (ctypes.c_char_p, [_i32]),
     "hrs_abi_version": (_i32, []),
     "hrs_last_hip_error": (_i32, []),
@@ -593,3 +628,282 @@ def ring_set_2d(ring, packed, runs, stream=None):
 def ring_get_2d(ring, packed, runs, stream=None):
     d, _keep = _ring_desc(ring, packed, runs)
     _check(lib.ring_get_2d(ctypes.byref(d), _ptr(ring), _ptr(packed), _stream(stream)), "ring_get_2d")
+
+
+# --- full-attention layers and sampling --------------------------------------
+
+class PreparedCall:
+    """One call of an entry point with its checks done and its arguments laid
+    out. Calling it launches on ``stream`` (torch stream or raw handle;
+    default: the current one) and reads whatever the same tensors hold by
+    then; it keeps them alive. The tensors must not be moved or resized."""
+
+    __slots__ = ("_name", "_fn", "_args", "_keep", "_device")
+
+    def __init__(self, name, args, keep, tensors):
+        self._name, self._fn, self._args = name, getattr(lib, name), args
+        self._keep, self._device = (keep, tensors), tensors[0].device
+
+    def __call__(self, stream=None) -> None:
+        torch = _torch()
+        if torch.cuda.current_device() != self._device.index:
+            raise ValueError(f"{self._name}: tensors are on {self._device}, the current device is "
+                             f"cuda:{torch.cuda.current_device()}")
+        st = self._fn(*self._args, _stream(stream))
+        if st != HRS_OK:
+            raise HrsError(st, self._name)
+
+
+class _SpanChecks(_Checks):
+    """_Checks with span tensors that may be views of a wider projection, and
+    one device for every tensor of the call."""
+
+    def strided(self, name: str, t, shape, dtypes) -> int:
+        """Elements from one position to the next of t [..., heads, d]: the
+        heads of a position are contiguous and all positions equally far
+        apart."""
+        if t is None:
+            raise ValueError(f"{name} is required")
+        if tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+        if t.dtype not in dtypes:
+            raise TypeError(f"{name}: dtype {t.dtype}, expected {' or '.join(str(d) for d in dtypes)}")
+        h, d = t.shape[-2:]
+        if t.stride(-1) != 1 or (h > 1 and t.stride(-2) != d):
+            raise ValueError(f"{name}: the heads of a position must be contiguous")
+        stride, n = None, 1
+        for size, st in zip(reversed(t.shape[:-2]), reversed(t.stride()[:-2])):
+            if size > 1:
+                if stride is None:
+                    stride = st // n
+                if st != stride * n:
+                    raise ValueError(f"{name}: positions must be equally far apart")
+            n *= size
+        stride = h * d if stride is None else stride
+        if stride < h * d or stride % 8 != 0:
+            raise ValueError(f"{name}: positions {stride} elements apart (at least {h * d}, a multiple of 8)")
+        self.seen.append((name, t))
+        return stride
+
+    def on_gpu(self) -> None:
+        super().on_gpu()
+        dev = self.seen[0][1].device
+        for name, t in self.seen:
+            if t.device != dev:
+                raise ValueError(f"{name} is on {t.device}, {self.seen[0][0]} on {dev}")
+
+    def call(self, name, args, *keep) -> PreparedCall:
+        return PreparedCall(name, args, keep, [t for _, t in self.seen])
+
+
+def _rank(name: str, t, n: int) -> None:
+    if t is None or t.dim() != n:
+        raise ValueError(f"{name}: {'required' if t is None else f'{t.dim()} dimensions'}, expected {n} dimensions")
+
+
+def _cache_code(dtype, span_dtype, name: str) -> int:
+    torch = _torch()
+    ok = (torch.float32,) if span_dtype == torch.float32 else (torch.bfloat16, torch.float8_e4m3fn)
+    if dtype not in ok:
+        raise TypeError(f"{name}: dtype {dtype}, expected {' or '.join(str(d) for d in ok)} beside {span_dtype} spans")
+    return {torch.float32: HRS_F32, torch.bfloat16: HRS_BF16}.get(dtype, HRS_F8E4M3)
+
+
+def _topo(parent) -> int:
+    return HRS_TREE if parent is not None else HRS_CHAIN
+
+
+def _data(t) -> Optional[int]:
+    return None if t is None else t.data_ptr()
+
+
+def _scales(chk, shape, cache_code: int, **scales) -> None:
+    for name, t in scales.items():
+        if t is not None and cache_code != HRS_F8E4M3:
+            raise ValueError(f"{name} goes with float8_e4m3fn caches only")
+        chk(name, t, shape, _f32(), optional=True)
+
+
+def qk_norm_rope_call(q, k, q_weight, k_weight, freq, seq_len, q_out, k_out, parent=None, eps: float = 1e-6,
+                      weight_offset: float = 0.0, interleaved: bool = False) -> PreparedCall:
+    """The PreparedCall of qk_norm_rope (same arguments, without the stream)."""
+    _rank("q", q, 4)
+    _rank("k", k, 4)
+    R, T, Hq, D = q.shape
+    Hkv = k.shape[2]
+    dt = _in_dtypes("q", q)
+    chk = _SpanChecks()
+    qs = chk.strided("q", q, (R, T, Hq, D), dt)
+    ks = chk.strided("k", k, (R, T, Hkv, D), dt)
+    chk("q_weight", q_weight, (D,), dt, optional=True)
+    chk("k_weight", k_weight, (D,), dt, optional=True)
+    if freq is not None:
+        _rank("freq", freq, 1)
+    chk("freq", freq, None, (_torch().float64,), optional=True)
+    chk("seq_len", seq_len, (R,), _i32t())
+    chk("q_out", q_out, (R, T, Hq, D), dt)
+    chk("k_out", k_out, (R, T, Hkv, D), dt)
+    par, par_p = _parent_array(parent, R, T)
+    chk.on_gpu()
+    rot = 0 if freq is None else 2 * freq.shape[0]
+    d = QkDesc(R, T, Hq, Hkv, D, rot, _dtype_code(q), qs, ks, float(eps), float(weight_offset),
+               int(bool(interleaved)), _topo(parent), par_p)
+    return chk.call("qk_norm_rope", (ctypes.byref(d), _data(q), _data(k), _data(q_weight), _data(k_weight),
+                                     _data(freq) if rot else None, _data(seq_len), _data(q_out), _data(k_out)),
+                    d, par)
+
+
+def qk_norm_rope(q, k, q_weight, k_weight, freq, seq_len, q_out, k_out, parent=None, eps: float = 1e-6,
+                 weight_offset: float = 0.0, interleaved: bool = False, stream=None):
+    """RMS norm of every head of q [R,T,Hq,D] and k [R,T,Hkv,D] (weights [D]
+    or None) and the rotation of its first 2 * len(freq) elements by the
+    position seq_len[r] + depth(t); freq: float64 radians per position, or
+    None for no rotation. q and k may be views of one projection's rows;
+    q_out, k_out are dense (q_out may be q itself where q is)."""
+    qk_norm_rope_call(q, k, q_weight, k_weight, freq, seq_len, q_out, k_out, parent, eps, weight_offset,
+                      interleaved)(stream)
+
+
+def attn_verify_span_workspace_bytes(n_req: int, n_pos: int, n_heads: int, n_kvheads: int, d: int) -> int:
+    """Device workspace bytes attn_verify_span needs for these sizes."""
+    a = AttnDesc(n_req, n_pos, n_heads, n_kvheads, d, HRS_BF16, 0, 0, 0, 1.0, 0, CacheDesc(1, 16, 1, HRS_BF16),
+                 HRS_CHAIN, None)
+    return int(lib.attn_verify_span_workspace_bytes(ctypes.byref(a)))
+
+
+def attn_verify_span_call(q, k, v, k_cache, v_cache, page_table, seq_len, out, workspace, parent=None, scale=None,
+                          window: int = 0, k_scale=None, v_scale=None, status=None) -> PreparedCall:
+    """The PreparedCall of attn_verify_span (same arguments, without the stream)."""
+    _rank("q", q, 4)
+    _rank("k", k, 4)
+    _rank("k_cache", k_cache, 4)
+    _rank("page_table", page_table, 2)
+    R, T, Hq, D = q.shape
+    Hkv = k.shape[2]
+    N, _, S, _ = k_cache.shape
+    dt = _in_dtypes("q", q)
+    code = _cache_code(k_cache.dtype, q.dtype, "k_cache")
+    chk = _SpanChecks()
+    qs = chk.strided("q", q, (R, T, Hq, D), dt)
+    ks = chk.strided("k", k, (R, T, Hkv, D), dt)
+    vs = chk.strided("v", v, (R, T, Hkv, D), dt)
+    chk("k_cache", k_cache, (N, Hkv, S, D), (k_cache.dtype,))
+    chk("v_cache", v_cache, (N, Hkv, S, D), (k_cache.dtype,))
+    chk("page_table", page_table, (R, page_table.shape[1]), _i32t())
+    chk("seq_len", seq_len, (R,), _i32t())
+    chk("out", out, (R, T, Hq, D), dt)
+    chk("workspace", workspace)
+    _scales(chk, (Hkv,), code, k_scale=k_scale, v_scale=v_scale)
+    chk.status(status)
+    par, par_p = _parent_array(parent, R, T)
+    chk.on_gpu()
+    cache = CacheDesc(N, S, page_table.shape[1], code)
+    d = AttnDesc(R, T, Hq, Hkv, D, _dtype_code(q), qs, ks, vs, float(D ** -0.5 if scale is None else scale),
+                 int(window), cache, _topo(parent), par_p)
+    nbytes = workspace.numel() * workspace.element_size()
+    return chk.call("attn_verify_span",
+                    (ctypes.byref(d), _data(q), _data(k), _data(v), _data(k_cache), _data(v_cache), _data(page_table),
+                     _data(seq_len), _data(k_scale), _data(v_scale), _data(out), _data(status), _data(workspace),
+                     nbytes), d, par)
+
+
+def attn_verify_span(q, k, v, k_cache, v_cache, page_table, seq_len, out, workspace, parent=None, scale=None,
+                     window: int = 0, k_scale=None, v_scale=None, status=None, stream=None):
+    """Attention of the span q [R,T,Hq,D] over the paged context (k_cache,
+    v_cache [pages,Hkv,slots,D], page_table [R,P], seq_len [R]) and the span's
+    own rows k, v [R,T,Hkv,D] along each position's root path. parent: None
+    (chain) or host ints [R,T] / [T] (tree). scale: default D ** -0.5. window:
+    0 = everything. k_scale, v_scale [Hkv] f32: float8_e4m3fn caches."""
+    attn_verify_span_call(q, k, v, k_cache, v_cache, page_table, seq_len, out, workspace, parent, scale, window,
+                          k_scale, v_scale, status)(stream)
+
+
+def kv_cache_append_call(k, v, k_cache, v_cache, page_table, seq_len, accept_len, seq_len_out=None, path=None,
+                         k_scale=None, v_scale=None, status=None) -> PreparedCall:
+    """The PreparedCall of kv_cache_append (same arguments, without the stream)."""
+    _rank("k", k, 5)
+    _rank("k_cache", k_cache, 5)
+    _rank("page_table", page_table, 2)
+    L, R, T, Hkv, D = k.shape
+    N, S = k_cache.shape[1], k_cache.shape[3]
+    dt = _in_dtypes("k", k)
+    code = _cache_code(k_cache.dtype, k.dtype, "k_cache")
+    chk = _SpanChecks()
+    ks = chk.strided("k", k, (L, R, T, Hkv, D), dt)
+    vs = chk.strided("v", v, (L, R, T, Hkv, D), dt)
+    chk("k_cache", k_cache, (L, N, Hkv, S, D), (k_cache.dtype,))
+    chk("v_cache", v_cache, (L, N, Hkv, S, D), (k_cache.dtype,))
+    chk("page_table", page_table, (R, page_table.shape[1]), _i32t())
+    chk("seq_len", seq_len, (R,), _i32t())
+    chk("accept_len", accept_len, (R,), _i32t())
+    chk("seq_len_out", seq_len_out, (R,), _i32t(), optional=True)
+    chk("path", path, (R, T), _i32t(), optional=True)
+    _scales(chk, (L, Hkv), code, k_scale=k_scale, v_scale=v_scale)
+    chk.status(status)
+    chk.on_gpu()
+    d = AppendDesc(L, R, T, Hkv, D, _dtype_code(k), ks, vs, CacheDesc(N, S, page_table.shape[1], code))
+    return chk.call("kv_cache_append",
+                    (ctypes.byref(d), _data(k), _data(v), _data(k_cache), _data(v_cache), _data(page_table),
+                     _data(seq_len), _data(accept_len), _data(path), _data(k_scale), _data(v_scale),
+                     _data(seq_len_out), _data(status)), d)
+
+
+def kv_cache_append(k, v, k_cache, v_cache, page_table, seq_len, accept_len, seq_len_out=None, path=None,
+                    k_scale=None, v_scale=None, status=None, stream=None):
+    """Rows path[r][0..accept_len[r]] (path None: 0..accept_len[r]) of the
+    span's k, v [L,R,T,Hkv,D] into slots seq_len[r] ... of every layer's pages
+    (k_cache, v_cache [L,pages,Hkv,slots,D]); seq_len_out [R] (seq_len itself,
+    a buffer apart from it, or None) receives the new lengths."""
+    kv_cache_append_call(k, v, k_cache, v_cache, page_table, seq_len, accept_len, seq_len_out, path, k_scale,
+                         v_scale, status)(stream)
+
+
+def sample_desc(n_req: int, n_pos: int, vocab: int, logit_dtype: int, draft_dtype: int = HRS_F32, parent=None):
+    par, par_p = _parent_array(parent, n_req, n_pos)
+    return SampleDesc(n_req, n_pos, vocab, logit_dtype, draft_dtype, _topo(parent), par_p), par
+
+
+def accept_sample_workspace_bytes(n_req: int, n_pos: int, vocab: int) -> int:
+    """Device workspace bytes accept_sample needs for these sizes."""
+    d, _keep = sample_desc(n_req, n_pos, vocab, HRS_BF16)
+    return int(lib.accept_sample_workspace_bytes(ctypes.byref(d)))
+
+
+def accept_sample_call(logits, tokens, uniforms, token_prob, accept_node, accept_len, path, bonus, workspace,
+                       draft_probs=None, temperature=None, parent=None, status=None) -> PreparedCall:
+    """The PreparedCall of accept_sample (same arguments, without the stream)."""
+    _rank("logits", logits, 3)
+    R, T, V = logits.shape
+    chk = _SpanChecks()
+    chk("logits", logits, None, _in_dtypes("logits", logits))
+    chk("tokens", tokens, (R, T), _i32t())
+    chk("uniforms", uniforms, (R, T), _f32())
+    chk("token_prob", token_prob, (R, T), _f32())
+    for name, t, shape in (("accept_node", accept_node, (R,)), ("accept_len", accept_len, (R,)), ("path", path, (R, T)),
+                           ("bonus", bonus, (R,))):
+        chk(name, t, shape, _i32t())
+    chk("workspace", workspace)
+    if draft_probs is not None:
+        chk("draft_probs", draft_probs, (R, T, V), _in_dtypes("draft_probs", draft_probs))
+    chk("temperature", temperature, (R,), _f32(), optional=True)
+    chk.status(status)
+    d, par = sample_desc(R, T, V, _dtype_code(logits), HRS_F32 if draft_probs is None else _dtype_code(draft_probs),
+                         parent)
+    chk.on_gpu()
+    nbytes = workspace.numel() * workspace.element_size()
+    return chk.call("accept_sample",
+                    (ctypes.byref(d), _data(logits), _data(tokens), _data(uniforms), _data(draft_probs),
+                     _data(temperature), _data(token_prob), _data(accept_node), _data(accept_len), _data(path),
+                     _data(bonus), _data(status), _data(workspace), nbytes), d, par)
+
+
+def accept_sample(logits, tokens, uniforms, token_prob, accept_node, accept_len, path, bonus, workspace,
+                  draft_probs=None, temperature=None, parent=None, status=None, stream=None):
+    """Acceptance of one draft block per request by sampling. logits [R,T,V];
+    tokens [R,T] int32; uniforms [R,T] f32 in [0, 1) (column 0 draws the
+    bonus token); draft_probs [R,T,V] (row t: what token t + 1 was drawn
+    from; chains) or None (drafts were picked); temperature [R] f32 or None;
+    outputs token_prob [R,T] f32 and int32 accept_node [R], accept_len [R],
+    path [R,T], bonus [R]."""
+    accept_sample_call(logits, tokens, uniforms, token_prob, accept_node, accept_len, path, bonus, workspace,
+                       draft_probs, temperature, parent, status)(stream)

@@ -24,7 +24,8 @@ PKG = os.path.dirname(CSRC)
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libhrs.so")
 
-HIP_SOURCES = ["gdn.hip", "chunked.hip", "conv.hip", "accept.hip", "rollback.hip", "ring.hip"]
+HIP_SOURCES = ["gdn.hip", "chunked.hip", "conv.hip", "accept.hip", "rollback.hip", "ring.hip",
+               "rope.hip", "attn.hip", "kvcache.hip", "sample.hip"]
 HOST_SOURCES = ["validate.cpp"]
 
 ARCH = "gfx950"

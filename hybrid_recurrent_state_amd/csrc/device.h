@@ -39,6 +39,14 @@ __device__ __forceinline__ float bf16_lo(uint32_t pair) { return __uint_as_float
 __device__ __forceinline__ float bf16_hi(uint32_t pair) { return __uint_as_float(pair & 0xFFFF0000u); }
 __device__ __forceinline__ float bf16_one(uint16_t h) { return __uint_as_float(static_cast<uint32_t>(h) << 16); }
 
+// Two f32 values rounded to bf16 (nearest, ties to even; NaN stays NaN), the
+// first in the low half: one conversion instruction on gfx950.
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  typedef float f32x2_ __attribute__((ext_vector_type(2)));
+  typedef __bf16 bf16x2_ __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2_{lo, hi}), bf16x2_));
+}
+
 // Load one element of a float or bf16 array as f32.
 template <typename T> __device__ __forceinline__ float load_elem(const T* p, size_t i);
 template <> __device__ __forceinline__ float load_elem<float>(const float* p, size_t i) { return p[i]; }

@@ -23,7 +23,9 @@ constexpr int kStashSlots = 8;        // most stash slots a schedule uses
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-inline size_t dtype_size(hrs_dtype d) { return d == HRS_F32 ? 4 : 2; }
+inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+inline size_t dtype_size(hrs_dtype d) { return d == HRS_F32 ? 4 : d == HRS_BF16 ? 2 : 1; }
 
 inline bool dtype_ok(int d) { return d == HRS_F32 || d == HRS_BF16; }
 
@@ -31,6 +33,17 @@ inline bool dtype_ok(int d) { return d == HRS_F32 || d == HRS_BF16; }
 // n_req parent rows of n_pos entries each (tree mode), or n_pos alone
 // (chain mode). Returns HRS_OK or HRS_EGEOMETRY.
 int check_topology(int topo, const int32_t* parent, int32_t n_req, int32_t n_pos);
+
+// Sizes and dtype of a paged cache beside spans of span_dtype. HRS_OK or
+// HRS_EINVAL.
+int check_cache(const hrs_cache_desc& c, int span_dtype);
+
+// A span's position stride in elements: *stride with 0 replaced by the dense
+// one. False if it is too small, not a multiple of 8 or out of range.
+bool span_stride(int64_t given, int64_t dense, int64_t* stride);
+
+// depth[t] of every position of one request's tree (parent checked before).
+void tree_depths(const int32_t* parent, int32_t n_pos, int8_t* depth);
 
 // Per-thread record of the last HIP error seen by an entry point (0 = none).
 void set_last_hip_error(int err);

@@ -1,0 +1,258 @@
+// qk_norm_rope: RMS norm over every query and key head and the rotation of
+// its first `rot` elements by position, in one pass over q and k.
+//
+//   n = x / sqrt(mean(x^2) + eps) * (offset + w)
+//   (n[a], n[b]) -> (n[a] cos - n[b] sin, n[b] cos + n[a] sin)
+//
+// openinfer PR #626 ("feat(qwen35): add opt-in DFlash speculative decoding"),
+// file table: batched query/key norm and rotation ahead of the attention.
+//
+// MI355X design: a copy with a little arithmetic, bound by memory for long
+// spans and by launch latency for one token. A head is held by a group of 8,
+// 16 or 32 lanes, eight elements each (one 16-byte load of bf16); the sum of
+// squares is a butterfly inside the group and the partner half of a rotated
+// pair comes from another lane of it, so a head is read and written once and
+// never leaves registers. The angles depend on the position alone: a block
+// forms them once per position (the product with the frequency and its
+// reduction to a turn in 64 bits: at position 262,144 a float32 product is
+// off by up to 0.016 radians) while its first heads are on the way, and all
+// heads of the position read the sines from LDS.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+
+#include "device.h"
+#include "internal.h"
+
+namespace hrs {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMaxRot = 256;
+constexpr int kMaxTokens = 4;   // positions a block takes at most
+
+struct RopeArgs {
+  const void* q;
+  const void* k;
+  const void* qw;
+  const void* kw;
+  const double* freq;
+  const int32_t* seq_len;
+  void* q_out;
+  void* k_out;
+  int64_t q_stride;
+  int64_t k_stride;
+  float eps;
+  float offset;
+  int32_t n_q;        // query heads
+  int32_t n_heads;    // query and key heads
+  int32_t d;
+  int32_t rot;
+  int32_t interleaved;
+  int32_t n_pos;
+  int32_t req0;
+  int32_t n_tok;      // positions of this launch (requests x n_pos)
+  int32_t per_block;  // positions per block
+  int32_t tree;
+  int8_t depth[kGeomBytes];
+};
+
+template <int LPH> __device__ __forceinline__ float head_sum(float x) {
+  if constexpr (LPH == 32) {
+    x = group_sum<16>(x);
+    return x + __shfl_xor(x, 16);
+  } else {
+    return group_sum<LPH>(x);
+  }
+}
+
+template <typename T> __device__ __forceinline__ void store8(T* p, const float* v);
+template <> __device__ __forceinline__ void store8<float>(float* p, const float* v) {
+  reinterpret_cast<f32x4*>(p)[0] = f32x4{v[0], v[1], v[2], v[3]};
+  reinterpret_cast<f32x4*>(p)[1] = f32x4{v[4], v[5], v[6], v[7]};
+}
+template <> __device__ __forceinline__ void store8<uint16_t>(uint16_t* p, const float* v) {
+  *reinterpret_cast<u32x4*>(p) =
+      u32x4{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])};
+}
+
+template <typename T, int LPH>
+__global__ __launch_bounds__(kThreads) void qk_norm_rope_kernel(const RopeArgs args) {
+  constexpr int kGroups = kThreads / LPH;
+  __shared__ float cs[kMaxTokens][kMaxRot / 2];
+  __shared__ float sn[kMaxTokens][kMaxRot / 2];
+  const int tok0 = blockIdx.x * args.per_block;
+  const int n_tok = min(args.per_block, args.n_tok - tok0);
+  const int group = threadIdx.x / LPH;
+  const int lane = threadIdx.x % LPH;       // eight elements from 8 * lane
+  const int half = args.rot >> 1;
+  const bool mine = lane * 8 < args.d;
+  const int items = n_tok * args.n_heads;
+  const int step = kGroups * gridDim.y;
+  int item = blockIdx.y * kGroups + group;
+
+  const T* const q = static_cast<const T*>(args.q);
+  const T* const k = static_cast<const T*>(args.k);
+  auto load_item = [&](int it, float* x) {
+    const int t = it / args.n_heads;
+    const int h = it - t * args.n_heads;
+    const int64_t row = static_cast<int64_t>(args.req0) * args.n_pos + tok0 + t;
+    const T* p = h < args.n_q ? q + row * args.q_stride + h * args.d
+                              : k + row * args.k_stride + (h - args.n_q) * args.d;
+    load8<T>(p + lane * 8, x);
+  };
+
+  float x[8] = {};
+  if (mine && item < items) load_item(item, x);
+  float wq[8] = {}, wk[8] = {};
+  if (mine && args.qw) load8<T>(static_cast<const T*>(args.qw) + lane * 8, wq);
+  if (mine && args.kw) load8<T>(static_cast<const T*>(args.kw) + lane * 8, wk);
+  for (int i = threadIdx.x; i < n_tok * half; i += kThreads) {
+    const int t = i / half;
+    const int f = i - t * half;
+    const int rt = tok0 + t;
+    const int rl = rt / args.n_pos;
+    const int pos = rt - rl * args.n_pos;
+    const int depth = args.tree ? args.depth[rl * args.n_pos + pos] : pos;
+    // Turns: at most 2^31 positions times 1 / 2 pi, off by a few 2^-53 of
+    // that; what is left after whole turns is good to 32 bits.
+    double a = static_cast<double>(static_cast<int64_t>(args.seq_len[args.req0 + rl]) + depth) * args.freq[f];
+    a *= 0.15915494309189533577;
+    a -= rint(a);
+    float s, c;
+    sincospif(2.0f * static_cast<float>(a), &s, &c);
+    cs[t][f] = c;
+    sn[t][f] = s;
+  }
+  __syncthreads();
+
+  const float inv_d = 1.0f / static_cast<float>(args.d);
+  // Every lane of a wave takes part in the exchanges, so the loop runs as
+  // long as any group of the block has a head left.
+  for (int base = blockIdx.y * kGroups; base < items; base += step, item += step) {
+    float nx[8] = {};
+    if (mine && item + step < items) load_item(item + step, nx);
+    const int t = min(item, items - 1) / args.n_heads;
+    const int h = min(item, items - 1) - t * args.n_heads;
+    const bool is_q = h < args.n_q;
+    float v[8];
+    if (is_q ? args.qw != nullptr : args.kw != nullptr) {
+      float ss = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
+      const float r = 1.0f / sqrtf(fmaf(head_sum<LPH>(ss), inv_d, args.eps));
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = x[i] * r * (args.offset + (is_q ? wq[i] : wk[i]));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = x[i];
+    }
+    if (args.interleaved) {
+      if (lane * 8 < args.rot) {
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) {
+          const float c = cs[t][lane * 4 + i / 2], s = sn[t][lane * 4 + i / 2];
+          const float a = v[i], b = v[i + 1];
+          v[i] = a * c - b * s;
+          v[i + 1] = b * c + a * s;
+        }
+      }
+    } else if (args.rot) {
+      // half is a multiple of 8: the partner elements are one lane's eight.
+      const int hl = half >> 3;
+      const bool low = lane < hl;
+      const int partner = low ? lane + hl : lane < 2 * hl ? lane - hl : lane;
+      const int src = (threadIdx.x & 63) - lane + partner;
+      float o[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) o[i] = __shfl(v[i], src);
+      if (lane < 2 * hl) {
+        const int f0 = (low ? lane : lane - hl) * 8;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float c = cs[t][f0 + i], s = sn[t][f0 + i];
+          v[i] = low ? v[i] * c - o[i] * s : v[i] * c + o[i] * s;
+        }
+      }
+    }
+    if (mine && item < items) {
+      const int64_t row = static_cast<int64_t>(args.req0) * args.n_pos + tok0 + t;
+      T* p = is_q ? static_cast<T*>(args.q_out) + (row * args.n_q + h) * args.d
+                  : static_cast<T*>(args.k_out) + (row * (args.n_heads - args.n_q) + (h - args.n_q)) * args.d;
+      store8<T>(p + lane * 8, v);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = nx[i];
+  }
+}
+
+template <typename T>
+void launch_rope(const RopeArgs& args, dim3 grid, hipStream_t s) {
+  if (args.d > 128)
+    hipLaunchKernelGGL((qk_norm_rope_kernel<T, 32>), grid, dim3(kThreads), 0, s, args);
+  else if (args.d > 64)
+    hipLaunchKernelGGL((qk_norm_rope_kernel<T, 16>), grid, dim3(kThreads), 0, s, args);
+  else
+    hipLaunchKernelGGL((qk_norm_rope_kernel<T, 8>), grid, dim3(kThreads), 0, s, args);
+}
+
+}  // namespace
+}  // namespace hrs
+
+using namespace hrs;
+
+extern "C" int qk_norm_rope(const hrs_qk_desc* d, const void* q, const void* k, const void* q_weight,
+                            const void* k_weight, const double* freq, const int32_t* seq_len, void* q_out,
+                            void* k_out, void* stream) {
+  if (d == nullptr || d->n_req < 1) return HRS_EINVAL;
+  if (d->topo == HRS_TREE) {
+    const int geo = check_topology(d->topo, d->parent, d->n_req, d->n_pos);
+    if (geo != HRS_OK) return geo;
+  } else if (d->topo != HRS_CHAIN || d->n_pos < 1 || d->n_pos > HRS_MAX_CHUNKED_POS) {
+    return HRS_EINVAL;
+  }
+  if (d->n_heads < 1 || d->n_kvheads < 1 || d->n_heads > 65535 || d->n_kvheads > 65535 || !dtype_ok(d->dtype))
+    return HRS_EINVAL;
+  if (static_cast<int64_t>(d->n_req) * d->n_pos > (1 << 24)) return HRS_EINVAL;
+  if (d->d < 16 || d->d > 256 || d->d % 16 != 0 || d->rot < 0 || d->rot > d->d || d->rot % 16 != 0)
+    return HRS_EUNSUPPORTED;
+  RopeArgs args;
+  if (!span_stride(d->q_stride, static_cast<int64_t>(d->n_heads) * d->d, &args.q_stride) ||
+      !span_stride(d->k_stride, static_cast<int64_t>(d->n_kvheads) * d->d, &args.k_stride))
+    return HRS_EINVAL;
+  if (!q || !k || !seq_len || !q_out || !k_out || (d->rot > 0 && !freq)) return HRS_EINVAL;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(q_weight) || !aligned16(k_weight) || !aligned16(freq) ||
+      !aligned16(seq_len) || !aligned16(q_out) || !aligned16(k_out))
+    return HRS_EALIGN;
+
+  args.q = q; args.k = k; args.qw = q_weight; args.kw = k_weight; args.freq = freq; args.seq_len = seq_len;
+  args.q_out = q_out; args.k_out = k_out;
+  args.eps = d->eps; args.offset = d->weight_offset;
+  args.n_q = d->n_heads; args.n_heads = d->n_heads + d->n_kvheads;
+  args.d = d->d; args.rot = d->rot; args.interleaved = d->interleaved != 0; args.n_pos = d->n_pos;
+  args.tree = d->topo == HRS_TREE;
+  const int groups = kThreads / (d->d > 128 ? 32 : d->d > 64 ? 16 : 8);
+  const int per_launch = args.tree ? std::max(1, kGeomBytes / d->n_pos) : d->n_req;
+  (void)hipGetLastError();
+  for (int r0 = 0; r0 < d->n_req; r0 += per_launch) {
+    const int n = std::min(per_launch, d->n_req - r0);
+    args.req0 = r0;
+    args.n_tok = n * d->n_pos;
+    if (args.tree)
+      for (int r = 0; r < n; ++r)
+        tree_depths(d->parent + static_cast<size_t>(r0 + r) * d->n_pos, d->n_pos, args.depth + r * d->n_pos);
+    // Few positions: one per block and its heads over several blocks, one
+    // head per lane group. Many: a block takes all heads of its positions,
+    // so that the angles are formed once.
+    const bool few = args.n_tok < 512;
+    args.per_block = few ? 1 : kMaxTokens;
+    const dim3 grid((args.n_tok + args.per_block - 1) / args.per_block,
+                    few ? std::min((args.n_heads + groups - 1) / groups, 65535) : 1);
+    if (d->dtype == HRS_BF16)
+      launch_rope<uint16_t>(args, grid, static_cast<hipStream_t>(stream));
+    else
+      launch_rope<float>(args, grid, static_cast<hipStream_t>(stream));
+    if (launch_error() != hipSuccess) return HRS_EDEVICE;
+  }
+  return HRS_OK;
+}

@@ -75,6 +75,26 @@ int check_topology(int topo, const int32_t* parent, int32_t n_req, int32_t n_pos
   return HRS_OK;
 }
 
+int check_cache(const hrs_cache_desc& c, int span_dtype) {
+  const bool pow2 = c.page_size >= 16 && c.page_size <= 1024 && (c.page_size & (c.page_size - 1)) == 0;
+  if (!pow2 || c.n_pages < 1 || c.table_len < 1) return HRS_EINVAL;
+  // Slot numbers are int32: the table's last slot plus one span must be one.
+  if (static_cast<int64_t>(c.table_len) * c.page_size > INT32_MAX - HRS_MAX_CHUNKED_POS) return HRS_EINVAL;
+  const bool f32 = span_dtype == HRS_F32 && c.dtype == HRS_F32;
+  const bool b16 = span_dtype == HRS_BF16 && (c.dtype == HRS_BF16 || c.dtype == HRS_F8E4M3);
+  return f32 || b16 ? HRS_OK : HRS_EINVAL;
+}
+
+bool span_stride(int64_t given, int64_t dense, int64_t* stride) {
+  *stride = given == 0 ? dense : given;
+  return *stride >= dense && *stride % 8 == 0 && *stride <= (int64_t{1} << 31);
+}
+
+void tree_depths(const int32_t* parent, int32_t n_pos, int8_t* depth) {
+  for (int32_t t = 0; t < n_pos; ++t)
+    depth[t] = parent[t] < 0 ? 0 : static_cast<int8_t>(depth[parent[t]] + 1);
+}
+
 void gdn_tree_schedule(const int32_t* parent, int32_t n_pos, int n_slots, int8_t* restore, int8_t* save) {
   if (n_slots > kStashSlots) n_slots = kStashSlots;
   std::vector<int32_t> last_child(n_pos, -1);   // last child that is not the next position

@@ -22,6 +22,17 @@
  * conv_state_advance (zero-copy rollback), gdn_layer_verify_span (one layer
  * fused into one kernel) and gdn_span_chunked (long spans in chunks).
  *
+ * For the same target's full-attention layers, and for targets that sample:
+ *
+ *   qk_norm_rope        RMS norm of every query and key head and the position
+ *                       rotation, in one pass
+ *   attn_verify_span    attention of the span (chain or draft tree) over a
+ *                       paged cache and the span's own root paths
+ *   kv_cache_append     the accepted path's keys and values into the cache
+ *                       pages of every layer, indices read on the device
+ *   accept_sample       verification of the drafts against the target's
+ *                       probabilities from given random numbers
+ *
  * Conventions shared by every entry point
  * ----------------------------------------
  *  - Memory: every device buffer is allocated and owned by the caller. The
@@ -42,7 +53,10 @@
  *    need (compute units, LDS per block), keyed by the current device.
  *  - Determinism: results are bit-identical from run to run, and the
  *    arithmetic of one position does not depend on the span length or on the
- *    tree topology.
+ *    tree topology (attn_verify_span: bit-identical from run to run of the
+ *    same call; where a context is split among blocks depends on every
+ *    length in the batch, so the same request in another batch agrees to
+ *    rounding only).
  *
  * Sources (the pages this path comes from):
  *  [P1] lucebox PR #533, "feat: DFlash support for tensor-parallel Qwen3.6
@@ -79,7 +93,8 @@ typedef enum {
   HRS_EUNSUPPORTED = -5  /* valid request outside the built kernel set    */
 } hrs_status;
 
-typedef enum { HRS_F32 = 0, HRS_BF16 = 1 } hrs_dtype;
+/* HRS_F8E4M3 (OCP e4m3, no infinities, largest 448) is a cache type only. */
+typedef enum { HRS_F32 = 0, HRS_BF16 = 1, HRS_F8E4M3 = 2 } hrs_dtype;
 
 typedef enum { HRS_CHAIN = 0, HRS_TREE = 1 } hrs_topology;
 
@@ -523,6 +538,245 @@ typedef struct {
  */
 int ring_set_2d(const hrs_ring_desc* desc, void* ring, const void* packed, void* stream);
 int ring_get_2d(const hrs_ring_desc* desc, const void* ring, void* packed, void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* Full-attention layers of the span                                        */
+/* ------------------------------------------------------------------------ */
+
+typedef struct {
+  int32_t n_req;      /* R                                                 */
+  int32_t n_pos;      /* T: chain up to HRS_MAX_CHUNKED_POS, tree up to
+                         HRS_MAX_POS                                       */
+  int32_t n_heads;    /* Hq query heads                                    */
+  int32_t n_kvheads;  /* Hkv key heads                                     */
+  int32_t d;          /* head dim: multiple of 16, at most 256             */
+  int32_t rot;        /* rotated elements of a head: multiple of 16, at
+                         most d; 0 = no rotation                           */
+  hrs_dtype dtype;    /* dtype of q, k, the weights and the outputs        */
+  int64_t q_stride;   /* elements from one position's heads to the next    */
+  int64_t k_stride;   /* position's, in q and in k (R and T collapse):
+                         multiples of 8, at least heads * d; 0 = dense     */
+  float eps;          /* added to the mean square                          */
+  float weight_offset;/* added to every weight (1.0 for zero-centred ones) */
+  int32_t interleaved;/* zero: element i turns with i + rot/2; nonzero: 2i
+                         with 2i + 1                                       */
+  hrs_topology topo;
+  const int32_t* parent; /* host [n_req][n_pos] when topo == HRS_TREE      */
+} hrs_qk_desc;
+
+/*
+ * qk_norm_rope - RMS norm over each query and key head and the rotation by
+ * position, in one pass ([P2] file table: batched Q/K norm and RoPE). Per
+ * request r, position t and head, with x the head's d elements:
+ *     n[i] = x[i] / sqrt(mean(x^2) + eps) * (weight_offset + w[i])
+ *     angle_i = (seq_len[r] + depth(t)) * freq[i],          i < rot / 2
+ *     (n[a], n[b]) -> (n[a] cos - n[b] sin, n[b] cos + n[a] sin)
+ * for the pair (a, b) of angle i; elements from rot on are not turned.
+ * depth(t) is t in a chain and the length of t's root path in a tree. The
+ * angle is formed and reduced to a turn in 64 bits, so far positions are
+ * exact; the rest is float32, rounded once. q_weight or k_weight NULL: that
+ * side is rotated without a norm.
+ *
+ * Layouts:  q [R][T][Hq][d], k [R][T][Hkv][d]   dtype, strided as above
+ *           q_weight, k_weight [d]              dtype (or NULL)
+ *           freq    [rot/2] float64             radians per position
+ *           seq_len [R] int32, device           tokens before the root
+ *           q_out [R][T][Hq][d], k_out [R][T][Hkv][d]  dtype, dense
+ * q_out may be q itself, and k_out k, where that side is dense; any other
+ * overlap is not allowed. Errors: HRS_EINVAL (also R * T > 2^24), HRS_EALIGN,
+ * HRS_EGEOMETRY, HRS_EUNSUPPORTED (d, rot), HRS_EDEVICE.
+ */
+int qk_norm_rope(const hrs_qk_desc* desc, const void* q, const void* k, const void* q_weight,
+                 const void* k_weight, const double* freq, const int32_t* seq_len, void* q_out,
+                 void* k_out, void* stream);
+
+/* A paged key/value cache. One layer's keys (and, in a buffer of its own, its
+ * values) are [n_pages][Hkv][page_size][d]; slot j of request r is row
+ * j % page_size of page page_table[r][j / page_size]. A table entry outside
+ * [0, n_pages) stands for a page that is not there: its slots take no part in
+ * attention and are not written. */
+typedef struct {
+  int32_t n_pages;
+  int32_t page_size;  /* slots per page: a power of two from 16 to 1024    */
+  int32_t table_len;  /* entries per request in the page table             */
+  hrs_dtype dtype;    /* HRS_BF16 or HRS_F8E4M3 beside bf16 spans, HRS_F32
+                         beside f32 spans                                  */
+} hrs_cache_desc;
+
+typedef struct {
+  int32_t n_req;      /* R                                                 */
+  int32_t n_pos;      /* T in [1, HRS_MAX_POS]; 1 = plain decoding         */
+  int32_t n_heads;    /* Hq query heads; Hq % Hkv == 0                     */
+  int32_t n_kvheads;  /* Hkv key/value heads                               */
+  int32_t d;          /* head dim: 64, 128 or 256                          */
+  hrs_dtype dtype;    /* dtype of q, k, v and out: HRS_F32 or HRS_BF16     */
+  int64_t q_stride;   /* elements from one position's heads to the next    */
+  int64_t k_stride;   /* position's (R and T collapse): multiples of 8, at */
+  int64_t v_stride;   /* least heads * d; 0 = dense                        */
+  float scale;        /* of the scores (1 / sqrt(d) as a rule)             */
+  int32_t window;     /* a position sees the last `window` positions, its
+                         own among them; 0 = all                           */
+  hrs_cache_desc cache;
+  hrs_topology topo;
+  const int32_t* parent; /* host [n_req][n_pos] when topo == HRS_TREE      */
+} hrs_attn_desc;
+
+/* Bytes of device workspace attn_verify_span needs for these sizes (0 for a
+ * NULL descriptor or sizes out of range). It does not depend on lengths. */
+size_t attn_verify_span_workspace_bytes(const hrs_attn_desc* desc);
+
+/*
+ * attn_verify_span - attention of a verify span over a paged cache: the
+ * full-attention layers' counterpart of gdn_verify_span ([P2] file table:
+ * causal-window attention over pages; [P1] Verification: DDTree). Query
+ * (r, t, h), key/value head g = h / (Hq/Hkv), n = seq_len[r]:
+ *     out = sum_j w_j v_j,  w = softmax over j of scale (q . k_j)
+ * over the context slots j in [0, n) of request r, read from the cache, and
+ * the span positions on t's root path (t among them), read from k and v, the
+ * span's own rows, which need not be in the cache. With a window W only slots
+ * j > n + depth(t) - W and path positions s with depth(t) - depth(s) < W
+ * count. Cached e4m3 values stand for k_scale[g], v_scale[g] times themselves
+ * (NULL: 1); span rows are taken as they are. What does not count has no
+ * influence, whatever it holds (infinities and NaN included); a query that
+ * nothing counts for gives zeros. Sums and softmax statistics are float32;
+ * bf16 spans round the weights to bf16 for the product with the values.
+ *
+ * Layouts:  q [R][T][Hq][d], k, v [R][T][Hkv][d]  dtype, strided as above
+ *           k_cache, v_cache [n_pages][Hkv][page_size][d]  cache.dtype
+ *           page_table [R][table_len] int32, seq_len [R] int32, device
+ *           k_scale, v_scale [Hkv] float32, device (e4m3 caches only;
+ *           4-byte aligned, so rows of an [L][Hkv] array will do)
+ *           out [R][T][Hq][d] dtype, dense
+ *           workspace: device scratch of at least
+ *           attn_verify_span_workspace_bytes(desc) bytes, contents ignored
+ * A request whose seq_len is outside [0, table_len * page_size] keeps its
+ * rows of out as they were; status (optional device int32) receives the
+ * number of such requests. Calls that may run at the same time need
+ * workspaces of their own. Errors: HRS_EINVAL (sizes, dtype combination,
+ * R > 4096, Hq / Hkv > 64), HRS_EALIGN, HRS_EGEOMETRY, HRS_EUNSUPPORTED
+ * (d), HRS_EDEVICE.
+ */
+int attn_verify_span(const hrs_attn_desc* desc, const void* q, const void* k, const void* v,
+                     const void* k_cache, const void* v_cache, const int32_t* page_table,
+                     const int32_t* seq_len, const float* k_scale, const float* v_scale, void* out,
+                     int32_t* status, void* workspace, size_t workspace_bytes, void* stream);
+
+typedef struct {
+  int32_t n_layers;   /* L                                                 */
+  int32_t n_req;      /* R                                                 */
+  int32_t n_pos;      /* T of the span; up to HRS_MAX_POS with a path, up to
+                         HRS_MAX_CHUNKED_POS without                       */
+  int32_t n_kvheads;  /* Hkv                                               */
+  int32_t d;          /* head dim: multiple of 16, at most 256             */
+  hrs_dtype dtype;    /* dtype of k and v                                  */
+  int64_t k_stride;   /* elements from one position's heads to the next    */
+  int64_t v_stride;   /* position's (L, R and T collapse): multiples of 8,
+                         at least Hkv * d; 0 = dense                       */
+  hrs_cache_desc cache;
+} hrs_append_desc;
+
+/*
+ * kv_cache_append - the accepted rows of a span into the cache pages of every
+ * layer, in one launch, with the accepted path read from device memory: the
+ * full-attention layers' counterpart of conv_state_advance. For every layer
+ * l, request r and i in [0, accept_len[r]], j = seq_len[r] + i:
+ *     cache[l][page_table[r][j / page_size]][h][j % page_size]
+ *         = span[l][r][path[r][i]][h]                (keys and values)
+ *     seq_len_out[r] = seq_len[r] + accept_len[r] + 1
+ * path NULL: the identity (chains, prefill). Same dtype: exact copies. e4m3
+ * caches: divided by k_scale[l][h], v_scale[l][h] (NULL: 1), limited to
+ * +-448 and rounded to the nearest e4m3, ties to even; NaN stays NaN.
+ *
+ * Layouts:  k, v [L][R][T][Hkv][d] dtype, strided as above
+ *           k_cache, v_cache [L][n_pages][Hkv][page_size][d] cache.dtype
+ *           page_table [R][table_len], seq_len [R], accept_len [R],
+ *           path [R][T] (or NULL) int32, device
+ *           k_scale, v_scale [L][Hkv] float32, device (e4m3 caches only;
+ *           4-byte aligned)
+ *           seq_len_out [R] int32, device: seq_len itself, a buffer apart
+ *           from it, or NULL
+ * A request is left untouched (seq_len_out[r] = seq_len[r]) and counted in
+ * status (optional device int32) when accept_len is outside [0, T), seq_len
+ * is negative, seq_len + accept_len + 1 > table_len * page_size, or one of
+ * its path entries is outside [0, T). Rows whose page is not there are not
+ * written. Two requests of one call must not write the same slot. Errors:
+ * HRS_EINVAL (sizes, dtype combination, L or R > 65535, R * T > 2^24),
+ * HRS_EALIGN, HRS_EUNSUPPORTED (d), HRS_EDEVICE.
+ */
+int kv_cache_append(const hrs_append_desc* desc, const void* k, const void* v, void* k_cache,
+                    void* v_cache, const int32_t* page_table, const int32_t* seq_len,
+                    const int32_t* accept_len, const int32_t* path, const float* k_scale,
+                    const float* v_scale, int32_t* seq_len_out, int32_t* status, void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* Acceptance by sampling                                                   */
+/* ------------------------------------------------------------------------ */
+
+typedef struct {
+  int32_t n_req;   /* R                                                    */
+  int32_t n_pos;   /* T (rows of logits per request)                       */
+  int32_t vocab;   /* V, multiple of 8                                     */
+  hrs_dtype logit_dtype;
+  hrs_dtype draft_dtype; /* dtype of draft_probs (ignored without them)    */
+  hrs_topology topo;
+  const int32_t* parent; /* host [n_req][n_pos] when topo == HRS_TREE      */
+} hrs_sample_desc;
+
+/* Bytes of device workspace accept_sample needs for this descriptor
+ * (0 if the descriptor is invalid). */
+size_t accept_sample_workspace_bytes(const hrs_sample_desc* desc);
+
+/*
+ * accept_sample - verification of one draft block per request against the
+ * target's probabilities, from given random numbers: the kept tokens and the
+ * next one are distributed as if drawn from the target itself. It stands
+ * beside accept_greedy for requests that sample. With p_t the softmax of
+ * logits[r][t] / temperature[r], x_t = tokens[r][t], u_t = uniforms[r][t]:
+ *
+ *  With draft_probs (chain only; row t is the distribution q_t that x_{t+1}
+ *  was drawn from): starting at the root, t = 1, 2, ... is accepted while
+ *      u_t q_{t-1}(x_t) < p_{t-1}(x_t);
+ *  at the first position that is not, the rest is max(p_{t-1} - q_{t-1}, 0).
+ *  Without draft_probs (chain or tree; drafts were picked, not drawn): at a
+ *  node n the rest starts as p_n; n's children are tried in index order, and
+ *  child t is accepted, and the walk goes on from it, when
+ *      u_t (1 - sum of p_n over the tokens already rejected at n) < p_n(x_t);
+ *  a token that is not accepted is taken out of the rest (a second child
+ *  with the same token is never accepted).
+ *  accept_node, accept_len, path: the last accepted position, its depth and
+ *  root path (then -1), as accept_greedy.
+ *  bonus[r] = the first v in index order with a positive weight and
+ *      weight(0) + ... + weight(v) > u_0 (total weight)
+ *  where weight is the rest at accept_node (p itself where every draft of the
+ *  chain was accepted, where the node has no children, or where the rest is
+ *  zero everywhere); the last v with a positive weight if there is none.
+ *  token_prob[r][t] = p_{parent(t)}(x_t), float32; 1 for the root.
+ *
+ * Random numbers are meant to be in [0, 1) and independent. A NaN logit has
+ * probability zero; +inf logits share the whole probability; a row without
+ * any finite or +inf logit has p = 0 everywhere and bonus 0. Temperature 0 is
+ * the limit (the largest logits share the probability); NULL means 1. A
+ * token outside [0, V) has probability zero. A request whose temperature is
+ * negative or NaN keeps its outputs as they were; status (optional device
+ * int32) receives the number of such requests. Probabilities are float32
+ * with 64-bit sums; the bonus draw (weights, total and cumulative sums) is in
+ * 64 bits, where the border of a long float32 sum would decide.
+ *
+ * Layouts:  logits [R][T][V] logit_dtype; tokens [R][T] int32;
+ *           uniforms [R][T] float32; draft_probs [R][T][V] draft_dtype or
+ *           NULL; temperature [R] float32 or NULL; token_prob [R][T] float32;
+ *           accept_node, accept_len, bonus [R], path [R][T] int32; all
+ *           device. workspace: device scratch of at least
+ *           accept_sample_workspace_bytes(desc) bytes, contents ignored.
+ * Size limits as accept_greedy, and R <= 65535. Errors: HRS_EINVAL,
+ * HRS_EALIGN, HRS_EGEOMETRY, HRS_EUNSUPPORTED (draft_probs with a tree),
+ * HRS_EDEVICE.
+ */
+int accept_sample(const hrs_sample_desc* desc, const void* logits, const int32_t* tokens,
+                  const float* uniforms, const void* draft_probs, const float* temperature,
+                  float* token_prob, int32_t* accept_node, int32_t* accept_len, int32_t* path,
+                  int32_t* bonus, int32_t* status, void* workspace, size_t workspace_bytes,
+                  void* stream);
 
 /* ------------------------------------------------------------------------ */
 /* Misc                                                                     */

@@ -38,7 +38,12 @@ What each module computes and where it comes from:
   fused     - one layer in its own order: conv with SiLU, split into q/k/v
               heads, q/k L2 norm, gated delta rule (composition of the above).
 
+  attn      - the full-attention layer: per-head norm and rotation, attention
+              over a paged cache and the span's root paths, accepted rows
+              into the pages (openinfer PR #626, file table)
+  sample    - acceptance by sampling from given random numbers
+
 Parity status of each function is stated in its module header.
 """
-from . import accept, conv, fused, gdn, geometry, ring, rollback  # noqa: F401
+from . import accept, attn, conv, fused, gdn, geometry, ring, rollback, sample  # noqa: F401
 from .common import widen  # noqa: F401
