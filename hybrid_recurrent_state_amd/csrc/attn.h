@@ -1,0 +1,106 @@
+// Device side of attn_verify_span, shared by the translation units that build
+// it for one span and cache type each (attn.hip: host side and join;
+// attn_f32.hip, attn_bf16.hip, attn_f8.hip: the kernels).
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include "device.h"
+#include "internal.h"
+
+namespace hrs {
+
+constexpr int kAttnBlocks = 256;       // blocks of a launch at most: one per CU
+constexpr int kAttnReqs = 256;         // requests of a launch at most
+constexpr int kF32 = 0, kB16 = 1, kF8 = 2;   // span/cache types: f32/f32, bf16/bf16, bf16/e4m3
+
+struct AttnArgs {
+  const void* q;
+  const void* k;
+  const void* v;
+  const char* k_cache;
+  const char* v_cache;
+  const int32_t* page_table;
+  const int32_t* seq_len;
+  const float* k_scale;
+  const float* v_scale;
+  void* out;
+  int32_t* status;
+  int64_t* plan;      // workspace: units before every request [n + 1], for the join
+  float* part;        // workspace: partial sums [2 * blocks][rows][d]
+  float2* part_ml;    // workspace: their maximum and sum [2 * blocks][rows]
+  int64_t q_stride;
+  int64_t k_stride;
+  int64_t v_stride;
+  float scale;
+  int32_t window;
+  int32_t n_req;      // of the whole call
+  int32_t req0;       // of this launch
+  int32_t n_here;
+  int32_t n_pos;
+  int32_t kvheads;
+  int32_t group;      // query heads per key/value head
+  int32_t rows;       // n_pos * group
+  int32_t row_blocks;
+  int32_t n_pages;
+  int32_t page_shift;
+  int32_t table_len;
+  int32_t tree;
+  int8_t parent[kGeomBytes];
+};
+
+// How a block is built for a type, a head size and a class of row counts
+// (0: at most 16 rows a key/value head, 1: 32, 2: 64, 3: blocks of 128). WR
+// waves share the slots of a tile with different rows, WK such groups take
+// different slots; a wave holds RT tiles of 16 rows and SS slots of a tile.
+template <int KIND, int D, int CLS> struct AttnCfg {
+  static constexpr int ESZ = KIND == kF32 ? 4 : 2;          // bytes of an element in LDS
+  static constexpr bool WIDE = D == 256;
+  static constexpr int RT = CLS == 0 || (CLS == 3 && WIDE) ? 1 : 2;
+  static constexpr int WR = CLS < 2 ? 1 : CLS == 2 ? 2 : WIDE ? 8 : 4;
+  static constexpr int WK = CLS < 2 ? (KIND == kF32 && WIDE ? 2 : 4) : CLS == 3 && WIDE ? 1 : 2;
+  static constexpr int SS = CLS < 2 ? 16 : CLS == 2 ? (WIDE && KIND != kB16 ? 16 : 32)
+                                                    : (KIND == kF32 && D == 128 ? 16 : 32);
+  static constexpr int NW = WR * WK;
+  static constexpr int NT = 64 * NW;
+  static constexpr int ROWS = 16 * RT * WR;
+  static constexpr int TS = SS * WK;                        // slots of a tile
+  static constexpr int STAGE = 2 * TS * D * ESZ;            // keys and values of a tile, in the products' type
+  static constexpr int NB = KIND == kF8 && WR > 1 ? 2 : 1;  // converted tiles (e4m3)
+  static constexpr int RAW = KIND == kF8 ? STAGE / 2 : STAGE;
+  static constexpr int ROOM = 131072 - (KIND == kF8 ? NB * STAGE : 0);
+  static constexpr int NST = ROOM / RAW < 4 ? ROOM / RAW : 4;   // tiles on their way
+  static constexpr int RING = KIND == kF8 ? NB * STAGE : 0;     // where the ring of loaded tiles starts
+  static constexpr int OROW = D * 4 + 16;                   // joined row in LDS, shifted by four banks a row
+  static constexpr int JOIN = WK * ROWS * (OROW + 8);
+  static constexpr int LDS = RING + NST * RAW > JOIN ? RING + NST * RAW : JOIN;
+  static constexpr int SPAN_UNITS = 64 / TS > 0 ? 64 / TS : 1;
+  static_assert(NST >= 2 && LDS <= 155 * 1024, "tiles fit");
+};
+
+// Work is counted in units: a unit is one tile of one (request, key/value
+// head, row block); the context's tiles come first, the span's last.
+struct AttnUnits {
+  int first;   // first context tile that a window leaves in reach
+  int ctx;     // context tiles
+  int all;     // and the span's
+};
+
+__device__ __forceinline__ AttnUnits attn_units(const AttnArgs& a, int r, int ts, int* len_out) {
+  const int len = a.seq_len[r];
+  *len_out = len;
+  if (len < 0 || len > (a.table_len << a.page_shift)) return {0, 0, 0};
+  const int first = a.window > 0 && len + 1 > a.window ? (len + 1 - a.window) / ts : 0;
+  const int ctx = max(0, (len + ts - 1) / ts - first);
+  return {first, ctx, ctx + (a.n_pos + ts - 1) / ts};
+}
+
+// Launches of one type (rows class cls, head size d); the number of rows a
+// block holds and the slots of its tile for it.
+struct AttnShape {
+  int rows, ts, nt;
+};
+template <int KIND> AttnShape attn_shape(int d, int cls);
+template <int KIND> void attn_launch(const AttnArgs& args, int d, int cls, int blocks, hipStream_t s);
+
+}  // namespace hrs

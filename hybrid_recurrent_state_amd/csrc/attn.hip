@@ -1,181 +1,108 @@
 // attn_verify_span: attention of a verify span (chain or draft tree) over a
-// paged cache and the span's own root paths.
-//
-//   out = sum_j w_j v_j,  w = softmax_j(scale q . k_j)
+// paged cache and the span's own root paths. Host side, and the join of the
+// parts that the kernel (attn_kernel.h) leaves where a block's run of tiles
+// ends inside a (request, key/value head).
 //
 // openinfer PR #626 ("feat(qwen35): add opt-in DFlash speculative decoding"),
 // file table: the paged causal-window attention of the verify forward;
 // lucebox PR #533 ("feat: DFlash support for tensor-parallel Qwen3.6
 // targets"), Verification: DDTree.
-//
-// One wave per query head and position, slots in groups of 64 with a running
-// maximum and sum: the plain form of the softmax in one pass.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
 
-#include "device.h"
-#include "internal.h"
+#include "attn.h"
 
 namespace hrs {
 namespace {
 
-struct AttnArgs {
-  const void* q;
-  const void* k;
-  const void* v;
-  const void* k_cache;
-  const void* v_cache;
-  const int32_t* page_table;
-  const int32_t* seq_len;
-  const float* k_scale;
-  const float* v_scale;
-  void* out;
-  int32_t* status;
-  int64_t q_stride;
-  int64_t k_stride;
-  int64_t v_stride;
-  float scale;
-  int32_t window;
-  int32_t n_req;      // of the whole call
-  int32_t n_pos;
-  int32_t heads;
-  int32_t kvheads;
-  int32_t n_pages;
-  int32_t page_shift;
-  int32_t table_len;
-  int32_t req0;
-  int32_t tree;
-  int8_t parent[kGeomBytes];
-};
-
-struct F8 { uint8_t b; };   // e4m3
-
-template <typename T> __device__ __forceinline__ float elem(const T* p);
-template <> __device__ __forceinline__ float elem<float>(const float* p) { return *p; }
-template <> __device__ __forceinline__ float elem<uint16_t>(const uint16_t* p) { return bf16_one(*p); }
-template <> __device__ __forceinline__ float elem<F8>(const F8* p) {
-  return __builtin_amdgcn_cvt_f32_fp8(static_cast<int>(p->b), 0);
+// Sum of a segment's parts: out = sum_b 2^(m_b - M) O_b / sum_b 2^(m_b - M)
+// l_b. Block x: segment x (request, head, row block), y: rows. A thread holds
+// four elements of a row; its loads of the parts do not depend on each other.
+template <bool F32, int D>
+__global__ __launch_bounds__(256) void attn_join_kernel(const AttnArgs args, int rows_per_block, int ts, int grid) {
+  const int heads = args.kvheads * args.row_blocks;
+  const int i = blockIdx.x / heads;
+  const int seg = blockIdx.x - i * heads;
+  const int h = seg / args.row_blocks, rb = seg - h * args.row_blocks;
+  const int r = args.req0 + i;
+  const int64_t total = args.plan[args.n_here];
+  const int64_t first = args.plan[i], end = args.plan[i + 1];
+  if (end == first) return;
+  const int64_t units = (end - first) / heads;
+  const int64_t s0 = first + seg * units, s1 = s0 + units;
+  const int64_t blocks = min(static_cast<int64_t>(grid), total);
+  // Block of a unit: the last whose run starts at or before it.
+  const int b0 = static_cast<int>(((s0 + 1) * blocks - 1) / total);
+  const int b1 = static_cast<int>((s1 * blocks - 1) / total);
+  if (b0 == b1) return;                       // one block had all of it and wrote the result
+  const int row = blockIdx.y * (256 / (D / 4)) + threadIdx.x / (D / 4);
+  const int d4 = threadIdx.x % (D / 4);
+  const int rows = min(rows_per_block, args.rows - rb * rows_per_block);
+  if (row >= rows) return;
+  // The segment's first block left it as its last, the others as their first.
+  auto slot = [&](int b) { return 2 * b + (b == b0 ? 1 : 0); };
+  float M = -__builtin_inff();
+#pragma unroll 8
+  for (int b = b0; b <= b1; ++b) M = fmaxf(M, args.part_ml[static_cast<int64_t>(slot(b)) * rows_per_block + row].x);
+  f32x4 sum = {};
+  float ls = 0.0f;
+#pragma unroll 8
+  for (int b = b0; b <= b1; ++b) {
+    const int64_t at = static_cast<int64_t>(slot(b)) * rows_per_block + row;
+    const float2 w = args.part_ml[at];
+    const f32x4 x = *reinterpret_cast<const f32x4*>(args.part + at * D + d4 * 4);
+    if (w.x == -__builtin_inff() && w.y == 0.0f) continue;     // no slot counted
+    const float f = w.x == M ? 1.0f : __builtin_amdgcn_exp2f(w.x - M);
+    ls += w.y * f;
+    sum += x * f;
+  }
+  const int at_row = rb * rows_per_block + row;
+  const int t = at_row / args.group, hq = h * args.group + at_row - t * args.group;
+  const f32x4 y = ls == 0.0f ? f32x4{} : sum * (1.0f / ls);
+  const int64_t at = ((static_cast<int64_t>(r) * args.n_pos + t) * (args.kvheads * args.group) + hq) * D + d4 * 4;
+  if constexpr (F32)
+    *reinterpret_cast<f32x4*>(static_cast<float*>(args.out) + at) = y;
+  else
+    *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(args.out) + at) =
+        u32x2{pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3])};
 }
 
-template <typename T, typename C, int D>
-__global__ __launch_bounds__(64) void attn_simple_kernel(const AttnArgs args) {
-  const int lane = threadIdx.x;
-  const int h = blockIdx.x, t = blockIdx.y, rl = blockIdx.z, r = args.req0 + rl;
-  const int g = h / (args.heads / args.kvheads);
-  if (h == 0 && t == 0 && r == 0 && lane == 0 && args.status) {
-    int bad = 0;
-    for (int i = 0; i < args.n_req; ++i) {
-      const int n = args.seq_len[i];
-      bad += n < 0 || n > (args.table_len << args.page_shift);
-    }
-    *args.status = bad;
-  }
-  const int len = args.seq_len[r];
-  if (len < 0 || len > (args.table_len << args.page_shift)) return;
-  // Root path and window inside the span.
-  uint64_t path = 0;
-  int depth = 0;
-  for (int a = t; a >= 0; a = args.tree ? args.parent[rl * args.n_pos + a] : a - 1) ++depth;
-  --depth;
-  for (int a = t, i = 0; a >= 0 && (args.window == 0 || i < args.window);
-       a = args.tree ? args.parent[rl * args.n_pos + a] : a - 1, ++i)
-    path |= uint64_t{1} << a;
-  const int first = args.window ? max(0, len + depth + 1 - args.window) : 0;
-
-  const int64_t row = static_cast<int64_t>(r) * args.n_pos + t;
-  __shared__ float qs[D];
-  __shared__ float ps[64];
-  const T* q = static_cast<const T*>(args.q) + row * args.q_stride + static_cast<int64_t>(h) * D;
-  for (int i = lane; i < D; i += 64) qs[i] = elem<T>(q + i);
-  __syncthreads();
-  float o[D / 64] = {};
-  float m = -__builtin_inff(), l = 0.0f;
-  const float ks = args.k_scale ? args.k_scale[g] : 1.0f, vs = args.v_scale ? args.v_scale[g] : 1.0f;
-  const int end = len + args.n_pos;
-  for (int j0 = first & ~63; j0 < end; j0 += 64) {
-    const int j = j0 + lane;
-    const bool ctx = j < len;
-    bool on = ctx ? j >= first : j < end && ((path >> (j - len)) & 1);
-    const C* kc = nullptr;
-    const T* kt = nullptr;
-    int64_t off = 0;
-    if (on) {
-      if (ctx) {
-        const int page = args.page_table[static_cast<int64_t>(r) * args.table_len + (j >> args.page_shift)];
-        on = page >= 0 && page < args.n_pages;
-        off = (((static_cast<int64_t>(page) * args.kvheads + g) << args.page_shift) + (j & ((1 << args.page_shift) - 1))) * D;
-        kc = static_cast<const C*>(args.k_cache) + off;
-      } else {
-        kt = static_cast<const T*>(args.k) + (static_cast<int64_t>(r) * args.n_pos + j - len) * args.k_stride +
-             static_cast<int64_t>(g) * D;
-      }
-    }
-    float s = -__builtin_inff();
-    if (on) {
-      float a = 0.0f;
-      if (ctx)
-        for (int i = 0; i < D; ++i) a = fmaf(qs[i], elem<C>(kc + i), a);
-      else
-        for (int i = 0; i < D; ++i) a = fmaf(qs[i], elem<T>(kt + i), a);
-      s = a * args.scale * (ctx ? ks : 1.0f);
-    }
-    float mx = s;
-    for (int x = 32; x >= 1; x >>= 1) mx = fmaxf(mx, __shfl_xor(mx, x));
-    const float mn = fmaxf(m, mx);
-    const float base = mn == -__builtin_inff() ? 0.0f : mn;
-    const float keep = expf(m - base);
-    const float p = on ? expf(s - base) : 0.0f;
-    float sum = p;
-    for (int x = 32; x >= 1; x >>= 1) sum += __shfl_xor(sum, x);
-    l = l * keep + sum;
-    m = mn;
-    for (int i = 0; i < D / 64; ++i) o[i] *= keep;
-    ps[lane] = p;
-    const uint64_t live = __ballot(on);
-    __syncthreads();
-    for (uint64_t b = live; b; b &= b - 1) {
-      const int i = __builtin_ctzll(b);
-      const int jj = j0 + i;
-      const int64_t o2 = __shfl(off, i);
-      for (int e = 0; e < D / 64; ++e) {
-        float v;
-        if (jj < len)
-          v = elem<C>(static_cast<const C*>(args.v_cache) + o2 + e * 64 + lane) * vs;
-        else
-          v = elem<T>(static_cast<const T*>(args.v) +
-                      (static_cast<int64_t>(r) * args.n_pos + jj - len) * args.v_stride +
-                      static_cast<int64_t>(g) * D + e * 64 + lane);
-        o[e] = fmaf(ps[i], v, o[e]);
-      }
-    }
-    __syncthreads();
-  }
-  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-  for (int e = 0; e < D / 64; ++e) {
-    const float y = l == 0.0f ? 0.0f : o[e] * inv;
-    const int64_t at = (row * args.heads + h) * D + e * 64 + lane;
-    if constexpr (sizeof(T) == 2)
-      static_cast<uint16_t*>(args.out)[at] = static_cast<uint16_t>(pack_bf16(y, 0.0f) & 0xFFFFu);
-    else
-      static_cast<float*>(args.out)[at] = y;
-  }
+template <bool F32> void launch_join(const AttnArgs& args, int d, const AttnShape& sh, int grid, hipStream_t s) {
+  const int rows = std::min(sh.rows, args.rows);
+  const int per = 256 / (d / 4);
+  const dim3 g(args.n_here * args.kvheads * args.row_blocks, (rows + per - 1) / per);
+  if (d == 64) hipLaunchKernelGGL((attn_join_kernel<F32, 64>), g, dim3(256), 0, s, args, sh.rows, sh.ts, grid);
+  if (d == 128) hipLaunchKernelGGL((attn_join_kernel<F32, 128>), g, dim3(256), 0, s, args, sh.rows, sh.ts, grid);
+  if (d == 256) hipLaunchKernelGGL((attn_join_kernel<F32, 256>), g, dim3(256), 0, s, args, sh.rows, sh.ts, grid);
 }
+
+bool sizes_ok(const hrs_attn_desc* d) {
+  return d && d->n_req >= 1 && d->n_req <= 4096 && d->n_pos >= 1 && d->n_pos <= HRS_MAX_POS && d->n_heads >= 1 &&
+         d->n_kvheads >= 1 && d->n_kvheads <= 1024 && d->n_heads % d->n_kvheads == 0 &&
+         d->n_heads / d->n_kvheads <= 64;
+}
+
+int rows_class(int rows) { return rows <= 16 ? 0 : rows <= 32 ? 1 : rows <= 64 ? 2 : 3; }
+
+AttnShape shape_of(const hrs_attn_desc* d, int kind) {
+  const int cls = rows_class(d->n_pos * (d->n_heads / d->n_kvheads));
+  return kind == kF32 ? attn_shape<kF32>(d->d, cls) : kind == kB16 ? attn_shape<kB16>(d->d, cls)
+                                                                   : attn_shape<kF8>(d->d, cls);
+}
+
+constexpr size_t kPlanBytes = ((kAttnReqs + 1) * sizeof(int64_t) + 255) / 256 * 256;
 
 }  // namespace
 }  // namespace hrs
 
 using namespace hrs;
 
-static bool attn_sizes_ok(const hrs_attn_desc* d) {
-  return d && d->n_req >= 1 && d->n_req <= 4096 && d->n_pos >= 1 && d->n_pos <= HRS_MAX_POS && d->n_heads >= 1 &&
-         d->n_kvheads >= 1 && d->n_kvheads <= 1024 && d->n_heads % d->n_kvheads == 0 &&
-         d->n_heads / d->n_kvheads <= 64;
-}
-
 extern "C" size_t attn_verify_span_workspace_bytes(const hrs_attn_desc* d) {
-  if (!attn_sizes_ok(d) || (d->d != 64 && d->d != 128 && d->d != 256)) return 0;
-  return 16;
+  if (!sizes_ok(d) || (d->d != 64 && d->d != 128 && d->d != 256)) return 0;
+  // The rows that a block holds depend on the sizes alone, not on the types.
+  const size_t rows = shape_of(d, kB16).rows;
+  return kPlanBytes + 2 * kAttnBlocks * rows * (static_cast<size_t>(d->d) * sizeof(float) + sizeof(float2));
 }
 
 extern "C" int attn_verify_span(const hrs_attn_desc* d, const void* q, const void* k, const void* v,
@@ -189,7 +116,7 @@ extern "C" int attn_verify_span(const hrs_attn_desc* d, const void* q, const voi
   } else {
     return HRS_EINVAL;
   }
-  if (!attn_sizes_ok(d) || !dtype_ok(d->dtype) || d->window < 0) return HRS_EINVAL;
+  if (!sizes_ok(d) || !dtype_ok(d->dtype) || d->window < 0) return HRS_EINVAL;
   const int cc = check_cache(d->cache, d->dtype);
   if (cc != HRS_OK) return cc;
   if (d->d != 64 && d->d != 128 && d->d != 256) return HRS_EUNSUPPORTED;
@@ -206,36 +133,43 @@ extern "C" int attn_verify_span(const hrs_attn_desc* d, const void* q, const voi
       !aligned16(out) || !aligned16(status) || !aligned16(workspace))
     return HRS_EALIGN;
 
-  args.q = q; args.k = k; args.v = v; args.k_cache = k_cache; args.v_cache = v_cache; args.page_table = page_table;
-  args.seq_len = seq_len; args.k_scale = k_scale; args.v_scale = v_scale; args.out = out; args.status = status;
+  const int kind = d->dtype == HRS_F32 ? kF32 : d->cache.dtype == HRS_BF16 ? kB16 : kF8;
+  const AttnShape sh = shape_of(d, kind);
+  args.q = q; args.k = k; args.v = v;
+  args.k_cache = static_cast<const char*>(k_cache); args.v_cache = static_cast<const char*>(v_cache);
+  args.page_table = page_table; args.seq_len = seq_len; args.k_scale = k_scale; args.v_scale = v_scale;
+  args.out = out; args.status = status;
+  char* const ws = static_cast<char*>(workspace);
+  args.plan = reinterpret_cast<int64_t*>(ws);
+  args.part = reinterpret_cast<float*>(ws + kPlanBytes);
+  args.part_ml = reinterpret_cast<float2*>(ws + kPlanBytes + sizeof(float) * 2 * kAttnBlocks * sh.rows * d->d);
   args.scale = d->scale; args.window = d->window; args.n_req = d->n_req; args.n_pos = d->n_pos;
-  args.heads = d->n_heads; args.kvheads = d->n_kvheads;
+  args.kvheads = d->n_kvheads; args.group = d->n_heads / d->n_kvheads;
+  args.rows = args.n_pos * args.group;
+  args.row_blocks = (args.rows + sh.rows - 1) / sh.rows;
   args.n_pages = d->cache.n_pages; args.table_len = d->cache.table_len;
   args.page_shift = __builtin_ctz(static_cast<unsigned>(d->cache.page_size));
   args.tree = d->topo == HRS_TREE;
-  const int per_launch = args.tree ? std::max(1, kGeomBytes / d->n_pos) : d->n_req;
+  const int per_launch = args.tree ? std::min(kAttnReqs, std::max(1, kGeomBytes / d->n_pos)) : kAttnReqs;
+  const int cls = rows_class(args.rows);
   const hipStream_t s = static_cast<hipStream_t>(stream);
   (void)hipGetLastError();
   for (int r0 = 0; r0 < d->n_req; r0 += per_launch) {
-    const int n = std::min(per_launch, d->n_req - r0);
     args.req0 = r0;
+    args.n_here = std::min(per_launch, d->n_req - r0);
     if (args.tree)
-      for (int i = 0; i < n * d->n_pos; ++i)
+      for (int i = 0; i < args.n_here * d->n_pos; ++i)
         args.parent[i] = static_cast<int8_t>(d->parent[static_cast<size_t>(r0) * d->n_pos + i]);
-    const dim3 grid(d->n_heads, d->n_pos, n);
-#define HRS_ATTN(T, C)                                                                                  \
-  do {                                                                                                  \
-    if (d->d == 64) hipLaunchKernelGGL((attn_simple_kernel<T, C, 64>), grid, dim3(64), 0, s, args);     \
-    if (d->d == 128) hipLaunchKernelGGL((attn_simple_kernel<T, C, 128>), grid, dim3(64), 0, s, args);   \
-    if (d->d == 256) hipLaunchKernelGGL((attn_simple_kernel<T, C, 256>), grid, dim3(64), 0, s, args);   \
-  } while (0)
-    if (d->dtype == HRS_F32)
-      HRS_ATTN(float, float);
-    else if (d->cache.dtype == HRS_BF16)
-      HRS_ATTN(uint16_t, uint16_t);
-    else
-      HRS_ATTN(uint16_t, F8);
-#undef HRS_ATTN
+    // No more blocks than the longest contexts the table could hold have tiles.
+    const int64_t slots = (static_cast<int64_t>(args.table_len) << args.page_shift) + HRS_MAX_POS;
+    const int64_t most = static_cast<int64_t>(args.n_here) * args.kvheads * args.row_blocks * (slots / sh.ts + 2);
+    const int grid = static_cast<int>(std::min<int64_t>(kAttnBlocks, most));
+    if (kind == kF32) attn_launch<kF32>(args, d->d, cls, grid, s);
+    else if (kind == kB16) attn_launch<kB16>(args, d->d, cls, grid, s);
+    else attn_launch<kF8>(args, d->d, cls, grid, s);
+    if (launch_error() != hipSuccess) return HRS_EDEVICE;
+    if (kind == kF32) launch_join<true>(args, d->d, sh, grid, s);
+    else launch_join<false>(args, d->d, sh, grid, s);
     if (launch_error() != hipSuccess) return HRS_EDEVICE;
   }
   return HRS_OK;

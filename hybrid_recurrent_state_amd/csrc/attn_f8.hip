@@ -1,0 +1,7 @@
+// attn_verify_span for one span and cache type (attn_kernel.h).
+#include "attn_kernel.h"
+
+namespace hrs {
+template AttnShape attn_shape<kF8>(int, int);
+template void attn_launch<kF8>(const AttnArgs&, int, int, int, hipStream_t);
+}  // namespace hrs
