@@ -61,9 +61,18 @@ __device__ __forceinline__ void block_barrier() {
   mem_fence();
 }
 
-__device__ __forceinline__ u32x2 read_tr16(const char* p) {
-  const s16x4 v =
-      __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(const_cast<char*>(p)));
+__device__ __forceinline__ uint32_t lds_address(const char* p) {
+  return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((const lds_char*)p));
+}
+// LDS by its byte address.
+template <typename T> __device__ __forceinline__ const __attribute__((address_space(3))) T* lds_at(uint32_t a) {
+  return reinterpret_cast<const __attribute__((address_space(3))) T*>(a);
+}
+
+// Within each group of 16 lanes, lane i receives as its j-th value element
+// i % 4 of the four 16-bit values that lane 4 j + i / 4 addresses.
+__device__ __forceinline__ u32x2 read_tr16(uint32_t a) {
+  const s16x4 v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)a);
   return __builtin_bit_cast(u32x2, v);
 }
 
@@ -90,6 +99,12 @@ template <int CPR> __device__ __forceinline__ int swizzle(int row) {
 
 __device__ __forceinline__ bool not_finite(float x) { return (__float_as_uint(x) & 0x7F800000u) == 0x7F800000u; }
 
+// What a mask needs to know of a block's query rows.
+template <int ROWS> struct AttnRows {
+  uint64_t anc[ROWS];     // span positions that count, one bit each
+  int32_t first[ROWS];    // first context slot that counts; no row: past all
+};
+
 template <int KIND, int D, int CLS> struct AttnBlock {
   using C = AttnCfg<KIND, D, CLS>;
   static constexpr int ESZ = C::ESZ, CPR = D * ESZ / 16, SB = C::SS / 16;
@@ -103,13 +118,11 @@ template <int KIND, int D, int CLS> struct AttnBlock {
 
   const AttnArgs& a;
   char* lds;
+  AttnRows<C::ROWS>* rows;
   int wave, lane, wr, kg, n16, g;
   // the segment
   int r, h, len, n_units, rb;
   AttnUnits un;
-  int row_t[C::RT];            // span position of this lane's query rows (n_pos: no row)
-  uint64_t anc[C::RT];
-  int depth[C::RT];
   bool idle;                   // no row of the wave exists
   u32x4 q[C::RT][QC];
   f32x4 o[C::RT][DT];
@@ -118,7 +131,7 @@ template <int KIND, int D, int CLS> struct AttnBlock {
   uint64_t present;            // 4 bits a tile: 16-slot groups whose page is there
   int pg[SB];                  // pages of the next tile to load
 
-  __device__ __forceinline__ AttnBlock(const AttnArgs& args, char* l_) : a(args), lds(l_) {
+  __device__ __forceinline__ AttnBlock(const AttnArgs& args, char* l_, AttnRows<C::ROWS>* rows_) : a(args), lds(l_), rows(rows_) {
     wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     lane = threadIdx.x & 63;
     wr = wave % C::WR;
@@ -193,6 +206,7 @@ template <int KIND, int D, int CLS> struct AttnBlock {
   // Address of piece p of the wave group's part of span tile u, permuted;
   // rows behind the span repeat its last one.
   __device__ __forceinline__ const char* span_piece(int u, int p) const {
+    asm volatile("" : "+v"(p));     // formed here, not kept in registers over the context's tiles
     const int row = p / CPR;
     const int c = (p % CPR) ^ swizzle<CPR>(row);
     const int s = min((u - un.ctx) * C::TS + kg * C::SS + row % C::SS, a.n_pos - 1);
@@ -243,7 +257,6 @@ template <int KIND, int D, int CLS> struct AttnBlock {
       const int row = rb * C::ROWS + (wr * C::RT + rt) * 16 + n16;
       const bool on = row < a.rows;
       const int t = on ? row / a.group : 0;
-      row_t[rt] = on ? t : a.n_pos;
       const int hq = h * a.group + (on ? row - t * a.group : 0);
       const char* src = static_cast<const char*>(a.q) +
                         ((static_cast<int64_t>(r) * a.n_pos + t) * a.q_stride + static_cast<int64_t>(hq) * D) * ESZ;
@@ -265,8 +278,10 @@ template <int KIND, int D, int CLS> struct AttnBlock {
         if (a.window > 0 && a.window <= t) path &= ~uint64_t{0} << (t + 1 - a.window);
         dep = t;
       }
-      anc[rt] = on ? path : 0;
-      depth[rt] = dep;
+      if (kg == 0 && g == 0) {
+        rows->anc[(wr * C::RT + rt) * 16 + n16] = on ? path : 0;
+        rows->first[(wr * C::RT + rt) * 16 + n16] = !on ? INT32_MAX : a.window > 0 ? max(0, len + dep - a.window + 1) : 0;
+      }
       m[rt] = -__builtin_inff();
       l[rt] = 0.0f;
 #pragma unroll
@@ -277,31 +292,47 @@ template <int KIND, int D, int CLS> struct AttnBlock {
   // Which of a tile's slots that this lane holds count for its row (bit 4 sb
   // + i: slot 16 sb + 4 g + i of the wave group's part).
   __device__ __forceinline__ uint32_t visible(int u, int rt, bool span) const {
+    const int lrow = (wr * C::RT + rt) * 16 + n16;
     uint32_t bits = 0;
     if (span) {
+      const uint64_t anc = rows->anc[lrow];
       const int s0 = (u - un.ctx) * C::TS + kg * C::SS + 4 * g;
 #pragma unroll
       for (int sb = 0; sb < SB; ++sb)
-        if (s0 + 16 * sb < 64) bits |= static_cast<uint32_t>((anc[rt] >> (s0 + 16 * sb)) & 15) << (4 * sb);
+        if (s0 + 16 * sb < 64) bits |= static_cast<uint32_t>((anc >> (s0 + 16 * sb)) & 15) << (4 * sb);
       return bits;
     }
     const int j0 = slot0(u) + 4 * g;
-    const int last = len;
-    const int first = a.window > 0 ? len + depth[rt] - a.window + 1 : 0;
+    const int first = rows->first[lrow];
 #pragma unroll
     for (int sb = 0; sb < SB; ++sb) {
       if (!((present >> (4 * (u & 15) + sb)) & 1)) continue;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int j = j0 + 16 * sb + i;
-        bits |= j >= first && j < last ? 1u << (4 * sb + i) : 0u;
+        bits |= j >= first && j < len ? 1u << (4 * sb + i) : 0u;
       }
     }
-    return row_t[rt] < a.n_pos ? bits : 0;
+    return bits;
+  }
+
+  // Whether the wave group's values of a tile hold an infinity or a NaN.
+  __device__ __forceinline__ bool any_odd(const char* vt) const {
+    bool odd = false;
+#pragma unroll
+    for (int x = 0; x < C::SS * CPR / 64; ++x) {
+      const u32x4 w = *reinterpret_cast<const u32x4*>(vt + (x * 64 + lane) * 16);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        odd = odd || (w[e] & 0x7F800000u) == 0x7F800000u;
+        if (ESZ == 2) odd = odd || (w[e] & 0x7F80u) == 0x7F80u;
+      }
+    }
+    return __any(odd);
   }
 
   // One tile: its scores, weights and the product with the values.
-  template <bool MASK> __device__ __forceinline__ void tile(int u, const char* base, bool span) {
+  __device__ __forceinline__ void tile(int u, const char* base, bool span, bool mask) {
     const char* const kt = base + kg * (C::STAGE / C::WK);
     const char* const vt = kt + C::SS * D * ESZ;
     f32x4 s[C::RT][SB];
@@ -309,12 +340,15 @@ template <int KIND, int D, int CLS> struct AttnBlock {
     for (int rt = 0; rt < C::RT; ++rt)
 #pragma unroll
       for (int sb = 0; sb < SB; ++sb) s[rt][sb] = f32x4{};
-    const int fk = swizzle<CPR>(n16);
+    // Piece 4 c + g of row n16, permuted: the permutation is an exclusive or
+    // of address bits, so the pieces are one address apart from constants.
+    const uint32_t ka = lds_address(kt) + n16 * (D * ESZ) +
+                        ((g ^ swizzle<CPR>(n16)) << 4);
 #pragma unroll
     for (int c = 0; c < QC; ++c) {
 #pragma unroll
       for (int sb = 0; sb < SB; ++sb) {
-        const u32x4 kk = *reinterpret_cast<const u32x4*>(kt + ((sb * 16 + n16) * CPR + ((4 * c + g) ^ fk)) * 16);
+        const u32x4 kk = *lds_at<u32x4>((ka ^ (c << 6)) + sb * 16 * D * ESZ);
 #pragma unroll
         for (int rt = 0; rt < C::RT; ++rt) {
           if constexpr (KIND == kF32) {
@@ -329,22 +363,33 @@ template <int KIND, int D, int CLS> struct AttnBlock {
         }
       }
     }
-    const float c = span ? c_span : c_ctx;
     // Scores in log2 units; what does not count is below everything.
-    uint32_t seen[C::RT];      // bit 4 sb + i: the slot counts for the row (masked tiles)
+    const float c = span ? c_span : c_ctx;
+#pragma unroll
+    for (int rt = 0; rt < C::RT; ++rt)
+#pragma unroll
+      for (int sb = 0; sb < SB; ++sb) s[rt][sb] *= c;
+    bool odd = false;
+    if (mask) {
+#pragma unroll
+      for (int rt = 0; rt < C::RT; ++rt) {
+        const uint32_t seen = visible(u, rt, span);
+#pragma unroll
+        for (int sb = 0; sb < SB; ++sb)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (!((seen >> (4 * sb + i)) & 1)) s[rt][sb][i] = -__builtin_inff();
+      }
+      odd = any_odd(vt);
+    }
+    u32x2 pb[C::RT][SB];       // P^T as the products' second operand (bf16)
 #pragma unroll
     for (int rt = 0; rt < C::RT; ++rt) {
-      seen[rt] = MASK ? visible(u, rt, span) : 0;
       float top = -__builtin_inff();
 #pragma unroll
       for (int sb = 0; sb < SB; ++sb)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float x = s[rt][sb][i] * c;
-          if (MASK && !((seen[rt] >> (4 * sb + i)) & 1)) x = -__builtin_inff();
-          s[rt][sb][i] = x;
-          top = fmaxf(top, x);
-        }
+        for (int i = 0; i < 4; ++i) top = fmaxf(top, s[rt][sb][i]);
       if (__any(top > m[rt] + 8.0f)) {
         const float mn = fmaxf(m[rt], row_max(top));
         const float keep = m[rt] == mn ? 1.0f : __builtin_amdgcn_exp2f(m[rt] - mn);
@@ -354,63 +399,115 @@ template <int KIND, int D, int CLS> struct AttnBlock {
         for (int dt = 0; dt < DT; ++dt) o[rt][dt] *= keep;
       }
       const float mb = m[rt] == -__builtin_inff() ? 0.0f : m[rt];
+      float sum = 0.0f;
 #pragma unroll
-      for (int sb = 0; sb < SB; ++sb)
+      for (int sb = 0; sb < SB; ++sb) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           float p = __builtin_amdgcn_exp2f(s[rt][sb][i] - mb);
-          if (MASK && !((seen[rt] >> (4 * sb + i)) & 1)) p = 0.0f;
-          l[rt] += p;
-          if (KIND == kF8 && !span) p *= vs;
+          sum += p;
+          if (KIND == kF8) p *= span ? 1.0f : vs;
           s[rt][sb][i] = p;
         }
-    }
-    // P^T as the products' second operand.
-    u32x2 pb[C::RT][SB];
-    if constexpr (KIND != kF32) {
-#pragma unroll
-      for (int rt = 0; rt < C::RT; ++rt)
-#pragma unroll
-        for (int sb = 0; sb < SB; ++sb)
+        if constexpr (KIND != kF32)
           pb[rt][sb] = u32x2{pack_bf16(s[rt][sb][0], s[rt][sb][1]), pack_bf16(s[rt][sb][2], s[rt][sb][3])};
+      }
+      l[rt] += sum;
     }
-    bool odd = false;        // a value that is not finite was left out
-    if constexpr (KIND == kF32) {
+    if (odd) {
+      values<true>(vt, s, pb, u, span);
+    } else {
+      values<false>(vt, s, pb, u, span);
+    }
+  }
+
+  // O^T += V^T P^T. ODD: values that are not finite leave the product; the
+  // products of "counts" with "+inf or NaN" and with "-inf or NaN" say which
+  // rows' sums get +inf, -inf or both (NaN).
+  template <bool ODD>
+  __device__ __forceinline__ void values(const char* vt, const f32x4 (&s)[C::RT][SB], const u32x2 (&pb)[C::RT][SB], int u,
+                                         bool span) {
+    const float inf = __builtin_inff();
+    uint32_t seen[C::RT];
+    if (ODD) {
 #pragma unroll
-      for (int dt = 0; dt < DT; ++dt)
+      for (int rt = 0; rt < C::RT; ++rt) seen[rt] = visible(u, rt, span);
+    }
+    const uint32_t vb = lds_address(vt);
+    if constexpr (KIND == kF32) {
+      // Row 16 sb + 4 g + i, element 16 dt + n16: one address per i.
+      uint32_t va[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        va[i] = vb + (4 * g + i) * (D * 4) + (((n16 >> 2) ^ swizzle<CPR>(4 * g + i)) << 4) + (n16 & 3) * 4;
+#pragma unroll
+      for (int dt = 0; dt < DT; ++dt) {
+        f32x4 up[C::RT], down[C::RT];
+#pragma unroll
+        for (int rt = 0; rt < C::RT; ++rt) up[rt] = down[rt] = f32x4{};
 #pragma unroll
         for (int sb = 0; sb < SB; ++sb)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const int row = sb * 16 + 4 * g + i;
-            float v = *reinterpret_cast<const float*>(
-                vt + (row * CPR + ((dt * 4 + (n16 >> 2)) ^ swizzle<CPR>(row))) * 16 + (n16 & 3) * 4);
-            if (MASK && not_finite(v)) {
-              v = 0.0f;
-              odd = true;
+            float v = *lds_at<float>((va[i] ^ (dt << 6)) + sb * 16 * D * 4);
+            if (ODD) {
+              const float hi = v == inf || v != v ? 1.0f : 0.0f, lo = v == -inf || v != v ? 1.0f : 0.0f;
+              v = not_finite(v) ? 0.0f : v;
+#pragma unroll
+              for (int rt = 0; rt < C::RT; ++rt) {
+                const float p = (seen[rt] >> (4 * sb + i)) & 1 ? 1.0f : 0.0f;
+                up[rt] = __builtin_amdgcn_mfma_f32_16x16x4f32(hi, p, up[rt], 0, 0, 0);
+                down[rt] = __builtin_amdgcn_mfma_f32_16x16x4f32(lo, p, down[rt], 0, 0, 0);
+              }
             }
 #pragma unroll
             for (int rt = 0; rt < C::RT; ++rt)
               o[rt][dt] = __builtin_amdgcn_mfma_f32_16x16x4f32(v, s[rt][sb][i], o[rt][dt], 0, 0, 0);
           }
+        if (ODD) {
+#pragma unroll
+          for (int rt = 0; rt < C::RT; ++rt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[rt][dt][e] += (up[rt][e] > 0.0f ? inf : 0.0f) - (down[rt][e] > 0.0f ? inf : 0.0f);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
     } else {
       const int vrow = 4 * g + (n16 >> 2);
-      const int fv = swizzle<CPR>(vrow);
+      const uint32_t va = vb + vrow * (D * ESZ) + ((((n16 & 3) >> 1) ^ swizzle<CPR>(vrow)) << 4) + (n16 & 1) * 8;
 #pragma unroll
       for (int dt = 0; dt < DT; ++dt) {
-        const char* const vp = vt + (vrow * CPR + ((dt * 2 + ((n16 & 3) >> 1)) ^ fv)) * 16 + (n16 & 1) * 8;
         u32x2 w[SB];
 #pragma unroll
-        for (int sb = 0; sb < SB; ++sb) {
-          w[sb] = read_tr16(vp + sb * 16 * D * ESZ);
-          if (MASK) {
+        for (int sb = 0; sb < SB; ++sb) w[sb] = read_tr16((va ^ (dt << 5)) + sb * 16 * D * ESZ);
+        if (ODD) {
+          f32x4 up[C::RT], down[C::RT];
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const bool lo = (w[sb][e] & 0x7F80u) == 0x7F80u, hi = (w[sb][e] & 0x7F800000u) == 0x7F800000u;
-              odd = odd || lo || hi;
-              w[sb][e] &= (lo ? 0xFFFF0000u : 0xFFFFFFFFu) & (hi ? 0x0000FFFFu : 0xFFFFFFFFu);
+          for (int rt = 0; rt < C::RT; ++rt) up[rt] = down[rt] = f32x4{};
+#pragma unroll
+          for (int sb = 0; sb < SB; ++sb) {
+            s16x4 hi, lo;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t half = (w[sb][i >> 1] >> (16 * (i & 1))) & 0xFFFFu;
+              const bool nan = (half & 0x7FFFu) > 0x7F80u;
+              hi[i] = half == 0x7F80u || nan ? 0x3F80 : 0;
+              lo[i] = half == 0xFF80u || nan ? 0x3F80 : 0;
+              if ((half & 0x7F80u) == 0x7F80u) w[sb][i >> 1] &= 0xFFFFu << (16 * (1 - (i & 1)));
+            }
+#pragma unroll
+            for (int rt = 0; rt < C::RT; ++rt) {
+              s16x4 p;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) p[i] = (seen[rt] >> (4 * sb + i)) & 1 ? 0x3F80 : 0;
+              up[rt] = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(hi, p, up[rt], 0, 0, 0);
+              down[rt] = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(lo, p, down[rt], 0, 0, 0);
             }
           }
+#pragma unroll
+          for (int rt = 0; rt < C::RT; ++rt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[rt][dt][e] += (up[rt][e] > 0.0f ? inf : 0.0f) - (down[rt][e] > 0.0f ? inf : 0.0f);
         }
 #pragma unroll
         for (int rt = 0; rt < C::RT; ++rt) {
@@ -426,53 +523,9 @@ template <int KIND, int D, int CLS> struct AttnBlock {
                   o[rt][dt], 0, 0, 0);
           }
         }
+        if (ODD) __builtin_amdgcn_sched_barrier(0);
       }
     }
-    if (MASK && __any(odd)) add_odd(seen, vt);
-  }
-
-  // Values that are not finite, for the rows that count their slots: the
-  // products of "counts" with "+inf or NaN" and with "-inf or NaN" say where
-  // a sum holds +inf, -inf or both (NaN).
-  __device__ __forceinline__ void add_odd(const uint32_t (&seen)[C::RT], const char* vt) {
-    const float inf = __builtin_inff();
-    const int vrow = 4 * g + (n16 >> 2);
-    const int fv = swizzle<CPR>(vrow);
-#pragma unroll
-    for (int dt = 0; dt < DT; ++dt)
-#pragma unroll
-      for (int rt = 0; rt < C::RT; ++rt) {
-        f32x4 up = {}, down = {};
-#pragma unroll
-        for (int sb = 0; sb < SB; ++sb) {
-          if constexpr (KIND == kF32) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int row = sb * 16 + 4 * g + i;
-              const float v = *reinterpret_cast<const float*>(
-                  vt + (row * CPR + ((dt * 4 + (n16 >> 2)) ^ swizzle<CPR>(row))) * 16 + (n16 & 3) * 4);
-              const float p = (seen[rt] >> (4 * sb + i)) & 1 ? 1.0f : 0.0f;
-              up = __builtin_amdgcn_mfma_f32_16x16x4f32(v == inf || v != v ? 1.0f : 0.0f, p, up, 0, 0, 0);
-              down = __builtin_amdgcn_mfma_f32_16x16x4f32(v == -inf || v != v ? 1.0f : 0.0f, p, down, 0, 0, 0);
-            }
-          } else {
-            const char* const vp = vt + (vrow * CPR + ((dt * 2 + ((n16 & 3) >> 1)) ^ fv)) * 16 + (n16 & 1) * 8;
-            const u32x2 w = read_tr16(vp + sb * 16 * D * ESZ);
-            s16x4 hi, lo, p;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float v = bf16_one(static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1))));
-              hi[i] = v == inf || v != v ? 0x3F80 : 0;
-              lo[i] = v == -inf || v != v ? 0x3F80 : 0;
-              p[i] = (seen[rt] >> (4 * sb + i)) & 1 ? 0x3F80 : 0;
-            }
-            up = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(hi, p, up, 0, 0, 0);
-            down = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(lo, p, down, 0, 0, 0);
-          }
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[rt][dt][e] += (up[e] > 0.0f ? inf : 0.0f) - (down[e] > 0.0f ? inf : 0.0f);
-      }
   }
 
   __device__ __forceinline__ bool masked(int u) const {
@@ -485,8 +538,7 @@ template <int KIND, int D, int CLS> struct AttnBlock {
 
   __device__ __forceinline__ void compute(int u, const char* base) {
     if (idle) return;
-    if (masked(u)) tile<true>(u, base, u >= un.ctx);
-    else tile<false>(u, base, false);
+    tile(u, base, u >= un.ctx, masked(u));
   }
 
   // Waits for a tile of this wave's loads with `after` later tiles on their way.
@@ -605,10 +657,11 @@ template <int KIND, int D, int CLS> struct AttnBlock {
 template <int KIND, int D, int CLS>
 __global__ __launch_bounds__((AttnCfg<KIND, D, CLS>::NT)) void attn_kernel(const AttnArgs args) {
   using C = AttnCfg<KIND, D, CLS>;
-  extern __shared__ __align__(16) char lds[];
+  extern __shared__ __align__(1024) char lds[];   // rows of a tile start at multiples of their size
   __shared__ int64_t before[kAttnReqs + 1];
   __shared__ int64_t wave_sum[kAttnReqs / 64];
   __shared__ int8_t par[HRS_MAX_POS];
+  __shared__ AttnRows<C::ROWS> rows;
   const int tid = threadIdx.x, lane = tid & 63;
   const int heads = args.kvheads * args.row_blocks;
   // Units before every request: a scan over the lengths, 256 at most.
@@ -654,7 +707,7 @@ __global__ __launch_bounds__((AttnCfg<KIND, D, CLS>::NT)) void attn_kernel(const
   for (int step = kAttnReqs / 2; step; step >>= 1)
     if (i + step < args.n_here && before[i + step] <= u) i += step;
 
-  AttnBlock<KIND, D, CLS> blk(args, lds);
+  AttnBlock<KIND, D, CLS> blk(args, lds, &rows);
   while (u < u1) {
     while (before[i + 1] <= u) ++i;
     i = __builtin_amdgcn_readfirstlane(i);
@@ -675,6 +728,7 @@ __global__ __launch_bounds__((AttnCfg<KIND, D, CLS>::NT)) void attn_kernel(const
       __syncthreads();
     }
     blk.load_rows(par);
+    __syncthreads();
     blk.run(u0, __builtin_amdgcn_readfirstlane(ue));
     blk.finish(u0 == 0 && ue == blk.un.all, 2 * static_cast<int>(blockIdx.x) + (u0 == 0 ? 1 : 0));
     u += ue - u0;
