@@ -55,6 +55,7 @@ struct AttnArgs {
 // different slots; a wave holds RT tiles of 16 rows and SS slots of a tile.
 template <int KIND, int D, int CLS> struct AttnCfg {
   static constexpr int ESZ = KIND == kF32 ? 4 : 2;          // bytes of an element in LDS
+  static constexpr int ESZC = KIND == kF32 ? 4 : KIND == kB16 ? 2 : 1;   // of a cached one
   static constexpr bool WIDE = D == 256;
   static constexpr int RT = CLS == 0 || (CLS == 3 && WIDE) ? 1 : 2;
   static constexpr int WR = CLS < 2 ? 1 : CLS == 2 ? 2 : WIDE ? 8 : 4;

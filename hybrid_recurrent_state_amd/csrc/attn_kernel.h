@@ -128,6 +128,8 @@ template <int KIND, int D, int CLS> struct AttnBlock {
   f32x4 o[C::RT][DT];
   float m[C::RT], l[C::RT];
   float c_ctx, c_span, vs;
+  uint32_t head_bytes;         // a page of all heads
+  uint64_t h_bytes;            // this head's part of it
   uint64_t present;            // 4 bits a tile: 16-slot groups whose page is there
   int pg[SB];                  // pages of the next tile to load
 
@@ -162,28 +164,29 @@ template <int KIND, int D, int CLS> struct AttnBlock {
     const bool span = u >= un.ctx;
     if (!span) {
       uint32_t here = 0;
-      const char* kb[SB];
-      const char* vb[SB];
+      int64_t at[SB];
 #pragma unroll
       for (int i = 0; i < SB; ++i) {
         const bool ok = pg[i] >= 0 && pg[i] < a.n_pages;
         here |= ok ? 1u << i : 0u;
         const int in_page = (slot0(u) + 16 * i) & ((1 << a.page_shift) - 1);
-        const int64_t off = (((static_cast<int64_t>(ok ? pg[i] : 0) * a.kvheads + h) << a.page_shift) + in_page) *
-                            (D * CSZ);
-        kb[i] = a.k_cache + off;
-        vb[i] = a.v_cache + off;
+        // Bytes: (page * heads + head) rows of a page, then the row.
+        at[i] = static_cast<int64_t>(static_cast<uint64_t>(static_cast<uint32_t>(ok ? pg[i] : 0)) * head_bytes) +
+                static_cast<int64_t>(h_bytes + static_cast<uint32_t>(in_page) * (D * CSZ));
       }
       present = (present & ~(uint64_t{15} << (4 * (u & 15)))) | (static_cast<uint64_t>(here) << (4 * (u & 15)));
+      constexpr int kRows = 64 * C::WR / RCPR;              // rows that one load of all the group's waves covers
 #pragma unroll
       for (int i = 0; i < LPS; ++i) {
         const int p0 = (i * C::WR + wr) * 64;               // first piece of this load
-        const int row0 = p0 / RCPR;                         // uniform
+        // Its group of 16 rows: known here where the waves' rows fit in one.
+        const int row0 = kRows <= 16 ? i * kRows : p0 / RCPR;
         const bool is_v = row0 >= C::SS;
         const int grp = (row0 % C::SS) / 16;
-        const char* base = is_v ? vb[0] : kb[0];
+        int64_t off64 = at[0];
 #pragma unroll
-        for (int x = 1; x < SB; ++x) base = grp == x ? (is_v ? vb[x] : kb[x]) : base;
+        for (int x = 1; x < SB; ++x) off64 = grp == x ? at[x] : off64;
+        const char* const base = (is_v ? a.v_cache : a.k_cache) + off64;
         const int p = p0 + lane;
         const int row = p / RCPR;
         int c = p % RCPR;
@@ -363,12 +366,17 @@ template <int KIND, int D, int CLS> struct AttnBlock {
         }
       }
     }
-    // Scores in log2 units; what does not count is below everything.
-    const float c = span ? c_span : c_ctx;
+    // c S - m is one operation on the raw products; c is positive (a negative
+    // one turns the products' sign).
+    float c = span ? c_span : c_ctx;
+    if (c < 0.0f) {
+      c = -c;
 #pragma unroll
-    for (int rt = 0; rt < C::RT; ++rt)
+      for (int rt = 0; rt < C::RT; ++rt)
 #pragma unroll
-      for (int sb = 0; sb < SB; ++sb) s[rt][sb] *= c;
+        for (int sb = 0; sb < SB; ++sb) s[rt][sb] = -s[rt][sb];
+    }
+    c = fmaxf(c, 1e-37f);          // masked scores stay below everything at a scale of zero
     bool odd = false;
     if (mask) {
 #pragma unroll
@@ -390,6 +398,7 @@ template <int KIND, int D, int CLS> struct AttnBlock {
       for (int sb = 0; sb < SB; ++sb)
 #pragma unroll
         for (int i = 0; i < 4; ++i) top = fmaxf(top, s[rt][sb][i]);
+      top *= c;
       if (__any(top > m[rt] + 8.0f)) {
         const float mn = fmaxf(m[rt], row_max(top));
         const float keep = m[rt] == mn ? 1.0f : __builtin_amdgcn_exp2f(m[rt] - mn);
@@ -404,7 +413,7 @@ template <int KIND, int D, int CLS> struct AttnBlock {
       for (int sb = 0; sb < SB; ++sb) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          float p = __builtin_amdgcn_exp2f(s[rt][sb][i] - mb);
+          float p = __builtin_amdgcn_exp2f(fmaf(s[rt][sb][i], c, -mb));
           sum += p;
           if (KIND == kF8) p *= span ? 1.0f : vs;
           s[rt][sb][i] = p;
@@ -723,6 +732,8 @@ __global__ __launch_bounds__((AttnCfg<KIND, D, CLS>::NT)) void attn_kernel(const
     blk.vs = KIND == kF8 && args.v_scale ? args.v_scale[blk.h] : 1.0f;
     blk.c_span = args.scale * 1.4426950408889634f;
     blk.c_ctx = blk.c_span * ks;
+    blk.head_bytes = static_cast<uint32_t>(args.kvheads) * (D * C::ESZC << args.page_shift);
+    blk.h_bytes = static_cast<uint64_t>(blk.h) * (D * C::ESZC << args.page_shift);
     if (args.tree) {
       if (tid < args.n_pos) par[tid] = args.parent[i * args.n_pos + tid];
       __syncthreads();

@@ -6,8 +6,24 @@
 // (openinfer PR #626, "feat(qwen35): add opt-in DFlash speculative decoding",
 // Summary: greedy requests only; sampling falls back to plain decoding).
 //
-// Simple form: one block per row for its maximum and sum, then one block per
-// request for the walk and the draw.
+// MI355X design: three or four dependent launches, no host round trip.
+//  1. Row statistics: every 16384-logit chunk of every row that has a child
+//     (a leaf's probabilities are needed only if the walk ends there) is read
+//     once with nontemporal loads into registers, reduced to its maximum m and
+//     then to sum e^((z - m) / tau), float32 per thread, 64 bits across the
+//     block: bound by the read of the logits, at about ten vector operations a
+//     logit.
+//  2. Walk and node sums: blocks of 2048 logits of the row where the walk
+//     ends. Every block first repeats its request's walk (the statistics are
+//     small and cached; handing the node over would be one more launch): lane
+//     t holds position t, a chain is one ballot, a tree visits a node's
+//     children by lane reads. Then it sums its logits' weights in 64 bits.
+//  3. With draft probabilities: the sums of max(p - q, 0), which need the
+//     row's total from 2.
+//  4. One block per request finds the drawn token's 2048-logit piece by a
+//     cumulative sum of the pieces and the token by one inside it.
+// Why 64 bits in 2 to 4: a cumulative float32 sum over 151,936 weights is off
+// by about 1e-6 of the total, and a token of an even distribution spans 7e-6.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -19,6 +35,19 @@ namespace hrs {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kChunk = 16384;                       // logits per statistics block
+constexpr int kIter = kChunk / (kThreads * 8);      // 8-logit slices per thread
+constexpr int kPiece = kThreads * 8;                // logits per node block
+
+enum : int32_t { kPlain = 0, kWithout = 1, kRest = 2 };   // weights: p; p without tokens; max(p - q, 0)
+
+struct NodeInfo {
+  int32_t node;
+  int32_t mode;
+  int32_t n_gone;
+  int32_t bad;       // temperature refused: nothing is written
+  int32_t gone[HRS_MAX_POS];
+};
 
 struct SampleArgs {
   const void* logits;
@@ -32,22 +61,29 @@ struct SampleArgs {
   int32_t* path;
   int32_t* bonus;
   int32_t* status;
-  double2* stats;     // workspace [rows]: maximum, sum
+  double2* stats;     // workspace [rows][n_chunks]: maximum, sum
+  double2* part;      // workspace [R][n_pieces]: maximum, sum of the node's row
+  double* rest;       // workspace [R][n_pieces]: sum of max(p - q, 0)
+  NodeInfo* info;     // workspace [R]
   int32_t n_req;
   int32_t n_pos;
   int32_t vocab;
+  int32_t n_chunks;
+  int32_t n_pieces;
   int32_t req0;
   int32_t tree;
   int32_t draft_bf16;
   int8_t parent[kGeomBytes];
 };
 
-__device__ __forceinline__ bool bad_temperature(const SampleArgs& a, int r) {
-  return a.temperature && !(a.temperature[r] >= 0.0f);
+__device__ __forceinline__ float temperature_of(const SampleArgs& a, int r) {
+  return a.temperature ? a.temperature[r] : 1.0f;
 }
+__device__ __forceinline__ bool bad_temperature(float tau) { return !(tau >= 0.0f); }
 
-// Weight of a logit below the row's maximum m: e^((z - m) / tau). Hard rows
-// (temperature 0, or +inf logits) give the largest logits one, the rest zero.
+// Weight of a logit beside the maximum m: e^((z - m) / tau). Hard rows
+// (temperature 0, or +inf logits) give the largest logits one, the rest zero;
+// NaN has none, and neither has anything where there is no maximum.
 struct Weigher {
   double m, inv;
   bool hard, none;
@@ -56,172 +92,495 @@ struct Weigher {
     hard = tau == 0.0f || m == __builtin_inf();
     inv = tau > 0.0f ? fmax(1.0 / static_cast<double>(tau), 1e-300) : 1.0;
   }
-  __device__ double operator()(float z) const {
+  __device__ __forceinline__ double operator()(double z) const {
     if (none || z != z) return 0.0;
     if (hard) return z == m ? 1.0 : 0.0;
-    return exp((static_cast<double>(z) - m) * inv);
+    return exp((z - m) * inv);
   }
 };
 
-template <typename T>
-__global__ __launch_bounds__(kThreads) void row_stats_kernel(const SampleArgs args) {
-  const int row = blockIdx.x;
-  const T* z = static_cast<const T*>(args.logits) + static_cast<int64_t>(row) * args.vocab;
-  __shared__ double red[kThreads];
-  float m = -__builtin_inff();
-  for (int i = threadIdx.x; i < args.vocab; i += kThreads) m = fmaxf(m, load_elem<T>(z, i));
-  red[threadIdx.x] = m;
+// Sums and maxima over the block, in a fixed order, the same in every thread.
+template <typename Op> __device__ __forceinline__ double block_reduce(double x, Op op, double* lds) {
+#pragma unroll
+  for (int d = 32; d; d >>= 1) x = op(x, __shfl_xor(x, d));
   __syncthreads();
-  for (int s = kThreads / 2; s; s >>= 1) {
-    if (threadIdx.x < s) red[threadIdx.x] = fmax(red[threadIdx.x], red[threadIdx.x + s]);
-    __syncthreads();
-  }
-  const Weigher w(red[0], args.temperature ? args.temperature[row / args.n_pos] : 1.0f);
+  if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = x;
   __syncthreads();
-  double sum = 0.0;
-  for (int i = threadIdx.x; i < args.vocab; i += kThreads) sum += w(load_elem<T>(z, i));
-  red[threadIdx.x] = sum;
-  __syncthreads();
-  for (int s = kThreads / 2; s; s >>= 1) {
-    if (threadIdx.x < s) red[threadIdx.x] += red[threadIdx.x + s];
-    __syncthreads();
-  }
-  if (threadIdx.x == 0) args.stats[row] = double2{w.m, red[0]};
+  x = lds[0];
+#pragma unroll
+  for (int i = 1; i < kThreads / 64; ++i) x = op(x, lds[i]);
+  return x;
+}
+__device__ __forceinline__ double add(double a, double b) { return a + b; }
+__device__ __forceinline__ double larger(double a, double b) { return fmax(a, b); }
+
+// Eight logits with nontemporal loads (read once by the statistics).
+template <typename T> __device__ __forceinline__ void load8_nt(const T* p, float* o);
+template <> __device__ __forceinline__ void load8_nt<uint16_t>(const uint16_t* p, float* o) {
+  const u32x4 w = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p));
+  o[0] = bf16_lo(w.x); o[1] = bf16_hi(w.x);
+  o[2] = bf16_lo(w.y); o[3] = bf16_hi(w.y);
+  o[4] = bf16_lo(w.z); o[5] = bf16_hi(w.z);
+  o[6] = bf16_lo(w.w); o[7] = bf16_hi(w.w);
+}
+template <> __device__ __forceinline__ void load8_nt<float>(const float* p, float* o) {
+  const f32x4 x = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(p));
+  const f32x4 y = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(p + 4));
+  o[0] = x.x; o[1] = x.y; o[2] = x.z; o[3] = x.w;
+  o[4] = y.x; o[5] = y.y; o[6] = y.z; o[7] = y.w;
 }
 
+// 1. Grid: (request, position with a child, chunk).
 template <typename T>
-__global__ __launch_bounds__(kThreads) void sample_kernel(const SampleArgs args) {
-  const int rl = blockIdx.x, r = args.req0 + rl, T_ = args.n_pos, V = args.vocab;
-  const int tid = threadIdx.x;
-  if (r == 0 && tid == 0 && args.status) {
-    int bad = 0;
-    for (int i = 0; i < args.n_req; ++i) bad += bad_temperature(args, i);
-    *args.status = bad;
+__global__ __launch_bounds__(kThreads) void row_stats_kernel(const SampleArgs args) {
+  const int rows = args.tree ? args.n_pos : args.n_pos - 1;
+  const int chunk = blockIdx.x % args.n_chunks;
+  const int rt = blockIdx.x / args.n_chunks;
+  const int rl = rt / rows, t = rt - rl * rows;
+  const int64_t row = static_cast<int64_t>(args.req0 + rl) * args.n_pos + t;
+  if (args.tree) {
+    const int lane = threadIdx.x & 63;
+    const int p = args.parent[rl * args.n_pos + min(lane, args.n_pos - 1)];
+    if (!__any(p == t && lane > 0)) return;
   }
-  if (bad_temperature(args, r)) return;
-  const float tau = args.temperature ? args.temperature[r] : 1.0f;
-  const int64_t row0 = static_cast<int64_t>(r) * T_;
-  const T* logits = static_cast<const T*>(args.logits) + row0 * V;
-  __shared__ double prob[HRS_MAX_POS];
-  __shared__ int32_t par[HRS_MAX_POS], tok[HRS_MAX_POS], gone[HRS_MAX_POS];
-  __shared__ int32_t node_s, gone_n, drafted_s;
-  auto draft_at = [&](int t, int v) -> double {
-    const int64_t i = (row0 + t) * V + v;
-    return args.draft_bf16 ? bf16_one(static_cast<const uint16_t*>(args.draft)[i])
-                           : static_cast<const float*>(args.draft)[i];
-  };
-  if (tid < T_) {
-    const int p = args.tree ? args.parent[rl * T_ + tid] : tid - 1;
-    const int x = args.tokens[row0 + tid];
-    par[tid] = p;
-    tok[tid] = x;
-    double pr = tid == 0 ? 1.0 : 0.0;
-    if (tid > 0 && x >= 0 && x < V) {
-      const double2 st = args.stats[row0 + p];
-      const Weigher w(st.x, tau);
-      if (st.y > 0.0) pr = w(load_elem<T>(logits, static_cast<int64_t>(p) * V + x)) / st.y;
+  const float tau = temperature_of(args, args.req0 + rl);
+  const T* base = static_cast<const T*>(args.logits) + row * args.vocab;
+  const int begin = chunk * kChunk;
+  const int end = min(args.vocab, begin + kChunk);
+  float v[kIter][8];
+  float m = -__builtin_inff();
+  // Slices past the row's end re-read its last eight logits: they change no
+  // maximum, and their weights are left out.
+#pragma unroll
+  for (int it = 0; it < kIter; ++it) {
+    const int e = begin + (it * kThreads + threadIdx.x) * 8;
+    load8_nt<T>(base + min(e, end - 8), v[it]);
+  }
+#pragma unroll
+  for (int it = 0; it < kIter; ++it)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      v[it][i] = __builtin_canonicalizef(v[it][i]);   // a quiet NaN loses against every number
+      m = fmaxf(m, v[it][i]);
     }
-    prob[tid] = pr;
-    args.token_prob[row0 + tid] = static_cast<float>(pr);
-  }
+#pragma unroll
+  for (int d = 32; d; d >>= 1) m = fmaxf(m, __shfl_xor(m, d));
+  __shared__ float wave_m[kThreads / 64];
+  __shared__ double lds[kThreads / 64];
+  if ((threadIdx.x & 63) == 0) wave_m[threadIdx.x >> 6] = m;
   __syncthreads();
-  if (tid == 0) {
-    const float* u = args.uniforms + row0;
-    int node = 0, len = 0, n_gone = 0, path_n = 1;
-    bool drafted = false;
-    args.path[row0] = 0;
-    for (;;) {
-      int next = -1;
-      double left = 1.0;
-      n_gone = 0;
-      for (int t = node + 1; t < T_ && next < 0; ++t) {
-        if (par[t] != node) continue;
-        if (args.draft) {
-          const bool valid = tok[t] >= 0 && tok[t] < V;
-          if (valid && static_cast<double>(u[t]) * draft_at(node, tok[t]) < prob[t]) next = t;
-          else drafted = true;
-          continue;
-        }
-        bool seen = false;
-        for (int i = 0; i < n_gone; ++i) seen = seen || gone[i] == tok[t];
-        if (seen) continue;
-        if (static_cast<double>(u[t]) * left < prob[t]) {
-          next = t;
-        } else {
-          left -= prob[t];
-          gone[n_gone++] = tok[t];
-        }
-      }
-      if (next < 0) break;
-      node = next;
-      ++len;
-      args.path[row0 + path_n++] = node;
+#pragma unroll
+  for (int i = 0; i < kThreads / 64; ++i) m = fmaxf(m, wave_m[i]);
+  float sum = 0.0f;
+  if (tau == 0.0f || m == __builtin_inff()) {
+#pragma unroll
+    for (int it = 0; it < kIter; ++it)
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (begin + (it * kThreads + threadIdx.x) * 8 < end) sum += v[it][i] == m ? 1.0f : 0.0f;
+  } else if (m > -__builtin_inff()) {
+    const float c = fminf(fmaxf(1.4426950408889634f / tau, 1.2e-38f), 3.4e38f);
+#pragma unroll
+    for (int it = 0; it < kIter; ++it) {
+      float s8 = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)       // a NaN becomes -inf, of weight zero
+        s8 += __builtin_amdgcn_exp2f(fmaxf((v[it][i] - m) * c, -__builtin_inff()));
+      if (begin + (it * kThreads + threadIdx.x) * 8 < end) sum += s8;
     }
-    for (int i = path_n; i < T_; ++i) args.path[row0 + i] = -1;
-    args.accept_node[r] = node;
-    args.accept_len[r] = len;
-    node_s = node;
-    gone_n = n_gone;
-    drafted_s = drafted;
   }
-  __syncthreads();
-  const int node = node_s;
-  const T* z = logits + static_cast<int64_t>(node) * V;
-  const double2 st = args.stats[row0 + node];
-  const Weigher w(st.x, tau);
-  const int per = (V + kThreads - 1) / kThreads;
-  const int v0 = min(V, tid * per), v1 = min(V, v0 + per);
-  __shared__ double sums[kThreads];
-  __shared__ int32_t pick_s;
-  for (int mode = drafted_s || gone_n ? 1 : 0; mode >= 0; --mode) {
-    auto weight = [&](int v) -> double {
-      double x = w(load_elem<T>(z, v));
-      if (mode == 0) return x;
-      if (drafted_s) {
-        x = x / st.y - draft_at(node, v);
-        return x > 0.0 ? x : 0.0;
-      }
-      for (int i = 0; i < gone_n; ++i) x = gone[i] == v ? 0.0 : x;
-      return x;
-    };
-    double sum = 0.0;
-    for (int v = v0; v < v1; ++v) sum += weight(v);
-    sums[tid] = sum;
-    __syncthreads();
-    double total = 0.0;
-    for (int i = 0; i < kThreads; ++i) total += sums[i];
-    if (total > 0.0) {
-      const double target = static_cast<double>(args.uniforms[row0]) * total;
-      double before = 0.0;
-      int owner = -1, last = 0;
-      for (int i = 0; i < kThreads; ++i) {
-        if (sums[i] > 0.0) last = i;
-        if (owner < 0 && sums[i] > 0.0 && before + sums[i] > target) owner = i;
-        if (owner < 0) before += sums[i];
-      }
-      if (owner < 0) {   // no cumulative sum passes: the last positive weight
-        owner = last;
-        before = -__builtin_inf();
-      }
-      if (tid == owner) {
-        int pick = v0;
-        for (int v = v0; v < v1; ++v) {
-          const double x = weight(v);
-          if (!(x > 0.0)) continue;
-          pick = v;
-          before += x;
-          if (before > target) break;
-        }
-        pick_s = pick;
-      }
-      __syncthreads();
-      if (tid == 0) args.bonus[r] = pick_s;
-      return;
-    }
-    __syncthreads();
-  }
-  if (tid == 0) args.bonus[r] = 0;
+  const double total = block_reduce(sum, add, lds);
+  if (threadIdx.x == 0) args.stats[row * args.n_chunks + chunk] = double2{m, total};
 }
+
+__device__ __forceinline__ double draft_value(const SampleArgs& a, int64_t i) {
+  return a.draft_bf16 ? bf16_one(static_cast<const uint16_t*>(a.draft)[i]) : static_cast<const float*>(a.draft)[i];
+}
+
+struct WalkLds {
+  double prob[HRS_MAX_POS];
+  NodeInfo info;
+};
+
+// The walk of request r, by the whole block; the first block of the request
+// writes its outputs.
+template <typename T>
+__device__ __forceinline__ void walk(const SampleArgs& args, int rl, bool write, WalkLds& w) {
+  const int r = args.req0 + rl, T_ = args.n_pos, V = args.vocab;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const float tau = temperature_of(args, r);
+  const int64_t row0 = static_cast<int64_t>(r) * T_;
+  if (bad_temperature(tau)) {
+    if (threadIdx.x == 0) w.info.bad = 1;
+    __syncthreads();
+    return;
+  }
+  // Probability of every draft: one wave per position in turn, its lanes over
+  // the chunks of the parent's row.
+  for (int t = wave; t < T_; t += kThreads / 64) {
+    const int p = args.tree ? args.parent[rl * T_ + t] : t - 1;
+    const int x = args.tokens[row0 + t];
+    double pr = t == 0 ? 1.0 : 0.0;
+    if (t > 0 && x >= 0 && x < V) {
+      const double z = load_elem<T>(static_cast<const T*>(args.logits), (row0 + p) * V + x);
+      double M = -__builtin_inf(), s = 0.0;
+      const double2* st = args.stats + (row0 + p) * args.n_chunks;
+      for (int i = lane; i < args.n_chunks; i += 64) M = fmax(M, st[i].x);
+#pragma unroll
+      for (int d = 32; d; d >>= 1) M = fmax(M, __shfl_xor(M, d));
+      const Weigher weigh(M, tau);
+      for (int i = lane; i < args.n_chunks; i += 64) s += st[i].y * weigh(st[i].x);
+#pragma unroll
+      for (int d = 32; d; d >>= 1) s += __shfl_xor(s, d);
+      if (s > 0.0) pr = weigh(z) / s;
+    }
+    if (lane == 0) {
+      w.prob[t] = pr;
+      if (write) args.token_prob[row0 + t] = static_cast<float>(pr);
+    }
+  }
+  __syncthreads();
+  if (wave == 0) {
+    const int tl = min(lane, T_ - 1);
+    const int par = lane >= T_ ? -2 : args.tree ? args.parent[rl * T_ + tl] : lane - 1;
+    const int tok = args.tokens[row0 + tl];
+    const double u = args.uniforms[row0 + tl];
+    const double prob = w.prob[tl];
+    int node = 0, len = 0, mode = kPlain, n_gone = 0;
+    uint64_t on_path = 1;
+    if (!args.tree) {
+      // u q < p with q = 1 for a picked draft: one comparison per position,
+      // the accepted length is the run of successes from position 1.
+      bool ok = false;
+      if (lane >= 1 && lane < T_ && tok >= 0 && tok < V) {
+        const double q = args.draft ? draft_value(args, (row0 + lane - 1) * V + tok) : 1.0;
+        ok = u * q < prob;
+      }
+      const uint64_t hits = __ballot(ok);
+      len = __builtin_ctzll(~(hits >> 1));
+      node = len;
+      on_path = ~uint64_t{0} >> (63 - len);
+      if (node < T_ - 1) {
+        mode = args.draft ? kRest : kWithout;
+        n_gone = args.draft ? 0 : 1;
+        if (lane == node + 1) w.info.gone[0] = tok;
+      }
+    } else {
+      for (;;) {
+        uint64_t kids = __ballot(par == node && lane > 0);
+        uint64_t out = 0;              // rejected children, one per token
+        double left = 1.0;
+        int next = -1;
+        while (kids) {
+          const int c = __builtin_ctzll(kids);
+          kids &= kids - 1;
+          const int tc = __builtin_amdgcn_readlane(tok, c);
+          if (__ballot(tok == tc) & out) continue;
+          const double pc = __shfl(prob, c), uc = __shfl(u, c);
+          if (uc * left < pc) {
+            next = c;
+            break;
+          }
+          left -= pc;
+          out |= uint64_t{1} << c;
+        }
+        if (next < 0) {
+          n_gone = __popcll(out);
+          mode = n_gone ? kWithout : kPlain;
+          if ((out >> lane) & 1) w.info.gone[__popcll(out & ((uint64_t{1} << lane) - 1))] = tok;
+          break;
+        }
+        node = __builtin_amdgcn_readfirstlane(next);
+        on_path |= uint64_t{1} << node;
+        ++len;
+      }
+    }
+    if (lane == 0) {
+      w.info.node = node;
+      w.info.mode = mode;
+      w.info.n_gone = n_gone;
+      w.info.bad = 0;
+      if (write) {
+        args.accept_node[r] = node;
+        args.accept_len[r] = len;
+      }
+    }
+    if (write && lane < T_) {
+      // A path's positions increase, so the i-th one is the i-th bit.
+      if ((on_path >> lane) & 1) args.path[row0 + __popcll(on_path & ((uint64_t{1} << lane) - 1))] = lane;
+      if (lane > len) args.path[row0 + lane] = -1;
+    }
+  }
+  __syncthreads();
+}
+
+// The thread's eight logits of a piece (those past the row's end: count 0).
+template <typename T> __device__ __forceinline__ int load_piece(const T* row, int V, int piece, float* z) {
+  const int e = piece * kPiece + threadIdx.x * 8;
+  load8<T>(row + min(e, V - 8), z);
+  return e < V ? 8 : 0;
+}
+
+__device__ __forceinline__ bool is_gone(const NodeInfo& info, int v) {
+  bool hit = false;
+  for (int i = 0; i < info.n_gone; ++i) hit = hit || info.gone[i] == v;
+  return hit;
+}
+
+// 2. Grid: (piece, request).
+template <typename T>
+__global__ __launch_bounds__(kThreads) void node_kernel(const SampleArgs args) {
+  __shared__ WalkLds w;
+  __shared__ double lds[kThreads / 64];
+  const int piece = blockIdx.x, rl = blockIdx.y, r = args.req0 + rl;
+  if (piece == 0 && r == 0 && args.status) {
+    int bad = 0;
+    for (int i = threadIdx.x; i < args.n_req; i += kThreads) bad += bad_temperature(temperature_of(args, i));
+    const double all = block_reduce(bad, add, lds);
+    if (threadIdx.x == 0) *args.status = static_cast<int32_t>(all);
+  }
+  walk<T>(args, rl, piece == 0, w);
+  if (piece == 0) {
+    const int32_t* src = reinterpret_cast<const int32_t*>(&w.info);
+    int32_t* dst = reinterpret_cast<int32_t*>(args.info + r);
+    for (int i = threadIdx.x; i < static_cast<int>(sizeof(NodeInfo) / 4); i += kThreads) dst[i] = src[i];
+  }
+  if (w.info.bad) return;
+  const T* row = static_cast<const T*>(args.logits) +
+                 (static_cast<int64_t>(r) * args.n_pos + w.info.node) * args.vocab;
+  float z[8];
+  const int n = load_piece(row, args.vocab, piece, z);
+  float m = -__builtin_inff();
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = fmaxf(m, __builtin_canonicalizef(z[i]));
+  const double M = block_reduce(m, larger, lds);
+  const Weigher weigh(M, temperature_of(args, r));
+  double sum = 0.0;
+  if (n) {
+    const int v0 = piece * kPiece + threadIdx.x * 8;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const double x = weigh(z[i]);
+      sum += w.info.mode == kWithout && is_gone(w.info, v0 + i) ? 0.0 : x;
+    }
+  }
+  sum = block_reduce(sum, add, lds);
+  if (threadIdx.x == 0) args.part[static_cast<int64_t>(r) * args.n_pieces + piece] = double2{M, sum};
+}
+
+// Maximum and total of the node's row from the pieces.
+__device__ __forceinline__ double2 row_total(const SampleArgs& a, int r, float tau, double* lds) {
+  const double2* p = a.part + static_cast<int64_t>(r) * a.n_pieces;
+  double M = -__builtin_inf(), s = 0.0;
+  for (int i = threadIdx.x; i < a.n_pieces; i += kThreads) M = fmax(M, p[i].x);
+  M = block_reduce(M, larger, lds);
+  const Weigher weigh(M, tau);
+  for (int i = threadIdx.x; i < a.n_pieces; i += kThreads) s += p[i].y * weigh(p[i].x);
+  return double2{M, block_reduce(s, add, lds)};
+}
+
+// Weights of the thread's eight logits: mode kRest with the row's maximum and
+// total (max(p - q, 0); a NaN in q leaves none), otherwise unnormalised.
+template <typename T>
+__device__ __forceinline__ double piece_weights(const SampleArgs& a, const NodeInfo& info, int mode, int r, int piece,
+                                                double2 mz, float tau, double* x) {
+  const int64_t row = (static_cast<int64_t>(r) * a.n_pos + info.node) * a.vocab;
+  float z[8];
+  const int n = load_piece(static_cast<const T*>(a.logits) + row, a.vocab, piece, z);
+  const int v0 = piece * kPiece + threadIdx.x * 8;
+  const Weigher weigh(mz.x, tau);
+  float q[8] = {};
+  if (mode == kRest && n) {
+    if (a.draft_bf16) load8<uint16_t>(static_cast<const uint16_t*>(a.draft) + row + v0, q);
+    else load8<float>(static_cast<const float*>(a.draft) + row + v0, q);
+  }
+  const double inv = 1.0 / mz.y;
+  double sum = 0.0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    double y = n ? weigh(z[i]) : 0.0;
+    if (mode == kRest) {
+      y = y * inv - static_cast<double>(q[i]);
+      y = n && y > 0.0 ? y : 0.0;
+    } else if (mode == kWithout && is_gone(info, v0 + i)) {
+      y = 0.0;
+    }
+    x[i] = y;
+    sum += y;
+  }
+  return sum;
+}
+
+// 3. Grid: (piece, request).
+template <typename T>
+__global__ __launch_bounds__(kThreads) void rest_kernel(const SampleArgs args) {
+  __shared__ double lds[kThreads / 64];
+  const int piece = blockIdx.x, r = args.req0 + blockIdx.y;
+  const NodeInfo& info = args.info[r];
+  if (info.bad || info.mode != kRest) return;
+  const float tau = temperature_of(args, r);
+  const double2 mz = row_total(args, r, tau, lds);
+  double x[8];
+  double sum = mz.y > 0.0 ? piece_weights<T>(args, info, kRest, r, piece, mz, tau, x) : 0.0;
+  sum = block_reduce(sum, add, lds);
+  if (threadIdx.x == 0) args.rest[static_cast<int64_t>(r) * args.n_pieces + piece] = sum;
+}
+
+// Inclusive sum over the block's threads, in order.
+__device__ __forceinline__ double block_scan(double x, double* lds) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const double y = __shfl_up(x, d);
+    x += lane >= d ? y : 0.0;
+  }
+  __syncthreads();
+  if (lane == 63) lds[wave] = x;
+  __syncthreads();
+  double before = 0.0;
+#pragma unroll
+  for (int i = 0; i < kThreads / 64; ++i) before += i < wave ? lds[i] : 0.0;
+  return before + x;
+}
+
+// First thread for which hit holds, or kThreads; the same in every thread.
+__device__ __forceinline__ int first_hit(bool hit, int32_t* lds) {
+  const uint64_t b = __ballot(hit);
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = b ? __builtin_ctzll(b) : 64;
+  __syncthreads();
+  int first = kThreads;
+  for (int i = kThreads / 64 - 1; i >= 0; --i) first = lds[i] < 64 ? i * 64 + lds[i] : first;
+  return first;
+}
+// Last one, or -1.
+__device__ __forceinline__ int last_hit(bool hit, int32_t* lds) {
+  const uint64_t b = __ballot(hit);
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = b ? 63 - __builtin_clzll(b) : -1;
+  __syncthreads();
+  int last = -1;
+  for (int i = 0; i < kThreads / 64; ++i) last = lds[i] >= 0 ? i * 64 + lds[i] : last;
+  return last;
+}
+
+// The piece where the cumulative sum of weight(piece) passes target: its
+// number and the sum before it. None passes: the last piece with any weight,
+// and a sum before it that nothing passes.
+template <typename W>
+__device__ __forceinline__ int find_piece(int n, W weight, double target, double* before, double* lds, int32_t* ilds) {
+  double carry = 0.0;
+  int last = -1;
+  for (int i0 = 0; i0 < n; i0 += kThreads) {
+    const int i = i0 + threadIdx.x;
+    const double x = i < n ? weight(i) : 0.0;
+    const double c = carry + block_scan(x, lds);
+    const int hit = first_hit(x > 0.0 && c > target, ilds);
+    __shared__ double edge;
+    if (hit < kThreads) {
+      if (static_cast<int>(threadIdx.x) == hit) edge = c - x;
+      __syncthreads();
+      *before = edge;
+      return i0 + hit;
+    }
+    const int lh = last_hit(x > 0.0, ilds);
+    last = lh >= 0 ? i0 + lh : last;
+    if (threadIdx.x == kThreads - 1) edge = c;
+    __syncthreads();
+    carry = edge;
+    __syncthreads();
+  }
+  *before = -__builtin_inf();
+  return last;
+}
+
+// 4. Grid: request.
+template <typename T>
+__global__ __launch_bounds__(kThreads) void draw_kernel(const SampleArgs args) {
+  __shared__ double lds[kThreads / 64];
+  __shared__ int32_t ilds[kThreads / 64];
+  const int r = args.req0 + blockIdx.x;
+  const NodeInfo& info = args.info[r];
+  if (info.bad) return;
+  const float tau = temperature_of(args, r);
+  const double u = args.uniforms[static_cast<int64_t>(r) * args.n_pos];
+  const double2 mz = row_total(args, r, tau, lds);
+  const Weigher weigh(mz.x, tau);
+  const double2* const part = args.part + static_cast<int64_t>(r) * args.n_pieces;
+  const double* const rest = args.rest + static_cast<int64_t>(r) * args.n_pieces;
+  int mode = info.mode;
+  double total = mz.y;
+  if (mode == kRest) {
+    double s = 0.0;
+    for (int i = threadIdx.x; i < args.n_pieces; i += kThreads) s += rest[i];
+    total = block_reduce(s, add, lds);
+  }
+  int pick = 0;
+  int piece = -1;
+  double before = 0.0;
+  if (total > 0.0) {
+    if (mode == kRest)
+      piece = find_piece(args.n_pieces, [&](int i) { return rest[i]; }, u * total, &before, lds, ilds);
+    else
+      piece = find_piece(args.n_pieces, [&](int i) { return part[i].y * weigh(part[i].x); }, u * total, &before, lds,
+                         ilds);
+  } else if (mode != kPlain) {
+    // Nothing is left over: the row itself. Its pieces' sums are at hand after
+    // a rest; with tokens taken out they are formed here, piece by piece.
+    mode = kPlain;
+    if (info.mode == kRest) {
+      total = mz.y;
+      if (total > 0.0)
+        piece = find_piece(args.n_pieces, [&](int i) { return part[i].y * weigh(part[i].x); }, u * total, &before, lds,
+                           ilds);
+    } else {
+      double x[8];
+      for (int i = 0; i < args.n_pieces; ++i)
+        total += block_reduce(piece_weights<T>(args, info, kPlain, r, i, mz, tau, x), add, lds);
+      double c = 0.0;
+      for (int i = 0; total > 0.0 && i < args.n_pieces; ++i) {
+        const double s = block_reduce(piece_weights<T>(args, info, kPlain, r, i, mz, tau, x), add, lds);
+        if (s > 0.0) {
+          piece = i;
+          before = c;
+          if (c + s > u * total) break;
+        }
+        c += s;
+      }
+    }
+  }
+  if (piece >= 0) {
+    double x[8];
+    const double sum = piece_weights<T>(args, info, mode, r, piece, mz, tau, x);
+    const double c = before + block_scan(sum, lds);
+    const double target = u * total;
+    int owner = first_hit(sum > 0.0 && c > target, ilds);
+    const bool passes = owner < kThreads;
+    if (!passes) owner = last_hit(sum > 0.0, ilds);
+    __shared__ int32_t pick_s;
+    if (threadIdx.x == 0) pick_s = 0;
+    __syncthreads();
+    if (static_cast<int>(threadIdx.x) == owner) {
+      double run = c - sum;
+      int p = 0;
+      bool done = false;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        run += x[i];
+        if (x[i] > 0.0 && !done) {
+          p = i;
+          done = passes && run > target;
+        }
+      }
+      pick_s = piece * kPiece + threadIdx.x * 8 + p;
+    }
+    __syncthreads();
+    pick = pick_s;
+  }
+  if (threadIdx.x == 0) args.bonus[r] = pick;
+}
+
+size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
 }  // namespace
 }  // namespace hrs
@@ -234,9 +593,41 @@ static bool sample_desc_ok(const hrs_sample_desc* d) {
          static_cast<int64_t>(d->n_req) * d->n_pos * ((static_cast<int64_t>(d->vocab) + 16383) / 16384) <= (1 << 24);
 }
 
+static int sample_chunks(const hrs_sample_desc* d) { return (d->vocab + kChunk - 1) / kChunk; }
+static int sample_pieces(const hrs_sample_desc* d) { return (d->vocab + kPiece - 1) / kPiece; }
+
 extern "C" size_t accept_sample_workspace_bytes(const hrs_sample_desc* d) {
   if (!sample_desc_ok(d)) return 0;
-  return static_cast<size_t>(d->n_req) * d->n_pos * sizeof(double2);
+  const size_t r = d->n_req;
+  return round256(r * d->n_pos * sample_chunks(d) * sizeof(double2)) + round256(r * sample_pieces(d) * sizeof(double2)) +
+         round256(r * sample_pieces(d) * sizeof(double)) + r * sizeof(NodeInfo);
+}
+
+template <typename T> static int sample_launch(const hrs_sample_desc* d, SampleArgs& args, hipStream_t s) {
+  const int per_launch = args.tree ? std::max(1, kGeomBytes / d->n_pos) : d->n_req;
+  (void)hipGetLastError();
+  for (int r0 = 0; r0 < d->n_req; r0 += per_launch) {
+    const int n = std::min(per_launch, d->n_req - r0);
+    args.req0 = r0;
+    if (args.tree)
+      for (int i = 0; i < n * d->n_pos; ++i)
+        args.parent[i] = static_cast<int8_t>(d->parent[static_cast<size_t>(r0) * d->n_pos + i]);
+    const int rows = args.tree ? d->n_pos : d->n_pos - 1;
+    const dim3 pieces(args.n_pieces, n);
+    if (rows > 0) {
+      hipLaunchKernelGGL(row_stats_kernel<T>, dim3(n * rows * args.n_chunks), dim3(kThreads), 0, s, args);
+      if (launch_error() != hipSuccess) return HRS_EDEVICE;
+    }
+    hipLaunchKernelGGL(node_kernel<T>, pieces, dim3(kThreads), 0, s, args);
+    if (launch_error() != hipSuccess) return HRS_EDEVICE;
+    if (args.draft) {
+      hipLaunchKernelGGL(rest_kernel<T>, pieces, dim3(kThreads), 0, s, args);
+      if (launch_error() != hipSuccess) return HRS_EDEVICE;
+    }
+    hipLaunchKernelGGL(draw_kernel<T>, dim3(n), dim3(kThreads), 0, s, args);
+    if (launch_error() != hipSuccess) return HRS_EDEVICE;
+  }
+  return HRS_OK;
 }
 
 extern "C" int accept_sample(const hrs_sample_desc* d, const void* logits, const int32_t* tokens,
@@ -263,31 +654,19 @@ extern "C" int accept_sample(const hrs_sample_desc* d, const void* logits, const
   args.logits = logits; args.tokens = tokens; args.uniforms = uniforms; args.draft = draft_probs;
   args.temperature = temperature; args.token_prob = token_prob; args.accept_node = accept_node;
   args.accept_len = accept_len; args.path = path; args.bonus = bonus; args.status = status;
-  args.stats = static_cast<double2*>(workspace);
-  args.n_req = d->n_req; args.n_pos = d->n_pos; args.vocab = d->vocab; args.req0 = 0;
+  args.n_req = d->n_req; args.n_pos = d->n_pos; args.vocab = d->vocab;
+  args.n_chunks = sample_chunks(d); args.n_pieces = sample_pieces(d);
   args.tree = d->topo == HRS_TREE;
   args.draft_bf16 = d->draft_dtype == HRS_BF16;
-  const hipStream_t s = static_cast<hipStream_t>(stream);
-  const bool bf16 = d->logit_dtype == HRS_BF16;
-  (void)hipGetLastError();
-  const dim3 rows(d->n_req * d->n_pos);
-  if (bf16)
-    hipLaunchKernelGGL(row_stats_kernel<uint16_t>, rows, dim3(kThreads), 0, s, args);
-  else
-    hipLaunchKernelGGL(row_stats_kernel<float>, rows, dim3(kThreads), 0, s, args);
-  if (launch_error() != hipSuccess) return HRS_EDEVICE;
-  const int per_launch = args.tree ? std::max(1, kGeomBytes / d->n_pos) : d->n_req;
-  for (int r0 = 0; r0 < d->n_req; r0 += per_launch) {
-    const int n = std::min(per_launch, d->n_req - r0);
-    args.req0 = r0;
-    if (args.tree)
-      for (int i = 0; i < n * d->n_pos; ++i)
-        args.parent[i] = static_cast<int8_t>(d->parent[static_cast<size_t>(r0) * d->n_pos + i]);
-    if (bf16)
-      hipLaunchKernelGGL(sample_kernel<uint16_t>, dim3(n), dim3(kThreads), 0, s, args);
-    else
-      hipLaunchKernelGGL(sample_kernel<float>, dim3(n), dim3(kThreads), 0, s, args);
-    if (launch_error() != hipSuccess) return HRS_EDEVICE;
-  }
-  return HRS_OK;
+  char* at = static_cast<char*>(workspace);
+  const size_t r = d->n_req;
+  args.stats = reinterpret_cast<double2*>(at);
+  at += round256(r * d->n_pos * args.n_chunks * sizeof(double2));
+  args.part = reinterpret_cast<double2*>(at);
+  at += round256(r * args.n_pieces * sizeof(double2));
+  args.rest = reinterpret_cast<double*>(at);
+  at += round256(r * args.n_pieces * sizeof(double));
+  args.info = reinterpret_cast<NodeInfo*>(at);
+  return d->logit_dtype == HRS_BF16 ? sample_launch<uint16_t>(d, args, static_cast<hipStream_t>(stream))
+                                    : sample_launch<float>(d, args, static_cast<hipStream_t>(stream));
 }
