@@ -7,7 +7,7 @@
 // Summary: greedy requests only; sampling falls back to plain decoding).
 //
 // MI355X design: three or four dependent launches, no host round trip.
-//  1. Row statistics: every 16384-logit chunk of every row that has a child
+//  1. Row statistics: every 32 KB chunk of every row that has a child
 //     (a leaf's probabilities are needed only if the walk ends there) is read
 //     once with nontemporal loads into registers, reduced to its maximum m and
 //     then to sum e^((z - m) / tau), float32 per thread, 64 bits across the
@@ -35,8 +35,10 @@ namespace hrs {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kChunk = 16384;                       // logits per statistics block
-constexpr int kIter = kChunk / (kThreads * 8);      // 8-logit slices per thread
+// Logits per statistics block, 32 KB of either type (16 rows of 151,936 bf16
+// logits: 8192 logits a block level, 32,768 8% slower; float32: 16,384 7%
+// slower).
+template <typename T> constexpr int kChunk = 32768 / sizeof(T);
 constexpr int kPiece = kThreads * 8;                // logits per node block
 
 enum : int32_t { kPlain = 0, kWithout = 1, kRest = 2 };   // weights: p; p without tokens; max(p - q, 0)
@@ -84,6 +86,30 @@ __device__ __forceinline__ bool bad_temperature(float tau) { return !(tau >= 0.0
 // Weight of a logit beside the maximum m: e^((z - m) / tau). Hard rows
 // (temperature 0, or +inf logits) give the largest logits one, the rest zero;
 // NaN has none, and neither has anything where there is no maximum.
+// e^x for x <= 0: x = n ln 2 + r with |r| <= ln 2 / 2, the power series of
+// e^r to r^12 (what is left out is below 2e-16 of it), n into the exponent.
+// About half the operations of the general function.
+__device__ __forceinline__ double exp_down(double x) {
+  x = fmax(x, -746.0);                    // below: zero
+  const double n = rint(x * 1.4426950408889634074);
+  double r = fma(n, -0.69314718055994530942, x);      // ln 2 in two parts: the nearest double
+  r = fma(n, -2.3190468138462995584e-17, r);          // and what it leaves
+  double y = 1.0 / 479001600.0;
+  y = fma(y, r, 1.0 / 39916800.0);
+  y = fma(y, r, 1.0 / 3628800.0);
+  y = fma(y, r, 1.0 / 362880.0);
+  y = fma(y, r, 1.0 / 40320.0);
+  y = fma(y, r, 1.0 / 5040.0);
+  y = fma(y, r, 1.0 / 720.0);
+  y = fma(y, r, 1.0 / 120.0);
+  y = fma(y, r, 1.0 / 24.0);
+  y = fma(y, r, 1.0 / 6.0);
+  y = fma(y, r, 0.5);
+  y = fma(y, r, 1.0);
+  y = fma(y, r, 1.0);
+  return ldexp(y, static_cast<int>(n));
+}
+
 struct Weigher {
   double m, inv;
   bool hard, none;
@@ -95,14 +121,40 @@ struct Weigher {
   __device__ __forceinline__ double operator()(double z) const {
     if (none || z != z) return 0.0;
     if (hard) return z == m ? 1.0 : 0.0;
-    return exp((z - m) * inv);
+    return exp_down((z - m) * inv);
   }
 };
 
-// Sums and maxima over the block, in a fixed order, the same in every thread.
+// A double's two halves through the same lane move.
+template <int CTRL> __device__ __forceinline__ double dpp_move(double x) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, x);
+  const uint32_t lo = __builtin_amdgcn_update_dpp(0, static_cast<int>(b), CTRL, 0xF, 0xF, false);
+  const uint32_t hi = __builtin_amdgcn_update_dpp(0, static_cast<int>(b >> 32), CTRL, 0xF, 0xF, false);
+  return __builtin_bit_cast(double, (static_cast<uint64_t>(hi) << 32) | lo);
+}
+
+// Sum or maximum over the wave, in a fixed order, the same in every lane:
+// four moves inside 16 lanes, two exchanges of rows.
+template <typename Op> __device__ __forceinline__ double wave_reduce(double x, Op op) {
+  x = op(x, dpp_move<0xB1>(x));
+  x = op(x, dpp_move<0x4E>(x));
+  x = op(x, dpp_move<0x141>(x));
+  x = op(x, dpp_move<0x140>(x));
+  auto join = [&](auto swap) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, x);
+    const auto lo = swap(static_cast<uint32_t>(b));
+    const auto hi = swap(static_cast<uint32_t>(b >> 32));
+    x = op(__builtin_bit_cast(double, (static_cast<uint64_t>(hi[0]) << 32) | lo[0]),
+           __builtin_bit_cast(double, (static_cast<uint64_t>(hi[1]) << 32) | lo[1]));
+  };
+  join([](uint32_t v) { return __builtin_amdgcn_permlane16_swap(v, v, false, false); });
+  join([](uint32_t v) { return __builtin_amdgcn_permlane32_swap(v, v, false, false); });
+  return x;
+}
+
+// The same over the block.
 template <typename Op> __device__ __forceinline__ double block_reduce(double x, Op op, double* lds) {
-#pragma unroll
-  for (int d = 32; d; d >>= 1) x = op(x, __shfl_xor(x, d));
+  x = wave_reduce(x, op);
   __syncthreads();
   if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = x;
   __syncthreads();
@@ -145,8 +197,9 @@ __global__ __launch_bounds__(kThreads) void row_stats_kernel(const SampleArgs ar
   }
   const float tau = temperature_of(args, args.req0 + rl);
   const T* base = static_cast<const T*>(args.logits) + row * args.vocab;
-  const int begin = chunk * kChunk;
-  const int end = min(args.vocab, begin + kChunk);
+  constexpr int kIter = kChunk<T> / (kThreads * 8);   // 8-logit slices per thread
+  const int begin = chunk * kChunk<T>;
+  const int end = min(args.vocab, begin + kChunk<T>);
   float v[kIter][8];
   float m = -__builtin_inff();
   // Slices past the row's end re-read its last eight logits: they change no
@@ -199,6 +252,8 @@ __device__ __forceinline__ double draft_value(const SampleArgs& a, int64_t i) {
 
 struct WalkLds {
   double prob[HRS_MAX_POS];
+  double need[HRS_MAX_POS];      // u q (q = 1 for a picked draft)
+  int32_t tok[HRS_MAX_POS];
   NodeInfo info;
 };
 
@@ -215,27 +270,44 @@ __device__ __forceinline__ void walk(const SampleArgs& args, int rl, bool write,
     __syncthreads();
     return;
   }
-  // Probability of every draft: one wave per position in turn, its lanes over
-  // the chunks of the parent's row.
-  for (int t = wave; t < T_; t += kThreads / 64) {
-    const int p = args.tree ? args.parent[rl * T_ + t] : t - 1;
+  // Probability of every draft: four lanes per position, each with every
+  // fourth chunk of the parent's row; all positions' loads go out together.
+  {
+    const int t = min(static_cast<int>(threadIdx.x) >> 2, T_ - 1);
+    const int sub = threadIdx.x & 3;
+    const int p = max(0, args.tree ? args.parent[rl * T_ + t] : t - 1);
     const int x = args.tokens[row0 + t];
+    const double u = args.uniforms[row0 + t];
+    const bool valid = t > 0 && x >= 0 && x < V;
     double pr = t == 0 ? 1.0 : 0.0;
-    if (t > 0 && x >= 0 && x < V) {
-      const double z = load_elem<T>(static_cast<const T*>(args.logits), (row0 + p) * V + x);
-      double M = -__builtin_inf(), s = 0.0;
+    double q = 1.0;
+    constexpr int kHeld = 5;           // chunks a lane keeps in registers
+    if (T_ > 1) {
       const double2* st = args.stats + (row0 + p) * args.n_chunks;
-      for (int i = lane; i < args.n_chunks; i += 64) M = fmax(M, st[i].x);
+      double2 held[kHeld];
+      double M = -__builtin_inf(), s = 0.0;
 #pragma unroll
-      for (int d = 32; d; d >>= 1) M = fmax(M, __shfl_xor(M, d));
+      for (int i = 0; i < kHeld; ++i) held[i] = st[min(sub + 4 * i, args.n_chunks - 1)];
+      const double z =
+          load_elem<T>(static_cast<const T*>(args.logits), (row0 + p) * V + (valid ? x : 0));
+      if (args.draft) q = draft_value(args, (row0 + p) * V + (valid ? x : 0));
+#pragma unroll
+      for (int i = 0; i < kHeld; ++i) M = fmax(M, held[i].x);
+      for (int i = sub + 4 * kHeld; i < args.n_chunks; i += 4) M = fmax(M, st[i].x);
+      M = fmax(M, __shfl_xor(M, 1));
+      M = fmax(M, __shfl_xor(M, 2));
       const Weigher weigh(M, tau);
-      for (int i = lane; i < args.n_chunks; i += 64) s += st[i].y * weigh(st[i].x);
 #pragma unroll
-      for (int d = 32; d; d >>= 1) s += __shfl_xor(s, d);
-      if (s > 0.0) pr = weigh(z) / s;
+      for (int i = 0; i < kHeld; ++i) s += sub + 4 * i < args.n_chunks ? held[i].y * weigh(held[i].x) : 0.0;
+      for (int i = sub + 4 * kHeld; i < args.n_chunks; i += 4) s += st[i].y * weigh(st[i].x);
+      s += __shfl_xor(s, 1);
+      s += __shfl_xor(s, 2);
+      if (valid && s > 0.0) pr = weigh(z) / s;
     }
-    if (lane == 0) {
+    if (sub == 0 && static_cast<int>(threadIdx.x) >> 2 < T_) {
       w.prob[t] = pr;
+      w.need[t] = valid || !args.draft ? u * q : __builtin_inf();
+      w.tok[t] = x;
       if (write) args.token_prob[row0 + t] = static_cast<float>(pr);
     }
   }
@@ -243,19 +315,15 @@ __device__ __forceinline__ void walk(const SampleArgs& args, int rl, bool write,
   if (wave == 0) {
     const int tl = min(lane, T_ - 1);
     const int par = lane >= T_ ? -2 : args.tree ? args.parent[rl * T_ + tl] : lane - 1;
-    const int tok = args.tokens[row0 + tl];
-    const double u = args.uniforms[row0 + tl];
+    const int tok = w.tok[tl];
+    const double need = w.need[tl];
     const double prob = w.prob[tl];
     int node = 0, len = 0, mode = kPlain, n_gone = 0;
     uint64_t on_path = 1;
     if (!args.tree) {
-      // u q < p with q = 1 for a picked draft: one comparison per position,
-      // the accepted length is the run of successes from position 1.
-      bool ok = false;
-      if (lane >= 1 && lane < T_ && tok >= 0 && tok < V) {
-        const double q = args.draft ? draft_value(args, (row0 + lane - 1) * V + tok) : 1.0;
-        ok = u * q < prob;
-      }
+      // One comparison per position; the accepted length is the run of
+      // successes from position 1.
+      const bool ok = lane >= 1 && lane < T_ && need < prob;
       const uint64_t hits = __ballot(ok);
       len = __builtin_ctzll(~(hits >> 1));
       node = len;
@@ -276,7 +344,7 @@ __device__ __forceinline__ void walk(const SampleArgs& args, int rl, bool write,
           kids &= kids - 1;
           const int tc = __builtin_amdgcn_readlane(tok, c);
           if (__ballot(tok == tc) & out) continue;
-          const double pc = __shfl(prob, c), uc = __shfl(u, c);
+          const double pc = __shfl(prob, c), uc = __shfl(need, c);
           if (uc * left < pc) {
             next = c;
             break;
@@ -321,10 +389,14 @@ template <typename T> __device__ __forceinline__ int load_piece(const T* row, in
   return e < V ? 8 : 0;
 }
 
-__device__ __forceinline__ bool is_gone(const NodeInfo& info, int v) {
-  bool hit = false;
-  for (int i = 0; i < info.n_gone; ++i) hit = hit || info.gone[i] == v;
-  return hit;
+// Which of the eight tokens from v0 were taken out, one bit each.
+__device__ __forceinline__ uint32_t gone_mask(const NodeInfo& info, int v0) {
+  uint32_t mask = 0;
+  for (int i = 0; i < info.n_gone; ++i) {
+    const uint32_t d = static_cast<uint32_t>(info.gone[i]) - static_cast<uint32_t>(v0);
+    mask |= d < 8 ? 1u << d : 0u;
+  }
+  return mask;
 }
 
 // 2. Grid: (piece, request).
@@ -357,26 +429,46 @@ __global__ __launch_bounds__(kThreads) void node_kernel(const SampleArgs args) {
   const Weigher weigh(M, temperature_of(args, r));
   double sum = 0.0;
   if (n) {
-    const int v0 = piece * kPiece + threadIdx.x * 8;
+    const uint32_t gone = w.info.mode == kWithout ? gone_mask(w.info, piece * kPiece + threadIdx.x * 8) : 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const double x = weigh(z[i]);
-      sum += w.info.mode == kWithout && is_gone(w.info, v0 + i) ? 0.0 : x;
-    }
+    for (int i = 0; i < 8; ++i) sum += (gone >> i) & 1 ? 0.0 : weigh(z[i]);
   }
   sum = block_reduce(sum, add, lds);
   if (threadIdx.x == 0) args.part[static_cast<int64_t>(r) * args.n_pieces + piece] = double2{M, sum};
 }
 
-// Maximum and total of the node's row from the pieces.
-__device__ __forceinline__ double2 row_total(const SampleArgs& a, int r, float tau, double* lds) {
-  const double2* p = a.part + static_cast<int64_t>(r) * a.n_pieces;
+// The pieces of a request, by every wave for itself (no barrier): each lane
+// takes consecutive ones, the first kHeld of them in registers, so that all
+// loads go out at once (up to 524,288 logits a row).
+constexpr int kHeld = 4;
+template <typename V> struct Pieces {
+  const V* p;
+  int i0, i1;
+  V held[kHeld];
+  __device__ __forceinline__ Pieces(const V* p_, int n) : p(p_) {
+    const int lane = threadIdx.x & 63;
+    const int per = (n + 63) / 64;
+    i0 = min(n, lane * per);
+    i1 = min(n, i0 + per);
+#pragma unroll
+    for (int k = 0; k < kHeld; ++k) held[k] = p[min(i0 + k, n - 1)];
+  }
+  template <typename F> __device__ __forceinline__ void each(F f) const {
+#pragma unroll
+    for (int k = 0; k < kHeld; ++k)
+      if (i0 + k < i1) f(i0 + k, held[k]);
+    for (int i = i0 + kHeld; i < i1; ++i) f(i, p[i]);
+  }
+};
+
+// Maximum and total of the node's row.
+__device__ __forceinline__ double2 row_total(const Pieces<double2>& part, float tau) {
   double M = -__builtin_inf(), s = 0.0;
-  for (int i = threadIdx.x; i < a.n_pieces; i += kThreads) M = fmax(M, p[i].x);
-  M = block_reduce(M, larger, lds);
+  part.each([&](int, double2 x) { M = fmax(M, x.x); });
+  M = wave_reduce(M, larger);
   const Weigher weigh(M, tau);
-  for (int i = threadIdx.x; i < a.n_pieces; i += kThreads) s += p[i].y * weigh(p[i].x);
-  return double2{M, block_reduce(s, add, lds)};
+  part.each([&](int, double2 x) { s += x.y * weigh(x.x); });
+  return double2{M, wave_reduce(s, add)};
 }
 
 // Weights of the thread's eight logits: mode kRest with the row's maximum and
@@ -394,6 +486,7 @@ __device__ __forceinline__ double piece_weights(const SampleArgs& a, const NodeI
     if (a.draft_bf16) load8<uint16_t>(static_cast<const uint16_t*>(a.draft) + row + v0, q);
     else load8<float>(static_cast<const float*>(a.draft) + row + v0, q);
   }
+  const uint32_t gone = mode == kWithout ? gone_mask(info, v0) : 0;
   const double inv = 1.0 / mz.y;
   double sum = 0.0;
 #pragma unroll
@@ -402,7 +495,7 @@ __device__ __forceinline__ double piece_weights(const SampleArgs& a, const NodeI
     if (mode == kRest) {
       y = y * inv - static_cast<double>(q[i]);
       y = n && y > 0.0 ? y : 0.0;
-    } else if (mode == kWithout && is_gone(info, v0 + i)) {
+    } else if ((gone >> i) & 1) {
       y = 0.0;
     }
     x[i] = y;
@@ -417,9 +510,10 @@ __global__ __launch_bounds__(kThreads) void rest_kernel(const SampleArgs args) {
   __shared__ double lds[kThreads / 64];
   const int piece = blockIdx.x, r = args.req0 + blockIdx.y;
   const NodeInfo& info = args.info[r];
-  if (info.bad || info.mode != kRest) return;
   const float tau = temperature_of(args, r);
-  const double2 mz = row_total(args, r, tau, lds);
+  const Pieces<double2> part(args.part + static_cast<int64_t>(r) * args.n_pieces, args.n_pieces);
+  if (info.bad || info.mode != kRest) return;
+  const double2 mz = row_total(part, tau);
   double x[8];
   double sum = mz.y > 0.0 ? piece_weights<T>(args, info, kRest, r, piece, mz, tau, x) : 0.0;
   sum = block_reduce(sum, add, lds);
@@ -453,7 +547,7 @@ __device__ __forceinline__ int first_hit(bool hit, int32_t* lds) {
   for (int i = kThreads / 64 - 1; i >= 0; --i) first = lds[i] < 64 ? i * 64 + lds[i] : first;
   return first;
 }
-// Last one, or -1.
+// Last thread for which hit holds, or -1.
 __device__ __forceinline__ int last_hit(bool hit, int32_t* lds) {
   const uint64_t b = __ballot(hit);
   __syncthreads();
@@ -464,34 +558,47 @@ __device__ __forceinline__ int last_hit(bool hit, int32_t* lds) {
   return last;
 }
 
-// The piece where the cumulative sum of weight(piece) passes target: its
-// number and the sum before it. None passes: the last piece with any weight,
-// and a sum before it that nothing passes.
-template <typename W>
-__device__ __forceinline__ int find_piece(int n, W weight, double target, double* before, double* lds, int32_t* ilds) {
-  double carry = 0.0;
-  int last = -1;
-  for (int i0 = 0; i0 < n; i0 += kThreads) {
-    const int i = i0 + threadIdx.x;
-    const double x = i < n ? weight(i) : 0.0;
-    const double c = carry + block_scan(x, lds);
-    const int hit = first_hit(x > 0.0 && c > target, ilds);
-    __shared__ double edge;
-    if (hit < kThreads) {
-      if (static_cast<int>(threadIdx.x) == hit) edge = c - x;
-      __syncthreads();
-      *before = edge;
-      return i0 + hit;
-    }
-    const int lh = last_hit(x > 0.0, ilds);
-    last = lh >= 0 ? i0 + lh : last;
-    if (threadIdx.x == kThreads - 1) edge = c;
-    __syncthreads();
-    carry = edge;
-    __syncthreads();
+// The piece where the cumulative sum of weight(piece) passes u times the
+// total, the sum before it and the total; by every wave for itself. None
+// passes: the last piece with any weight and a sum before it that nothing
+// passes; no weight at all: -1. Each lane takes consecutive pieces.
+struct Found {
+  int piece;
+  double before, total;
+};
+template <typename V, typename W> __device__ __forceinline__ Found find_piece(const Pieces<V>& pieces, W weight, double u) {
+  const int lane = threadIdx.x & 63;
+  double sum = 0.0;
+  pieces.each([&](int, V x) { sum += weight(x); });
+  double c = sum;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const double y = __shfl_up(c, d);
+    c += lane >= d ? y : 0.0;
   }
-  *before = -__builtin_inf();
-  return last;
+  Found f{-1, 0.0, __shfl(c, 63)};
+  const uint64_t some = __ballot(sum > 0.0);
+  if (!some) return f;
+  const double target = u * f.total;
+  const uint64_t hits = __ballot(sum > 0.0 && c > target);
+  const int owner = hits ? __builtin_ctzll(hits) : 63 - __builtin_clzll(some);
+  // The owner lane's pieces one by one.
+  double run = c - sum;
+  int piece = -1;
+  double before = 0.0;
+  bool done = false;
+  pieces.each([&](int i, V v) {
+    const double x = weight(v);
+    if (x > 0.0 && !done) {
+      piece = i;
+      before = run;
+      done = hits && run + x > target;
+    }
+    run += x;
+  });
+  f.piece = __shfl(piece, owner);
+  f.before = hits ? __shfl(before, owner) : -__builtin_inf();
+  return f;
 }
 
 // 4. Grid: request.
@@ -501,54 +608,42 @@ __global__ __launch_bounds__(kThreads) void draw_kernel(const SampleArgs args) {
   __shared__ int32_t ilds[kThreads / 64];
   const int r = args.req0 + blockIdx.x;
   const NodeInfo& info = args.info[r];
-  if (info.bad) return;
   const float tau = temperature_of(args, r);
   const double u = args.uniforms[static_cast<int64_t>(r) * args.n_pos];
-  const double2 mz = row_total(args, r, tau, lds);
+  const Pieces<double2> part(args.part + static_cast<int64_t>(r) * args.n_pieces, args.n_pieces);
+  const Pieces<double> rest((args.draft ? args.rest : &args.part[0].x) + static_cast<int64_t>(r) * args.n_pieces,
+                            args.n_pieces);
+  if (info.bad) return;
+  const double2 mz = row_total(part, tau);
   const Weigher weigh(mz.x, tau);
-  const double2* const part = args.part + static_cast<int64_t>(r) * args.n_pieces;
-  const double* const rest = args.rest + static_cast<int64_t>(r) * args.n_pieces;
+  auto whole = [&](double2 x) { return x.y * weigh(x.x); };
   int mode = info.mode;
-  double total = mz.y;
-  if (mode == kRest) {
-    double s = 0.0;
-    for (int i = threadIdx.x; i < args.n_pieces; i += kThreads) s += rest[i];
-    total = block_reduce(s, add, lds);
-  }
-  int pick = 0;
-  int piece = -1;
-  double before = 0.0;
-  if (total > 0.0) {
-    if (mode == kRest)
-      piece = find_piece(args.n_pieces, [&](int i) { return rest[i]; }, u * total, &before, lds, ilds);
-    else
-      piece = find_piece(args.n_pieces, [&](int i) { return part[i].y * weigh(part[i].x); }, u * total, &before, lds,
-                         ilds);
-  } else if (mode != kPlain) {
+  Found f = mode == kRest ? find_piece(rest, [](double x) { return x; }, u) : find_piece(part, whole, u);
+  if (f.piece < 0 && mode != kPlain) {
     // Nothing is left over: the row itself. Its pieces' sums are at hand after
     // a rest; with tokens taken out they are formed here, piece by piece.
     mode = kPlain;
     if (info.mode == kRest) {
-      total = mz.y;
-      if (total > 0.0)
-        piece = find_piece(args.n_pieces, [&](int i) { return part[i].y * weigh(part[i].x); }, u * total, &before, lds,
-                           ilds);
+      f = find_piece(part, whole, u);
     } else {
       double x[8];
       for (int i = 0; i < args.n_pieces; ++i)
-        total += block_reduce(piece_weights<T>(args, info, kPlain, r, i, mz, tau, x), add, lds);
+        f.total += block_reduce(piece_weights<T>(args, info, kPlain, r, i, mz, tau, x), add, lds);
       double c = 0.0;
-      for (int i = 0; total > 0.0 && i < args.n_pieces; ++i) {
+      for (int i = 0; f.total > 0.0 && i < args.n_pieces; ++i) {
         const double s = block_reduce(piece_weights<T>(args, info, kPlain, r, i, mz, tau, x), add, lds);
         if (s > 0.0) {
-          piece = i;
-          before = c;
-          if (c + s > u * total) break;
+          f.piece = i;
+          f.before = c;
+          if (c + s > u * f.total) break;
         }
         c += s;
       }
     }
   }
+  const int piece = f.piece;
+  const double before = f.before, total = f.total;
+  int pick = 0;
   if (piece >= 0) {
     double x[8];
     const double sum = piece_weights<T>(args, info, mode, r, piece, mz, tau, x);
@@ -588,18 +683,22 @@ size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 using namespace hrs;
 
 static bool sample_desc_ok(const hrs_sample_desc* d) {
-  return d && d->n_req >= 1 && d->n_req <= 65535 && d->vocab >= 8 && d->vocab % 8 == 0 && dtype_ok(d->logit_dtype) &&
+  return d && d->n_req >= 1 && d->n_req <= 65535 && d->vocab >= 8 && d->vocab <= (1 << 30) && d->vocab % 8 == 0 && dtype_ok(d->logit_dtype) &&
          (d->topo == HRS_CHAIN || d->topo == HRS_TREE) && d->n_pos >= 1 && d->n_pos <= HRS_MAX_POS &&
          static_cast<int64_t>(d->n_req) * d->n_pos * ((static_cast<int64_t>(d->vocab) + 16383) / 16384) <= (1 << 24);
 }
 
-static int sample_chunks(const hrs_sample_desc* d) { return (d->vocab + kChunk - 1) / kChunk; }
+static int sample_chunks(const hrs_sample_desc* d) {
+  const int chunk = d->logit_dtype == HRS_F32 ? kChunk<float> : kChunk<uint16_t>;
+  return (d->vocab + chunk - 1) / chunk;
+}
 static int sample_pieces(const hrs_sample_desc* d) { return (d->vocab + kPiece - 1) / kPiece; }
 
 extern "C" size_t accept_sample_workspace_bytes(const hrs_sample_desc* d) {
   if (!sample_desc_ok(d)) return 0;
   const size_t r = d->n_req;
-  return round256(r * d->n_pos * sample_chunks(d) * sizeof(double2)) + round256(r * sample_pieces(d) * sizeof(double2)) +
+  const size_t chunks = (d->vocab + kChunk<float> - 1) / kChunk<float>;   // enough for either type
+  return round256(r * d->n_pos * chunks * sizeof(double2)) + round256(r * sample_pieces(d) * sizeof(double2)) +
          round256(r * sample_pieces(d) * sizeof(double)) + r * sizeof(NodeInfo);
 }
 

@@ -768,7 +768,7 @@ size_t accept_sample_workspace_bytes(const hrs_sample_desc* desc);
  *           accept_node, accept_len, bonus [R], path [R][T] int32; all
  *           device. workspace: device scratch of at least
  *           accept_sample_workspace_bytes(desc) bytes, contents ignored.
- * Size limits as accept_greedy, and R <= 65535. Errors: HRS_EINVAL,
+ * Size limits as accept_greedy, R <= 65535 and V <= 2^30. Errors: HRS_EINVAL,
  * HRS_EALIGN, HRS_EGEOMETRY, HRS_EUNSUPPORTED (draft_probs with a tree),
  * HRS_EDEVICE.
  */
