@@ -10,7 +10,7 @@
 
 namespace hrs {
 
-constexpr int kAttnBlocks = 256;       // blocks of a launch at most: one per CU
+constexpr int kAttnCus = 256;          // compute units that a launch is cut for
 constexpr int kAttnReqs = 256;         // requests of a launch at most
 constexpr int kF32 = 0, kB16 = 1, kF8 = 2;   // span/cache types: f32/f32, bf16/bf16, bf16/e4m3
 
@@ -26,7 +26,7 @@ struct AttnArgs {
   const float* v_scale;
   void* out;
   int32_t* status;
-  int64_t* plan;      // workspace: units before every request [n + 1], for the join
+  int32_t* plan;      // workspace: units before every request [n + 1], for the join
   float* part;        // workspace: partial sums [2 * blocks][rows][d]
   float2* part_ml;    // workspace: their maximum and sum [2 * blocks][rows]
   int64_t q_stride;
@@ -46,6 +46,7 @@ struct AttnArgs {
   int32_t page_shift;
   int32_t table_len;
   int32_t tree;
+  int32_t log_blocks; // of the launch's blocks
   int8_t parent[kGeomBytes];
 };
 
@@ -59,9 +60,10 @@ template <int KIND, int D, int CLS> struct AttnCfg {
   static constexpr bool WIDE = D == 256;
   static constexpr int RT = CLS == 0 || (CLS == 3 && WIDE) ? 1 : 2;
   static constexpr int WR = CLS < 2 ? 1 : CLS == 2 ? 2 : WIDE ? 8 : 4;
-  static constexpr int WK = CLS < 2 ? (KIND == kF32 && WIDE ? 2 : 4) : CLS == 3 && WIDE ? 1 : 2;
-  static constexpr int SS = CLS < 2 ? 16 : CLS == 2 ? (WIDE && KIND != kB16 ? 16 : 32)
-                                                    : (KIND == kF32 && D == 128 ? 16 : 32);
+  static constexpr int WK = CLS < 2 ? (WIDE ? 2 : 4) : CLS == 2 ? 2 : 1;
+  static constexpr int SS = CLS < 2 ? 16 : CLS == 2 ? (WIDE ? 16 : 32) : (KIND == kF32 && D == 128 ? 16 : 32);
+  // Blocks of a CU: two where they fit (their waits and sums overlap).
+  static constexpr int PER_CU = CLS == 3 && !WIDE ? 2 : 1;
   static constexpr int NW = WR * WK;
   static constexpr int NT = 64 * NW;
   static constexpr int ROWS = 16 * RT * WR;
@@ -69,14 +71,12 @@ template <int KIND, int D, int CLS> struct AttnCfg {
   static constexpr int STAGE = 2 * TS * D * ESZ;            // keys and values of a tile, in the products' type
   static constexpr int NB = KIND == kF8 && WR > 1 ? 2 : 1;  // converted tiles (e4m3)
   static constexpr int RAW = KIND == kF8 ? STAGE / 2 : STAGE;
-  static constexpr int ROOM = 131072 - (KIND == kF8 ? NB * STAGE : 0);
+  static constexpr int ROOM = 131072 / PER_CU - (KIND == kF8 ? NB * STAGE : 0);
   static constexpr int NST = ROOM / RAW < 4 ? ROOM / RAW : 4;   // tiles on their way
   static constexpr int RING = KIND == kF8 ? NB * STAGE : 0;     // where the ring of loaded tiles starts
-  static constexpr int OROW = D * 4 + 16;                   // joined row in LDS, shifted by four banks a row
-  static constexpr int JOIN = WK * ROWS * (OROW + 8);
+  static constexpr int JOIN = WK / 2 * WR * RT * 64 * (D + 8);   // sums of half the wave groups
   static constexpr int LDS = RING + NST * RAW > JOIN ? RING + NST * RAW : JOIN;
-  static constexpr int SPAN_UNITS = 64 / TS > 0 ? 64 / TS : 1;
-  static_assert(NST >= 2 && LDS <= 155 * 1024, "tiles fit");
+  static_assert(NST >= 2 && LDS <= 155 * 1024 / PER_CU, "tiles fit");
 };
 
 // Work is counted in units: a unit is one tile of one (request, key/value
@@ -87,21 +87,27 @@ struct AttnUnits {
   int all;     // and the span's
 };
 
-__device__ __forceinline__ AttnUnits attn_units(const AttnArgs& a, int r, int ts, int* len_out) {
-  const int len = a.seq_len[r];
-  *len_out = len;
-  if (len < 0 || len > (a.table_len << a.page_shift)) return {0, 0, 0};
-  const int first = a.window > 0 && len + 1 > a.window ? (len + 1 - a.window) / ts : 0;
-  const int ctx = max(0, (len + ts - 1) / ts - first);
-  return {first, ctx, ctx + (a.n_pos + ts - 1) / ts};
+__device__ __forceinline__ AttnUnits attn_units(const AttnArgs& a, int len, unsigned ts) {
+  const bool ok = len >= 0 && len <= (a.table_len << a.page_shift);
+  const unsigned n = ok ? len : 0;
+  const unsigned first = a.window > 0 ? static_cast<unsigned>(max(static_cast<int>(n) + 1 - a.window, 0)) / ts : 0;
+  const int ctx = static_cast<int>((n + ts - 1) / ts - min(first, (n + ts - 1) / ts));
+  return {static_cast<int>(first), ctx, ok ? ctx + static_cast<int>((a.n_pos + ts - 1) / ts) : 0};
+}
+
+// Where block b's run of units starts: an even cut where there are at least
+// as many units as blocks (a power of two), one unit a block otherwise.
+__device__ __forceinline__ int attn_cut(int b, int total, int log_blocks) {
+  if (total <= (1 << log_blocks)) return min(b, total);
+  return static_cast<int>((static_cast<int64_t>(b) * total) >> log_blocks);
 }
 
 // Launches of one type (rows class cls, head size d); the number of rows a
 // block holds and the slots of its tile for it.
 struct AttnShape {
-  int rows, ts, nt;
+  int rows, ts, blocks;
 };
 template <int KIND> AttnShape attn_shape(int d, int cls);
-template <int KIND> void attn_launch(const AttnArgs& args, int d, int cls, int blocks, hipStream_t s);
+template <int KIND> void attn_launch(const AttnArgs& args, int d, int cls, hipStream_t s);
 
 }  // namespace hrs

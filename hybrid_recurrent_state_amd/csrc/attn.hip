@@ -24,22 +24,24 @@ namespace {
 // in flight (4 heads x 102 rows x 64 parts of 256: 35.7 us with one thread
 // group per row and all parts in it).
 template <bool F32, int D, int NS>
-__global__ __launch_bounds__(256) void attn_join_kernel(const AttnArgs args, int rows_per_block, int grid) {
+__global__ __launch_bounds__(256) void attn_join_kernel(const AttnArgs args, int rows_per_block) {
   constexpr int kPer = 256 / (D / 4) / NS;    // rows of a block
   const int heads = args.kvheads * args.row_blocks;
   const int i = blockIdx.x / heads;
   const int seg = blockIdx.x - i * heads;
   const int h = seg / args.row_blocks, rb = seg - h * args.row_blocks;
   const int r = args.req0 + i;
-  const int64_t total = args.plan[args.n_here];
-  const int64_t first = args.plan[i], end = args.plan[i + 1];
+  const int total = args.plan[args.n_here];
+  const int first = args.plan[i], end = args.plan[i + 1];
   if (end == first) return;
-  const int64_t units = (end - first) / heads;
-  const int64_t s0 = first + seg * units, s1 = s0 + units;
-  const int64_t blocks = min(static_cast<int64_t>(grid), total);
+  const int units = (end - first) / heads;
+  const int s0 = first + seg * units, s1 = s0 + units;
   // Block of a unit: the last whose run starts at or before it.
-  const int b0 = static_cast<int>(((s0 + 1) * blocks - 1) / total);
-  const int b1 = static_cast<int>((s1 * blocks - 1) / total);
+  auto block_of = [&](int u) {
+    if (total <= (1 << args.log_blocks)) return u;
+    return static_cast<int>((((static_cast<int64_t>(u) + 1) << args.log_blocks) - 1) / total);
+  };
+  const int b0 = block_of(s0), b1 = block_of(s1 - 1);
   if (b0 == b1) return;                       // one block had all of it and wrote the result
   const int d4 = threadIdx.x % (D / 4);
   const int ns = threadIdx.x / (D / 4) % NS;
@@ -111,21 +113,21 @@ __global__ __launch_bounds__(256) void attn_join_kernel(const AttnArgs args, int
         u32x2{pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3])};
 }
 
-template <bool F32, int D> void launch_join_d(const AttnArgs& args, const AttnShape& sh, int grid, hipStream_t s) {
+template <bool F32, int D> void launch_join_d(const AttnArgs& args, const AttnShape& sh, hipStream_t s) {
   const int rows = std::min(sh.rows, args.rows);
   const int segs = args.n_here * args.kvheads * args.row_blocks;
   constexpr int kMost = 256 / (D / 4);        // copies of a row that fill a block
   if (static_cast<int64_t>(segs) * rows <= 2048)
-    hipLaunchKernelGGL((attn_join_kernel<F32, D, kMost>), dim3(segs, rows), dim3(256), 0, s, args, sh.rows, grid);
+    hipLaunchKernelGGL((attn_join_kernel<F32, D, kMost>), dim3(segs, rows), dim3(256), 0, s, args, sh.rows);
   else
     hipLaunchKernelGGL((attn_join_kernel<F32, D, 1>), dim3(segs, (rows + kMost - 1) / kMost), dim3(256), 0, s, args,
-                       sh.rows, grid);
+                       sh.rows);
 }
 
-template <bool F32> void launch_join(const AttnArgs& args, int d, const AttnShape& sh, int grid, hipStream_t s) {
-  if (d == 64) launch_join_d<F32, 64>(args, sh, grid, s);
-  if (d == 128) launch_join_d<F32, 128>(args, sh, grid, s);
-  if (d == 256) launch_join_d<F32, 256>(args, sh, grid, s);
+template <bool F32> void launch_join(const AttnArgs& args, int d, const AttnShape& sh, hipStream_t s) {
+  if (d == 64) launch_join_d<F32, 64>(args, sh, s);
+  if (d == 128) launch_join_d<F32, 128>(args, sh, s);
+  if (d == 256) launch_join_d<F32, 256>(args, sh, s);
 }
 
 bool sizes_ok(const hrs_attn_desc* d) {
@@ -142,7 +144,7 @@ AttnShape shape_of(const hrs_attn_desc* d, int kind) {
                                                                    : attn_shape<kF8>(d->d, cls);
 }
 
-constexpr size_t kPlanBytes = ((kAttnReqs + 1) * sizeof(int64_t) + 255) / 256 * 256;
+constexpr size_t kPlanBytes = ((kAttnReqs + 1) * sizeof(int32_t) + 255) / 256 * 256;
 
 }  // namespace
 }  // namespace hrs
@@ -151,9 +153,11 @@ using namespace hrs;
 
 extern "C" size_t attn_verify_span_workspace_bytes(const hrs_attn_desc* d) {
   if (!sizes_ok(d) || (d->d != 64 && d->d != 128 && d->d != 256)) return 0;
-  // The rows that a block holds depend on the sizes alone, not on the types.
-  const size_t rows = shape_of(d, kB16).rows;
-  return kPlanBytes + 2 * kAttnBlocks * rows * (static_cast<size_t>(d->d) * sizeof(float) + sizeof(float2));
+  // A block's rows and the number of blocks depend on the sizes alone, not on
+  // the types.
+  const AttnShape sh = shape_of(d, kB16);
+  const size_t rows = sh.rows;
+  return kPlanBytes + 2 * static_cast<size_t>(sh.blocks) * rows * (static_cast<size_t>(d->d) * sizeof(float) + sizeof(float2));
 }
 
 extern "C" int attn_verify_span(const hrs_attn_desc* d, const void* q, const void* k, const void* v,
@@ -191,9 +195,9 @@ extern "C" int attn_verify_span(const hrs_attn_desc* d, const void* q, const voi
   args.page_table = page_table; args.seq_len = seq_len; args.k_scale = k_scale; args.v_scale = v_scale;
   args.out = out; args.status = status;
   char* const ws = static_cast<char*>(workspace);
-  args.plan = reinterpret_cast<int64_t*>(ws);
+  args.plan = reinterpret_cast<int32_t*>(ws);
   args.part = reinterpret_cast<float*>(ws + kPlanBytes);
-  args.part_ml = reinterpret_cast<float2*>(ws + kPlanBytes + sizeof(float) * 2 * kAttnBlocks * sh.rows * d->d);
+  args.part_ml = reinterpret_cast<float2*>(ws + kPlanBytes + sizeof(float) * 2 * sh.blocks * sh.rows * d->d);
   args.scale = d->scale; args.window = d->window; args.n_req = d->n_req; args.n_pos = d->n_pos;
   args.kvheads = d->n_kvheads; args.group = d->n_heads / d->n_kvheads;
   args.rows = args.n_pos * args.group;
@@ -201,7 +205,14 @@ extern "C" int attn_verify_span(const hrs_attn_desc* d, const void* q, const voi
   args.n_pages = d->cache.n_pages; args.table_len = d->cache.table_len;
   args.page_shift = __builtin_ctz(static_cast<unsigned>(d->cache.page_size));
   args.tree = d->topo == HRS_TREE;
-  const int per_launch = args.tree ? std::min(kAttnReqs, std::max(1, kGeomBytes / d->n_pos)) : kAttnReqs;
+  // Units are counted in 32 bits: fewer requests a launch for tables of very
+  // many slots.
+  const int64_t slots = (static_cast<int64_t>(args.table_len) << args.page_shift) + HRS_MAX_POS;
+  const int64_t most = static_cast<int64_t>(args.kvheads) * args.row_blocks * (slots / sh.ts + 2);
+  if (most > INT32_MAX) return HRS_EINVAL;
+  const int per_launch =
+      static_cast<int>(std::min<int64_t>(args.tree ? std::min(kAttnReqs, std::max(1, kGeomBytes / d->n_pos)) : kAttnReqs,
+                                         INT32_MAX / most));
   const int cls = rows_class(args.rows);
   const hipStream_t s = static_cast<hipStream_t>(stream);
   (void)hipGetLastError();
@@ -211,16 +222,16 @@ extern "C" int attn_verify_span(const hrs_attn_desc* d, const void* q, const voi
     if (args.tree)
       for (int i = 0; i < args.n_here * d->n_pos; ++i)
         args.parent[i] = static_cast<int8_t>(d->parent[static_cast<size_t>(r0) * d->n_pos + i]);
-    // No more blocks than the longest contexts the table could hold have tiles.
-    const int64_t slots = (static_cast<int64_t>(args.table_len) << args.page_shift) + HRS_MAX_POS;
-    const int64_t most = static_cast<int64_t>(args.n_here) * args.kvheads * args.row_blocks * (slots / sh.ts + 2);
-    const int grid = static_cast<int>(std::min<int64_t>(kAttnBlocks, most));
-    if (kind == kF32) attn_launch<kF32>(args, d->d, cls, grid, s);
-    else if (kind == kB16) attn_launch<kB16>(args, d->d, cls, grid, s);
-    else attn_launch<kF8>(args, d->d, cls, grid, s);
+    // No more blocks than the longest contexts the table could hold have
+    // tiles, a power of two.
+    args.log_blocks = 0;
+    while ((1 << args.log_blocks) < sh.blocks && (1 << args.log_blocks) < args.n_here * most) ++args.log_blocks;
+    if (kind == kF32) attn_launch<kF32>(args, d->d, cls, s);
+    else if (kind == kB16) attn_launch<kB16>(args, d->d, cls, s);
+    else attn_launch<kF8>(args, d->d, cls, s);
     if (launch_error() != hipSuccess) return HRS_EDEVICE;
-    if (kind == kF32) launch_join<true>(args, d->d, sh, grid, s);
-    else launch_join<false>(args, d->d, sh, grid, s);
+    if (kind == kF32) launch_join<true>(args, d->d, sh, s);
+    else launch_join<false>(args, d->d, sh, s);
     if (launch_error() != hipSuccess) return HRS_EDEVICE;
   }
   return HRS_OK;

@@ -45,6 +45,15 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) char lds_char;
 
+// The same number, but what is computed from it is computed after this point:
+// keeps addresses that are needed once per segment out of the registers of the
+// tile loop (where a spilled register's reload waits for all tiles on their
+// way).
+__device__ __forceinline__ int fresh(int x) {
+  asm volatile("" : "+v"(x));
+  return x;
+}
+
 __device__ __forceinline__ void mem_fence() { asm volatile("" ::: "memory"); }
 
 // Waits until at most n of this wave's vector memory operations are on their
@@ -54,6 +63,13 @@ template <int N> __device__ __forceinline__ void wait_vm() {
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
 
+// All waves have read what they read before (their reads' results are in
+// registers that they have used) and waited for their own loads.
+__device__ __forceinline__ void read_barrier() {
+  mem_fence();
+  __builtin_amdgcn_s_barrier();
+  mem_fence();
+}
 // All waves' LDS writes before, all reads after.
 __device__ __forceinline__ void block_barrier() {
   asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
@@ -69,11 +85,40 @@ template <typename T> __device__ __forceinline__ const __attribute__((address_sp
   return reinterpret_cast<const __attribute__((address_space(3))) T*>(a);
 }
 
-// Within each group of 16 lanes, lane i receives as its j-th value element
-// i % 4 of the four 16-bit values that lane 4 j + i / 4 addresses.
-__device__ __forceinline__ u32x2 read_tr16(uint32_t a) {
-  const s16x4 v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)a);
-  return __builtin_bit_cast(u32x2, v);
+// Four transposing LDS reads at a0 .. a3 plus OFF, and four more at OFF2 (if
+// not negative): within each group of 16 lanes, lane i receives as its j-th
+// value element i % 4 of the four 16-bit values that lane 4 j + i / 4
+// addresses. In assembly with their wait: the compiler puts a wait for every
+// load to LDS on its way (vmcnt(0)) ahead of the builtin, which would drain
+// the ring of tiles once per tile.
+template <int OFF, int OFF2>
+__device__ __forceinline__ void read_tr16(uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, u32x2 (&x)[4],
+                                          u32x2 (&y)[4]) {
+  if constexpr (OFF2 < 0) {
+    asm volatile(
+        "ds_read_b64_tr_b16 %0, %4 offset:%8\n\t"
+        "ds_read_b64_tr_b16 %1, %5 offset:%8\n\t"
+        "ds_read_b64_tr_b16 %2, %6 offset:%8\n\t"
+        "ds_read_b64_tr_b16 %3, %7 offset:%8\n\t"
+        "s_waitcnt lgkmcnt(0)"
+        : "=&v"(x[0]), "=&v"(x[1]), "=&v"(x[2]), "=&v"(x[3])
+        : "v"(a0), "v"(a1), "v"(a2), "v"(a3), "n"(OFF)
+        : "memory");
+  } else {
+    asm volatile(
+        "ds_read_b64_tr_b16 %0, %8 offset:%12\n\t"
+        "ds_read_b64_tr_b16 %4, %8 offset:%13\n\t"
+        "ds_read_b64_tr_b16 %1, %9 offset:%12\n\t"
+        "ds_read_b64_tr_b16 %5, %9 offset:%13\n\t"
+        "ds_read_b64_tr_b16 %2, %10 offset:%12\n\t"
+        "ds_read_b64_tr_b16 %6, %10 offset:%13\n\t"
+        "ds_read_b64_tr_b16 %3, %11 offset:%12\n\t"
+        "ds_read_b64_tr_b16 %7, %11 offset:%13\n\t"
+        "s_waitcnt lgkmcnt(0)"
+        : "=&v"(x[0]), "=&v"(x[1]), "=&v"(x[2]), "=&v"(x[3]), "=&v"(y[0]), "=&v"(y[1]), "=&v"(y[2]), "=&v"(y[3])
+        : "v"(a0), "v"(a1), "v"(a2), "v"(a3), "n"(OFF), "n"(OFF2)
+        : "memory");
+  }
 }
 
 // Larger (or sum) over the four lanes that hold one query row.
@@ -114,6 +159,7 @@ template <int KIND, int D, int CLS> struct AttnBlock {
   static constexpr int SPS = 2 * C::SS * CPR / (64 * C::WR);              // pieces of a wave per tile in LDS
   static constexpr int DT = D / 16;
   static constexpr int QC = D * ESZ / 64;                                 // pieces of a query row per lane
+  static_assert(SB <= 2, "one or two blocks of 16 slots");
   static_assert(LPS >= 1 && LPS * 64 * C::WR == 2 * C::SS * RCPR && (C::NST - 1) * LPS < 64, "whole loads");
 
   const AttnArgs& a;
@@ -130,7 +176,8 @@ template <int KIND, int D, int CLS> struct AttnBlock {
   float c_ctx, c_span, vs;
   uint32_t head_bytes;         // a page of all heads
   uint64_t h_bytes;            // this head's part of it
-  uint64_t present;            // 4 bits a tile: 16-slot groups whose page is there
+  uint32_t ring;               // SB bits a started tile: 16-slot groups whose page is there
+  int next;                    // next tile to start
   int pg[SB];                  // pages of the next tile to load
 
   __device__ __forceinline__ AttnBlock(const AttnArgs& args, char* l_, AttnRows<C::ROWS>* rows_) : a(args), lds(l_), rows(rows_) {
@@ -163,18 +210,18 @@ template <int KIND, int D, int CLS> struct AttnBlock {
     char* const dst = lds + C::RING + i_ring * C::RAW + kg * (C::RAW / C::WK);
     const bool span = u >= un.ctx;
     if (!span) {
-      uint32_t here = 0;
+      uint32_t there = 0;
       int64_t at[SB];
 #pragma unroll
       for (int i = 0; i < SB; ++i) {
         const bool ok = pg[i] >= 0 && pg[i] < a.n_pages;
-        here |= ok ? 1u << i : 0u;
+        there |= ok ? 1u << i : 0u;
         const int in_page = (slot0(u) + 16 * i) & ((1 << a.page_shift) - 1);
         // Bytes: (page * heads + head) rows of a page, then the row.
         at[i] = static_cast<int64_t>(static_cast<uint64_t>(static_cast<uint32_t>(ok ? pg[i] : 0)) * head_bytes) +
                 static_cast<int64_t>(h_bytes + static_cast<uint32_t>(in_page) * (D * CSZ));
       }
-      present = (present & ~(uint64_t{15} << (4 * (u & 15)))) | (static_cast<uint64_t>(here) << (4 * (u & 15)));
+      ring = ring << SB | there;
       constexpr int kRows = 64 * C::WR / RCPR;              // rows that one load of all the group's waves covers
 #pragma unroll
       for (int i = 0; i < LPS; ++i) {
@@ -196,6 +243,7 @@ template <int KIND, int D, int CLS> struct AttnBlock {
                                          (__attribute__((address_space(3))) void*)(dst + p0 * 16), 16, 0, 0);
       }
     } else if constexpr (KIND != kF8) {
+      ring <<= SB;
 #pragma unroll
       for (int i = 0; i < LPS; ++i) {
         const int p0 = (i * C::WR + wr) * 64;
@@ -209,7 +257,7 @@ template <int KIND, int D, int CLS> struct AttnBlock {
   // Address of piece p of the wave group's part of span tile u, permuted;
   // rows behind the span repeat its last one.
   __device__ __forceinline__ const char* span_piece(int u, int p) const {
-    asm volatile("" : "+v"(p));     // formed here, not kept in registers over the context's tiles
+    p = fresh(p);
     const int row = p / CPR;
     const int c = (p % CPR) ^ swizzle<CPR>(row);
     const int s = min((u - un.ctx) * C::TS + kg * C::SS + row % C::SS, a.n_pos - 1);
@@ -252,8 +300,9 @@ template <int KIND, int D, int CLS> struct AttnBlock {
     }
   }
 
-  // Query rows of the segment: pieces, root paths.
-  __device__ __forceinline__ void load_rows(const int8_t* par) {
+  // Query rows of the segment: pieces, and what masks need to know.
+  __device__ __forceinline__ void load_rows() {
+    const int n16 = fresh(this->n16), g = fresh(this->g);
     idle = rb * C::ROWS + wr * (16 * C::RT) >= a.rows;
 #pragma unroll
     for (int rt = 0; rt < C::RT; ++rt) {
@@ -268,6 +317,34 @@ template <int KIND, int D, int CLS> struct AttnBlock {
         q[rt][c] = u32x4{};
         if (on) q[rt][c] = *reinterpret_cast<const u32x4*>(src + (4 * c + g) * 16);
       }
+      m[rt] = -__builtin_inff();
+      l[rt] = 0.0f;
+#pragma unroll
+      for (int dt = 0; dt < DT; ++dt) o[rt][dt] = f32x4{};
+    }
+  }
+  // Waits for the rows (and scales) here: in the tile loop, a wait for a load
+  // of the past would be a wait for the tiles on their way.
+  static __device__ __forceinline__ float uniform(float x) {
+    return __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(x)));
+  }
+  __device__ __forceinline__ void settle() {
+#pragma unroll
+    for (int rt = 0; rt < C::RT; ++rt)
+#pragma unroll
+      for (int c = 0; c < QC; ++c) asm volatile("" : "+v"(q[rt][c]));
+    vs = uniform(vs);
+    c_ctx = uniform(c_ctx);
+  }
+  __device__ __forceinline__ void mask_rows(const int8_t* par) {
+    if (kg != 0) return;
+    const int n16 = fresh(this->n16), g = fresh(this->g);
+#pragma unroll
+    for (int rt = 0; rt < C::RT; ++rt) {
+      const int lrow = (wr * C::RT + rt) * 16 + n16;
+      const int row = rb * C::ROWS + lrow;
+      const bool on = row < a.rows;
+      const int t = on ? row / a.group : 0;
       uint64_t path = 0;
       int dep = 0;
       if (a.tree) {
@@ -281,16 +358,15 @@ template <int KIND, int D, int CLS> struct AttnBlock {
         if (a.window > 0 && a.window <= t) path &= ~uint64_t{0} << (t + 1 - a.window);
         dep = t;
       }
-      if (kg == 0 && g == 0) {
-        rows->anc[(wr * C::RT + rt) * 16 + n16] = on ? path : 0;
-        rows->first[(wr * C::RT + rt) * 16 + n16] = !on ? INT32_MAX : a.window > 0 ? max(0, len + dep - a.window + 1) : 0;
+      if (g == 0) {
+        rows->anc[lrow] = on ? path : 0;
+        rows->first[lrow] = !on ? INT32_MAX : a.window > 0 ? max(0, len + dep - a.window + 1) : 0;
       }
-      m[rt] = -__builtin_inff();
-      l[rt] = 0.0f;
-#pragma unroll
-      for (int dt = 0; dt < DT; ++dt) o[rt][dt] = f32x4{};
     }
   }
+
+  // Groups of 16 slots of a started context tile whose page is there.
+  __device__ __forceinline__ uint32_t here(int u) const { return (ring >> ((next - 1 - u) * SB)) & ((1u << SB) - 1); }
 
   // Which of a tile's slots that this lane holds count for its row (bit 4 sb
   // + i: slot 16 sb + 4 g + i of the wave group's part).
@@ -309,7 +385,7 @@ template <int KIND, int D, int CLS> struct AttnBlock {
     const int first = rows->first[lrow];
 #pragma unroll
     for (int sb = 0; sb < SB; ++sb) {
-      if (!((present >> (4 * (u & 15) + sb)) & 1)) continue;
+      if (!((here(u) >> sb) & 1)) continue;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int j = j0 + 16 * sb + i;
@@ -423,25 +499,15 @@ template <int KIND, int D, int CLS> struct AttnBlock {
       }
       l[rt] += sum;
     }
-    if (odd) {
-      values<true>(vt, s, pb, u, span);
-    } else {
-      values<false>(vt, s, pb, u, span);
-    }
+    values(vt, s, pb, u, span, odd);
   }
 
-  // O^T += V^T P^T. ODD: values that are not finite leave the product; the
-  // products of "counts" with "+inf or NaN" and with "-inf or NaN" say which
-  // rows' sums get +inf, -inf or both (NaN).
-  template <bool ODD>
+  // O^T += V^T P^T. odd (rare): values that are not finite leave the product;
+  // the products of "counts" with "+inf or NaN" and with "-inf or NaN" say
+  // which rows' sums get +inf, -inf or both (NaN).
   __device__ __forceinline__ void values(const char* vt, const f32x4 (&s)[C::RT][SB], const u32x2 (&pb)[C::RT][SB], int u,
-                                         bool span) {
+                                         bool span, bool odd) {
     const float inf = __builtin_inff();
-    uint32_t seen[C::RT];
-    if (ODD) {
-#pragma unroll
-      for (int rt = 0; rt < C::RT; ++rt) seen[rt] = visible(u, rt, span);
-    }
     const uint32_t vb = lds_address(vt);
     if constexpr (KIND == kF32) {
       // Row 16 sb + 4 g + i, element 16 dt + n16: one address per i.
@@ -451,90 +517,105 @@ template <int KIND, int D, int CLS> struct AttnBlock {
         va[i] = vb + (4 * g + i) * (D * 4) + (((n16 >> 2) ^ swizzle<CPR>(4 * g + i)) << 4) + (n16 & 3) * 4;
 #pragma unroll
       for (int dt = 0; dt < DT; ++dt) {
-        f32x4 up[C::RT], down[C::RT];
-#pragma unroll
-        for (int rt = 0; rt < C::RT; ++rt) up[rt] = down[rt] = f32x4{};
+        float v[SB][4];
 #pragma unroll
         for (int sb = 0; sb < SB; ++sb)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float v = *lds_at<float>((va[i] ^ (dt << 6)) + sb * 16 * D * 4);
-            if (ODD) {
-              const float hi = v == inf || v != v ? 1.0f : 0.0f, lo = v == -inf || v != v ? 1.0f : 0.0f;
-              v = not_finite(v) ? 0.0f : v;
+          for (int i = 0; i < 4; ++i) v[sb][i] = *lds_at<float>((va[i] ^ (dt << 6)) + sb * 16 * D * 4);
+        if (odd) {
 #pragma unroll
-              for (int rt = 0; rt < C::RT; ++rt) {
-                const float p = (seen[rt] >> (4 * sb + i)) & 1 ? 1.0f : 0.0f;
-                up[rt] = __builtin_amdgcn_mfma_f32_16x16x4f32(hi, p, up[rt], 0, 0, 0);
-                down[rt] = __builtin_amdgcn_mfma_f32_16x16x4f32(lo, p, down[rt], 0, 0, 0);
+          for (int rt = 0; rt < C::RT; ++rt) {
+            const uint32_t seen = visible(u, rt, span);
+            f32x4 up = {}, down = {};
+#pragma unroll
+            for (int sb = 0; sb < SB; ++sb)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const float x = v[sb][i];
+                const float p = (seen >> (4 * sb + i)) & 1 ? 1.0f : 0.0f;
+                up = __builtin_amdgcn_mfma_f32_16x16x4f32(x == inf || x != x ? 1.0f : 0.0f, p, up, 0, 0, 0);
+                down = __builtin_amdgcn_mfma_f32_16x16x4f32(x == -inf || x != x ? 1.0f : 0.0f, p, down, 0, 0, 0);
               }
-            }
+            add_odd(o[rt][dt], up, down);
+            __builtin_amdgcn_sched_barrier(0);     // one at a time: registers
+          }
+#pragma unroll
+          for (int sb = 0; sb < SB; ++sb)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[sb][i] = not_finite(v[sb][i]) ? 0.0f : v[sb][i];
+        }
+#pragma unroll
+        for (int sb = 0; sb < SB; ++sb)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int rt = 0; rt < C::RT; ++rt)
-              o[rt][dt] = __builtin_amdgcn_mfma_f32_16x16x4f32(v, s[rt][sb][i], o[rt][dt], 0, 0, 0);
-          }
-        if (ODD) {
-#pragma unroll
-          for (int rt = 0; rt < C::RT; ++rt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[rt][dt][e] += (up[rt][e] > 0.0f ? inf : 0.0f) - (down[rt][e] > 0.0f ? inf : 0.0f);
-          __builtin_amdgcn_sched_barrier(0);
-        }
+              o[rt][dt] = __builtin_amdgcn_mfma_f32_16x16x4f32(v[sb][i], s[rt][sb][i], o[rt][dt], 0, 0, 0);
       }
     } else {
       const int vrow = 4 * g + (n16 >> 2);
       const uint32_t va = vb + vrow * (D * ESZ) + ((((n16 & 3) >> 1) ^ swizzle<CPR>(vrow)) << 4) + (n16 & 1) * 8;
 #pragma unroll
-      for (int dt = 0; dt < DT; ++dt) {
-        u32x2 w[SB];
+      for (int d4 = 0; d4 < DT; d4 += 4) {
+        u32x2 w[SB > 1 ? SB : 2][4];
+        read_tr16<0, (SB > 1 ? 16 * D * ESZ : -1)>(va ^ (d4 << 5), va ^ ((d4 + 1) << 5), va ^ ((d4 + 2) << 5),
+                                                   va ^ ((d4 + 3) << 5), w[0], w[1]);
+        if (odd) {
 #pragma unroll
-        for (int sb = 0; sb < SB; ++sb) w[sb] = read_tr16((va ^ (dt << 5)) + sb * 16 * D * ESZ);
-        if (ODD) {
-          f32x4 up[C::RT], down[C::RT];
-#pragma unroll
-          for (int rt = 0; rt < C::RT; ++rt) up[rt] = down[rt] = f32x4{};
-#pragma unroll
-          for (int sb = 0; sb < SB; ++sb) {
-            s16x4 hi, lo;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint32_t half = (w[sb][i >> 1] >> (16 * (i & 1))) & 0xFFFFu;
-              const bool nan = (half & 0x7FFFu) > 0x7F80u;
-              hi[i] = half == 0x7F80u || nan ? 0x3F80 : 0;
-              lo[i] = half == 0xFF80u || nan ? 0x3F80 : 0;
-              if ((half & 0x7F80u) == 0x7F80u) w[sb][i >> 1] &= 0xFFFFu << (16 * (1 - (i & 1)));
-            }
+          for (int x = 0; x < 4; ++x)
 #pragma unroll
             for (int rt = 0; rt < C::RT; ++rt) {
-              s16x4 p;
+              const uint32_t seen = visible(u, rt, span);
+              f32x4 up = {}, down = {};
 #pragma unroll
-              for (int i = 0; i < 4; ++i) p[i] = (seen[rt] >> (4 * sb + i)) & 1 ? 0x3F80 : 0;
-              up[rt] = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(hi, p, up[rt], 0, 0, 0);
-              down[rt] = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(lo, p, down[rt], 0, 0, 0);
+              for (int sb = 0; sb < SB; ++sb) {
+                s16x4 hi, lo, p;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const uint32_t half = (w[sb][x][i >> 1] >> (16 * (i & 1))) & 0xFFFFu;
+                  const bool nan = (half & 0x7FFFu) > 0x7F80u;
+                  hi[i] = half == 0x7F80u || nan ? 0x3F80 : 0;
+                  lo[i] = half == 0xFF80u || nan ? 0x3F80 : 0;
+                  p[i] = (seen >> (4 * sb + i)) & 1 ? 0x3F80 : 0;
+                }
+                up = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(hi, p, up, 0, 0, 0);
+                down = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(lo, p, down, 0, 0, 0);
+              }
+              add_odd(o[rt][d4 + x], up, down);
+              __builtin_amdgcn_sched_barrier(0);     // one at a time: registers
             }
-          }
 #pragma unroll
-          for (int rt = 0; rt < C::RT; ++rt)
+          for (int sb = 0; sb < SB; ++sb)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[rt][dt][e] += (up[rt][e] > 0.0f ? inf : 0.0f) - (down[rt][e] > 0.0f ? inf : 0.0f);
+            for (int x = 0; x < 4; ++x)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const uint32_t y = w[sb][x][e];
+                w[sb][x][e] = ((y & 0x7F80u) == 0x7F80u ? 0u : y & 0xFFFFu) |
+                              ((y & 0x7F800000u) == 0x7F800000u ? 0u : y & 0xFFFF0000u);
+              }
         }
 #pragma unroll
-        for (int rt = 0; rt < C::RT; ++rt) {
-          if constexpr (SB == 1) {
-            o[rt][dt] = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(__builtin_bit_cast(s16x4, w[0]),
-                                                                 __builtin_bit_cast(s16x4, pb[rt][0]), o[rt][dt], 0, 0, 0);
-          } else {
+        for (int x = 0; x < 4; ++x)
 #pragma unroll
-            for (int sb = 0; sb < SB; sb += 2)
-              o[rt][dt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                  __builtin_bit_cast(bf16x8, u32x4{w[sb].x, w[sb].y, w[sb + 1].x, w[sb + 1].y}),
-                  __builtin_bit_cast(bf16x8, u32x4{pb[rt][sb].x, pb[rt][sb].y, pb[rt][sb + 1].x, pb[rt][sb + 1].y}),
-                  o[rt][dt], 0, 0, 0);
+          for (int rt = 0; rt < C::RT; ++rt) {
+            f32x4& acc = o[rt][d4 + x];
+            if constexpr (SB == 1)
+              acc = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(__builtin_bit_cast(s16x4, w[0][x]),
+                                                             __builtin_bit_cast(s16x4, pb[rt][0]), acc, 0, 0, 0);
+            else
+              acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                  __builtin_bit_cast(bf16x8, u32x4{w[0][x].x, w[0][x].y, w[1][x].x, w[1][x].y}),
+                  __builtin_bit_cast(bf16x8, u32x4{pb[rt][0].x, pb[rt][0].y, pb[rt][1].x, pb[rt][1].y}), acc, 0, 0, 0);
           }
-        }
-        if (ODD) __builtin_amdgcn_sched_barrier(0);
       }
     }
+  }
+
+  static __device__ __forceinline__ void add_odd(f32x4& sum, f32x4 up, f32x4 down) {
+    const float inf = __builtin_inff();
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sum[e] += (up[e] > 0.0f ? inf : 0.0f) - (down[e] > 0.0f ? inf : 0.0f);
   }
 
   __device__ __forceinline__ bool masked(int u) const {
@@ -542,7 +623,7 @@ template <int KIND, int D, int CLS> struct AttnBlock {
     const int j0 = slot0(u);
     if (j0 + C::SS > len) return true;
     if (a.window > 0 && j0 <= len + a.n_pos - 1 - a.window) return true;
-    return ((present >> (4 * (u & 15))) & ((1u << SB) - 1)) != (1u << SB) - 1;
+    return here(u) != (1u << SB) - 1;
   }
 
   __device__ __forceinline__ void compute(int u, const char* base) {
@@ -558,34 +639,33 @@ template <int KIND, int D, int CLS> struct AttnBlock {
     else wait_vm<0>();
   }
 
-  // Units [i0, i1) of the segment.
+  // Units [i0, i1) of the segment; pages of the first are being fetched.
   __device__ __forceinline__ void run(int i0, int i1) {
-    present = 0;
+    ring = 0;
+    next = i0;
     const int loaded = KIND == kF8 ? min(i1, un.ctx) : i1;   // tiles that pass through the ring
-    int next = i0;
     auto start = [&]() {
       if (next < loaded) {
-        issue(next, (next - i0) % C::NST);
+        issue(next, static_cast<uint32_t>(next - i0) % C::NST);
         ++next;
         if (next < un.ctx && next < loaded) fetch_pages(next);
       }
     };
-    if (i0 < un.ctx) fetch_pages(i0);
     if constexpr (KIND != kF8) {
       for (int x = 0; x < C::NST - 1; ++x) start();
       for (int u = i0; u < i1; ++u) {
         wait_tile(next - 1 - u);
-        if (C::WR > 1) block_barrier();
+        if (C::WR > 1) read_barrier();
         start();
         mem_fence();
-        compute(u, lds + C::RING + ((u - i0) % C::NST) * C::RAW);
+        compute(u, lds + C::RING + (static_cast<uint32_t>(u - i0) % C::NST) * C::RAW);
         mem_fence();
       }
     } else {
       for (int x = 0; x < C::NST; ++x) start();
       auto convert = [&](int u) {
         if (u < loaded) wait_tile(next - 1 - u);
-        widen_tile(u, (u - i0) % C::NST, C::NB == 2 ? (u - i0) & 1 : 0);
+        widen_tile(u, static_cast<uint32_t>(u - i0) % C::NST, C::NB == 2 ? (u - i0) & 1 : 0);
         // The raw pieces are in registers (they were converted) before their
         // place is loaded again.
         mem_fence();
@@ -609,138 +689,219 @@ template <int KIND, int D, int CLS> struct AttnBlock {
     }
   }
 
-  // Joins the wave groups' sums in LDS and writes the segment's result (whole)
-  // or its part for the join kernel.
+  // The segment's result (whole) or its part for the join kernel. The wave
+  // groups' sums are added in halves: a lane of one group takes over what the
+  // same lane of another group holds, so LDS is used in order of the lanes.
   __device__ __forceinline__ void finish(bool whole, int slot) {
-    __syncthreads();
-    float2* const ml = reinterpret_cast<float2*>(lds + C::WK * C::ROWS * C::OROW);
+    constexpr int kLanes = C::WR * C::RT * 64;       // lanes and row tiles of a group
+    const int n16 = fresh(this->n16), g = fresh(this->g), lane = fresh(this->lane);
+#pragma unroll
+    for (int half = C::WK / 2; half >= 1; half >>= 1) {
+      block_barrier();
+      const int from = (kg >= half ? kg - half : kg) * kLanes;
+      f32x4* const sums = reinterpret_cast<f32x4*>(lds);
+      float2* const ml = reinterpret_cast<float2*>(lds + C::WK / 2 * kLanes * D);
+      if (!idle && kg >= half && kg < 2 * half) {
+#pragma unroll
+        for (int rt = 0; rt < C::RT; ++rt) {
+          const int at = from + (wr * C::RT + rt) * 64 + lane;
+          ml[at] = float2{m[rt], l[rt]};
+#pragma unroll
+          for (int dt = 0; dt < DT; ++dt) sums[(from + (wr * C::RT + rt) * 64) * DT + dt * 64 + lane] = o[rt][dt];
+        }
+      }
+      block_barrier();
+      if (!idle && kg < half) {
+#pragma unroll
+        for (int rt = 0; rt < C::RT; ++rt) {
+          const float2 w = ml[from + (wr * C::RT + rt) * 64 + lane];
+          const float M = fmaxf(m[rt], w.x);
+          const float mb = M == -__builtin_inff() ? 0.0f : M;
+          const float f0 = __builtin_amdgcn_exp2f(m[rt] - mb), f1 = __builtin_amdgcn_exp2f(w.x - mb);
+          m[rt] = M;
+          l[rt] = l[rt] * f0 + w.y * f1;
+#pragma unroll
+          for (int dt = 0; dt < DT; ++dt)
+            o[rt][dt] = o[rt][dt] * f0 + sums[(from + (wr * C::RT + rt) * 64) * DT + dt * 64 + lane] * f1;
+        }
+      }
+    }
+    if (idle || kg != 0) return;
 #pragma unroll
     for (int rt = 0; rt < C::RT; ++rt) {
-      const int row = (wr * C::RT + rt) * 16 + n16;
       const float ls = row_sum(l[rt]);
-      if (g == 0) ml[kg * C::ROWS + row] = float2{m[rt], ls};
-#pragma unroll
-      for (int dt = 0; dt < DT; ++dt)
-        *reinterpret_cast<f32x4*>(lds + (kg * C::ROWS + row) * C::OROW + (dt * 16 + 4 * g) * 4) = o[rt][dt];
-    }
-    __syncthreads();
-    const int n_rows = min(C::ROWS, a.rows - rb * C::ROWS);
-    for (int x = threadIdx.x; x < n_rows * (D / 4); x += C::NT) {
-      const int row = x / (D / 4), d4 = x % (D / 4);
-      float M = -__builtin_inff();
-#pragma unroll
-      for (int i = 0; i < C::WK; ++i) M = fmaxf(M, ml[i * C::ROWS + row].x);
-      f32x4 sum = {};
-      float ls = 0.0f;
-#pragma unroll
-      for (int i = 0; i < C::WK; ++i) {
-        const float2 w = ml[i * C::ROWS + row];
-        if (w.x == -__builtin_inff() && w.y == 0.0f) continue;
-        const float f = w.x == M ? 1.0f : __builtin_amdgcn_exp2f(w.x - M);
-        ls += w.y * f;
-        sum += *reinterpret_cast<const f32x4*>(lds + (i * C::ROWS + row) * C::OROW + d4 * 16) * f;
-      }
+      const int row = (wr * C::RT + rt) * 16 + n16;
+      if (rb * C::ROWS + row >= a.rows) continue;
       if (whole) {
-        write_out(a, r, h, rb * C::ROWS + row, d4, sum, ls);
+        write_out(rb * C::ROWS + row, g, o[rt], ls);
       } else {
-        *reinterpret_cast<f32x4*>(a.part + (static_cast<int64_t>(slot) * C::ROWS + row) * D + d4 * 4) = sum;
-        if (d4 == 0) a.part_ml[slot * C::ROWS + row] = float2{M, ls};
+        float* const at = a.part + (static_cast<int64_t>(slot) * C::ROWS + row) * D + 4 * g;
+#pragma unroll
+        for (int dt = 0; dt < DT; ++dt) *reinterpret_cast<f32x4*>(at + dt * 16) = o[rt][dt];
+        if (g == 0) a.part_ml[slot * C::ROWS + row] = float2{m[rt], ls};
       }
     }
-    __syncthreads();
   }
 
-  static __device__ __forceinline__ void write_out(const AttnArgs& a, int r, int h, int row, int d4, f32x4 sum, float ls) {
+  __device__ __forceinline__ void write_out(int row, int g, const f32x4 (&sum)[DT], float ls) const {
     const int t = row / a.group, hq = h * a.group + row - t * a.group;
     const float inv = ls == 0.0f ? 0.0f : 1.0f / ls;
-    const f32x4 y = ls == 0.0f ? f32x4{} : sum * inv;
-    const int64_t at = ((static_cast<int64_t>(r) * a.n_pos + t) * (a.kvheads * a.group) + hq) * D + d4 * 4;
-    if constexpr (KIND == kF32)
-      *reinterpret_cast<f32x4*>(static_cast<float*>(a.out) + at) = y;
-    else
-      *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.out) + at) =
-          u32x2{pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3])};
+    const int64_t at = ((static_cast<int64_t>(r) * a.n_pos + t) * (a.kvheads * a.group) + hq) * D + 4 * g;
+#pragma unroll
+    for (int dt = 0; dt < DT; ++dt) {
+      const f32x4 y = ls == 0.0f ? f32x4{} : sum[dt] * inv;
+      if constexpr (KIND == kF32)
+        *reinterpret_cast<f32x4*>(static_cast<float*>(a.out) + at + dt * 16) = y;
+      else
+        *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.out) + at + dt * 16) =
+            u32x2{pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3])};
+    }
   }
 };
 
+// The units of up to 256 requests, four consecutive ones a lane, the same in
+// every wave: no barrier and one round of loads.
+struct AttnPlan {
+  int len[kAttnReqs / 64], all[kAttnReqs / 64];
+  int before;     // units before the lane's requests
+  int total;
+
+  __device__ __forceinline__ AttnPlan(const AttnArgs& a, int ts) {
+    const int lane = fresh(threadIdx.x) & 63;
+    const int heads = a.kvheads * a.row_blocks;
+#pragma unroll
+    for (int k = 0; k < kAttnReqs / 64; ++k)
+      len[k] = a.seq_len[a.req0 + min(lane * (kAttnReqs / 64) + k, a.n_here - 1)];
+    int sum = 0;
+#pragma unroll
+    for (int k = 0; k < kAttnReqs / 64; ++k) {
+      const int n = attn_units(a, len[k], ts).all * heads;
+      all[k] = lane * (kAttnReqs / 64) + k < a.n_here ? n : 0;
+      sum += all[k];
+    }
+    // Inclusive sum over the lanes: within rows of 16, then across them.
+    int c = sum;
+    c += __builtin_amdgcn_update_dpp(0, c, 0x111, 0xF, 0xF, false);
+    c += __builtin_amdgcn_update_dpp(0, c, 0x112, 0xF, 0xF, false);
+    c += __builtin_amdgcn_update_dpp(0, c, 0x114, 0xF, 0xF, false);
+    c += __builtin_amdgcn_update_dpp(0, c, 0x118, 0xF, 0xF, false);
+    c += __builtin_amdgcn_update_dpp(0, c, 0x142, 0xA, 0xF, false);
+    c += __builtin_amdgcn_update_dpp(0, c, 0x143, 0xC, 0xF, false);
+    before = c - sum;
+    total = __builtin_amdgcn_readlane(c, 63);
+  }
+
+  // For the join kernel: units before every request, and the total.
+  __device__ __forceinline__ void write(const AttnArgs& a) const {
+    if (threadIdx.x >= 64) return;
+    int at = before;
+#pragma unroll
+    for (int k = 0; k < kAttnReqs / 64; ++k) {
+      const int i = threadIdx.x * (kAttnReqs / 64) + k;
+      if (i <= a.n_here) a.plan[i] = at;
+      at += all[k];
+    }
+    if (threadIdx.x == 63 && a.n_here == kAttnReqs) a.plan[kAttnReqs] = at;
+  }
+
+  // Request of unit u (uniform, below the total), the unit's number in it and
+  // the request's length.
+  __device__ __forceinline__ int find(int u, int* in_req, int* n) const {
+    int lane_units = 0;
+#pragma unroll
+    for (int k = 0; k < kAttnReqs / 64; ++k) lane_units += all[k];
+    const int L = __builtin_ctzll(__ballot(before + lane_units > u));
+    int x = u - __builtin_amdgcn_readlane(before, L);
+    int i = L * (kAttnReqs / 64);
+    int at = __builtin_amdgcn_readlane(len[0], L);
+    int got = 0;
+#pragma unroll
+    for (int k = 0; k < kAttnReqs / 64; ++k) {
+      const int here = __builtin_amdgcn_readlane(all[k], L), ln = __builtin_amdgcn_readlane(len[k], L);
+      if (!got) {
+        at = ln;
+        if (x < here) {
+          got = 1;
+        } else {
+          x -= here;
+          ++i;
+        }
+      }
+    }
+    *in_req = x;
+    *n = at;
+    return i;
+  }
+};
+
+// Refused requests of the whole call: a count per thread, added in order.
+template <int NT> __device__ __forceinline__ void count_refused(const AttnArgs& a, int32_t* sums) {
+  int bad = 0;
+  for (int i = threadIdx.x; i < a.n_req; i += NT) {
+    const int n = a.seq_len[i];
+    bad += n < 0 || n > (a.table_len << a.page_shift);
+  }
+  sums[threadIdx.x] = bad;
+  block_barrier();
+  if (threadIdx.x == 0) {
+    bad = 0;
+    for (int i = 0; i < NT; ++i) bad += sums[i];
+    *a.status = bad;
+  }
+  block_barrier();
+}
+
 template <int KIND, int D, int CLS>
-__global__ __launch_bounds__((AttnCfg<KIND, D, CLS>::NT)) void attn_kernel(const AttnArgs args) {
+__global__ __launch_bounds__((AttnCfg<KIND, D, CLS>::NT), (AttnCfg<KIND, D, CLS>::NT * AttnCfg<KIND, D, CLS>::PER_CU + 255) / 256)
+void attn_kernel(const AttnArgs args) {
   using C = AttnCfg<KIND, D, CLS>;
   extern __shared__ __align__(1024) char lds[];   // rows of a tile start at multiples of their size
-  __shared__ int64_t before[kAttnReqs + 1];
-  __shared__ int64_t wave_sum[kAttnReqs / 64];
   __shared__ int8_t par[HRS_MAX_POS];
   __shared__ AttnRows<C::ROWS> rows;
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int heads = args.kvheads * args.row_blocks;
-  // Units before every request: a scan over the lengths, 256 at most.
-  for (int i0 = 0; i0 < kAttnReqs; i0 += C::NT) {
-    const int i = i0 + tid;
-    if (i < kAttnReqs) {
-      int len;
-      int64_t x = i < args.n_here ? static_cast<int64_t>(attn_units(args, args.req0 + i, C::TS, &len).all) * heads : 0;
-#pragma unroll
-      for (int d = 1; d < 64; d <<= 1) {
-        const int64_t y = __shfl_up(x, d);
-        x += lane >= d ? y : 0;
-      }
-      before[i + 1] = x;
-      if (lane == 63) wave_sum[i >> 6] = x;
+  const int tid = threadIdx.x;
+  int u, u1;
+  {
+    const AttnPlan plan(args, C::TS);
+    u = attn_cut(blockIdx.x, plan.total, args.log_blocks);
+    u1 = attn_cut(blockIdx.x + 1, plan.total, args.log_blocks);
+    if (blockIdx.x == 0) {
+      plan.write(args);
+      if (args.status && args.req0 == 0) count_refused<C::NT>(args, reinterpret_cast<int32_t*>(lds));
     }
   }
-  if (tid == 0) before[0] = 0;
-  __syncthreads();
-  for (int i = tid; i < kAttnReqs; i += C::NT) {
-    int64_t add = 0;
-    for (int w = 0; w < (i >> 6); ++w) add += wave_sum[w];
-    before[i + 1] += add;
-  }
-  __syncthreads();
-  const int64_t total = before[args.n_here];
-  if (blockIdx.x == 0) {
-    for (int i = tid; i <= args.n_here; i += C::NT) args.plan[i] = before[i];
-    if (args.status && args.req0 == 0 && tid == 0) {
-      int bad = 0;
-      for (int i = 0; i < args.n_req; ++i) {
-        const int n = args.seq_len[i];
-        bad += n < 0 || n > (args.table_len << args.page_shift);
-      }
-      *args.status = bad;
-    }
-  }
-  const int64_t blocks = min(static_cast<int64_t>(gridDim.x), total);
-  if (blockIdx.x >= blocks) return;
-  int64_t u = blockIdx.x * total / blocks;
-  const int64_t u1 = (blockIdx.x + 1) * total / blocks;
-  int i = 0;                           // the request of unit u: the last with before <= u and units of its own
-  for (int step = kAttnReqs / 2; step; step >>= 1)
-    if (i + step < args.n_here && before[i + step] <= u) i += step;
 
   AttnBlock<KIND, D, CLS> blk(args, lds, &rows);
+  bool again = false;
   while (u < u1) {
-    while (before[i + 1] <= u) ++i;
-    i = __builtin_amdgcn_readfirstlane(i);
+    // Counted again for every segment (two or three a block) rather than kept
+    // in registers over the tiles.
+    int in_req;
+    const int i = AttnPlan(args, C::TS).find(u, &in_req, &blk.len);
     blk.r = args.req0 + i;
-    blk.un = attn_units(args, blk.r, C::TS, &blk.len);
-    const int64_t in_req = u - before[i];
-    const int seg = __builtin_amdgcn_readfirstlane(static_cast<int>(in_req / blk.un.all));
-    const int u0 = __builtin_amdgcn_readfirstlane(static_cast<int>(in_req - static_cast<int64_t>(seg) * blk.un.all));
-    const int ue = static_cast<int>(min(static_cast<int64_t>(blk.un.all), u0 + (u1 - u)));
-    blk.h = seg / args.row_blocks;
+    blk.un = attn_units(args, blk.len, C::TS);
+    const int seg = __builtin_amdgcn_readfirstlane(in_req / blk.un.all);
+    const int u0 = in_req - seg * blk.un.all;
+    const int ue = min(blk.un.all, u0 + (u1 - u));
+    blk.h = __builtin_amdgcn_readfirstlane(seg / args.row_blocks);
     blk.rb = seg - blk.h * args.row_blocks;
+    blk.head_bytes = static_cast<uint32_t>(args.kvheads) * (D * C::ESZC << args.page_shift);
+    blk.h_bytes = static_cast<uint64_t>(blk.h) * (D * C::ESZC << args.page_shift);
+    blk.load_rows();
+    if (u0 < blk.un.ctx) blk.fetch_pages(u0);
     const float ks = KIND == kF8 && args.k_scale ? args.k_scale[blk.h] : 1.0f;
     blk.vs = KIND == kF8 && args.v_scale ? args.v_scale[blk.h] : 1.0f;
     blk.c_span = args.scale * 1.4426950408889634f;
     blk.c_ctx = blk.c_span * ks;
-    blk.head_bytes = static_cast<uint32_t>(args.kvheads) * (D * C::ESZC << args.page_shift);
-    blk.h_bytes = static_cast<uint64_t>(blk.h) * (D * C::ESZC << args.page_shift);
+    if (again) block_barrier();        // everybody is done with the last segment's tiles and masks
+    again = true;
     if (args.tree) {
       if (tid < args.n_pos) par[tid] = args.parent[i * args.n_pos + tid];
-      __syncthreads();
+      block_barrier();
     }
-    blk.load_rows(par);
-    __syncthreads();
-    blk.run(u0, __builtin_amdgcn_readfirstlane(ue));
+    blk.mask_rows(par);
+    blk.settle();
+    block_barrier();
+    blk.run(u0, ue);
     blk.finish(u0 == 0 && ue == blk.un.all, 2 * static_cast<int>(blockIdx.x) + (u0 == 0 ? 1 : 0));
     u += ue - u0;
   }
@@ -751,13 +912,13 @@ __global__ __launch_bounds__((AttnCfg<KIND, D, CLS>::NT)) void attn_kernel(const
 namespace {
 
 template <int KIND, int D, int CLS>
-void launch_one(const AttnArgs& args, int blocks, hipStream_t s) {
+void launch_one(const AttnArgs& args, hipStream_t s) {
   using C = AttnCfg<KIND, D, CLS>;
-  hipLaunchKernelGGL((attn_kernel<KIND, D, CLS>), dim3(blocks), dim3(C::NT), C::LDS, s, args);
+  hipLaunchKernelGGL((attn_kernel<KIND, D, CLS>), dim3(1 << args.log_blocks), dim3(C::NT), C::LDS, s, args);
 }
 template <int KIND, int D, int CLS> AttnShape shape_one() {
   using C = AttnCfg<KIND, D, CLS>;
-  return {C::ROWS, C::TS, C::NT};
+  return {C::ROWS, C::TS, kAttnCus * C::PER_CU};
 }
 
 }  // namespace
@@ -780,20 +941,20 @@ template <int KIND> AttnShape attn_shape(int d, int cls) {
   }
 }
 
-template <int KIND> void attn_launch(const AttnArgs& args, int d, int cls, int blocks, hipStream_t s) {
+template <int KIND> void attn_launch(const AttnArgs& args, int d, int cls, hipStream_t s) {
   switch (d * 4 + cls) {
-    case 256: return launch_one<KIND, 64, 0>(args, blocks, s);
-    case 257: return launch_one<KIND, 64, 1>(args, blocks, s);
-    case 258: return launch_one<KIND, 64, 2>(args, blocks, s);
-    case 259: return launch_one<KIND, 64, 3>(args, blocks, s);
-    case 512: return launch_one<KIND, 128, 0>(args, blocks, s);
-    case 513: return launch_one<KIND, 128, 1>(args, blocks, s);
-    case 514: return launch_one<KIND, 128, 2>(args, blocks, s);
-    case 515: return launch_one<KIND, 128, 3>(args, blocks, s);
-    case 1024: return launch_one<KIND, 256, 0>(args, blocks, s);
-    case 1025: return launch_one<KIND, 256, 1>(args, blocks, s);
-    case 1026: return launch_one<KIND, 256, 2>(args, blocks, s);
-    case 1027: return launch_one<KIND, 256, 3>(args, blocks, s);
+    case 256: return launch_one<KIND, 64, 0>(args, s);
+    case 257: return launch_one<KIND, 64, 1>(args, s);
+    case 258: return launch_one<KIND, 64, 2>(args, s);
+    case 259: return launch_one<KIND, 64, 3>(args, s);
+    case 512: return launch_one<KIND, 128, 0>(args, s);
+    case 513: return launch_one<KIND, 128, 1>(args, s);
+    case 514: return launch_one<KIND, 128, 2>(args, s);
+    case 515: return launch_one<KIND, 128, 3>(args, s);
+    case 1024: return launch_one<KIND, 256, 0>(args, s);
+    case 1025: return launch_one<KIND, 256, 1>(args, s);
+    case 1026: return launch_one<KIND, 256, 2>(args, s);
+    case 1027: return launch_one<KIND, 256, 3>(args, s);
   }
 }
 
