@@ -27,7 +27,7 @@ struct AttnArgs {
   void* out;
   int32_t* status;
   int32_t* plan;      // workspace: units before every request [n + 1], for the join
-  float* part;        // workspace: partial sums [2 * blocks][rows][d]
+  float* part;        // workspace: partial sums [2 * blocks][rows / 16][d / 16][64 lanes][4]
   float2* part_ml;    // workspace: their maximum and sum [2 * blocks][rows]
   int64_t q_stride;
   int64_t k_stride;
@@ -79,12 +79,19 @@ template <int KIND, int D, int CLS> struct AttnCfg {
   static_assert(NST >= 2 && LDS <= 155 * 1024 / PER_CU, "tiles fit");
 };
 
+// Units without a tile at the end of every head: its last run of tiles also
+// takes the span's masks, the end of a sum and, for most blocks, the start of
+// another one, about the time of that many tiles (measured at 26,758 slots of
+// 256: the blocks with a span tile ended 5 us behind the others).
+constexpr int kExtraUnits = 2;
+
 // Work is counted in units: a unit is one tile of one (request, key/value
 // head, row block); the context's tiles come first, the span's last.
 struct AttnUnits {
   int first;   // first context tile that a window leaves in reach
   int ctx;     // context tiles
-  int all;     // and the span's
+  int all;     // and the span's, and kExtraUnits
+  __device__ __forceinline__ int tiles() const { return all - kExtraUnits; }
 };
 
 __device__ __forceinline__ AttnUnits attn_units(const AttnArgs& a, int len, unsigned ts) {
@@ -92,7 +99,7 @@ __device__ __forceinline__ AttnUnits attn_units(const AttnArgs& a, int len, unsi
   const unsigned n = ok ? len : 0;
   const unsigned first = a.window > 0 ? static_cast<unsigned>(max(static_cast<int>(n) + 1 - a.window, 0)) / ts : 0;
   const int ctx = static_cast<int>((n + ts - 1) / ts - min(first, (n + ts - 1) / ts));
-  return {static_cast<int>(first), ctx, ok ? ctx + static_cast<int>((a.n_pos + ts - 1) / ts) : 0};
+  return {static_cast<int>(first), ctx, ok ? ctx + static_cast<int>((a.n_pos + ts - 1) / ts) + kExtraUnits : 0};
 }
 
 // Where block b's run of units starts: an even cut where there are at least

@@ -17,15 +17,15 @@ namespace hrs {
 namespace {
 
 // Sum of a segment's parts: out = sum_b 2^(m_b - M) O_b / sum_b 2^(m_b - M)
-// l_b. Grid: x segments (request, head, row block), y groups of rows. A row is
-// held by D/4 threads, four elements each, NS times over: the copies take
-// every NS-th part and are added in LDS (in order, so results repeat). With
-// few rows and many parts, as for one long request, the copies keep more loads
-// in flight (4 heads x 102 rows x 64 parts of 256: 35.7 us with one thread
-// group per row and all parts in it).
+// l_b. A wave takes two column groups (four columns of a lane each) of 16
+// rows of a segment (request, head, row block), in the lanes' order of the
+// kernel that wrote them. NS waves take every NS-th part and are added in LDS
+// (in order, so results repeat): with few rows and many parts, as for one
+// long request, more loads are on their way (4 heads x 102 rows x 64 parts of
+// 256: 35.7 us with all parts in one thread group per row).
 template <bool F32, int D, int NS>
-__global__ __launch_bounds__(256) void attn_join_kernel(const AttnArgs args, int rows_per_block) {
-  constexpr int kPer = 256 / (D / 4) / NS;    // rows of a block
+__global__ __launch_bounds__(NS > 1 ? 64 * NS : 256) void attn_join_kernel(const AttnArgs args, int rows_per_block) {
+  constexpr int DT = D / 16;
   const int heads = args.kvheads * args.row_blocks;
   const int i = blockIdx.x / heads;
   const int seg = blockIdx.x - i * heads;
@@ -43,25 +43,30 @@ __global__ __launch_bounds__(256) void attn_join_kernel(const AttnArgs args, int
   };
   const int b0 = block_of(s0), b1 = block_of(s1 - 1);
   if (b0 == b1) return;                       // one block had all of it and wrote the result
-  const int d4 = threadIdx.x % (D / 4);
-  const int ns = threadIdx.x / (D / 4) % NS;
-  const int lrow = threadIdx.x / (D / 4 * NS);
-  const int rows = min(rows_per_block, args.rows - rb * rows_per_block);
-  const int row = min(static_cast<int>(blockIdx.y) * kPer + lrow, rows - 1);
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int task = NS > 1 ? blockIdx.y : blockIdx.y * 4 + wave;
+  const int tiles = (min(rows_per_block, args.rows - rb * rows_per_block) + 15) / 16;
+  const int tile = task / (DT / 2), dp = task % (DT / 2);
+  if (tile >= tiles) return;
+  const int n16 = lane & 15, g = lane >> 4;
+  const int row = tile * 16 + n16;
+  const int ns = NS > 1 ? wave : 0;
   float M = -__builtin_inff(), ls = 0.0f;
-  f32x4 sum = {};
+  f32x4 sum[2] = {};
   constexpr int kAtOnce = 8;
   for (int b = b0 + ns; b <= b1; b += NS * kAtOnce) {
     float2 w[kAtOnce];
-    f32x4 x[kAtOnce];
+    f32x4 x[kAtOnce][2];
 #pragma unroll
     for (int j = 0; j < kAtOnce; ++j) {
       const int bj = min(b + j * NS, b1);
       // The segment's first block left its part as its last, the others theirs
       // as their first.
-      const int64_t at = static_cast<int64_t>(2 * bj + (bj == b0 ? 1 : 0)) * rows_per_block + row;
-      w[j] = args.part_ml[at];
-      x[j] = *reinterpret_cast<const f32x4*>(args.part + at * D + d4 * 4);
+      const int64_t slot = 2 * bj + (bj == b0 ? 1 : 0);
+      w[j] = args.part_ml[slot * rows_per_block + row];
+      const f32x4* at = reinterpret_cast<const f32x4*>(args.part) + (slot * (rows_per_block / 16) + tile) * (DT * 64) + lane;
+      x[j][0] = at[(2 * dp) * 64];
+      x[j][1] = at[(2 * dp + 1) * 64];
     }
     float top = M;
 #pragma unroll
@@ -69,59 +74,72 @@ __global__ __launch_bounds__(256) void attn_join_kernel(const AttnArgs args, int
     const float keep = M == top ? 1.0f : __builtin_amdgcn_exp2f(M - top);
     M = top;
     ls *= keep;
-    sum *= keep;
+    sum[0] *= keep;
+    sum[1] *= keep;
 #pragma unroll
     for (int j = 0; j < kAtOnce; ++j) {
       // Parts past the last, and parts that no slot counted in, weigh nothing.
       if (b + j * NS > b1 || (w[j].x == -__builtin_inff() && w[j].y == 0.0f)) continue;
       const float f = w[j].x == M ? 1.0f : __builtin_amdgcn_exp2f(w[j].x - M);
       ls += w[j].y * f;
-      sum += x[j] * f;
+      sum[0] += x[j][0] * f;
+      sum[1] += x[j][1] * f;
     }
   }
   if constexpr (NS > 1) {
-    __shared__ f32x4 sums[256];
-    __shared__ float2 ml[256];
-    sums[threadIdx.x] = sum;
-    ml[threadIdx.x] = float2{M, ls};
+    __shared__ f32x4 sums[NS][2][64];
+    __shared__ float2 ml[NS][64];
+    sums[wave][0][lane] = sum[0];
+    sums[wave][1][lane] = sum[1];
+    ml[wave][lane] = float2{M, ls};
     __syncthreads();
-    if (ns != 0) return;
+    if (wave != 0) return;
     float top = M;
 #pragma unroll
-    for (int j = 1; j < NS; ++j) top = fmaxf(top, ml[threadIdx.x + j * (D / 4)].x);
+    for (int j = 1; j < NS; ++j) top = fmaxf(top, ml[j][lane].x);
     const float f0 = M == top ? 1.0f : __builtin_amdgcn_exp2f(M - top);
     ls *= f0;
-    sum *= f0;
+    sum[0] *= f0;
+    sum[1] *= f0;
 #pragma unroll
     for (int j = 1; j < NS; ++j) {
-      const float2 w = ml[threadIdx.x + j * (D / 4)];
+      const float2 w = ml[j][lane];
       if (w.x == -__builtin_inff() && w.y == 0.0f) continue;
       const float f = w.x == top ? 1.0f : __builtin_amdgcn_exp2f(w.x - top);
       ls += w.y * f;
-      sum += sums[threadIdx.x + j * (D / 4)] * f;
+      sum[0] += sums[j][0][lane] * f;
+      sum[1] += sums[j][1][lane] * f;
     }
   }
-  if (static_cast<int>(blockIdx.y) * kPer + lrow >= rows) return;
   const int at_row = rb * rows_per_block + row;
+  if (at_row >= args.rows) return;
   const int t = at_row / args.group, hq = h * args.group + at_row - t * args.group;
-  const f32x4 y = ls == 0.0f ? f32x4{} : sum * (1.0f / ls);
-  const int64_t at = ((static_cast<int64_t>(r) * args.n_pos + t) * (args.kvheads * args.group) + hq) * D + d4 * 4;
-  if constexpr (F32)
-    *reinterpret_cast<f32x4*>(static_cast<float*>(args.out) + at) = y;
-  else
-    *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(args.out) + at) =
-        u32x2{pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3])};
+  const float inv = ls == 0.0f ? 0.0f : 1.0f / ls;
+  const int64_t at = ((static_cast<int64_t>(r) * args.n_pos + t) * (args.kvheads * args.group) + hq) * D;
+#pragma unroll
+  for (int e = 0; e < 2; ++e) sum[e] = ls == 0.0f ? f32x4{} : sum[e] * inv;
+  if constexpr (F32) {
+    float* const out = static_cast<float*>(args.out) + at + 32 * dp + 4 * g;
+    *reinterpret_cast<f32x4*>(out) = sum[0];
+    *reinterpret_cast<f32x4*>(out + 16) = sum[1];
+  } else {
+    // Group dt = EPL half + x holds columns 16 EPL half + EPL (4 g + i) + x.
+    constexpr int EPL = D >= 128 ? 8 : 4;
+    const int half = 2 * dp / EPL, x = 2 * dp % EPL;
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(args.out) + at + 16 * EPL * half + EPL * (4 * g + c) + x) =
+          pack_bf16(sum[0][c], sum[1][c]);
+  }
 }
 
 template <bool F32, int D> void launch_join_d(const AttnArgs& args, const AttnShape& sh, hipStream_t s) {
-  const int rows = std::min(sh.rows, args.rows);
   const int segs = args.n_here * args.kvheads * args.row_blocks;
-  constexpr int kMost = 256 / (D / 4);        // copies of a row that fill a block
-  if (static_cast<int64_t>(segs) * rows <= 2048)
-    hipLaunchKernelGGL((attn_join_kernel<F32, D, kMost>), dim3(segs, rows), dim3(256), 0, s, args, sh.rows);
+  const int tasks = (std::min(sh.rows, args.rows) + 15) / 16 * (D / 32);
+  if (static_cast<int64_t>(segs) * tasks <= 1024)
+    hipLaunchKernelGGL((attn_join_kernel<F32, D, 8>), dim3(segs, tasks), dim3(512), 0, s, args, sh.rows);
   else
-    hipLaunchKernelGGL((attn_join_kernel<F32, D, 1>), dim3(segs, (rows + kMost - 1) / kMost), dim3(256), 0, s, args,
-                       sh.rows);
+    hipLaunchKernelGGL((attn_join_kernel<F32, D, 1>), dim3(segs, (tasks + 3) / 4), dim3(256), 0, s, args, sh.rows);
 }
 
 template <bool F32> void launch_join(const AttnArgs& args, int d, const AttnShape& sh, hipStream_t s) {
@@ -208,8 +226,10 @@ extern "C" int attn_verify_span(const hrs_attn_desc* d, const void* q, const voi
   // Units are counted in 32 bits: fewer requests a launch for tables of very
   // many slots.
   const int64_t slots = (static_cast<int64_t>(args.table_len) << args.page_shift) + HRS_MAX_POS;
-  const int64_t most = static_cast<int64_t>(args.kvheads) * args.row_blocks * (slots / sh.ts + 2);
-  if (most > INT32_MAX) return HRS_EINVAL;
+  const int64_t most = static_cast<int64_t>(args.kvheads) * args.row_blocks * (slots / sh.ts + 4 + kExtraUnits);
+  // Rows of the cache are counted by groups of 16, in 32 bits.
+  const int64_t groups = static_cast<int64_t>(args.n_pages) * args.kvheads * (d->cache.page_size / 16);
+  if (most > INT32_MAX || groups > UINT32_MAX) return HRS_EINVAL;
   const int per_launch =
       static_cast<int>(std::min<int64_t>(args.tree ? std::min(kAttnReqs, std::max(1, kGeomBytes / d->n_pos)) : kAttnReqs,
                                          INT32_MAX / most));

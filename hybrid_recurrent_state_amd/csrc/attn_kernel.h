@@ -85,42 +85,6 @@ template <typename T> __device__ __forceinline__ const __attribute__((address_sp
   return reinterpret_cast<const __attribute__((address_space(3))) T*>(a);
 }
 
-// Four transposing LDS reads at a0 .. a3 plus OFF, and four more at OFF2 (if
-// not negative): within each group of 16 lanes, lane i receives as its j-th
-// value element i % 4 of the four 16-bit values that lane 4 j + i / 4
-// addresses. In assembly with their wait: the compiler puts a wait for every
-// load to LDS on its way (vmcnt(0)) ahead of the builtin, which would drain
-// the ring of tiles once per tile.
-template <int OFF, int OFF2>
-__device__ __forceinline__ void read_tr16(uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, u32x2 (&x)[4],
-                                          u32x2 (&y)[4]) {
-  if constexpr (OFF2 < 0) {
-    asm volatile(
-        "ds_read_b64_tr_b16 %0, %4 offset:%8\n\t"
-        "ds_read_b64_tr_b16 %1, %5 offset:%8\n\t"
-        "ds_read_b64_tr_b16 %2, %6 offset:%8\n\t"
-        "ds_read_b64_tr_b16 %3, %7 offset:%8\n\t"
-        "s_waitcnt lgkmcnt(0)"
-        : "=&v"(x[0]), "=&v"(x[1]), "=&v"(x[2]), "=&v"(x[3])
-        : "v"(a0), "v"(a1), "v"(a2), "v"(a3), "n"(OFF)
-        : "memory");
-  } else {
-    asm volatile(
-        "ds_read_b64_tr_b16 %0, %8 offset:%12\n\t"
-        "ds_read_b64_tr_b16 %4, %8 offset:%13\n\t"
-        "ds_read_b64_tr_b16 %1, %9 offset:%12\n\t"
-        "ds_read_b64_tr_b16 %5, %9 offset:%13\n\t"
-        "ds_read_b64_tr_b16 %2, %10 offset:%12\n\t"
-        "ds_read_b64_tr_b16 %6, %10 offset:%13\n\t"
-        "ds_read_b64_tr_b16 %3, %11 offset:%12\n\t"
-        "ds_read_b64_tr_b16 %7, %11 offset:%13\n\t"
-        "s_waitcnt lgkmcnt(0)"
-        : "=&v"(x[0]), "=&v"(x[1]), "=&v"(x[2]), "=&v"(x[3]), "=&v"(y[0]), "=&v"(y[1]), "=&v"(y[2]), "=&v"(y[3])
-        : "v"(a0), "v"(a1), "v"(a2), "v"(a3), "n"(OFF), "n"(OFF2)
-        : "memory");
-  }
-}
-
 // Larger (or sum) over the four lanes that hold one query row.
 __device__ __forceinline__ float row_max(float x) {
   const auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
@@ -170,12 +134,13 @@ template <int KIND, int D, int CLS> struct AttnBlock {
   int r, h, len, n_units, rb;
   AttnUnits un;
   bool idle;                   // no row of the wave exists
+  bool odd_seen;               // a masked tile held values that are not finite
   u32x4 q[C::RT][QC];
   f32x4 o[C::RT][DT];
   float m[C::RT], l[C::RT];
   float c_ctx, c_span, vs;
-  uint32_t head_bytes;         // a page of all heads
-  uint64_t h_bytes;            // this head's part of it
+  uint32_t head_groups;        // groups of 16 rows of a page of all heads
+  uint32_t h_groups;           // and those ahead of this head's
   uint32_t ring;               // SB bits a started tile: 16-slot groups whose page is there
   int next;                    // next tile to start
   int pg[SB];                  // pages of the next tile to load
@@ -205,23 +170,30 @@ template <int KIND, int D, int CLS> struct AttnBlock {
     }
   }
 
+  // Where the rows of context tile u (whose pages were fetched) are in the
+  // caches, in bytes, by groups of 16; which groups' pages are there (others
+  // stand for the first page). A group's number counts 16-row groups: page
+  // times heads times groups of a page, and so on.
+  __device__ __forceinline__ uint32_t page_rows(int u, int64_t (&at)[SB]) const {
+    uint32_t there = 0;
+#pragma unroll
+    for (int i = 0; i < SB; ++i) {
+      const bool ok = static_cast<uint32_t>(pg[i]) < static_cast<uint32_t>(a.n_pages);
+      there |= ok ? 1u << i : 0u;
+      const uint32_t in_page = ((slot0(u) >> 4) + i) & ((1u << (a.page_shift - 4)) - 1);
+      const uint32_t group = (ok ? pg[i] : 0) * head_groups + h_groups + in_page;
+      at[i] = static_cast<int64_t>(group) * (16 * D * CSZ);
+    }
+    return there;
+  }
+
   // Starts the loads of tile u into its place of the ring.
   __device__ __forceinline__ void issue(int u, int i_ring) {
     char* const dst = lds + C::RING + i_ring * C::RAW + kg * (C::RAW / C::WK);
     const bool span = u >= un.ctx;
     if (!span) {
-      uint32_t there = 0;
       int64_t at[SB];
-#pragma unroll
-      for (int i = 0; i < SB; ++i) {
-        const bool ok = pg[i] >= 0 && pg[i] < a.n_pages;
-        there |= ok ? 1u << i : 0u;
-        const int in_page = (slot0(u) + 16 * i) & ((1 << a.page_shift) - 1);
-        // Bytes: (page * heads + head) rows of a page, then the row.
-        at[i] = static_cast<int64_t>(static_cast<uint64_t>(static_cast<uint32_t>(ok ? pg[i] : 0)) * head_bytes) +
-                static_cast<int64_t>(h_bytes + static_cast<uint32_t>(in_page) * (D * CSZ));
-      }
-      ring = ring << SB | there;
+      ring = ring << SB | page_rows(u, at);
       constexpr int kRows = 64 * C::WR / RCPR;              // rows that one load of all the group's waves covers
 #pragma unroll
       for (int i = 0; i < LPS; ++i) {
@@ -304,6 +276,7 @@ template <int KIND, int D, int CLS> struct AttnBlock {
   __device__ __forceinline__ void load_rows() {
     const int n16 = fresh(this->n16), g = fresh(this->g);
     idle = rb * C::ROWS + wr * (16 * C::RT) >= a.rows;
+    odd_seen = false;
 #pragma unroll
     for (int rt = 0; rt < C::RT; ++rt) {
       const int row = rb * C::ROWS + (wr * C::RT + rt) * 16 + n16;
@@ -370,7 +343,7 @@ template <int KIND, int D, int CLS> struct AttnBlock {
 
   // Which of a tile's slots that this lane holds count for its row (bit 4 sb
   // + i: slot 16 sb + 4 g + i of the wave group's part).
-  __device__ __forceinline__ uint32_t visible(int u, int rt, bool span) const {
+  __device__ __forceinline__ uint32_t visible(int u, int rt, bool span, uint32_t there) const {
     const int lrow = (wr * C::RT + rt) * 16 + n16;
     uint32_t bits = 0;
     if (span) {
@@ -385,7 +358,7 @@ template <int KIND, int D, int CLS> struct AttnBlock {
     const int first = rows->first[lrow];
 #pragma unroll
     for (int sb = 0; sb < SB; ++sb) {
-      if (!((here(u) >> sb) & 1)) continue;
+      if (!((there >> sb) & 1)) continue;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int j = j0 + 16 * sb + i;
@@ -395,23 +368,8 @@ template <int KIND, int D, int CLS> struct AttnBlock {
     return bits;
   }
 
-  // Whether the wave group's values of a tile hold an infinity or a NaN.
-  __device__ __forceinline__ bool any_odd(const char* vt) const {
-    bool odd = false;
-#pragma unroll
-    for (int x = 0; x < C::SS * CPR / 64; ++x) {
-      const u32x4 w = *reinterpret_cast<const u32x4*>(vt + (x * 64 + lane) * 16);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        odd = odd || (w[e] & 0x7F800000u) == 0x7F800000u;
-        if (ESZ == 2) odd = odd || (w[e] & 0x7F80u) == 0x7F80u;
-      }
-    }
-    return __any(odd);
-  }
-
   // One tile: its scores, weights and the product with the values.
-  __device__ __forceinline__ void tile(int u, const char* base, bool span, bool mask) {
+  __device__ __forceinline__ void tile(int u, const char* base, bool span, bool mask, uint32_t there) {
     const char* const kt = base + kg * (C::STAGE / C::WK);
     const char* const vt = kt + C::SS * D * ESZ;
     f32x4 s[C::RT][SB];
@@ -421,27 +379,31 @@ template <int KIND, int D, int CLS> struct AttnBlock {
       for (int sb = 0; sb < SB; ++sb) s[rt][sb] = f32x4{};
     // Piece 4 c + g of row n16, permuted: the permutation is an exclusive or
     // of address bits, so the pieces are one address apart from constants.
-    const uint32_t ka = lds_address(kt) + n16 * (D * ESZ) +
-                        ((g ^ swizzle<CPR>(n16)) << 4);
+    const uint32_t ka = lds_address(kt) + n16 * (D * ESZ) + ((g ^ swizzle<CPR>(n16)) << 4);
+    u32x4 kk[QC][SB];
 #pragma unroll
-    for (int c = 0; c < QC; ++c) {
+    for (int c = 0; c < QC; ++c)
 #pragma unroll
-      for (int sb = 0; sb < SB; ++sb) {
-        const u32x4 kk = *lds_at<u32x4>((ka ^ (c << 6)) + sb * 16 * D * ESZ);
+      for (int sb = 0; sb < SB; ++sb) kk[c][sb] = *lds_at<u32x4>((ka ^ (c << 6)) + sb * 16 * D * ESZ);
+#pragma unroll
+    for (int c = 0; c < QC; ++c)
+#pragma unroll
+      for (int sb = 0; sb < SB; ++sb)
 #pragma unroll
         for (int rt = 0; rt < C::RT; ++rt) {
           if constexpr (KIND == kF32) {
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              s[rt][sb] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(kk[e]), __uint_as_float(q[rt][c][e]),
-                                                               s[rt][sb], 0, 0, 0);
+              s[rt][sb] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(kk[c][sb][e]),
+                                                               __uint_as_float(q[rt][c][e]), s[rt][sb], 0, 0, 0);
           } else {
-            s[rt][sb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, kk),
+            s[rt][sb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, kk[c][sb]),
                                                                 __builtin_bit_cast(bf16x8, q[rt][c]), s[rt][sb], 0, 0, 0);
           }
         }
-      }
-    }
+    // The values' reads go out before the weights are formed.
+    Values v;
+    if constexpr (KIND != kF32) v.load(vt, n16, g, 0);
     // c S - m is one operation on the raw products; c is positive (a negative
     // one turns the products' sign).
     float c = span ? c_span : c_ctx;
@@ -453,36 +415,43 @@ template <int KIND, int D, int CLS> struct AttnBlock {
         for (int sb = 0; sb < SB; ++sb) s[rt][sb] = -s[rt][sb];
     }
     c = fmaxf(c, 1e-37f);          // masked scores stay below everything at a scale of zero
-    bool odd = false;
     if (mask) {
 #pragma unroll
       for (int rt = 0; rt < C::RT; ++rt) {
-        const uint32_t seen = visible(u, rt, span);
+        const uint32_t seen = visible(u, rt, span, there);
 #pragma unroll
         for (int sb = 0; sb < SB; ++sb)
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             if (!((seen >> (4 * sb + i)) & 1)) s[rt][sb][i] = -__builtin_inff();
       }
-      odd = any_odd(vt);
     }
-    u32x2 pb[C::RT][SB];       // P^T as the products' second operand (bf16)
+    float top[C::RT];
+    bool more = false;
 #pragma unroll
     for (int rt = 0; rt < C::RT; ++rt) {
-      float top = -__builtin_inff();
+      top[rt] = -__builtin_inff();
 #pragma unroll
       for (int sb = 0; sb < SB; ++sb)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) top = fmaxf(top, s[rt][sb][i]);
-      top *= c;
-      if (__any(top > m[rt] + 8.0f)) {
-        const float mn = fmaxf(m[rt], row_max(top));
+        for (int i = 0; i < 4; ++i) top[rt] = fmaxf(top[rt], s[rt][sb][i]);
+      top[rt] *= c;
+      more = more || top[rt] > m[rt] + 8.0f;
+    }
+    if (__any(more)) {
+#pragma unroll
+      for (int rt = 0; rt < C::RT; ++rt) {
+        const float mn = fmaxf(m[rt], row_max(top[rt]));
         const float keep = m[rt] == mn ? 1.0f : __builtin_amdgcn_exp2f(m[rt] - mn);
         m[rt] = mn;
         l[rt] *= keep;
 #pragma unroll
         for (int dt = 0; dt < DT; ++dt) o[rt][dt] *= keep;
       }
+    }
+    u32x2 pb[C::RT][SB];       // P^T as the products' second operand (bf16)
+#pragma unroll
+    for (int rt = 0; rt < C::RT; ++rt) {
       const float mb = m[rt] == -__builtin_inff() ? 0.0f : m[rt];
       float sum = 0.0f;
 #pragma unroll
@@ -499,136 +468,194 @@ template <int KIND, int D, int CLS> struct AttnBlock {
       }
       l[rt] += sum;
     }
-    values(vt, s, pb, u, span, odd);
+    if constexpr (KIND == kF32) {
+      values_f32(vt, s, mask);
+    } else {
+#pragma unroll
+      for (int half = 0; half < Values::HALVES; ++half) {
+        if (half > 0) v.load(vt, n16, g, half);
+        if (mask) odd_seen = __any(v.drop_odd()) || odd_seen;
+        values_bf16(v, half, pb);
+      }
+    }
   }
 
-  // O^T += V^T P^T. odd (rare): values that are not finite leave the product;
-  // the products of "counts" with "+inf or NaN" and with "-inf or NaN" say
-  // which rows' sums get +inf, -inf or both (NaN).
-  __device__ __forceinline__ void values(const char* vt, const f32x4 (&s)[C::RT][SB], const u32x2 (&pb)[C::RT][SB], int u,
-                                         bool span, bool odd) {
-    const float inf = __builtin_inff();
-    const uint32_t vb = lds_address(vt);
-    if constexpr (KIND == kF32) {
-      // Row 16 sb + 4 g + i, element 16 dt + n16: one address per i.
-      uint32_t va[4];
+  // The values of a tile (or of 128 of its 256 columns) as a lane reads them:
+  // EPL consecutive elements, from EPL n16 on, of the slots 4 g + j and 16 + 4
+  // g + j. Element x of all of them is the lane's part of V^T for the columns
+  // EPL r + x, r = 0 .. 15: the lane's rows turned into columns by one byte
+  // permutation per word. (The transposing LDS read gives the same without
+  // the permutations, but the compiler waits for every load to LDS on its way
+  // ahead of it, and in assembly it has to be waited for on the spot.)
+  struct Values {
+    static constexpr int EPL = D >= 128 ? 8 : 4;
+    static constexpr int HALVES = D / (16 * EPL);
+    uint32_t w[SB][4][EPL / 2];
+    __device__ __forceinline__ void load(const char* vt, int n16, int g, int half) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        va[i] = vb + (4 * g + i) * (D * 4) + (((n16 >> 2) ^ swizzle<CPR>(4 * g + i)) << 4) + (n16 & 3) * 4;
+      for (int sb = 0; sb < SB; ++sb)
 #pragma unroll
-      for (int dt = 0; dt < DT; ++dt) {
-        float v[SB][4];
+        for (int j = 0; j < 4; ++j) {
+          const int row = 4 * g + j;       // 16 rows on: the same permutation
+          if constexpr (EPL == 8) {
+            const uint32_t at = lds_address(vt) + row * (D * 2) + ((n16 ^ swizzle<CPR>(row)) << 4);
+            const u32x4 x = *lds_at<u32x4>(at + half * 256 + sb * 16 * D * 2);
 #pragma unroll
-        for (int sb = 0; sb < SB; ++sb)
+            for (int e = 0; e < 4; ++e) w[sb][j][e] = x[e];
+          } else {
+            const uint32_t at = lds_address(vt) + row * (D * 2) + (((n16 >> 1) ^ swizzle<CPR>(row)) << 4) + (n16 & 1) * 8;
+            const u32x2 x = *lds_at<u32x2>(at + sb * 16 * D * 2);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) v[sb][i] = *lds_at<float>((va[i] ^ (dt << 6)) + sb * 16 * D * 4);
-        if (odd) {
-#pragma unroll
-          for (int rt = 0; rt < C::RT; ++rt) {
-            const uint32_t seen = visible(u, rt, span);
-            f32x4 up = {}, down = {};
-#pragma unroll
-            for (int sb = 0; sb < SB; ++sb)
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const float x = v[sb][i];
-                const float p = (seen >> (4 * sb + i)) & 1 ? 1.0f : 0.0f;
-                up = __builtin_amdgcn_mfma_f32_16x16x4f32(x == inf || x != x ? 1.0f : 0.0f, p, up, 0, 0, 0);
-                down = __builtin_amdgcn_mfma_f32_16x16x4f32(x == -inf || x != x ? 1.0f : 0.0f, p, down, 0, 0, 0);
-              }
-            add_odd(o[rt][dt], up, down);
-            __builtin_amdgcn_sched_barrier(0);     // one at a time: registers
+            for (int e = 0; e < 2; ++e) w[sb][j][e] = x[e];
           }
-#pragma unroll
-          for (int sb = 0; sb < SB; ++sb)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v[sb][i] = not_finite(v[sb][i]) ? 0.0f : v[sb][i];
         }
+    }
+    // Values that are not finite leave the product (0 * inf); whether there
+    // were any.
+    __device__ __forceinline__ bool drop_odd() {
+      uint32_t dropped = 0;
+#pragma unroll
+      for (int sb = 0; sb < SB; ++sb)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int e = 0; e < EPL / 2; ++e) {
+            const uint32_t y = w[sb][j][e];
+            w[sb][j][e] = ((y & 0x7F80u) == 0x7F80u ? 0u : y & 0xFFFFu) |
+                          ((y & 0x7F800000u) == 0x7F800000u ? 0u : y & 0xFFFF0000u);
+            dropped |= w[sb][j][e] ^ y;
+          }
+      return dropped != 0;
+    }
+    // Words 2 sb and 2 sb + 1 of the operand for element x.
+    __device__ __forceinline__ u32x2 operand(int sb, int x) const {
+      const uint32_t sel = x & 1 ? 0x07060302u : 0x05040100u;
+      return u32x2{__builtin_amdgcn_perm(w[sb][1][x >> 1], w[sb][0][x >> 1], sel),
+                   __builtin_amdgcn_perm(w[sb][3][x >> 1], w[sb][2][x >> 1], sel)};
+    }
+  };
+
+  // O^T += V^T P^T.
+  __device__ __forceinline__ void values_bf16(const Values& v, int half, const u32x2 (&pb)[C::RT][SB]) {
+#pragma unroll
+    for (int x = 0; x < Values::EPL; ++x) {
+      u32x2 w[SB];
+#pragma unroll
+      for (int sb = 0; sb < SB; ++sb) w[sb] = v.operand(sb, x);
+#pragma unroll
+      for (int rt = 0; rt < C::RT; ++rt) {
+        f32x4& acc = o[rt][half * Values::EPL + x];
+        acc = product(w, pb[rt], acc);
+      }
+    }
+  }
+  static __device__ __forceinline__ f32x4 product(const u32x2 (&w)[SB], const u32x2 (&p)[SB], f32x4 acc) {
+    if constexpr (SB == 1)
+      return __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(__builtin_bit_cast(s16x4, w[0]), __builtin_bit_cast(s16x4, p[0]),
+                                                      acc, 0, 0, 0);
+    else
+      return __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+          __builtin_bit_cast(bf16x8, u32x4{w[0].x, w[0].y, w[SB - 1].x, w[SB - 1].y}),
+          __builtin_bit_cast(bf16x8, u32x4{p[0].x, p[0].y, p[SB - 1].x, p[SB - 1].y}), acc, 0, 0, 0);
+  }
+
+  // The same for float32: row 16 sb + 4 g + i, column 16 dt + n16.
+  __device__ __forceinline__ void values_f32(const char* vt, const f32x4 (&s)[C::RT][SB], bool mask) {
+    uint32_t va[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      va[i] = lds_address(vt) + (4 * g + i) * (D * 4) + (((n16 >> 2) ^ swizzle<CPR>(4 * g + i)) << 4) + (n16 & 3) * 4;
+#pragma unroll
+    for (int dt = 0; dt < DT; ++dt) {
+      float v[SB][4];
+#pragma unroll
+      for (int sb = 0; sb < SB; ++sb)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[sb][i] = *lds_at<float>((va[i] ^ (dt << 6)) + sb * 16 * D * 4);
+      if (mask) {
+        bool dropped = false;
 #pragma unroll
         for (int sb = 0; sb < SB; ++sb)
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int rt = 0; rt < C::RT; ++rt)
-              o[rt][dt] = __builtin_amdgcn_mfma_f32_16x16x4f32(v[sb][i], s[rt][sb][i], o[rt][dt], 0, 0, 0);
+          for (int i = 0; i < 4; ++i) {
+            dropped = dropped || not_finite(v[sb][i]);
+            v[sb][i] = not_finite(v[sb][i]) ? 0.0f : v[sb][i];
+          }
+        odd_seen = __any(dropped) || odd_seen;
       }
-    } else {
-      const int vrow = 4 * g + (n16 >> 2);
-      const uint32_t va = vb + vrow * (D * ESZ) + ((((n16 & 3) >> 1) ^ swizzle<CPR>(vrow)) << 4) + (n16 & 1) * 8;
 #pragma unroll
-      for (int d4 = 0; d4 < DT; d4 += 4) {
-        u32x2 w[SB > 1 ? SB : 2][4];
-        read_tr16<0, (SB > 1 ? 16 * D * ESZ : -1)>(va ^ (d4 << 5), va ^ ((d4 + 1) << 5), va ^ ((d4 + 2) << 5),
-                                                   va ^ ((d4 + 3) << 5), w[0], w[1]);
-        if (odd) {
+      for (int sb = 0; sb < SB; ++sb)
 #pragma unroll
-          for (int x = 0; x < 4; ++x)
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int rt = 0; rt < C::RT; ++rt) {
-              const uint32_t seen = visible(u, rt, span);
-              f32x4 up = {}, down = {};
+          for (int rt = 0; rt < C::RT; ++rt)
+            o[rt][dt] = __builtin_amdgcn_mfma_f32_16x16x4f32(v[sb][i], s[rt][sb][i], o[rt][dt], 0, 0, 0);
+    }
+  }
+
+  // After the segment, where a masked tile held values that are not finite and
+  // left them out (rare): they are added for the rows that count
+  // their slots, one slot after the other.
+  __device__ __forceinline__ void add_odd(int i0, int i1) {
+    const int n16 = fresh(this->n16), g = fresh(this->g);
+#pragma unroll 1
+    for (int u = i0; u < i1; ++u) {
+      const bool span = u >= un.ctx;
+      uint32_t there = 0;
+      int64_t at[SB];
+      if (!span) {
+        fetch_pages(u);
+        there = page_rows(u, at);
+        if (!masked(u, there)) continue;
+      }
+      uint32_t seen[C::RT];
 #pragma unroll
-              for (int sb = 0; sb < SB; ++sb) {
-                s16x4 hi, lo, p;
+      for (int rt = 0; rt < C::RT; ++rt) seen[rt] = visible(u, rt, span, there);
+#pragma unroll 1
+      for (int x = 0; x < C::SS; ++x) {
+        const int bit = 4 * (x / 16) + x % 4, from = (x % 16) / 4 * 16 + n16;
+        bool vis[C::RT], any = false;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  const uint32_t half = (w[sb][x][i >> 1] >> (16 * (i & 1))) & 0xFFFFu;
-                  const bool nan = (half & 0x7FFFu) > 0x7F80u;
-                  hi[i] = half == 0x7F80u || nan ? 0x3F80 : 0;
-                  lo[i] = half == 0xFF80u || nan ? 0x3F80 : 0;
-                  p[i] = (seen >> (4 * sb + i)) & 1 ? 0x3F80 : 0;
-                }
-                up = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(hi, p, up, 0, 0, 0);
-                down = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(lo, p, down, 0, 0, 0);
-              }
-              add_odd(o[rt][d4 + x], up, down);
-              __builtin_amdgcn_sched_barrier(0);     // one at a time: registers
-            }
-#pragma unroll
-          for (int sb = 0; sb < SB; ++sb)
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const uint32_t y = w[sb][x][e];
-                w[sb][x][e] = ((y & 0x7F80u) == 0x7F80u ? 0u : y & 0xFFFFu) |
-                              ((y & 0x7F800000u) == 0x7F800000u ? 0u : y & 0xFFFF0000u);
-              }
+        for (int rt = 0; rt < C::RT; ++rt) {
+          vis[rt] = (__shfl(seen[rt], from) >> bit) & 1;
+          any = any || vis[rt];
+        }
+        if (!__any(any)) continue;
+        const char* row;
+        if (span) {
+          const int s = min((u - un.ctx) * C::TS + kg * C::SS + x, a.n_pos - 1);
+          row = static_cast<const char*>(a.v) +
+                ((static_cast<int64_t>(r) * a.n_pos + s) * a.v_stride + static_cast<int64_t>(h) * D) * ESZ;
+        } else {
+          row = a.v_cache + at[SB > 1 && x >= 16 ? SB - 1 : 0] + (x % 16) * (D * CSZ);
         }
 #pragma unroll
-        for (int x = 0; x < 4; ++x)
+        for (int j = 0; j < D / 16 / kRun * 4; ++j)
 #pragma unroll
-          for (int rt = 0; rt < C::RT; ++rt) {
-            f32x4& acc = o[rt][d4 + x];
-            if constexpr (SB == 1)
-              acc = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(__builtin_bit_cast(s16x4, w[0][x]),
-                                                             __builtin_bit_cast(s16x4, pb[rt][0]), acc, 0, 0, 0);
-            else
-              acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                  __builtin_bit_cast(bf16x8, u32x4{w[0][x].x, w[0][x].y, w[1][x].x, w[1][x].y}),
-                  __builtin_bit_cast(bf16x8, u32x4{pb[rt][0].x, pb[rt][0].y, pb[rt][1].x, pb[rt][1].y}), acc, 0, 0, 0);
+          for (int e = 0; e < kRun; ++e) {
+            const int col = run_column(j, g) + e;
+            float y;
+            if (KIND == kF32) y = reinterpret_cast<const float*>(row)[col];
+            else if (KIND == kB16 || span) y = bf16_one(reinterpret_cast<const uint16_t*>(row)[col]);
+            else y = (reinterpret_cast<const uint8_t*>(row)[col] & 0x7F) == 0x7F ? __builtin_nanf("") : 0.0f;
+#pragma unroll
+            for (int rt = 0; rt < C::RT; ++rt) o[rt][KIND == kF32 ? j : j / 4 * kRun + e][KIND == kF32 ? e : j % 4] += vis[rt] && not_finite(y) ? y : 0.0f;
           }
       }
     }
   }
 
-  static __device__ __forceinline__ void add_odd(f32x4& sum, f32x4 up, f32x4 down) {
-    const float inf = __builtin_inff();
-#pragma unroll
-    for (int e = 0; e < 4; ++e) sum[e] += (up[e] > 0.0f ? inf : 0.0f) - (down[e] > 0.0f ? inf : 0.0f);
-  }
-
-  __device__ __forceinline__ bool masked(int u) const {
-    if (u >= un.ctx) return true;
+  // Whether some row of the block does not count some slot of context tile u.
+  __device__ __forceinline__ bool masked(int u, uint32_t there) const {
     const int j0 = slot0(u);
-    if (j0 + C::SS > len) return true;
-    if (a.window > 0 && j0 <= len + a.n_pos - 1 - a.window) return true;
-    return here(u) != (1u << SB) - 1;
+    return j0 + C::SS > len || (a.window > 0 && j0 <= len + a.n_pos - 1 - a.window) || there != (1u << SB) - 1;
   }
 
   __device__ __forceinline__ void compute(int u, const char* base) {
     if (idle) return;
-    tile(u, base, u >= un.ctx, masked(u));
+    const bool span = u >= un.ctx;
+    const uint32_t there = here(u);
+    tile(u, base, span, span || masked(u, there), there);
   }
 
   // Waits for a tile of this wave's loads with `after` later tiles on their way.
@@ -639,37 +666,42 @@ template <int KIND, int D, int CLS> struct AttnBlock {
     else wait_vm<0>();
   }
 
-  // Units [i0, i1) of the segment; pages of the first are being fetched.
-  __device__ __forceinline__ void run(int i0, int i1) {
+  // The next tile of units [i0, i1) on its way, if there is one.
+  __device__ __forceinline__ void start(int i0, int i1) {
+    const int loaded = KIND == kF8 ? min(i1, un.ctx) : i1;   // tiles that pass through the ring
+    if (next < loaded) {
+      issue(next, static_cast<uint32_t>(next - i0) % C::NST);
+      ++next;
+      if (next < un.ctx && next < loaded) fetch_pages(next);
+    }
+  }
+  // The first tiles of the segment; pages of the very first were fetched.
+  __device__ __forceinline__ void start_ring(int i0, int i1) {
     ring = 0;
     next = i0;
-    const int loaded = KIND == kF8 ? min(i1, un.ctx) : i1;   // tiles that pass through the ring
-    auto start = [&]() {
-      if (next < loaded) {
-        issue(next, static_cast<uint32_t>(next - i0) % C::NST);
-        ++next;
-        if (next < un.ctx && next < loaded) fetch_pages(next);
-      }
-    };
+    for (int x = 0; x < (KIND == kF8 ? C::NST : C::NST - 1); ++x) start(i0, i1);
+  }
+
+  // Units [i0, i1) of the segment; the ring was started.
+  __device__ __forceinline__ void run(int i0, int i1) {
+    const int loaded = KIND == kF8 ? min(i1, un.ctx) : i1;
     if constexpr (KIND != kF8) {
-      for (int x = 0; x < C::NST - 1; ++x) start();
       for (int u = i0; u < i1; ++u) {
         wait_tile(next - 1 - u);
         if (C::WR > 1) read_barrier();
-        start();
+        start(i0, i1);
         mem_fence();
         compute(u, lds + C::RING + (static_cast<uint32_t>(u - i0) % C::NST) * C::RAW);
         mem_fence();
       }
     } else {
-      for (int x = 0; x < C::NST; ++x) start();
       auto convert = [&](int u) {
         if (u < loaded) wait_tile(next - 1 - u);
         widen_tile(u, static_cast<uint32_t>(u - i0) % C::NST, C::NB == 2 ? (u - i0) & 1 : 0);
         // The raw pieces are in registers (they were converted) before their
         // place is loaded again.
         mem_fence();
-        start();
+        start(i0, i1);
         mem_fence();
       };
       if (C::NB == 2) {
@@ -731,31 +763,48 @@ template <int KIND, int D, int CLS> struct AttnBlock {
     for (int rt = 0; rt < C::RT; ++rt) {
       const float ls = row_sum(l[rt]);
       const int row = (wr * C::RT + rt) * 16 + n16;
-      if (rb * C::ROWS + row >= a.rows) continue;
       if (whole) {
-        write_out(rb * C::ROWS + row, g, o[rt], ls);
-      } else {
-        float* const at = a.part + (static_cast<int64_t>(slot) * C::ROWS + row) * D + 4 * g;
+        if (rb * C::ROWS + row >= a.rows) continue;
+        const int at_row = rb * C::ROWS + row;
+        const int t = at_row / a.group, hq = h * a.group + at_row - t * a.group;
+        const float inv = ls == 0.0f ? 0.0f : 1.0f / ls;
+        const int64_t at = ((static_cast<int64_t>(r) * a.n_pos + t) * (a.kvheads * a.group) + hq) * D;
 #pragma unroll
-        for (int dt = 0; dt < DT; ++dt) *reinterpret_cast<f32x4*>(at + dt * 16) = o[rt][dt];
+        for (int j = 0; j < D / 16 / kRun * 4; ++j) {
+          float y[kRun];
+#pragma unroll
+          for (int e = 0; e < kRun; ++e) y[e] = ls == 0.0f ? 0.0f : run_at(o[rt], j, e) * inv;
+          if constexpr (KIND == kF32) {
+            *reinterpret_cast<f32x4*>(static_cast<float*>(a.out) + at + run_column(j, g)) = f32x4{y[0], y[1], y[2], y[3]};
+          } else {
+            uint32_t* const to = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + at + run_column(j, g));
+            if constexpr (kRun == 8)
+              *reinterpret_cast<u32x4*>(to) = u32x4{pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]),
+                                                    pack_bf16(y[6], y[7])};
+            else
+              *reinterpret_cast<u32x2*>(to) = u32x2{pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3])};
+          }
+        }
+      } else {
+        // In the order of the lanes: whole lines per store; the join undoes it.
+        f32x4* const at = reinterpret_cast<f32x4*>(a.part) +
+                          (static_cast<int64_t>(slot) * (C::ROWS / 16) + wr * C::RT + rt) * (DT * 64) + lane;
+#pragma unroll
+        for (int dt = 0; dt < DT; ++dt) at[dt * 64] = o[rt][dt];
         if (g == 0) a.part_ml[slot * C::ROWS + row] = float2{m[rt], ls};
       }
     }
   }
 
-  __device__ __forceinline__ void write_out(int row, int g, const f32x4 (&sum)[DT], float ls) const {
-    const int t = row / a.group, hq = h * a.group + row - t * a.group;
-    const float inv = ls == 0.0f ? 0.0f : 1.0f / ls;
-    const int64_t at = ((static_cast<int64_t>(r) * a.n_pos + t) * (a.kvheads * a.group) + hq) * D + 4 * g;
-#pragma unroll
-    for (int dt = 0; dt < DT; ++dt) {
-      const f32x4 y = ls == 0.0f ? f32x4{} : sum[dt] * inv;
-      if constexpr (KIND == kF32)
-        *reinterpret_cast<f32x4*>(static_cast<float*>(a.out) + at + dt * 16) = y;
-      else
-        *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.out) + at + dt * 16) =
-            u32x2{pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3])};
-    }
+  // A lane's sums by runs of consecutive columns: float32 holds columns 16 j +
+  // 4 g + e in one register group, bf16 columns 16 EPL half + EPL (4 g + i) +
+  // e in element i of EPL of them (j = 4 half + i).
+  static constexpr int kRun = KIND == kF32 ? 4 : Values::EPL;
+  static __device__ __forceinline__ float run_at(const f32x4 (&sum)[DT], int j, int e) {
+    return KIND == kF32 ? sum[j][e] : sum[j / 4 * kRun + e][j % 4];
+  }
+  static __device__ __forceinline__ int run_column(int j, int g) {
+    return KIND == kF32 ? 16 * j + 4 * g : 16 * kRun * (j / 4) + kRun * (4 * g + j % 4);
   }
 };
 
@@ -859,24 +908,29 @@ void attn_kernel(const AttnArgs args) {
   __shared__ int8_t par[HRS_MAX_POS];
   __shared__ AttnRows<C::ROWS> rows;
   const int tid = threadIdx.x;
-  int u, u1;
+  AttnBlock<KIND, D, CLS> blk(args, lds, &rows);
+  int u, u1, in_req = 0, i = 0;
   {
     const AttnPlan plan(args, C::TS);
     u = attn_cut(blockIdx.x, plan.total, args.log_blocks);
     u1 = attn_cut(blockIdx.x + 1, plan.total, args.log_blocks);
+    if (u < u1) i = plan.find(u, &in_req, &blk.len);
     if (blockIdx.x == 0) {
       plan.write(args);
       if (args.status && args.req0 == 0) count_refused<C::NT>(args, reinterpret_cast<int32_t*>(lds));
     }
   }
 
-  AttnBlock<KIND, D, CLS> blk(args, lds, &rows);
   bool again = false;
   while (u < u1) {
-    // Counted again for every segment (two or three a block) rather than kept
-    // in registers over the tiles.
-    int in_req;
-    const int i = AttnPlan(args, C::TS).find(u, &in_req, &blk.len);
+    if (again) {
+      // Counted again for every further segment rather than kept in registers
+      // over the tiles; everybody is done with the last segment's tiles and
+      // masks after the barrier.
+      i = AttnPlan(args, C::TS).find(u, &in_req, &blk.len);
+      block_barrier();
+    }
+    again = true;
     blk.r = args.req0 + i;
     blk.un = attn_units(args, blk.len, C::TS);
     const int seg = __builtin_amdgcn_readfirstlane(in_req / blk.un.all);
@@ -884,16 +938,19 @@ void attn_kernel(const AttnArgs args) {
     const int ue = min(blk.un.all, u0 + (u1 - u));
     blk.h = __builtin_amdgcn_readfirstlane(seg / args.row_blocks);
     blk.rb = seg - blk.h * args.row_blocks;
-    blk.head_bytes = static_cast<uint32_t>(args.kvheads) * (D * C::ESZC << args.page_shift);
-    blk.h_bytes = static_cast<uint64_t>(blk.h) * (D * C::ESZC << args.page_shift);
-    blk.load_rows();
+    blk.head_groups = static_cast<uint32_t>(args.kvheads) << (args.page_shift - 4);
+    blk.h_groups = static_cast<uint32_t>(blk.h) << (args.page_shift - 4);
     if (u0 < blk.un.ctx) blk.fetch_pages(u0);
     const float ks = KIND == kF8 && args.k_scale ? args.k_scale[blk.h] : 1.0f;
     blk.vs = KIND == kF8 && args.v_scale ? args.v_scale[blk.h] : 1.0f;
     blk.c_span = args.scale * 1.4426950408889634f;
     blk.c_ctx = blk.c_span * ks;
-    if (again) block_barrier();        // everybody is done with the last segment's tiles and masks
-    again = true;
+    blk.load_rows();
+    mem_fence();
+    // The tiles' part of the segment (what is left are units that stand for
+    // the time that the span's masks and a segment's end take).
+    const int last = min(ue, blk.un.tiles());
+    blk.start_ring(u0, last);
     if (args.tree) {
       if (tid < args.n_pos) par[tid] = args.parent[i * args.n_pos + tid];
       block_barrier();
@@ -901,7 +958,8 @@ void attn_kernel(const AttnArgs args) {
     blk.mask_rows(par);
     blk.settle();
     block_barrier();
-    blk.run(u0, ue);
+    blk.run(u0, last);
+    if (blk.odd_seen) blk.add_odd(u0, last);
     blk.finish(u0 == 0 && ue == blk.un.all, 2 * static_cast<int>(blockIdx.x) + (u0 == 0 ? 1 : 0));
     u += ue - u0;
   }
