@@ -83,7 +83,7 @@ template <int KIND, int D, int CLS> struct AttnCfg {
 // takes the span's masks, the end of a sum and, for most blocks, the start of
 // another one, about the time of that many tiles (measured at 26,758 slots of
 // 256: the blocks with a span tile ended 5 us behind the others).
-constexpr int kExtraUnits = 2;
+constexpr int kExtraUnits = 4;
 
 // Work is counted in units: a unit is one tile of one (request, key/value
 // head, row block); the context's tiles come first, the span's last.

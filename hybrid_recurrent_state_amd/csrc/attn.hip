@@ -53,7 +53,7 @@ __global__ __launch_bounds__(NS > 1 ? 64 * NS : 256) void attn_join_kernel(const
   const int ns = NS > 1 ? wave : 0;
   float M = -__builtin_inff(), ls = 0.0f;
   f32x4 sum[2] = {};
-  constexpr int kAtOnce = 8;
+  constexpr int kAtOnce = NS > 1 ? 8 : 4;     // parts whose loads go out together
   for (int b = b0 + ns; b <= b1; b += NS * kAtOnce) {
     float2 w[kAtOnce];
     f32x4 x[kAtOnce][2];

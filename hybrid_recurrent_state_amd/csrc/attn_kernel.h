@@ -157,16 +157,14 @@ template <int KIND, int D, int CLS> struct AttnBlock {
   // Slot of tile u where this wave group starts.
   __device__ __forceinline__ int slot0(int u) const { return (un.first + u) * C::TS + kg * C::SS; }
 
-  // Page numbers of context tile u (scalar loads; a number of -1 for slots
-  // past the length).
+  // Page numbers of context tile u: scalar loads, nothing waits for them here.
   __device__ __forceinline__ void fetch_pages(int u) {
     typedef const __attribute__((address_space(4))) int32_t* cptr;
     const cptr table = (cptr)(a.page_table + static_cast<int64_t>(r) * a.table_len);
 #pragma unroll
     for (int i = 0; i < SB; ++i) {
       const int j = slot0(u) + 16 * i;
-      const int p = table[min(j >> a.page_shift, a.table_len - 1)];
-      pg[i] = j < len ? p : -1;
+      pg[i] = table[min(j >> a.page_shift, a.table_len - 1)];
     }
   }
 
@@ -178,7 +176,7 @@ template <int KIND, int D, int CLS> struct AttnBlock {
     uint32_t there = 0;
 #pragma unroll
     for (int i = 0; i < SB; ++i) {
-      const bool ok = static_cast<uint32_t>(pg[i]) < static_cast<uint32_t>(a.n_pages);
+      const bool ok = static_cast<uint32_t>(pg[i]) < static_cast<uint32_t>(a.n_pages) && slot0(u) + 16 * i < len;
       there |= ok ? 1u << i : 0u;
       const uint32_t in_page = ((slot0(u) >> 4) + i) & ((1u << (a.page_shift - 4)) - 1);
       const uint32_t group = (ok ? pg[i] : 0) * head_groups + h_groups + in_page;
@@ -249,6 +247,9 @@ template <int KIND, int D, int CLS> struct AttnBlock {
         const int p = (i * C::WR + wr) * 64 + lane;
         *reinterpret_cast<u32x4*>(dst + p * 16) = *reinterpret_cast<const u32x4*>(span_piece(u, p));
       }
+      // Not shared with the end of the other branch: its last store would wait
+      // for these loads, and with them for the tiles on their way.
+      asm volatile("; span rows" ::: "memory");
       return;
     }
     const char* const src = lds + C::RING + i_ring * C::RAW + kg * (C::RAW / C::WK);
