@@ -11,8 +11,10 @@
 // verify step, by the launch. The span's rows stay outside the pages until
 // they are accepted, so drafts never occupy cache slots, a rejected branch
 // leaves no trace and no row has to move inside the cache (rows that move
-// onto each other's slots would need an order). One wave copies one row of
-// one layer's keys or values at a time, 16 bytes per lane.
+// onto each other's slots would need an order). A block takes four rows of one
+// layer: lengths and path come in one round of loads, the pages in the next,
+// then 16-byte pieces of all heads' keys and values, four per thread on their
+// way at once.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -47,7 +49,6 @@ struct AppendArgs {
   int32_t n_pages;
   int32_t page_shift;
   int32_t table_len;
-  int32_t rows_per_block;
   int32_t lens_here;   // this launch writes seq_len_out and status
 };
 
@@ -58,16 +59,6 @@ __device__ __forceinline__ bool request_ok(const AppendArgs& a, int r, int* len,
   *n = al + 1;
   if (al < 0 || al >= a.n_pos || *len < 0) return false;
   return static_cast<int64_t>(*len) + al + 1 <= (static_cast<int64_t>(a.table_len) << a.page_shift);
-}
-
-// Whether every accepted entry of the request's path names a span position
-// (n <= 64 where there is a path); the answer is the wave's, each lane looks
-// at one entry.
-__device__ __forceinline__ bool path_ok(const AppendArgs& a, int r, int n) {
-  if (a.path == nullptr) return true;
-  const int lane = threadIdx.x & 63;
-  const int p = a.path[static_cast<int64_t>(r) * a.n_pos + min(lane, n - 1)];
-  return __all(p >= 0 && p < a.n_pos);
 }
 
 // The new lengths and the count of refused requests, by one block, a request
@@ -92,77 +83,97 @@ __device__ void write_lengths(const AppendArgs& a) {
   if (a.status && threadIdx.x == 0) *a.status = bad;
 }
 
-// One 16-byte piece of a span row to the cache row.
-__device__ __forceinline__ void copy_row(const char* src, char* dst, int bytes, int lane, int lanes) {
-  for (int i = lane * 16; i < bytes; i += lanes * 16)
-    *reinterpret_cast<u32x4*>(dst + i) = *reinterpret_cast<const u32x4*>(src + i);
-}
-
-// bf16 row to e4m3: divided by the scale (rounded once), limited to the
-// largest e4m3 number, NaN kept.
+// Eight bf16 values to e4m3: divided by the scale (rounded once), limited to
+// the largest e4m3 number, NaN kept.
 __device__ __forceinline__ float e4m3_range(float x, float scale) {
   const float y = x / scale;
   return y != y ? y : fminf(fmaxf(y, -448.0f), 448.0f);
 }
-__device__ __forceinline__ void quant_row(const char* src, char* dst, int d, float scale, int lane, int lanes) {
-  for (int i = lane * 8; i < d; i += lanes * 8) {
-    float x[8];
-    load8<uint16_t>(reinterpret_cast<const uint16_t*>(src) + i, x);
+__device__ __forceinline__ u32x2 to_e4m3(u32x4 w, float scale) {
+  float x[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] = e4m3_range(x[j], scale);
-    uint32_t lo = __builtin_amdgcn_cvt_pk_fp8_f32(x[0], x[1], 0, false);
-    lo = __builtin_amdgcn_cvt_pk_fp8_f32(x[2], x[3], lo, true);
-    uint32_t hi = __builtin_amdgcn_cvt_pk_fp8_f32(x[4], x[5], 0, false);
-    hi = __builtin_amdgcn_cvt_pk_fp8_f32(x[6], x[7], hi, true);
-    *reinterpret_cast<u32x2*>(dst + i) = u32x2{lo, hi};
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = e4m3_range(bf16_lo(w[i]), scale);
+    x[2 * i + 1] = e4m3_range(bf16_hi(w[i]), scale);
   }
+  uint32_t lo = __builtin_amdgcn_cvt_pk_fp8_f32(x[0], x[1], 0, false);
+  lo = __builtin_amdgcn_cvt_pk_fp8_f32(x[2], x[3], lo, true);
+  uint32_t hi = __builtin_amdgcn_cvt_pk_fp8_f32(x[4], x[5], 0, false);
+  hi = __builtin_amdgcn_cvt_pk_fp8_f32(x[6], x[7], hi, true);
+  return u32x2{lo, hi};
 }
 
-// Grid: (blocks of rows, request, layer). ESZ: bytes of a span element; F8:
-// the cache is e4m3. A row here is one position's keys or values of all heads
-// of one layer; the block's items are (position, K or V, head).
+constexpr int kRows = 4;      // span rows of a block
+constexpr int kBatch = 4;     // pieces of a thread whose loads go out together
+
+// Grid: (blocks of kRows rows, request, layer). ESZ: bytes of a span element;
+// F8: the cache is e4m3. A piece is 16 bytes of the span; the block's pieces
+// are (row, K or V, head, piece of the head).
 template <int ESZ, bool F8>
 __global__ __launch_bounds__(kThreads) void append_kernel(const AppendArgs args) {
   const int r = blockIdx.y;
   const int layer = blockIdx.z;
   if (args.lens_here && blockIdx.x == 0 && r == 0 && layer == 0) write_lengths(args);
+  // Lengths and path in one round of loads.
+  const int lane = threadIdx.x & 63;
+  const int i0 = blockIdx.x * kRows;
+  int entry = lane;
+  if (args.path) entry = args.path[static_cast<int64_t>(r) * args.n_pos + min(lane, args.n_pos - 1)];
   int len, n;
-  if (!request_ok(args, r, &len, &n) || !path_ok(args, r, n)) return;
-  const int i0 = blockIdx.x * args.rows_per_block;
-  const int i1 = min(n, i0 + args.rows_per_block);
+  if (!request_ok(args, r, &len, &n)) return;
+  if (args.path && !__all(lane >= n || (entry >= 0 && entry < args.n_pos))) return;
+  const int i1 = min(n, i0 + kRows);
   if (i0 >= i1) return;
-  const int d = args.d;
-  constexpr int kPiece = F8 ? 8 : 16 / ESZ;      // elements per lane step
-  const int lanes = min(64, (d + kPiece - 1) / kPiece);
-  // Lanes per row: the power of two that holds it, so that a wave takes
-  // several short rows at once.
-  int lp = 1;
-  while (lp < lanes) lp <<= 1;
-  const int sub = threadIdx.x / lp, lane = threadIdx.x % lp;
-  const int subs = kThreads / lp;
-  const int items = (i1 - i0) * 2 * args.heads;
+  // Page and span position of every row of the block.
+  int page[kRows], pos[kRows];
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    const int row = min(i0 + i, n - 1);
+    page[i] = args.page_table[static_cast<int64_t>(r) * args.table_len + ((len + row) >> args.page_shift)];
+    pos[i] = args.path ? __builtin_amdgcn_readlane(entry, row) : row;
+  }
+  const int d = args.d, heads = args.heads;
+  const int per_head = d * ESZ / 16;
+  const int per_row = 2 * heads * per_head;
+  const int pieces = (i1 - i0) * per_row;
   const int64_t span_row0 = (static_cast<int64_t>(layer) * args.n_req + r) * args.n_pos;
   const int page_mask = (1 << args.page_shift) - 1;
-  const int csz = F8 ? 1 : ESZ;
-  for (int it = sub; it < items; it += subs) {
-    const int h = it % args.heads;
-    const int kv = (it / args.heads) & 1;
-    const int i = i0 + it / (2 * args.heads);
-    const int slot = len + i;
-    const int page = args.page_table[static_cast<int64_t>(r) * args.table_len + (slot >> args.page_shift)];
-    if (page < 0 || page >= args.n_pages) continue;
-    const int pos = args.path ? args.path[static_cast<int64_t>(r) * args.n_pos + i] : i;
-    const int64_t stride = kv ? args.v_stride : args.k_stride;
-    const char* src = static_cast<const char*>(kv ? args.v : args.k) +
-                      ((span_row0 + pos) * stride + static_cast<int64_t>(h) * d) * ESZ;
-    const int64_t row = ((static_cast<int64_t>(layer) * args.n_pages + page) * args.heads + h) *
-                            (page_mask + 1) + (slot & page_mask);
-    char* dst = static_cast<char*>(kv ? args.v_cache : args.k_cache) + row * d * csz;
-    if constexpr (F8) {
-      const float* sc = kv ? args.v_scale : args.k_scale;
-      quant_row(src, dst, d, sc ? sc[layer * args.heads + h] : 1.0f, lane, lp);
-    } else {
-      copy_row(src, dst, d * ESZ, lane, lp);
+  constexpr int kOut = F8 ? 8 : 16;               // bytes of a piece in the cache
+  for (int p0 = threadIdx.x; p0 < pieces; p0 += kThreads * kBatch) {
+    u32x4 x[kBatch];
+    float scale[kBatch];
+    char* to[kBatch];
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      const int p = min(p0 + b * kThreads, pieces - 1);
+      const int row = p / per_row, in_row = p - row * per_row;
+      const int item = in_row / per_head, piece = in_row - item * per_head;
+      const bool is_v = item >= heads;
+      const int h = is_v ? item - heads : item;
+      int pg = page[0], ps = pos[0];
+#pragma unroll
+      for (int i = 1; i < kRows; ++i) {
+        pg = row == i ? page[i] : pg;
+        ps = row == i ? pos[i] : ps;
+      }
+      const char* const src = static_cast<const char*>(is_v ? args.v : args.k) +
+                              ((span_row0 + ps) * (is_v ? args.v_stride : args.k_stride) + static_cast<int64_t>(h) * d) * ESZ;
+      x[b] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(src) + piece);
+      if constexpr (F8) {
+        const float* sc = is_v ? args.v_scale : args.k_scale;
+        scale[b] = sc ? sc[layer * heads + h] : 1.0f;
+      }
+      const int slot = len + i0 + row;
+      const int64_t at = ((static_cast<int64_t>(layer) * args.n_pages + pg) * heads + h) * (page_mask + 1) +
+                         (slot & page_mask);
+      const bool there = pg >= 0 && pg < args.n_pages && p0 + b * kThreads < pieces;
+      to[b] = there ? static_cast<char*>(is_v ? args.v_cache : args.k_cache) + (at * per_head + piece) * kOut : nullptr;
+    }
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      if (to[b] == nullptr) continue;
+      if constexpr (F8) *reinterpret_cast<u32x2*>(to[b]) = to_e4m3(x[b], scale[b]);
+      else *reinterpret_cast<u32x4*>(to[b]) = x[b];
     }
   }
 }
@@ -209,9 +220,8 @@ extern "C" int kv_cache_append(const hrs_append_desc* d, const void* k, const vo
   args.n_req = d->n_req; args.n_pos = d->n_pos; args.heads = d->n_kvheads; args.d = d->d;
   args.n_pages = d->cache.n_pages; args.table_len = d->cache.table_len;
   args.page_shift = __builtin_ctz(static_cast<unsigned>(d->cache.page_size));
-  args.rows_per_block = 16;
   args.lens_here = seq_len_out != seq_len;
-  const dim3 grid((d->n_pos + args.rows_per_block - 1) / args.rows_per_block, d->n_req, d->n_layers);
+  const dim3 grid((d->n_pos + kRows - 1) / kRows, d->n_req, d->n_layers);
   const hipStream_t s = static_cast<hipStream_t>(stream);
   (void)hipGetLastError();
   if (d->dtype == HRS_F32)
