@@ -632,6 +632,15 @@ def ring_get_2d(ring, packed, runs, stream=None):
 
 # --- full-attention layers and sampling --------------------------------------
 
+def _current_stream(device: int) -> int:
+    """Raw handle of the current stream. torch's own raw getter where it has
+    one: building a Stream object takes 2.5 us, more than the call's checks
+    and half of a small launch."""
+    torch = _torch()
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(device) if raw is not None else torch.cuda.current_stream().cuda_stream
+
+
 class PreparedCall:
     """One call of an entry point with its checks done and its arguments laid
     out. Calling it launches on ``stream`` (torch stream or raw handle;
@@ -645,11 +654,11 @@ class PreparedCall:
         self._keep, self._device = (keep, tensors), tensors[0].device
 
     def __call__(self, stream=None) -> None:
-        torch = _torch()
-        if torch.cuda.current_device() != self._device.index:
-            raise ValueError(f"{self._name}: tensors are on {self._device}, the current device is "
-                             f"cuda:{torch.cuda.current_device()}")
-        st = self._fn(*self._args, _stream(stream))
+        cuda = _torch().cuda
+        device = cuda.current_device()
+        if device != self._device.index:
+            raise ValueError(f"{self._name}: tensors are on {self._device}, the current device is cuda:{device}")
+        st = self._fn(*self._args, _current_stream(device) if stream is None else _stream(stream))
         if st != HRS_OK:
             raise HrsError(st, self._name)
 

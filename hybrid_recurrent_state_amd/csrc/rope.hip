@@ -8,15 +8,19 @@
 // file table: batched query/key norm and rotation ahead of the attention.
 //
 // MI355X design: a copy with a little arithmetic, bound by memory for long
-// spans and by launch latency for one token. A head is held by a group of 8,
-// 16 or 32 lanes, eight elements each (one 16-byte load of bf16); the sum of
-// squares is a butterfly inside the group and the partner half of a rotated
-// pair comes from another lane of it, so a head is read and written once and
-// never leaves registers. The angles depend on the position alone: a block
-// forms them once per position (the product with the frequency and its
-// reduction to a turn in 64 bits: at position 262,144 a float32 product is
-// off by up to 0.016 radians) while its first heads are on the way, and all
-// heads of the position read the sines from LDS.
+// spans (4096 positions of 28 heads of 256: 24.9 us, 4.7 TB/s) and by launch
+// latency for one token (a 3.6 us kernel). A head is held by a group of 8, 16
+// or 32 lanes, eight elements each (one 16-byte load of bf16), four heads of a
+// group on their way at once; the sum of squares is a butterfly inside the
+// group and the partner half of a rotated pair comes from another lane of it,
+// so a head is read and written once and never leaves registers. The angles
+// depend on the position alone: a block forms them once per position (the
+// product with the frequency and its reduction to a turn in 64 bits: at
+// position 262,144 a float32 product is off by up to 0.016 radians) while its
+// first heads are on the way; a lane keeps the sines of its elements in
+// registers over all heads of a position (with a division per head to find
+// its position and the sines read per head the arithmetic was the bound: 36
+// us).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -30,6 +34,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kMaxRot = 256;
 constexpr int kMaxTokens = 4;   // positions a block takes at most
+constexpr int kBatch = 4;       // heads of a lane group whose loads go out together
 
 struct RopeArgs {
   const void* q;
@@ -66,47 +71,83 @@ template <int LPH> __device__ __forceinline__ float head_sum(float x) {
   }
 }
 
-template <typename T> __device__ __forceinline__ void store8(T* p, const float* v);
-template <> __device__ __forceinline__ void store8<float>(float* p, const float* v) {
-  reinterpret_cast<f32x4*>(p)[0] = f32x4{v[0], v[1], v[2], v[3]};
-  reinterpret_cast<f32x4*>(p)[1] = f32x4{v[4], v[5], v[6], v[7]};
+// Eight elements; past the caches (nt) where a launch writes more than they
+// hold anyway (4096 positions of 28 heads of 256: 24.9 vs 30.3 us).
+__device__ __forceinline__ void store16(u32x4* p, u32x4 v, bool nt) {
+  if (nt) __builtin_nontemporal_store(v, p);
+  else *p = v;
 }
-template <> __device__ __forceinline__ void store8<uint16_t>(uint16_t* p, const float* v) {
-  *reinterpret_cast<u32x4*>(p) =
-      u32x4{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])};
+__device__ __forceinline__ void store8(float* p, const float* v, bool nt) {
+  store16(reinterpret_cast<u32x4*>(p), __builtin_bit_cast(u32x4, f32x4{v[0], v[1], v[2], v[3]}), nt);
+  store16(reinterpret_cast<u32x4*>(p) + 1, __builtin_bit_cast(u32x4, f32x4{v[4], v[5], v[6], v[7]}), nt);
+}
+__device__ __forceinline__ void store8(uint16_t* p, const float* v, bool nt) {
+  store16(reinterpret_cast<u32x4*>(p),
+          u32x4{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])}, nt);
 }
 
 template <typename T, int LPH>
 __global__ __launch_bounds__(kThreads) void qk_norm_rope_kernel(const RopeArgs args) {
   constexpr int kGroups = kThreads / LPH;
-  __shared__ float cs[kMaxTokens][kMaxRot / 2];
-  __shared__ float sn[kMaxTokens][kMaxRot / 2];
+  __shared__ __align__(16) float cs[kMaxTokens][kMaxRot / 2];
+  __shared__ __align__(16) float sn[kMaxTokens][kMaxRot / 2];
   const int tok0 = blockIdx.x * args.per_block;
   const int n_tok = min(args.per_block, args.n_tok - tok0);
   const int group = threadIdx.x / LPH;
   const int lane = threadIdx.x % LPH;       // eight elements from 8 * lane
   const int half = args.rot >> 1;
   const bool mine = lane * 8 < args.d;
-  const int items = n_tok * args.n_heads;
+  // A lane group takes heads h0, h0 + step, ... of every position, kBatch of
+  // them at a time.
   const int step = kGroups * gridDim.y;
-  int item = blockIdx.y * kGroups + group;
+  const int h0 = blockIdx.y * kGroups + group;
+  const int batches = (args.n_heads + step * kBatch - 1) / (step * kBatch);
 
+  // Eight elements as they were loaded; kBatch heads of a group on their way
+  // at once.
+  struct Raw {
+    u32x4 w[sizeof(T) / 2];
+    __device__ __forceinline__ void widen(float* o) const {
+      if constexpr (sizeof(T) == 2) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          o[2 * i] = bf16_lo(w[0][i]);
+          o[2 * i + 1] = bf16_hi(w[0][i]);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] = __uint_as_float(w[i / 4][i % 4]);
+      }
+    }
+  };
   const T* const q = static_cast<const T*>(args.q);
   const T* const k = static_cast<const T*>(args.k);
-  auto load_item = [&](int it, float* x) {
-    const int t = it / args.n_heads;
-    const int h = it - t * args.n_heads;
-    const int64_t row = static_cast<int64_t>(args.req0) * args.n_pos + tok0 + t;
+  auto load_head = [&](int t, int h) {
+    const int64_t row = static_cast<int64_t>(args.req0) * args.n_pos + tok0 + min(t, n_tok - 1);
+    h = min(h, args.n_heads - 1);
     const T* p = h < args.n_q ? q + row * args.q_stride + h * args.d
                               : k + row * args.k_stride + (h - args.n_q) * args.d;
-    load8<T>(p + lane * 8, x);
+    Raw x = {};
+    if (mine) {
+      const u32x4* src = reinterpret_cast<const u32x4*>(p + lane * 8);
+#pragma unroll
+      for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) x.w[i] = src[i];
+    }
+    return x;
   };
 
-  float x[8] = {};
-  if (mine && item < items) load_item(item, x);
+  Raw next[kBatch];
+#pragma unroll
+  for (int b = 0; b < kBatch; ++b)
+    if (b * step + h0 - group < args.n_heads) next[b] = load_head(0, h0 + b * step);
   float wq[8] = {}, wk[8] = {};
   if (mine && args.qw) load8<T>(static_cast<const T*>(args.qw) + lane * 8, wq);
   if (mine && args.kw) load8<T>(static_cast<const T*>(args.kw) + lane * 8, wk);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    wq[i] += args.offset;
+    wk[i] += args.offset;
+  }
   for (int i = threadIdx.x; i < n_tok * half; i += kThreads) {
     const int t = i / half;
     const int f = i - t * half;
@@ -127,62 +168,71 @@ __global__ __launch_bounds__(kThreads) void qk_norm_rope_kernel(const RopeArgs a
   __syncthreads();
 
   const float inv_d = 1.0f / static_cast<float>(args.d);
-  // Every lane of a wave takes part in the exchanges, so the loop runs as
-  // long as any group of the block has a head left.
-  for (int base = blockIdx.y * kGroups; base < items; base += step, item += step) {
-    float nx[8] = {};
-    if (mine && item + step < items) load_item(item + step, nx);
-    const int t = min(item, items - 1) / args.n_heads;
-    const int h = min(item, items - 1) - t * args.n_heads;
-    const bool is_q = h < args.n_q;
-    float v[8];
-    if (is_q ? args.qw != nullptr : args.kw != nullptr) {
-      float ss = 0.0f;
+  // The lane's angles: of its eight elements where a pair's halves are apart
+  // (half is a multiple of 8, so the partner's eight are one other lane's), of
+  // its four pairs otherwise.
+  const int hl = half >> 3;
+  const bool low = lane < hl;
+  const bool turns = args.interleaved ? lane * 8 < args.rot : lane < 2 * hl;
+  const int f0 = !turns ? 0 : args.interleaved ? lane * 4 : (low ? lane : lane - hl) * 8;
+  const int src = (threadIdx.x & 63) - lane + (!turns ? lane : low ? lane + hl : lane - hl);
+  for (int t = 0; t < n_tok; ++t) {
+    f32x4 c4[2], s4[2];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
-      const float r = 1.0f / sqrtf(fmaf(head_sum<LPH>(ss), inv_d, args.eps));
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = x[i] * r * (args.offset + (is_q ? wq[i] : wk[i]));
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = x[i];
+    for (int i = 0; i < 2; ++i) {
+      c4[i] = turns ? *reinterpret_cast<const f32x4*>(&cs[t][f0 + 4 * i]) : f32x4{1.0f, 1.0f, 1.0f, 1.0f};
+      s4[i] = turns ? *reinterpret_cast<const f32x4*>(&sn[t][f0 + 4 * i]) : f32x4{};
     }
-    if (args.interleaved) {
-      if (lane * 8 < args.rot) {
+    for (int hb = 0; hb < batches; ++hb) {
+      Raw now[kBatch];
+      const bool last = hb + 1 == batches;
 #pragma unroll
-        for (int i = 0; i < 8; i += 2) {
-          const float c = cs[t][lane * 4 + i / 2], s = sn[t][lane * 4 + i / 2];
-          const float a = v[i], b = v[i + 1];
-          v[i] = a * c - b * s;
-          v[i + 1] = b * c + a * s;
+      for (int b = 0; b < kBatch; ++b) {
+        now[b] = next[b];
+        const int h = (last ? 0 : (hb + 1) * kBatch * step) + b * step + h0;
+        if (h - group < args.n_heads && !(last && t + 1 == n_tok)) next[b] = load_head(t + last, h);
+      }
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {
+        const int h = (hb * kBatch + b) * step + h0;
+        if (h - group >= args.n_heads) break;         // no group of the block has this head
+        const bool is_q = h < args.n_q;
+        float v[8];
+        now[b].widen(v);
+        if (is_q ? args.qw != nullptr : args.kw != nullptr) {
+          float ss = 0.0f;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) ss = fmaf(v[i], v[i], ss);
+          const float r = __builtin_amdgcn_rsqf(fmaf(head_sum<LPH>(ss), inv_d, args.eps));
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] = v[i] * r * (is_q ? wq[i] : wk[i]);
+        }
+        if (args.interleaved) {
+#pragma unroll
+          for (int i = 0; i < 8; i += 2) {
+            const float c = c4[0][i / 2], sv = s4[0][i / 2];
+            const float x = v[i], y = v[i + 1];
+            v[i] = turns ? x * c - y * sv : x;
+            v[i + 1] = turns ? y * c + x * sv : y;
+          }
+        } else if (args.rot) {
+          float o[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) o[i] = __shfl(v[i], src);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float sv = low ? -s4[i / 4][i % 4] : s4[i / 4][i % 4];
+            v[i] = turns ? v[i] * c4[i / 4][i % 4] + o[i] * sv : v[i];
+          }
+        }
+        if (mine && h < args.n_heads) {
+          const int64_t row = static_cast<int64_t>(args.req0) * args.n_pos + tok0 + t;
+          T* p = is_q ? static_cast<T*>(args.q_out) + (row * args.n_q + h) * args.d
+                      : static_cast<T*>(args.k_out) + (row * (args.n_heads - args.n_q) + (h - args.n_q)) * args.d;
+          store8(p + lane * 8, v, args.per_block > 1);
         }
       }
-    } else if (args.rot) {
-      // half is a multiple of 8: the partner elements are one lane's eight.
-      const int hl = half >> 3;
-      const bool low = lane < hl;
-      const int partner = low ? lane + hl : lane < 2 * hl ? lane - hl : lane;
-      const int src = (threadIdx.x & 63) - lane + partner;
-      float o[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) o[i] = __shfl(v[i], src);
-      if (lane < 2 * hl) {
-        const int f0 = (low ? lane : lane - hl) * 8;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float c = cs[t][f0 + i], s = sn[t][f0 + i];
-          v[i] = low ? v[i] * c - o[i] * s : v[i] * c + o[i] * s;
-        }
-      }
     }
-    if (mine && item < items) {
-      const int64_t row = static_cast<int64_t>(args.req0) * args.n_pos + tok0 + t;
-      T* p = is_q ? static_cast<T*>(args.q_out) + (row * args.n_q + h) * args.d
-                  : static_cast<T*>(args.k_out) + (row * (args.n_heads - args.n_q) + (h - args.n_q)) * args.d;
-      store8<T>(p + lane * 8, v);
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = nx[i];
   }
 }
 
