@@ -73,20 +73,20 @@ template <int LPH> __device__ __forceinline__ float head_sum(float x) {
 
 // Eight elements; past the caches (nt) where a launch writes more than they
 // hold anyway (4096 positions of 28 heads of 256: 24.9 vs 30.3 us).
-__device__ __forceinline__ void store16(u32x4* p, u32x4 v, bool nt) {
-  if (nt) __builtin_nontemporal_store(v, p);
+template <bool NT> __device__ __forceinline__ void store16(u32x4* p, u32x4 v) {
+  if constexpr (NT) __builtin_nontemporal_store(v, p);
   else *p = v;
 }
-__device__ __forceinline__ void store8(float* p, const float* v, bool nt) {
-  store16(reinterpret_cast<u32x4*>(p), __builtin_bit_cast(u32x4, f32x4{v[0], v[1], v[2], v[3]}), nt);
-  store16(reinterpret_cast<u32x4*>(p) + 1, __builtin_bit_cast(u32x4, f32x4{v[4], v[5], v[6], v[7]}), nt);
+template <bool NT> __device__ __forceinline__ void store8(float* p, const float* v) {
+  store16<NT>(reinterpret_cast<u32x4*>(p), __builtin_bit_cast(u32x4, f32x4{v[0], v[1], v[2], v[3]}));
+  store16<NT>(reinterpret_cast<u32x4*>(p) + 1, __builtin_bit_cast(u32x4, f32x4{v[4], v[5], v[6], v[7]}));
 }
-__device__ __forceinline__ void store8(uint16_t* p, const float* v, bool nt) {
-  store16(reinterpret_cast<u32x4*>(p),
-          u32x4{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])}, nt);
+template <bool NT> __device__ __forceinline__ void store8(uint16_t* p, const float* v) {
+  store16<NT>(reinterpret_cast<u32x4*>(p),
+              u32x4{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])});
 }
 
-template <typename T, int LPH>
+template <typename T, int LPH, bool MANY>
 __global__ __launch_bounds__(kThreads) void qk_norm_rope_kernel(const RopeArgs args) {
   constexpr int kGroups = kThreads / LPH;
   __shared__ __align__(16) float cs[kMaxTokens][kMaxRot / 2];
@@ -229,21 +229,20 @@ __global__ __launch_bounds__(kThreads) void qk_norm_rope_kernel(const RopeArgs a
           const int64_t row = static_cast<int64_t>(args.req0) * args.n_pos + tok0 + t;
           T* p = is_q ? static_cast<T*>(args.q_out) + (row * args.n_q + h) * args.d
                       : static_cast<T*>(args.k_out) + (row * (args.n_heads - args.n_q) + (h - args.n_q)) * args.d;
-          store8(p + lane * 8, v, args.per_block > 1);
+          store8<MANY>(p + lane * 8, v);
         }
       }
     }
   }
 }
 
-template <typename T>
-void launch_rope(const RopeArgs& args, dim3 grid, hipStream_t s) {
+template <typename T, bool MANY> void launch_rope(const RopeArgs& args, dim3 grid, hipStream_t s) {
   if (args.d > 128)
-    hipLaunchKernelGGL((qk_norm_rope_kernel<T, 32>), grid, dim3(kThreads), 0, s, args);
+    hipLaunchKernelGGL((qk_norm_rope_kernel<T, 32, MANY>), grid, dim3(kThreads), 0, s, args);
   else if (args.d > 64)
-    hipLaunchKernelGGL((qk_norm_rope_kernel<T, 16>), grid, dim3(kThreads), 0, s, args);
+    hipLaunchKernelGGL((qk_norm_rope_kernel<T, 16, MANY>), grid, dim3(kThreads), 0, s, args);
   else
-    hipLaunchKernelGGL((qk_norm_rope_kernel<T, 8>), grid, dim3(kThreads), 0, s, args);
+    hipLaunchKernelGGL((qk_norm_rope_kernel<T, 8, MANY>), grid, dim3(kThreads), 0, s, args);
 }
 
 }  // namespace
@@ -298,10 +297,9 @@ extern "C" int qk_norm_rope(const hrs_qk_desc* d, const void* q, const void* k, 
     args.per_block = few ? 1 : kMaxTokens;
     const dim3 grid((args.n_tok + args.per_block - 1) / args.per_block,
                     few ? std::min((args.n_heads + groups - 1) / groups, 65535) : 1);
-    if (d->dtype == HRS_BF16)
-      launch_rope<uint16_t>(args, grid, static_cast<hipStream_t>(stream));
-    else
-      launch_rope<float>(args, grid, static_cast<hipStream_t>(stream));
+    const hipStream_t st = static_cast<hipStream_t>(stream);
+    if (d->dtype == HRS_BF16) few ? launch_rope<uint16_t, false>(args, grid, st) : launch_rope<uint16_t, true>(args, grid, st);
+    else few ? launch_rope<float, false>(args, grid, st) : launch_rope<float, true>(args, grid, st);
     if (launch_error() != hipSuccess) return HRS_EDEVICE;
   }
   return HRS_OK;
