@@ -19,7 +19,9 @@ Variants: ``ZeroCopyVerifyStep`` starts
 each span from the previous span's accepted checkpoint in place (no rollback
 copy, conv state rebuilt from the accepted path) and ``FusedVerifyStep`` adds
 one fused kernel per layer (conv, SiLU, q/k/v split, q/k L2 norm and the
-gated delta rule) to it.
+gated delta rule) to it. ``HybridVerifyStep`` adds the model's attention
+layers between the GDN layers (norm and rotation, attention over a paged
+cache, accepted rows into the pages) and acceptance by sampling.
 """
 from __future__ import annotations
 
@@ -30,7 +32,9 @@ from typing import List, Optional, Sequence
 import numpy as np
 
 from . import (AcceptDesc, ConvAdvanceDesc, ConvDesc, GdnDesc, GdnLayerDesc, HRS_BF16, HRS_CHAIN, HRS_F32, HRS_TREE,
-               HrsError, RingDesc, RingRun, RollbackDesc, SpanSource, accept_greedy_workspace_bytes, lib)
+               HrsError, RingDesc, RingRun, RollbackDesc, SpanSource, accept_greedy_workspace_bytes,
+               accept_sample_call, accept_sample_workspace_bytes, attn_verify_span_call,
+               attn_verify_span_workspace_bytes, kv_cache_append_call, lib, qk_norm_rope_call)
 
 
 @dataclasses.dataclass(frozen=True)
@@ -444,3 +448,119 @@ class FusedVerifyStep(ZeroCopyVerifyStep):
             state, src = None, ctypes.byref(self.srcs[self.cur][l])
         _check(lib.gdn_layer_verify_span(self.layer_p, *self.fused_in[l], state, src, ck, out, None, stream),
                "gdn_layer_verify_span")
+
+
+@dataclasses.dataclass(frozen=True)
+class AttnShape:
+    """The attention layers of a hybrid model and their paged cache."""
+    n_layers: int
+    n_heads: int
+    n_kvheads: int
+    head_dim: int
+    rotary_dim: int            # even, at most head_dim; 0: no rotation
+    n_pages: int               # pages of one layer
+    page_size: int             # slots of one page
+    table_len: int             # pages one request may hold
+    theta: float = 1e7
+    eps: float = 1e-6
+    weight_offset: float = 0.0
+    f8_cache: bool = False     # float8_e4m3fn pages with a scale per layer and key head
+    after: Optional[Sequence[int]] = None   # the GDN layer each attention layer follows; default: evenly spread
+
+
+class AttnBuffers:
+    """Device buffers of the attention layers beside a step's StepBuffers.
+
+    qkv [L,R,T,Hq+2Hkv,d] is each layer's projection; q_out, k_out its
+    normalised and rotated heads. page_table holds distinct pages per request
+    and seq_len [R] the slots that count (the step advances them itself).
+    uniforms [R,T] and temperature [R] are read where acceptance samples."""
+
+    def __init__(self, shape: AttnShape, step: StepShape, device="cuda"):
+        import torch
+        s, R, T = shape, step.n_req, step.n_pos
+        dt = torch.bfloat16 if step.bf16 else torch.float32
+        L, Hq, Hkv, d = s.n_layers, s.n_heads, s.n_kvheads, s.head_dim
+        e = lambda *shp, dtype=dt: torch.empty(shp, dtype=dtype, device=device)
+        z = lambda *shp, dtype=torch.int32: torch.zeros(shp, dtype=dtype, device=device)
+        self.shape = s
+        self.qkv = e(L, R, T, Hq + 2 * Hkv, d)
+        self.q, self.k, self.v = self.qkv.split([Hq, Hkv, Hkv], dim=3)
+        self.q_weight = torch.full((L, d), 1.0 - s.weight_offset, dtype=dt, device=device)
+        self.k_weight = self.q_weight.clone()
+        self.freq = None
+        if s.rotary_dim:
+            i = torch.arange(s.rotary_dim // 2, dtype=torch.float64, device=device)
+            self.freq = s.theta ** (-2.0 * i / s.rotary_dim)
+        self.q_out = e(L, R, T, Hq, d)
+        self.k_out = e(L, R, T, Hkv, d)
+        self.out = e(L, R, T, Hq, d)
+        pages = (L, s.n_pages, Hkv, s.page_size, d)
+        if s.f8_cache:
+            self.k_cache, self.v_cache = (z(*pages, dtype=torch.uint8).view(torch.float8_e4m3fn) for _ in range(2))
+            self.k_scale, self.v_scale = (torch.ones(L, Hkv, device=device) for _ in range(2))
+        else:
+            self.k_cache, self.v_cache = z(*pages, dtype=dt), z(*pages, dtype=dt)
+            self.k_scale = self.v_scale = None
+        self.page_table = z(R, s.table_len)
+        self.seq_len = z(R)
+        # Refused requests, one row per call (its first word counts): attention
+        # layers 0..L-1, then acceptance, then the append.
+        self.status = z(L + 2, 4)
+        self.uniforms = z(R, T, dtype=torch.float32)
+        self.token_prob = z(R, T, dtype=torch.float32)
+        self.temperature = torch.ones(R, device=device)
+        nbytes = max(attn_verify_span_workspace_bytes(R, T, Hq, Hkv, d),
+                     accept_sample_workspace_bytes(R, T, step.vocab) if step.vocab else 0)
+        self.workspace = e(max(16, nbytes), dtype=torch.uint8)   # one stream: the calls take turns
+
+
+class HybridVerifyStep(FusedVerifyStep):
+    """FusedVerifyStep of a model whose GDN layers alternate with attention
+    layers. After GDN layer ``after[i]`` comes attention layer i: norm and
+    rotation of its projection, then attention of the span over the layer's
+    pages and the draft's own paths. Behind acceptance (greedy, or by sampling
+    with ``sample``: ``uniforms`` and ``temperature`` of the AttnBuffers) the
+    accepted rows of all attention layers go into their pages and ``seq_len``
+    advances, so replays of the captured step carry on by themselves.
+    """
+
+    def __init__(self, bufs: StepBuffers, attn: AttnBuffers, parent=None, runs: Optional[Sequence[tuple]] = None,
+                 silu: bool = True, q_scale: float = 1.0, l2_eps: float = 1e-6, sample: bool = False):
+        super().__init__(bufs, parent, runs, silu, q_scale, l2_eps)
+        s, b, n = attn.shape, attn, bufs.shape.n_layers
+        self.attn = attn
+        after = [(i + 1) * n // s.n_layers - 1 for i in range(s.n_layers)] if s.after is None else list(s.after)
+        if len(after) != s.n_layers or any(not 0 <= l < n for l in after) or after != sorted(after):
+            raise ValueError(f"after: {after}, expected {s.n_layers} ascending GDN layers of {n}")
+        scale = lambda t, i: None if t is None else t[i]
+        self.attn_calls: List[list] = [[] for _ in range(n)]
+        for i, l in enumerate(after):
+            self.attn_calls[l] += [
+                qk_norm_rope_call(b.q[i], b.k[i], b.q_weight[i], b.k_weight[i], b.freq, b.seq_len, b.q_out[i],
+                                  b.k_out[i], self._parent, s.eps, s.weight_offset),
+                attn_verify_span_call(b.q_out[i], b.k_out[i], b.v[i], b.k_cache[i], b.v_cache[i], b.page_table,
+                                      b.seq_len, b.out[i], b.workspace, self._parent,
+                                      k_scale=scale(b.k_scale, i), v_scale=scale(b.v_scale, i), status=b.status[i])]
+        self.sample_call = accept_sample_call(
+            bufs.logits, bufs.tokens, b.uniforms, b.token_prob, bufs.accept_node, bufs.accept_len, bufs.path,
+            bufs.bonus, b.workspace, temperature=b.temperature, parent=self._parent,
+            status=b.status[-2]) if sample else None
+        self.append_call = kv_cache_append_call(
+            b.k_out, b.v, b.k_cache, b.v_cache, b.page_table, b.seq_len, bufs.accept_len, b.seq_len, bufs.path,
+            b.k_scale, b.v_scale, b.status[-1])
+
+    def launch_layer(self, l: int, stream: int, events=None) -> None:
+        super().launch_layer(l, stream, events)
+        for call in self.attn_calls[l]:
+            call(stream)
+
+    def launch_accept(self, stream: int) -> None:
+        if self.sample_call is None:
+            super().launch_accept(stream)
+        else:
+            self.sample_call(stream)
+
+    def launch_rollback(self, stream: int) -> None:
+        super().launch_rollback(stream)
+        self.append_call(stream)
