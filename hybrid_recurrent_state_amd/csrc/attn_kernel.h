@@ -63,16 +63,13 @@ template <int N> __device__ __forceinline__ void wait_vm() {
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
 
-// All waves have read what they read before (their reads' results are in
-// registers that they have used) and waited for their own loads.
-__device__ __forceinline__ void read_barrier() {
-  mem_fence();
-  __builtin_amdgcn_s_barrier();
-  mem_fence();
-}
-// All waves' LDS writes before, all reads after.
+// The wave's own LDS reads and writes have ended: what was read may be loaded
+// over.
+__device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+// All waves' LDS reads and writes before, all after; loads to LDS only where
+// each wave has waited for its own.
 __device__ __forceinline__ void block_barrier() {
-  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  wait_lds();
   __builtin_amdgcn_s_barrier();
   mem_fence();
 }
@@ -340,7 +337,7 @@ template <int KIND, int D, int CLS> struct AttnBlock {
   }
 
   // Groups of 16 slots of a started context tile whose page is there.
-  __device__ __forceinline__ uint32_t here(int u) const { return (ring >> ((next - 1 - u) * SB)) & ((1u << SB) - 1); }
+  __device__ __forceinline__ uint32_t here(int u) const { return (ring >> (((next - 1 - u) * SB) & 31)) & ((1u << SB) - 1); }
 
   // Which of a tile's slots that this lane holds count for its row (bit 4 sb
   // + i: slot 16 sb + 4 g + i of the wave group's part).
@@ -689,7 +686,8 @@ template <int KIND, int D, int CLS> struct AttnBlock {
     if constexpr (KIND != kF8) {
       for (int u = i0; u < i1; ++u) {
         wait_tile(next - 1 - u);
-        if (C::WR > 1) read_barrier();
+        if (C::WR > 1) block_barrier();
+        else wait_lds();
         start(i0, i1);
         mem_fence();
         compute(u, lds + C::RING + (static_cast<uint32_t>(u - i0) % C::NST) * C::RAW);
@@ -984,36 +982,36 @@ template <int KIND, int D, int CLS> AttnShape shape_one() {
 
 template <int KIND> AttnShape attn_shape(int d, int cls) {
   switch (d * 4 + cls) {
-    case 256: return shape_one<KIND, 64, 0>();
-    case 257: return shape_one<KIND, 64, 1>();
-    case 258: return shape_one<KIND, 64, 2>();
-    case 259: return shape_one<KIND, 64, 3>();
-    case 512: return shape_one<KIND, 128, 0>();
-    case 513: return shape_one<KIND, 128, 1>();
-    case 514: return shape_one<KIND, 128, 2>();
-    case 515: return shape_one<KIND, 128, 3>();
-    case 1024: return shape_one<KIND, 256, 0>();
-    case 1025: return shape_one<KIND, 256, 1>();
-    case 1026: return shape_one<KIND, 256, 2>();
-    case 1027: return shape_one<KIND, 256, 3>();
+    case 64 * 4 + 0: return shape_one<KIND, 64, 0>();
+    case 64 * 4 + 1: return shape_one<KIND, 64, 1>();
+    case 64 * 4 + 2: return shape_one<KIND, 64, 2>();
+    case 64 * 4 + 3: return shape_one<KIND, 64, 3>();
+    case 128 * 4 + 0: return shape_one<KIND, 128, 0>();
+    case 128 * 4 + 1: return shape_one<KIND, 128, 1>();
+    case 128 * 4 + 2: return shape_one<KIND, 128, 2>();
+    case 128 * 4 + 3: return shape_one<KIND, 128, 3>();
+    case 256 * 4 + 0: return shape_one<KIND, 256, 0>();
+    case 256 * 4 + 1: return shape_one<KIND, 256, 1>();
+    case 256 * 4 + 2: return shape_one<KIND, 256, 2>();
+    case 256 * 4 + 3: return shape_one<KIND, 256, 3>();
     default: return {0, 0, 0};
   }
 }
 
 template <int KIND> void attn_launch(const AttnArgs& args, int d, int cls, hipStream_t s) {
   switch (d * 4 + cls) {
-    case 256: return launch_one<KIND, 64, 0>(args, s);
-    case 257: return launch_one<KIND, 64, 1>(args, s);
-    case 258: return launch_one<KIND, 64, 2>(args, s);
-    case 259: return launch_one<KIND, 64, 3>(args, s);
-    case 512: return launch_one<KIND, 128, 0>(args, s);
-    case 513: return launch_one<KIND, 128, 1>(args, s);
-    case 514: return launch_one<KIND, 128, 2>(args, s);
-    case 515: return launch_one<KIND, 128, 3>(args, s);
-    case 1024: return launch_one<KIND, 256, 0>(args, s);
-    case 1025: return launch_one<KIND, 256, 1>(args, s);
-    case 1026: return launch_one<KIND, 256, 2>(args, s);
-    case 1027: return launch_one<KIND, 256, 3>(args, s);
+    case 64 * 4 + 0: return launch_one<KIND, 64, 0>(args, s);
+    case 64 * 4 + 1: return launch_one<KIND, 64, 1>(args, s);
+    case 64 * 4 + 2: return launch_one<KIND, 64, 2>(args, s);
+    case 64 * 4 + 3: return launch_one<KIND, 64, 3>(args, s);
+    case 128 * 4 + 0: return launch_one<KIND, 128, 0>(args, s);
+    case 128 * 4 + 1: return launch_one<KIND, 128, 1>(args, s);
+    case 128 * 4 + 2: return launch_one<KIND, 128, 2>(args, s);
+    case 128 * 4 + 3: return launch_one<KIND, 128, 3>(args, s);
+    case 256 * 4 + 0: return launch_one<KIND, 256, 0>(args, s);
+    case 256 * 4 + 1: return launch_one<KIND, 256, 1>(args, s);
+    case 256 * 4 + 2: return launch_one<KIND, 256, 2>(args, s);
+    case 256 * 4 + 3: return launch_one<KIND, 256, 3>(args, s);
   }
 }
 

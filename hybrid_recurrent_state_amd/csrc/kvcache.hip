@@ -161,7 +161,7 @@ __global__ __launch_bounds__(kThreads) void append_kernel(const AppendArgs args)
       x[b] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(src) + piece);
       if constexpr (F8) {
         const float* sc = is_v ? args.v_scale : args.k_scale;
-        scale[b] = sc ? sc[layer * heads + h] : 1.0f;
+        scale[b] = sc ? sc[static_cast<int64_t>(layer) * heads + h] : 1.0f;
       }
       const int slot = len + i0 + row;
       const int64_t at = ((static_cast<int64_t>(layer) * args.n_pages + pg) * heads + h) * (page_mask + 1) +

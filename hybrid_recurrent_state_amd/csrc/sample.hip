@@ -83,9 +83,6 @@ __device__ __forceinline__ float temperature_of(const SampleArgs& a, int r) {
 }
 __device__ __forceinline__ bool bad_temperature(float tau) { return !(tau >= 0.0f); }
 
-// Weight of a logit beside the maximum m: e^((z - m) / tau). Hard rows
-// (temperature 0, or +inf logits) give the largest logits one, the rest zero;
-// NaN has none, and neither has anything where there is no maximum.
 // e^x for x <= 0: x = n ln 2 + r with |r| <= ln 2 / 2, the power series of
 // e^r to r^12 (what is left out is below 2e-16 of it), n into the exponent.
 // About half the operations of the general function.
@@ -110,6 +107,9 @@ __device__ __forceinline__ double exp_down(double x) {
   return ldexp(y, static_cast<int>(n));
 }
 
+// Weight of a logit beside the maximum m: e^((z - m) / tau). Hard rows
+// (temperature 0, or +inf logits) give the largest logits one, the rest zero;
+// NaN has none, and neither has anything where there is no maximum.
 struct Weigher {
   double m, inv;
   bool hard, none;

@@ -211,6 +211,14 @@ GRID = [
     (1, 1, 8, 2, 128, 64, [20000], "bf16", "bf16", False, 0),
     (1, 4, 8, 2, 128, 64, [9001], "bf16", "f8", False, 2048),
     (1, 2, 4, 2, 64, 32, [6007], "f32", "f32", False, 0),
+    (2, 17, 8, 2, 128, 16, [517, 40], "bf16", "f8", False, 0),
+    (1, 20, 4, 1, 128, 64, [1500], "bf16", "f8", True, 77),
+    (3, 11, 6, 1, 64, 32, [0, 64, 799], "bf16", "f8", True, 0),
+    (1, 64, 6, 6, 256, 16, [300], "f32", "f32", True, 0),
+    (1, 29, 4, 2, 256, 64, [1100], "bf16", "f8", False, 500),
+    (1, 8, 12, 2, 128, 16, [222], "bf16", "f8", True, 0),
+    (1, 12, 2, 1, 256, 32, [130], "f32", "f32", False, 9),
+    (1, 64, 16, 1, 256, 16, [120], "bf16", "bf16", True, 0),
 ]
 
 
