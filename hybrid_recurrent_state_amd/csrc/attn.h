@@ -58,24 +58,23 @@ template <int KIND, int D, int CLS> struct AttnCfg {
   static constexpr int ESZ = KIND == kF32 ? 4 : 2;          // bytes of an element in LDS
   static constexpr int ESZC = KIND == kF32 ? 4 : KIND == kB16 ? 2 : 1;   // of a cached one
   static constexpr bool WIDE = D == 256;
-  static constexpr int RT = CLS == 0 || (CLS == 3 && WIDE) ? 1 : 2;
-  static constexpr int WR = CLS < 2 ? 1 : CLS == 2 ? 2 : WIDE ? 8 : 4;
-  static constexpr int WK = CLS < 2 ? (WIDE ? 2 : 4) : CLS == 2 ? 2 : 1;
-  static constexpr int SS = CLS < 2 ? 16 : CLS == 2 ? (WIDE ? 16 : 32) : (KIND == kF32 && D == 128 ? 16 : 32);
+  static constexpr int RT = CLS == 4 ? 3 : CLS < 3 || WIDE ? 1 : 2;
+  static constexpr int WR = CLS == 0 ? 1 : CLS == 1 || CLS == 4 ? 2 : CLS == 2 || !WIDE ? 4 : 8;
+  static constexpr int WK = CLS < 2 ? (WIDE ? 2 : 4) : CLS == 2 || CLS == 4 ? 2 : 1;
+  static constexpr int SS = CLS == 0 ? 16 : CLS == 1 ? (D * ESZC <= 128 ? 32 : 16) : CLS == 2 ? (WIDE ? 16 : 32) : (KIND == kF32 && D == 128 ? 16 : 32);
   // Blocks of a CU: two where they fit (their waits and sums overlap).
-  static constexpr int PER_CU = CLS == 3 && !WIDE ? 2 : 1;
+  static constexpr int PER_CU = CLS >= 3 && !WIDE ? 2 : 1;
   static constexpr int NW = WR * WK;
   static constexpr int NT = 64 * NW;
   static constexpr int ROWS = 16 * RT * WR;
   static constexpr int TS = SS * WK;                        // slots of a tile
-  static constexpr int STAGE = 2 * TS * D * ESZ;            // keys and values of a tile, in the products' type
-  static constexpr int NB = KIND == kF8 && WR > 1 ? 2 : 1;  // converted tiles (e4m3)
-  static constexpr int RAW = KIND == kF8 ? STAGE / 2 : STAGE;
-  static constexpr int ROOM = 131072 / PER_CU - (KIND == kF8 ? NB * STAGE : 0);
-  static constexpr int NST = ROOM / RAW < 4 ? ROOM / RAW : 4;   // tiles on their way
-  static constexpr int RING = KIND == kF8 ? NB * STAGE : 0;     // where the ring of loaded tiles starts
+  static constexpr int STAGE = 2 * TS * D * ESZ;            // keys and values of a tile, in the span's type
+  static constexpr int RAW = 2 * TS * D * ESZC;             // in the cache's
+  static constexpr int ROOM = 131072 / PER_CU;
+  static constexpr int NST = ROOM / RAW < 3 ? ROOM / RAW : 3;   // tiles on their way
   static constexpr int JOIN = WK / 2 * WR * RT * 64 * (D + 8);   // sums of half the wave groups
-  static constexpr int LDS = RING + NST * RAW > JOIN ? RING + NST * RAW : JOIN;
+  static constexpr int TILES = NST * RAW > STAGE ? NST * RAW : STAGE;   // an e4m3 cache's span tiles take the ring's place
+  static constexpr int LDS = TILES > JOIN ? TILES : JOIN;
   static_assert(NST >= 2 && LDS <= 155 * 1024 / PER_CU, "tiles fit");
 };
 

@@ -154,10 +154,13 @@ bool sizes_ok(const hrs_attn_desc* d) {
          d->n_heads / d->n_kvheads <= 64;
 }
 
-int rows_class(int rows) { return rows <= 16 ? 0 : rows <= 32 ? 1 : rows <= 64 ? 2 : 3; }
+int rows_class(int kind, int d, int rows) {
+  if (kind == kF8 && d <= 128 && rows > 64 && rows <= 96) return 4;
+  return rows <= 16 ? 0 : rows <= 32 ? 1 : rows <= 64 ? 2 : 3;
+}
 
 AttnShape shape_of(const hrs_attn_desc* d, int kind) {
-  const int cls = rows_class(d->n_pos * (d->n_heads / d->n_kvheads));
+  const int cls = rows_class(kind, d->d, d->n_pos * (d->n_heads / d->n_kvheads));
   return kind == kF32 ? attn_shape<kF32>(d->d, cls) : kind == kB16 ? attn_shape<kB16>(d->d, cls)
                                                                    : attn_shape<kF8>(d->d, cls);
 }
@@ -233,7 +236,7 @@ extern "C" int attn_verify_span(const hrs_attn_desc* d, const void* q, const voi
   const int per_launch =
       static_cast<int>(std::min<int64_t>(args.tree ? std::min(kAttnReqs, std::max(1, kGeomBytes / d->n_pos)) : kAttnReqs,
                                          INT32_MAX / most));
-  const int cls = rows_class(args.rows);
+  const int cls = rows_class(kind, d->d, args.rows);
   const hipStream_t s = static_cast<hipStream_t>(stream);
   (void)hipGetLastError();
   for (int r0 = 0; r0 < d->n_req; r0 += per_launch) {

@@ -99,8 +99,8 @@ __device__ __forceinline__ float row_sum(float x) {
 // Where piece c of a tile row lies: pieces are exchanged within groups of 16
 // (8 in a 128-byte row) so that equal pieces of 16 rows, and pairs of pieces
 // of 4 consecutive rows, are in different banks.
-template <int CPR> __device__ __forceinline__ int swizzle(int row) {
-  return CPR >= 16 ? ((row & 7) << 1) | ((row >> 3) & 1) : (((row >> 1) & 3) << 1) | ((row >> 3) & 1);
+template <int CPR> __device__ __forceinline__ uint32_t swizzle(uint32_t row) {
+  return CPR == 4 ? (row >> 2) & 3 : CPR >= 16 ? ((row & 7) << 1) | ((row >> 3) & 1) : (((row >> 1) & 3) << 1) | ((row >> 3) & 1);
 }
 
 __device__ __forceinline__ bool not_finite(float x) { return (__float_as_uint(x) & 0x7F800000u) == 0x7F800000u; }
@@ -154,6 +154,10 @@ template <int KIND, int D, int CLS> struct AttnBlock {
   // Slot of tile u where this wave group starts.
   __device__ __forceinline__ int slot0(int u) const { return (un.first + u) * C::TS + kg * C::SS; }
 
+  // In a scalar register: the compiler keeps some uniform numbers in vector
+  // ones, with the arithmetic on them.
+  static __device__ __forceinline__ uint32_t uniform_int(uint32_t x) { return __builtin_amdgcn_readfirstlane(x); }
+
   // Page numbers of context tile u: scalar loads, nothing waits for them here.
   __device__ __forceinline__ void fetch_pages(int u) {
     typedef const __attribute__((address_space(4))) int32_t* cptr;
@@ -176,7 +180,7 @@ template <int KIND, int D, int CLS> struct AttnBlock {
       const bool ok = static_cast<uint32_t>(pg[i]) < static_cast<uint32_t>(a.n_pages) && slot0(u) + 16 * i < len;
       there |= ok ? 1u << i : 0u;
       const uint32_t in_page = ((slot0(u) >> 4) + i) & ((1u << (a.page_shift - 4)) - 1);
-      const uint32_t group = (ok ? pg[i] : 0) * head_groups + h_groups + in_page;
+      const uint32_t group = uniform_int((ok ? pg[i] : 0) * uniform_int(head_groups) + uniform_int(h_groups) + in_page);
       at[i] = static_cast<int64_t>(group) * (16 * D * CSZ);
     }
     return there;
@@ -184,12 +188,13 @@ template <int KIND, int D, int CLS> struct AttnBlock {
 
   // Starts the loads of tile u into its place of the ring.
   __device__ __forceinline__ void issue(int u, int i_ring) {
-    char* const dst = lds + C::RING + i_ring * C::RAW + kg * (C::RAW / C::WK);
+    char* const dst = lds + i_ring * C::RAW + kg * (C::RAW / C::WK);
     const bool span = u >= un.ctx;
     if (!span) {
       int64_t at[SB];
-      ring = ring << SB | page_rows(u, at);
+      ring = uniform_int(ring << SB | page_rows(u, at));
       constexpr int kRows = 64 * C::WR / RCPR;              // rows that one load of all the group's waves covers
+      const uint32_t row_l = wr * (64 / RCPR) + static_cast<uint32_t>(lane) / RCPR;   // the lane's among them
 #pragma unroll
       for (int i = 0; i < LPS; ++i) {
         const int p0 = (i * C::WR + wr) * 64;               // first piece of this load
@@ -201,10 +206,8 @@ template <int KIND, int D, int CLS> struct AttnBlock {
 #pragma unroll
         for (int x = 1; x < SB; ++x) off64 = grp == x ? at[x] : off64;
         const char* const base = (is_v ? a.v_cache : a.k_cache) + off64;
-        const int p = p0 + lane;
-        const int row = p / RCPR;
-        int c = p % RCPR;
-        if constexpr (KIND != kF8) c ^= swizzle<CPR>(row);
+        const uint32_t row = i * kRows + row_l;
+        const uint32_t c = (static_cast<uint32_t>(lane) % RCPR) ^ swizzle<RCPR>(row);
         const uint32_t off = (row & 15) * (D * CSZ) + c * 16;
         __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(base + off),
                                          (__attribute__((address_space(3))) void*)(dst + p0 * 16), 16, 0, 0);
@@ -234,39 +237,15 @@ template <int KIND, int D, int CLS> struct AttnBlock {
     return static_cast<const char*>(is_v ? a.v : a.k) + at * ESZ + c * 16;
   }
 
-  // e4m3: the wave's own pieces of a loaded tile (or of the span) to the tile
-  // that the products read.
-  __device__ __forceinline__ void widen_tile(int u, int i_ring, int i_buf) {
-    char* const dst = lds + i_buf * C::STAGE + kg * (C::STAGE / C::WK);
-    if (u >= un.ctx) {
+  // e4m3 caches: the wave's part of a span tile, which is of the span's type,
+  // to the start of the ring.
+  __device__ __forceinline__ void issue_span(int u) {
+    char* const dst = lds + kg * (C::STAGE / C::WK);
 #pragma unroll
-      for (int i = 0; i < SPS; ++i) {
-        const int p = (i * C::WR + wr) * 64 + lane;
-        *reinterpret_cast<u32x4*>(dst + p * 16) = *reinterpret_cast<const u32x4*>(span_piece(u, p));
-      }
-      // Not shared with the end of the other branch: its last store would wait
-      // for these loads, and with them for the tiles on their way.
-      asm volatile("; span rows" ::: "memory");
-      return;
-    }
-    const char* const src = lds + C::RING + i_ring * C::RAW + kg * (C::RAW / C::WK);
-#pragma unroll
-    for (int i = 0; i < LPS; ++i) {
-      const int p = (i * C::WR + wr) * 64 + lane;
-      const u32x4 w = *reinterpret_cast<const u32x4*>(src + p * 16);
-      const int row = p / RCPR, c8 = p % RCPR;
-      const int f = swizzle<CPR>(row);
-      u32x4 lo, hi;
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        lo[2 * x] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[x], 1.0f, false));
-        lo[2 * x + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[x], 1.0f, true));
-        hi[2 * x] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[2 + x], 1.0f, false));
-        hi[2 * x + 1] =
-            __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[2 + x], 1.0f, true));
-      }
-      *reinterpret_cast<u32x4*>(dst + (row * CPR + ((2 * c8) ^ f)) * 16) = lo;
-      *reinterpret_cast<u32x4*>(dst + (row * CPR + ((2 * c8 + 1) ^ f)) * 16) = hi;
+    for (int i = 0; i < SPS; ++i) {
+      const int p0 = (i * C::WR + wr) * 64;
+      __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)span_piece(u, p0 + lane),
+                                       (__attribute__((address_space(3))) void*)(dst + p0 * 16), 16, 0, 0);
     }
   }
 
@@ -286,7 +265,7 @@ template <int KIND, int D, int CLS> struct AttnBlock {
 #pragma unroll
       for (int c = 0; c < QC; ++c) {
         q[rt][c] = u32x4{};
-        if (on) q[rt][c] = *reinterpret_cast<const u32x4*>(src + (4 * c + g) * 16);
+        if (on) q[rt][c] = *reinterpret_cast<const u32x4*>(src + (step_piece(c) + (KIND == kF8 ? 2 * g : g)) * 16);
       }
       m[rt] = -__builtin_inff();
       l[rt] = 0.0f;
@@ -366,41 +345,58 @@ template <int KIND, int D, int CLS> struct AttnBlock {
     return bits;
   }
 
-  // One tile: its scores, weights and the product with the values.
-  __device__ __forceinline__ void tile(int u, const char* base, bool span, bool mask, uint32_t there) {
-    const char* const kt = base + kg * (C::STAGE / C::WK);
-    const char* const vt = kt + C::SS * D * ESZ;
+  // Piece of a row (of the span's type) that lane group 0 takes in step c of
+  // the products; group g's is g on, or 2 g with an e4m3 cache, where one
+  // 16-byte read holds the keys' elements of two steps.
+  static __device__ __forceinline__ constexpr int step_piece(int c) {
+    return KIND == kF8 ? 8 * (c >> 1) + (c & 1) : 4 * c;
+  }
+
+  // One tile: its scores, weights and the product with the values. F8: the
+  // tile is e4m3, widened to bf16 (exactly) on the way to the products.
+  template <bool F8> __device__ __forceinline__ void tile(int u, const char* base, bool span, bool mask, uint32_t there) {
+    constexpr int EB = F8 ? 1 : ESZ, ROW = D * EB, PIECES = ROW / 16;
+    constexpr bool kRare = KIND == kF8 && !F8;       // a span tile after the loop over the cache's
+    constexpr bool kFew = kRare || (F8 && C::RT > 2);
+    const int lane = kFew ? fresh(this->lane) : this->lane, n16 = lane & 15, g = lane >> 4;
+    const char* const kt = base + kg * (2 * C::SS * ROW);
+    const char* const vt = kt + C::SS * ROW;
     f32x4 s[C::RT][SB];
 #pragma unroll
     for (int rt = 0; rt < C::RT; ++rt)
 #pragma unroll
       for (int sb = 0; sb < SB; ++sb) s[rt][sb] = f32x4{};
-    // Piece 4 c + g of row n16, permuted: the permutation is an exclusive or
-    // of address bits, so the pieces are one address apart from constants.
-    const uint32_t ka = lds_address(kt) + n16 * (D * ESZ) + ((g ^ swizzle<CPR>(n16)) << 4);
-    u32x4 kk[QC][SB];
+    // The lane's piece of row n16 in step 0, permuted: the permutation is an
+    // exclusive or of address bits, so the steps' pieces are one address apart
+    // from constants.
+    const uint32_t ka = lds_address(kt) + n16 * ROW + (((kRare ? 2 * g : g) ^ swizzle<PIECES>(n16)) << 4);
+    u32x4 kk[F8 ? QC / 2 : QC][SB];
+#pragma unroll
+    for (int c = 0; c < (F8 ? QC / 2 : QC); ++c)
+#pragma unroll
+      for (int sb = 0; sb < SB; ++sb) kk[c][sb] = *lds_at<u32x4>((ka ^ ((F8 ? 4 * c : step_piece(c)) << 4)) + sb * 16 * ROW);
 #pragma unroll
     for (int c = 0; c < QC; ++c)
 #pragma unroll
-      for (int sb = 0; sb < SB; ++sb) kk[c][sb] = *lds_at<u32x4>((ka ^ (c << 6)) + sb * 16 * D * ESZ);
-#pragma unroll
-    for (int c = 0; c < QC; ++c)
-#pragma unroll
-      for (int sb = 0; sb < SB; ++sb)
+      for (int sb = 0; sb < SB; ++sb) {
+        u32x4 k;
+        if constexpr (F8) k = widen8(kk[c / 2][sb][2 * (c & 1)], kk[c / 2][sb][2 * (c & 1) + 1]);
+        else k = kk[c][sb];
 #pragma unroll
         for (int rt = 0; rt < C::RT; ++rt) {
           if constexpr (KIND == kF32) {
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              s[rt][sb] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(kk[c][sb][e]),
-                                                               __uint_as_float(q[rt][c][e]), s[rt][sb], 0, 0, 0);
+              s[rt][sb] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(k[e]), __uint_as_float(q[rt][c][e]),
+                                                               s[rt][sb], 0, 0, 0);
           } else {
-            s[rt][sb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, kk[c][sb]),
+            s[rt][sb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, k),
                                                                 __builtin_bit_cast(bf16x8, q[rt][c]), s[rt][sb], 0, 0, 0);
           }
         }
+      }
     // The values' reads go out before the weights are formed.
-    Values v;
+    Values<F8> v;
     if constexpr (KIND != kF32) v.load(vt, n16, g, 0);
     // c S - m is one operation on the raw products; c is positive (a negative
     // one turns the products' sign).
@@ -458,7 +454,6 @@ template <int KIND, int D, int CLS> struct AttnBlock {
         for (int i = 0; i < 4; ++i) {
           float p = __builtin_amdgcn_exp2f(fmaf(s[rt][sb][i], c, -mb));
           sum += p;
-          if (KIND == kF8) p *= span ? 1.0f : vs;
           s[rt][sb][i] = p;
         }
         if constexpr (KIND != kF32)
@@ -470,41 +465,58 @@ template <int KIND, int D, int CLS> struct AttnBlock {
       values_f32(vt, s, mask);
     } else {
 #pragma unroll
-      for (int half = 0; half < Values::HALVES; ++half) {
+      for (int half = 0; half < kHalves; ++half) {
         if (half > 0) v.load(vt, n16, g, half);
         if (mask) odd_seen = __any(v.drop_odd()) || odd_seen;
-        values_bf16(v, half, pb);
+        values_bf16<F8>(v, half, pb);
       }
     }
   }
 
+  // Eight e4m3 numbers as bf16.
+  static __device__ __forceinline__ uint32_t widen2(uint32_t w, bool high) {
+    return __builtin_bit_cast(uint32_t, high ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, true)
+                                             : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, false));
+  }
+  static __device__ __forceinline__ u32x4 widen8(uint32_t a, uint32_t b) {
+    return u32x4{widen2(a, false), widen2(a, true), widen2(b, false), widen2(b, true)};
+  }
+
   // The values of a tile (or of 128 of its 256 columns) as a lane reads them:
-  // EPL consecutive elements, from EPL n16 on, of the slots 4 g + j and 16 + 4
-  // g + j. Element x of all of them is the lane's part of V^T for the columns
-  // EPL r + x, r = 0 .. 15: the lane's rows turned into columns by one byte
-  // permutation per word. (The transposing LDS read gives the same without
-  // the permutations, but the compiler waits for every load to LDS on its way
-  // ahead of it, and in assembly it has to be waited for on the spot.)
-  struct Values {
-    static constexpr int EPL = D >= 128 ? 8 : 4;
-    static constexpr int HALVES = D / (16 * EPL);
-    uint32_t w[SB][4][EPL / 2];
+  // kCols consecutive elements, from kCols n16 on, of the slots 4 g + j and 16
+  // + 4 g + j. Element x of all of them is the lane's part of V^T for the
+  // columns kCols r + x, r = 0 .. 15: the lane's rows turned into columns by
+  // byte permutations (one a word of bf16; of e4m3 one for two columns of two
+  // rows, which the widening takes apart). (The transposing LDS read gives the
+  // same without the permutations, but the compiler waits for every load to
+  // LDS on its way ahead of it, and in assembly it has to be waited for on the
+  // spot.)
+  static constexpr int kCols = D >= 128 ? 8 : 4;
+  static constexpr int kHalves = D / (16 * kCols);
+  template <bool F8> struct Values {
+    static constexpr int EB = F8 ? 1 : 2, ROW = D * EB;
+    static constexpr int RUN = kCols * EB;                  // bytes of a read
+    static constexpr int WORDS = RUN / 4;
+    uint32_t w[SB][4][WORDS];
     __device__ __forceinline__ void load(const char* vt, int n16, int g, int half) {
 #pragma unroll
       for (int sb = 0; sb < SB; ++sb)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const int row = 4 * g + j;       // 16 rows on: the same permutation
-          if constexpr (EPL == 8) {
-            const uint32_t at = lds_address(vt) + row * (D * 2) + ((n16 ^ swizzle<CPR>(row)) << 4);
-            const u32x4 x = *lds_at<u32x4>(at + half * 256 + sb * 16 * D * 2);
+          const int byte = half * (16 * RUN) + n16 * RUN;
+          const uint32_t at = lds_address(vt) + row * ROW + (((byte >> 4) ^ swizzle<ROW / 16>(row)) << 4) + (byte & 15) +
+                              sb * 16 * ROW;
+          if constexpr (WORDS == 4) {
+            const u32x4 x = *lds_at<u32x4>(at);
 #pragma unroll
             for (int e = 0; e < 4; ++e) w[sb][j][e] = x[e];
-          } else {
-            const uint32_t at = lds_address(vt) + row * (D * 2) + (((n16 >> 1) ^ swizzle<CPR>(row)) << 4) + (n16 & 1) * 8;
-            const u32x2 x = *lds_at<u32x2>(at + sb * 16 * D * 2);
+          } else if constexpr (WORDS == 2) {
+            const u32x2 x = *lds_at<u32x2>(at);
 #pragma unroll
             for (int e = 0; e < 2; ++e) w[sb][j][e] = x[e];
+          } else {
+            w[sb][j][0] = *lds_at<uint32_t>(at);
           }
         }
     }
@@ -517,32 +529,43 @@ template <int KIND, int D, int CLS> struct AttnBlock {
 #pragma unroll
         for (int j = 0; j < 4; ++j)
 #pragma unroll
-          for (int e = 0; e < EPL / 2; ++e) {
+          for (int e = 0; e < WORDS; ++e) {
             const uint32_t y = w[sb][j][e];
-            w[sb][j][e] = ((y & 0x7F80u) == 0x7F80u ? 0u : y & 0xFFFFu) |
-                          ((y & 0x7F800000u) == 0x7F800000u ? 0u : y & 0xFFFF0000u);
+            if constexpr (F8) {
+              const uint32_t odd = ((y & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;   // 0x7F with either sign
+              w[sb][j][e] = y & ~(odd | (odd - (odd >> 7)));
+            } else {
+              w[sb][j][e] = ((y & 0x7F80u) == 0x7F80u ? 0u : y & 0xFFFFu) |
+                            ((y & 0x7F800000u) == 0x7F800000u ? 0u : y & 0xFFFF0000u);
+            }
             dropped |= w[sb][j][e] ^ y;
           }
       return dropped != 0;
     }
     // Words 2 sb and 2 sb + 1 of the operand for element x.
     __device__ __forceinline__ u32x2 operand(int sb, int x) const {
-      const uint32_t sel = x & 1 ? 0x07060302u : 0x05040100u;
-      return u32x2{__builtin_amdgcn_perm(w[sb][1][x >> 1], w[sb][0][x >> 1], sel),
-                   __builtin_amdgcn_perm(w[sb][3][x >> 1], w[sb][2][x >> 1], sel)};
+      if constexpr (F8) {
+        const uint32_t sel = x & 2 ? 0x07030602u : 0x05010400u;
+        return u32x2{widen2(__builtin_amdgcn_perm(w[sb][1][x >> 2], w[sb][0][x >> 2], sel), x & 1),
+                     widen2(__builtin_amdgcn_perm(w[sb][3][x >> 2], w[sb][2][x >> 2], sel), x & 1)};
+      } else {
+        const uint32_t sel = x & 1 ? 0x07060302u : 0x05040100u;
+        return u32x2{__builtin_amdgcn_perm(w[sb][1][x >> 1], w[sb][0][x >> 1], sel),
+                     __builtin_amdgcn_perm(w[sb][3][x >> 1], w[sb][2][x >> 1], sel)};
+      }
     }
   };
 
   // O^T += V^T P^T.
-  __device__ __forceinline__ void values_bf16(const Values& v, int half, const u32x2 (&pb)[C::RT][SB]) {
+  template <bool F8> __device__ __forceinline__ void values_bf16(const Values<F8>& v, int half, const u32x2 (&pb)[C::RT][SB]) {
 #pragma unroll
-    for (int x = 0; x < Values::EPL; ++x) {
+    for (int x = 0; x < kCols; ++x) {
       u32x2 w[SB];
 #pragma unroll
       for (int sb = 0; sb < SB; ++sb) w[sb] = v.operand(sb, x);
 #pragma unroll
       for (int rt = 0; rt < C::RT; ++rt) {
-        f32x4& acc = o[rt][half * Values::EPL + x];
+        f32x4& acc = o[rt][half * kCols + x];
         acc = product(w, pb[rt], acc);
       }
     }
@@ -649,11 +672,12 @@ template <int KIND, int D, int CLS> struct AttnBlock {
     return j0 + C::SS > len || (a.window > 0 && j0 <= len + a.n_pos - 1 - a.window) || there != (1u << SB) - 1;
   }
 
+  // Tile u of the ring (an e4m3 cache's span tiles do not pass through it).
   __device__ __forceinline__ void compute(int u, const char* base) {
     if (idle) return;
-    const bool span = u >= un.ctx;
+    const bool span = KIND != kF8 && u >= un.ctx;
     const uint32_t there = here(u);
-    tile(u, base, span, span || masked(u, there), there);
+    tile<KIND == kF8>(u, base, span, span || masked(u, there), there);
   }
 
   // Waits for a tile of this wave's loads with `after` later tiles on their way.
@@ -677,45 +701,33 @@ template <int KIND, int D, int CLS> struct AttnBlock {
   __device__ __forceinline__ void start_ring(int i0, int i1) {
     ring = 0;
     next = i0;
-    for (int x = 0; x < (KIND == kF8 ? C::NST : C::NST - 1); ++x) start(i0, i1);
+    for (int x = 0; x < C::NST - 1; ++x) start(i0, i1);
   }
 
   // Units [i0, i1) of the segment; the ring was started.
   __device__ __forceinline__ void run(int i0, int i1) {
     const int loaded = KIND == kF8 ? min(i1, un.ctx) : i1;
-    if constexpr (KIND != kF8) {
-      for (int u = i0; u < i1; ++u) {
-        wait_tile(next - 1 - u);
-        if (C::WR > 1) block_barrier();
-        else wait_lds();
-        start(i0, i1);
-        mem_fence();
-        compute(u, lds + C::RING + (static_cast<uint32_t>(u - i0) % C::NST) * C::RAW);
-        mem_fence();
-      }
-    } else {
-      auto convert = [&](int u) {
-        if (u < loaded) wait_tile(next - 1 - u);
-        widen_tile(u, static_cast<uint32_t>(u - i0) % C::NST, C::NB == 2 ? (u - i0) & 1 : 0);
-        // The raw pieces are in registers (they were converted) before their
-        // place is loaded again.
-        mem_fence();
-        start(i0, i1);
-        mem_fence();
-      };
-      if (C::NB == 2) {
-        convert(i0);
-        for (int u = i0; u < i1; ++u) {
-          block_barrier();
-          if (u + 1 < i1) convert(u + 1);
-          compute(u, lds + ((u - i0) & 1) * C::STAGE);
-        }
-      } else {
-        for (int u = i0; u < i1; ++u) {
-          convert(u);
-          compute(u, lds);
-          mem_fence();
-        }
+    for (int u = i0; u < loaded; ++u) {
+      wait_tile(next - 1 - u);
+      if (C::WR > 1) block_barrier();
+      else wait_lds();
+      start(i0, i1);
+      mem_fence();
+      compute(u, lds + (static_cast<uint32_t>(u - i0) % C::NST) * C::RAW);
+      mem_fence();
+    }
+    if constexpr (KIND == kF8) {
+      // The values' scale, once for all tiles of the cache.
+#pragma unroll
+      for (int rt = 0; rt < C::RT; ++rt)
+#pragma unroll
+        for (int dt = 0; dt < DT; ++dt) o[rt][dt] *= vs;
+      for (int u = max(i0, un.ctx); u < i1; ++u) {
+        block_barrier();
+        issue_span(u);
+        wait_vm<0>();
+        block_barrier();
+        if (!idle) tile<false>(u, lds, true, true, 0);
       }
     }
   }
@@ -796,9 +808,9 @@ template <int KIND, int D, int CLS> struct AttnBlock {
   }
 
   // A lane's sums by runs of consecutive columns: float32 holds columns 16 j +
-  // 4 g + e in one register group, bf16 columns 16 EPL half + EPL (4 g + i) +
-  // e in element i of EPL of them (j = 4 half + i).
-  static constexpr int kRun = KIND == kF32 ? 4 : Values::EPL;
+  // 4 g + e in one register group, bf16 columns 16 kRun half + kRun (4 g + i) +
+  // e in element i of kRun of them (j = 4 half + i).
+  static constexpr int kRun = KIND == kF32 ? 4 : kCols;
   static __device__ __forceinline__ float run_at(const f32x4 (&sum)[DT], int j, int e) {
     return KIND == kF32 ? sum[j][e] : sum[j / 4 * kRun + e][j % 4];
   }
@@ -981,37 +993,43 @@ template <int KIND, int D, int CLS> AttnShape shape_one() {
 }  // namespace
 
 template <int KIND> AttnShape attn_shape(int d, int cls) {
-  switch (d * 4 + cls) {
-    case 64 * 4 + 0: return shape_one<KIND, 64, 0>();
-    case 64 * 4 + 1: return shape_one<KIND, 64, 1>();
-    case 64 * 4 + 2: return shape_one<KIND, 64, 2>();
-    case 64 * 4 + 3: return shape_one<KIND, 64, 3>();
-    case 128 * 4 + 0: return shape_one<KIND, 128, 0>();
-    case 128 * 4 + 1: return shape_one<KIND, 128, 1>();
-    case 128 * 4 + 2: return shape_one<KIND, 128, 2>();
-    case 128 * 4 + 3: return shape_one<KIND, 128, 3>();
-    case 256 * 4 + 0: return shape_one<KIND, 256, 0>();
-    case 256 * 4 + 1: return shape_one<KIND, 256, 1>();
-    case 256 * 4 + 2: return shape_one<KIND, 256, 2>();
-    case 256 * 4 + 3: return shape_one<KIND, 256, 3>();
-    default: return {0, 0, 0};
+  switch (d * 8 + cls) {
+    case 64 * 8 + 0: return shape_one<KIND, 64, 0>();
+    case 64 * 8 + 1: return shape_one<KIND, 64, 1>();
+    case 64 * 8 + 2: return shape_one<KIND, 64, 2>();
+    case 64 * 8 + 3: return shape_one<KIND, 64, 3>();
+    case 128 * 8 + 0: return shape_one<KIND, 128, 0>();
+    case 128 * 8 + 1: return shape_one<KIND, 128, 1>();
+    case 128 * 8 + 2: return shape_one<KIND, 128, 2>();
+    case 128 * 8 + 3: return shape_one<KIND, 128, 3>();
+    case 256 * 8 + 0: return shape_one<KIND, 256, 0>();
+    case 256 * 8 + 1: return shape_one<KIND, 256, 1>();
+    case 256 * 8 + 2: return shape_one<KIND, 256, 2>();
+    case 256 * 8 + 3: return shape_one<KIND, 256, 3>();
   }
+  if constexpr (KIND == kF8) {
+    if (cls == 4) return d == 64 ? shape_one<KIND, 64, 4>() : shape_one<KIND, 128, 4>();
+  }
+  return {0, 0, 0};
 }
 
 template <int KIND> void attn_launch(const AttnArgs& args, int d, int cls, hipStream_t s) {
-  switch (d * 4 + cls) {
-    case 64 * 4 + 0: return launch_one<KIND, 64, 0>(args, s);
-    case 64 * 4 + 1: return launch_one<KIND, 64, 1>(args, s);
-    case 64 * 4 + 2: return launch_one<KIND, 64, 2>(args, s);
-    case 64 * 4 + 3: return launch_one<KIND, 64, 3>(args, s);
-    case 128 * 4 + 0: return launch_one<KIND, 128, 0>(args, s);
-    case 128 * 4 + 1: return launch_one<KIND, 128, 1>(args, s);
-    case 128 * 4 + 2: return launch_one<KIND, 128, 2>(args, s);
-    case 128 * 4 + 3: return launch_one<KIND, 128, 3>(args, s);
-    case 256 * 4 + 0: return launch_one<KIND, 256, 0>(args, s);
-    case 256 * 4 + 1: return launch_one<KIND, 256, 1>(args, s);
-    case 256 * 4 + 2: return launch_one<KIND, 256, 2>(args, s);
-    case 256 * 4 + 3: return launch_one<KIND, 256, 3>(args, s);
+  switch (d * 8 + cls) {
+    case 64 * 8 + 0: return launch_one<KIND, 64, 0>(args, s);
+    case 64 * 8 + 1: return launch_one<KIND, 64, 1>(args, s);
+    case 64 * 8 + 2: return launch_one<KIND, 64, 2>(args, s);
+    case 64 * 8 + 3: return launch_one<KIND, 64, 3>(args, s);
+    case 128 * 8 + 0: return launch_one<KIND, 128, 0>(args, s);
+    case 128 * 8 + 1: return launch_one<KIND, 128, 1>(args, s);
+    case 128 * 8 + 2: return launch_one<KIND, 128, 2>(args, s);
+    case 128 * 8 + 3: return launch_one<KIND, 128, 3>(args, s);
+    case 256 * 8 + 0: return launch_one<KIND, 256, 0>(args, s);
+    case 256 * 8 + 1: return launch_one<KIND, 256, 1>(args, s);
+    case 256 * 8 + 2: return launch_one<KIND, 256, 2>(args, s);
+    case 256 * 8 + 3: return launch_one<KIND, 256, 3>(args, s);
+  }
+  if constexpr (KIND == kF8) {
+    if (cls == 4) return d == 64 ? launch_one<KIND, 64, 4>(args, s) : launch_one<KIND, 128, 4>(args, s);
   }
 }
 
