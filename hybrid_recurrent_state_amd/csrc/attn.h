@@ -51,9 +51,23 @@ struct AttnArgs {
 };
 
 // How a block is built for a type, a head size and a class of row counts
-// (0: at most 16 rows a key/value head, 1: 32, 2: 64, 3: blocks of 128). WR
-// waves share the slots of a tile with different rows, WK such groups take
-// different slots; a wave holds RT tiles of 16 rows and SS slots of a tile.
+// (0: at most 16 rows a key/value head, 1: 32, 2: 64, 3: blocks of 128, 4:
+// e4m3 caches with 65 to 96 rows of at most 128 elements). WR waves share the
+// slots of a tile with different rows, WK such groups take different slots; a
+// wave holds RT tiles of 16 rows and SS slots of a tile. Measured, one request
+// (time of the whole call):
+//  - 16 rows a wave below 64 rows, more waves instead: 32 rows a wave took 65
+//    instead of 37 us (30 rows, 9000 slots of 4 heads of 256, f32), 39 / 34
+//    (26,758 slots, bf16), 37.6 / 34.3 (48 rows, 30,000 slots of 8 heads of
+//    128, bf16), 34.3 / 30.5 (the same, e4m3).
+//  - class 4: an e4m3 tile is widened by every wave that reads it, so two
+//    waves of 48 rows (160 us at 262,144 slots of 8 heads of 128, 68 rows)
+//    instead of four of 32 (200 us); bf16 is bound by the read either way.
+//  - 32 slots a wave in class 1 where a row is at most 128 bytes (24.7 / 26.5
+//    us, 28 rows, e4m3); 16 for longer ones (34.0 / 35.4 us, bf16).
+//  - four waves with slots of their own in class 0: eight, or 32 slots each,
+//    took 14.5 and 14.8 instead of 13.6 us at 1000 slots of 128 and gained
+//    nothing at 30,000.
 template <int KIND, int D, int CLS> struct AttnCfg {
   static constexpr int ESZ = KIND == kF32 ? 4 : 2;          // bytes of an element in LDS
   static constexpr int ESZC = KIND == kF32 ? 4 : KIND == kB16 ? 2 : 1;   // of a cached one
@@ -61,7 +75,10 @@ template <int KIND, int D, int CLS> struct AttnCfg {
   static constexpr int RT = CLS == 4 ? 3 : CLS < 3 || WIDE ? 1 : 2;
   static constexpr int WR = CLS == 0 ? 1 : CLS == 1 || CLS == 4 ? 2 : CLS == 2 || !WIDE ? 4 : 8;
   static constexpr int WK = CLS < 2 ? (WIDE ? 2 : 4) : CLS == 2 || CLS == 4 ? 2 : 1;
-  static constexpr int SS = CLS == 0 ? 16 : CLS == 1 ? (D * ESZC <= 128 ? 32 : 16) : CLS == 2 ? (WIDE ? 16 : 32) : (KIND == kF32 && D == 128 ? 16 : 32);
+  static constexpr int SS = CLS == 0   ? 16
+                            : CLS == 1 ? (D * ESZC <= 128 ? 32 : 16)
+                            : CLS == 2 ? (WIDE ? 16 : 32)
+                                       : (KIND == kF32 && D == 128 ? 16 : 32);
   // Blocks of a CU: two where they fit (their waits and sums overlap).
   static constexpr int PER_CU = CLS >= 3 && !WIDE ? 2 : 1;
   static constexpr int NW = WR * WK;
@@ -71,7 +88,8 @@ template <int KIND, int D, int CLS> struct AttnCfg {
   static constexpr int STAGE = 2 * TS * D * ESZ;            // keys and values of a tile, in the span's type
   static constexpr int RAW = 2 * TS * D * ESZC;             // in the cache's
   static constexpr int ROOM = 131072 / PER_CU;
-  static constexpr int NST = ROOM / RAW < 3 ? ROOM / RAW : 3;   // tiles on their way
+  // Tiles of the ring; a fourth gained nothing (26,758 slots of 256: 47 / 46 us).
+  static constexpr int NST = ROOM / RAW < 3 ? ROOM / RAW : 3;
   static constexpr int JOIN = WK / 2 * WR * RT * 64 * (D + 8);   // sums of half the wave groups
   static constexpr int TILES = NST * RAW > STAGE ? NST * RAW : STAGE;   // an e4m3 cache's span tiles take the ring's place
   static constexpr int LDS = TILES > JOIN ? TILES : JOIN;

@@ -154,6 +154,7 @@ bool sizes_ok(const hrs_attn_desc* d) {
          d->n_heads / d->n_kvheads <= 64;
 }
 
+// The class of AttnCfg; its comment has both sides of each border.
 int rows_class(int kind, int d, int rows) {
   if (kind == kF8 && d <= 128 && rows > 64 && rows <= 96) return 4;
   return rows <= 16 ? 0 : rows <= 32 ? 1 : rows <= 64 ? 2 : 3;
@@ -174,8 +175,8 @@ using namespace hrs;
 
 extern "C" size_t attn_verify_span_workspace_bytes(const hrs_attn_desc* d) {
   if (!sizes_ok(d) || (d->d != 64 && d->d != 128 && d->d != 256)) return 0;
-  // A block's rows and the number of blocks depend on the sizes alone, not on
-  // the types.
+  // Enough for every type: the blocks depend on the sizes alone, and a class
+  // of one type only has fewer rows.
   const AttnShape sh = shape_of(d, kB16);
   const size_t rows = sh.rows;
   return kPlanBytes + 2 * static_cast<size_t>(sh.blocks) * rows * (static_cast<size_t>(d->d) * sizeof(float) + sizeof(float2));

@@ -6,34 +6,50 @@
 //
 // MI355X design. The rows of a key/value head are all query heads of its
 // group at all span positions (17 positions x 6 heads = 102), so its keys and
-// values are read from memory once for all of them; with few rows the job is
-// bound by that read. Blocks are one per CU. The tiles of all requests and
-// heads form one list that is cut into equal runs, so ragged lengths leave no
-// CU idle and the host needs no lengths; a run that ends inside a head leaves
-// a partial sum (f32) for the join.
+// values are read from memory once for all of them. That read is the bound of
+// every long context; short ones are bound by latency (lengths, page numbers,
+// tiles, the parts' join: four dependent reads and two launches). The tiles of
+// all requests and heads form one list that is cut into equal runs, one per
+// block, so ragged lengths leave no CU idle and the host needs no lengths; a
+// run that ends inside a head leaves a partial sum (f32) for the join.
 //  - Tiles travel from memory to LDS without registers (16 bytes per lane), a
-//    ring of tiles ahead; a wave waits for the loads it issued itself and one
+//    ring of three; a wave waits for the loads it issued itself and one
 //    barrier per tile makes them everybody's (none where a wave has its slots
-//    to itself). Page numbers are read a tile ahead by scalar loads; a page
-//    never ends inside 16 slots, so a load's base address is wave-uniform.
+//    to itself). A compiler-made wait for all loads inside the loop, as for a
+//    spilled register or a transposing LDS read, costs a memory latency per
+//    tile (e4m3, 262,144 slots: 160 vs 195 us for one spilled register).
+//    Page numbers are read a tile ahead by scalar loads; a page never ends
+//    inside 16 slots, so a load's base address is wave-uniform.
 //  - 16-byte pieces are permuted within a row (on the memory side, since the
 //    LDS side of such a load is linear) so that the 16 rows of an operand lie
 //    in different banks.
 //  - The transposed products need no data movement between them: a lane of
 //    S^T holds one query row's scores of four consecutive slots, which is the
 //    layout of P^T as the second operand when the slots of a 32-slot step are
-//    taken in the order 4 g + i, 16 + 4 g + i; V^T in that order is what the
-//    transposing LDS read returns. Row maxima and the rescaling of O are
-//    per-lane numbers.
+//    taken in the order 4 g + i, 16 + 4 g + i; V^T in that order comes from
+//    plain reads of rows and byte permutations (Values). Row maxima and the
+//    rescaling of O are per-lane numbers.
 //  - The reference m moves only when a row's maximum exceeds it by more than
 //    8 (in log2), so most tiles neither reduce across lanes nor rescale; P is
-//    at most 2^8 and l and O are f32, which loses nothing.
-//  - e4m3 tiles are widened to bf16 once per block, from a ring of raw tiles
-//    to the tile that the products read (the scales are factors of c and P).
+//    at most 2^8 and l and O are f32, which loses nothing. P is rounded to the
+//    span's type for the product with V, once, relative to itself.
+//  - e4m3 tiles stay e4m3 in LDS and are widened (exactly) to bf16 between LDS
+//    and the products; the scales are factors of c and of O. (Widened once per
+//    block into a second LDS tile: 215 us instead of 160 at 262,144 slots: the
+//    extra pass and its barrier were not hidden.) The span's own tile is of
+//    the span's type and takes the ring's place after the cache's tiles.
 //  - Tiles with a mask (the span, the context's end, a window's border,
-//    absent pages) take a second form of the tile: scores that do not count
-//    are dropped, and values that are not finite leave the product (0 * NaN)
-//    and are added back for the rows that count them.
+//    absent pages) drop scores that do not count; values that are not finite
+//    leave the product (0 * NaN) and are added after the segment for the rows
+//    that count them (add_odd).
+//
+// Measured (bf16 unless noted, whole call with the join): 1 position, 1000
+// slots of 4 heads of 256: 15 us (main kernel 9.3, join 5.3); chain of 17 over
+// 26,758 slots of 4 heads of 256 (110 MB): 46 us (35 and 8.8); 16 trees of 23
+// over 2000 to 8191 slots of 8 heads of 128: 111 us, 4.4 TB/s; chain of 17
+// over 262,144 e4m3 slots of 8 heads of 128 (537 MB): 160 us, 3.4 TB/s, where
+// the vector units' work per tile (widening, exponentials, permutations) is as
+// long as its read and hides behind it only in part.
 #pragma once
 
 #include "attn.h"

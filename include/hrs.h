@@ -653,8 +653,10 @@ size_t attn_verify_span_workspace_bytes(const hrs_attn_desc* desc);
  * rows of out as they were; status (optional device int32) receives the
  * number of such requests. Calls that may run at the same time need
  * workspaces of their own. Errors: HRS_EINVAL (sizes, dtype combination,
- * R > 4096, Hq / Hkv > 64), HRS_EALIGN, HRS_EGEOMETRY, HRS_EUNSUPPORTED
- * (d), HRS_EDEVICE.
+ * R > 4096, Hkv > 1024, Hq / Hkv > 64; also where one request's longest table
+ * has more than about 2^31 tiles over all heads, or the cache more than 2^32
+ * groups of 16 rows), HRS_EALIGN, HRS_EGEOMETRY, HRS_EUNSUPPORTED (d),
+ * HRS_EDEVICE.
  */
 int attn_verify_span(const hrs_attn_desc* desc, const void* q, const void* k, const void* v,
                      const void* k_cache, const void* v_cache, const int32_t* page_table,
