@@ -649,8 +649,8 @@ size_t attn_verify_span_workspace_bytes(const hrs_attn_desc* desc);
  *           out [R][T][Hq][d] dtype, dense
  *           workspace: device scratch of at least
  *           attn_verify_span_workspace_bytes(desc) bytes, contents ignored
- * A request whose seq_len is outside [0, table_len * page_size] keeps its
- * rows of out as they were; status (optional device int32) receives the
+ * out must not overlap q, k or v. A request whose seq_len is outside [0,
+ * table_len * page_size] keeps its rows of out as they were; status (optional device int32) receives the
  * number of such requests. Calls that may run at the same time need
  * workspaces of their own. Errors: HRS_EINVAL (sizes, dtype combination,
  * R > 4096, Hkv > 1024, Hq / Hkv > 64; also where one request's longest table

@@ -222,3 +222,29 @@ def test_binding_refuses_wrong_tensors():
                      (dict(tokens=t(2, 3, dtype=torch.int64)), TypeError), (dict(parent=[[-1, 0]]), ValueError)):
         with pytest.raises(err):
             hrs.accept_sample(**{**ok, **bad})
+
+
+def test_binding_refuses_outputs_over_inputs():
+    """Blocks write their part of an output while others still read: only a
+    whole dense side of qk_norm_rope may be its own output."""
+    import torch
+    n, f = t(2, dtype=torch.int32), t(16, dtype=torch.float64)
+    buf = t(4096)
+    at = lambda o, *s: buf[o:o + int(np.prod(s))].view(*s)
+    q, k = at(0, 2, 3, 4, 64), at(1536, 2, 3, 2, 64)
+    qo, ko = t(2, 3, 4, 64), t(2, 3, 2, 64)
+    rope = lambda q, k, qo, ko: hrs.qk_norm_rope(q, k, None, None, f, n, qo, ko)
+    for ok in ((q, k, q, ko), (q, k, qo, k), (q, k, q, k), (q, k, at(2304, 2, 3, 4, 64), ko)):
+        with pytest.raises(ValueError, match="GPU"):
+            rope(*ok)
+    packed = t(2, 3, 512)
+    qp = packed[..., :256].unflatten(-1, (4, 64))
+    for bad in ((q, k, at(8, 2, 3, 4, 64), ko), (q, k, at(1528, 2, 3, 4, 64), ko), (q, k, qo, at(1000, 2, 3, 2, 64)),
+                (q, k, qo, qo.view(-1)[:768].view(2, 3, 2, 64)), (qp, k, packed.view(-1)[:1536].view(2, 3, 4, 64), ko)):
+        with pytest.raises(ValueError, match="overlaps"):
+            rope(*bad)
+    kc, pt, ws = t(5, 2, 16, 64), t(2, 3, dtype=torch.int32), t(64, dtype=torch.float32)
+    v = t(2, 3, 2, 64)
+    for out in (q, at(8, 2, 3, 4, 64), at(1600, 2, 3, 4, 64)):
+        with pytest.raises(ValueError, match="overlaps"):
+            hrs.attn_verify_span(q, k, v, kc, kc, pt, n, out, ws)

@@ -281,6 +281,84 @@ def test_attn_what_does_not_count_has_no_influence(hrs, dtype, cache, tree):
         assert torch.equal(got[:, node], clean[:, node]), node
 
 
+KINDS = [("bf16", "bf16"), ("bf16", "f8"), ("f32", "f32")]
+
+
+@pytest.mark.parametrize("group", [1, 3, 7, 8, 12])       # 9 to 108 rows a key head: every class of blocks
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("dtype,cache", KINDS)
+def test_attn_odd_values_at_every_block_shape(hrs, dtype, cache, d, group):
+    """Infinities and NaN in places that count come through exactly where the
+    formula has them, in places that do not count they change nothing: a
+    context of three requests (one a whole number of tiles, one that ends inside
+    one, one without), a tree, an absent page."""
+    import torch
+    a = Attn(3, 9, 2 * group, 2, d, 16, [37, 256, 0], dtype, cache, tree=True, seed=d + group)
+    a.pages[1, 3] = -7
+    clean = a.run(hrs)
+    a.check(clean, what="clean")
+    bad = {"f32": np.float32(np.nan), "bf16": np.uint16(0x7FC0), "f8": np.uint8(0x7F)}
+    pos = {"f32": np.float32(np.inf), "bf16": np.uint16(0x7F80), "f8": np.uint8(0x7F)}
+    neg = {"f32": np.float32(-np.inf), "bf16": np.uint16(0xFF80), "f8": np.uint8(0xFF)}
+    used = np.zeros((a.N, 16), dtype=bool)
+    for r, n in enumerate(a.lens):
+        for j in range(n):
+            if 0 <= a.pages[r][j // 16] < a.N:
+                used[a.pages[r][j // 16], j % 16] = True
+    for c, fill in ((a.kc, neg), (a.vc, bad)):
+        c.transpose(0, 2, 1, 3)[~used] = fill[cache]
+    assert torch.equal(a.run(hrs), clean)
+    def put(r, j, col, x):                                # a value of a cached slot, second key head
+        a.vc[a.pages[r][j // 16], 1, j % 16, col] = x[cache]
+    put(0, 5, 3, pos)
+    put(0, 36, 7, neg)
+    put(0, 5, 11, pos)
+    put(0, 36, 11, neg)
+    put(1, 250, 2, neg)
+    put(1, 17, d - 1, bad)
+    a.v[2, 4, 0, 20] = pos[dtype]
+    a.v[1, 8, 1, 21] = bad[dtype]
+    got = widen(host(a.run(hrs)))
+    for r in range(3):
+        with np.errstate(invalid="ignore"):
+            ref, absv, reach, n = oa.attn_span(a.q[r], a.k[r], a.v[r], a.kc, a.vc, a.pages[r], a.lens[r], a.parent[r],
+                                               None, 0, a.ks, a.vs, want_bound=True)
+            assert np.array_equal(np.isnan(got[r]), np.isnan(ref)), r
+            assert np.array_equal(got[r][np.isinf(ref)], ref[np.isinf(ref)]), r
+            rel = 2 * (2 * (d + 4) * U) * reach + (2 * n + 16) * U + (2.0 ** -8 if dtype == "bf16" else 0)
+            tol = rel[..., None] * absv + OUT[dtype] * (np.abs(ref) + rel[..., None] * absv)
+            fin = np.isfinite(ref)
+            assert np.all(np.abs(got[r] - ref)[fin] <= tol[fin]), r
+    assert np.isnan(got).any()
+
+
+def test_attn_two_streams_at_once(hrs):
+    """Two calls on two streams, each with a workspace of its own."""
+    import torch
+    cases = [Attn(2, 17, 8, 2, 128, 16, [3000, 900], "bf16", "bf16", seed=1),
+             Attn(1, 5, 4, 2, 256, 32, [5000], "bf16", "f8", seed=2)]
+    want = [c.run(hrs) for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    calls, outs = [], []
+    for c, w in zip(cases, want):
+        R, T, Hq, Hkv, d, S = c.shape
+        ws = torch.empty(hrs.attn_verify_span_workspace_bytes(R, T, Hq, Hkv, d), dtype=torch.uint8, device="cuda")
+        outs.append(torch.zeros_like(w))
+        opt = lambda x: None if x is None else dev(x)
+        calls.append(hrs.attn_verify_span_call(dev(c.q), dev(c.k), dev(c.v), dev(c.kc), dev(c.vc), dev(c.pages),
+                                               dev(np.array(c.lens, dtype=np.int32)), outs[-1], ws,
+                                               k_scale=opt(c.ks), v_scale=opt(c.vs)))
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for o in outs:
+            o.zero_()
+        torch.cuda.synchronize()
+        for call, st in zip(calls, streams):
+            call(st)
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, w) for o, w in zip(outs, want))
+
+
 def test_attn_nan_that_counts_is_seen(hrs):
     import torch
     a = Attn(1, 3, 2, 1, 64, 16, [20], "f32", "f32")
