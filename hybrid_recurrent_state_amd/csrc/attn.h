@@ -14,7 +14,7 @@ constexpr int kAttnCus = 256;          // compute units that a launch is cut for
 constexpr int kAttnReqs = 256;         // requests of a launch at most
 constexpr int kF32 = 0, kB16 = 1, kF8 = 2;   // span/cache types: f32/f32, bf16/bf16, bf16/e4m3
 
-struct AttnArgs {
+struct AttnBase {
   const void* q;
   const void* k;
   const void* v;
@@ -47,6 +47,9 @@ struct AttnArgs {
   int32_t table_len;
   int32_t tree;
   int32_t log_blocks; // of the launch's blocks
+};
+// The join does without the trees: every launch copies its arguments.
+struct AttnArgs : AttnBase {
   int8_t parent[kGeomBytes];
 };
 
@@ -111,7 +114,7 @@ struct AttnUnits {
   __device__ __forceinline__ int tiles() const { return all - kExtraUnits; }
 };
 
-__device__ __forceinline__ AttnUnits attn_units(const AttnArgs& a, int len, unsigned ts) {
+__device__ __forceinline__ AttnUnits attn_units(const AttnBase& a, int len, unsigned ts) {
   const bool ok = len >= 0 && len <= (a.table_len << a.page_shift);
   const unsigned n = ok ? len : 0;
   const unsigned first = a.window > 0 ? static_cast<unsigned>(max(static_cast<int>(n) + 1 - a.window, 0)) / ts : 0;

@@ -24,7 +24,7 @@ namespace {
 // long request, more loads are on their way (4 heads x 102 rows x 64 parts of
 // 256: 35.7 us with all parts in one thread group per row).
 template <bool F32, int D, int NS>
-__global__ __launch_bounds__(NS > 1 ? 64 * NS : 256) void attn_join_kernel(const AttnArgs args, int rows_per_block) {
+__global__ __launch_bounds__(NS > 1 ? 64 * NS : 256) void attn_join_kernel(const AttnBase args, int rows_per_block) {
   constexpr int DT = D / 16;
   const int heads = args.kvheads * args.row_blocks;
   const int i = blockIdx.x / heads;
@@ -133,7 +133,7 @@ __global__ __launch_bounds__(NS > 1 ? 64 * NS : 256) void attn_join_kernel(const
   }
 }
 
-template <bool F32, int D> void launch_join_d(const AttnArgs& args, const AttnShape& sh, hipStream_t s) {
+template <bool F32, int D> void launch_join_d(const AttnBase& args, const AttnShape& sh, hipStream_t s) {
   const int segs = args.n_here * args.kvheads * args.row_blocks;
   const int tasks = (std::min(sh.rows, args.rows) + 15) / 16 * (D / 32);
   if (static_cast<int64_t>(segs) * tasks <= 1024)
@@ -142,7 +142,7 @@ template <bool F32, int D> void launch_join_d(const AttnArgs& args, const AttnSh
     hipLaunchKernelGGL((attn_join_kernel<F32, D, 1>), dim3(segs, (tasks + 3) / 4), dim3(256), 0, s, args, sh.rows);
 }
 
-template <bool F32> void launch_join(const AttnArgs& args, int d, const AttnShape& sh, hipStream_t s) {
+template <bool F32> void launch_join(const AttnBase& args, int d, const AttnShape& sh, hipStream_t s) {
   if (d == 64) launch_join_d<F32, 64>(args, sh, s);
   if (d == 128) launch_join_d<F32, 128>(args, sh, s);
   if (d == 256) launch_join_d<F32, 256>(args, sh, s);

@@ -27,6 +27,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "device.h"
 #include "internal.h"
@@ -73,10 +74,16 @@ struct SampleArgs {
   int32_t n_chunks;
   int32_t n_pieces;
   int32_t req0;
-  int32_t tree;
   int32_t draft_bf16;
+};
+// Trees carry their parents; chains and the kernels behind the walk do not,
+// since every launch copies its arguments.
+struct SampleTree : SampleArgs {
   int8_t parent[kGeomBytes];
 };
+template <typename Args> constexpr bool is_tree = std::is_same<Args, SampleTree>::value;
+__device__ __forceinline__ int parent_of(const SampleArgs&, int, int t) { return t - 1; }
+__device__ __forceinline__ int parent_of(const SampleTree& a, int i, int) { return a.parent[i]; }
 
 __device__ __forceinline__ float temperature_of(const SampleArgs& a, int r) {
   return a.temperature ? a.temperature[r] : 1.0f;
@@ -183,14 +190,14 @@ template <> __device__ __forceinline__ void load8_nt<float>(const float* p, floa
 }
 
 // 1. Grid: (request, position with a child, chunk).
-template <typename T>
-__global__ __launch_bounds__(kThreads) void row_stats_kernel(const SampleArgs args) {
-  const int rows = args.tree ? args.n_pos : args.n_pos - 1;
+template <typename T, typename Args>
+__global__ __launch_bounds__(kThreads) void row_stats_kernel(const Args args) {
+  const int rows = is_tree<Args> ? args.n_pos : args.n_pos - 1;
   const int chunk = blockIdx.x % args.n_chunks;
   const int rt = blockIdx.x / args.n_chunks;
   const int rl = rt / rows, t = rt - rl * rows;
   const int64_t row = static_cast<int64_t>(args.req0 + rl) * args.n_pos + t;
-  if (args.tree) {
+  if constexpr (is_tree<Args>) {
     const int lane = threadIdx.x & 63;
     const int p = args.parent[rl * args.n_pos + min(lane, args.n_pos - 1)];
     if (!__any(p == t && lane > 0)) return;
@@ -259,8 +266,8 @@ struct WalkLds {
 
 // The walk of request r, by the whole block; the first block of the request
 // writes its outputs.
-template <typename T>
-__device__ __forceinline__ void walk(const SampleArgs& args, int rl, bool write, WalkLds& w) {
+template <typename T, typename Args>
+__device__ __forceinline__ void walk(const Args& args, int rl, bool write, WalkLds& w) {
   const int r = args.req0 + rl, T_ = args.n_pos, V = args.vocab;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const float tau = temperature_of(args, r);
@@ -275,7 +282,7 @@ __device__ __forceinline__ void walk(const SampleArgs& args, int rl, bool write,
   {
     const int t = min(static_cast<int>(threadIdx.x) >> 2, T_ - 1);
     const int sub = threadIdx.x & 3;
-    const int p = max(0, args.tree ? args.parent[rl * T_ + t] : t - 1);
+    const int p = max(0, parent_of(args, rl * T_ + t, t));
     const int x = args.tokens[row0 + t];
     const double u = args.uniforms[row0 + t];
     const bool valid = t > 0 && x >= 0 && x < V;
@@ -314,13 +321,13 @@ __device__ __forceinline__ void walk(const SampleArgs& args, int rl, bool write,
   __syncthreads();
   if (wave == 0) {
     const int tl = min(lane, T_ - 1);
-    const int par = lane >= T_ ? -2 : args.tree ? args.parent[rl * T_ + tl] : lane - 1;
+    const int par = lane >= T_ ? -2 : parent_of(args, rl * T_ + tl, lane);
     const int tok = w.tok[tl];
     const double need = w.need[tl];
     const double prob = w.prob[tl];
     int node = 0, len = 0, mode = kPlain, n_gone = 0;
     uint64_t on_path = 1;
-    if (!args.tree) {
+    if constexpr (!is_tree<Args>) {
       // One comparison per position; the accepted length is the run of
       // successes from position 1.
       const bool ok = lane >= 1 && lane < T_ && need < prob;
@@ -400,8 +407,8 @@ __device__ __forceinline__ uint32_t gone_mask(const NodeInfo& info, int v0) {
 }
 
 // 2. Grid: (piece, request).
-template <typename T>
-__global__ __launch_bounds__(kThreads) void node_kernel(const SampleArgs args) {
+template <typename T, typename Args>
+__global__ __launch_bounds__(kThreads) void node_kernel(const Args args) {
   __shared__ WalkLds w;
   __shared__ double lds[kThreads / 64];
   const int piece = blockIdx.x, rl = blockIdx.y, r = args.req0 + rl;
@@ -702,25 +709,31 @@ extern "C" size_t accept_sample_workspace_bytes(const hrs_sample_desc* d) {
          round256(r * sample_pieces(d) * sizeof(double)) + r * sizeof(NodeInfo);
 }
 
-template <typename T> static int sample_launch(const hrs_sample_desc* d, SampleArgs& args, hipStream_t s) {
-  const int per_launch = args.tree ? std::max(1, kGeomBytes / d->n_pos) : d->n_req;
+// Statistics, walk and node sums of the n requests from req0.
+template <typename T, typename Args> static bool launch_walk(const Args& args, int n, hipStream_t s) {
+  const int rows = is_tree<Args> ? args.n_pos : args.n_pos - 1;
+  if (rows > 0) {
+    hipLaunchKernelGGL((row_stats_kernel<T, Args>), dim3(n * rows * args.n_chunks), dim3(kThreads), 0, s, args);
+    if (launch_error() != hipSuccess) return false;
+  }
+  hipLaunchKernelGGL((node_kernel<T, Args>), dim3(args.n_pieces, n), dim3(kThreads), 0, s, args);
+  return launch_error() == hipSuccess;
+}
+
+template <typename T> static int sample_launch(const hrs_sample_desc* d, SampleTree& tree_args, hipStream_t s) {
+  SampleArgs& args = tree_args;
+  const bool tree = d->topo == HRS_TREE;
+  const int per_launch = tree ? std::max(1, kGeomBytes / d->n_pos) : d->n_req;
   (void)hipGetLastError();
   for (int r0 = 0; r0 < d->n_req; r0 += per_launch) {
     const int n = std::min(per_launch, d->n_req - r0);
     args.req0 = r0;
-    if (args.tree)
+    if (tree)
       for (int i = 0; i < n * d->n_pos; ++i)
-        args.parent[i] = static_cast<int8_t>(d->parent[static_cast<size_t>(r0) * d->n_pos + i]);
-    const int rows = args.tree ? d->n_pos : d->n_pos - 1;
-    const dim3 pieces(args.n_pieces, n);
-    if (rows > 0) {
-      hipLaunchKernelGGL(row_stats_kernel<T>, dim3(n * rows * args.n_chunks), dim3(kThreads), 0, s, args);
-      if (launch_error() != hipSuccess) return HRS_EDEVICE;
-    }
-    hipLaunchKernelGGL(node_kernel<T>, pieces, dim3(kThreads), 0, s, args);
-    if (launch_error() != hipSuccess) return HRS_EDEVICE;
+        tree_args.parent[i] = static_cast<int8_t>(d->parent[static_cast<size_t>(r0) * d->n_pos + i]);
+    if (!(tree ? launch_walk<T>(tree_args, n, s) : launch_walk<T>(args, n, s))) return HRS_EDEVICE;
     if (args.draft) {
-      hipLaunchKernelGGL(rest_kernel<T>, pieces, dim3(kThreads), 0, s, args);
+      hipLaunchKernelGGL(rest_kernel<T>, dim3(args.n_pieces, n), dim3(kThreads), 0, s, args);
       if (launch_error() != hipSuccess) return HRS_EDEVICE;
     }
     hipLaunchKernelGGL(draw_kernel<T>, dim3(n), dim3(kThreads), 0, s, args);
@@ -749,13 +762,12 @@ extern "C" int accept_sample(const hrs_sample_desc* d, const void* logits, const
       !aligned16(path) || !aligned16(bonus) || !aligned16(status) || !aligned16(workspace))
     return HRS_EALIGN;
 
-  SampleArgs args;
+  SampleTree args;
   args.logits = logits; args.tokens = tokens; args.uniforms = uniforms; args.draft = draft_probs;
   args.temperature = temperature; args.token_prob = token_prob; args.accept_node = accept_node;
   args.accept_len = accept_len; args.path = path; args.bonus = bonus; args.status = status;
   args.n_req = d->n_req; args.n_pos = d->n_pos; args.vocab = d->vocab;
   args.n_chunks = sample_chunks(d); args.n_pieces = sample_pieces(d);
-  args.tree = d->topo == HRS_TREE;
   args.draft_bf16 = d->draft_dtype == HRS_BF16;
   char* at = static_cast<char*>(workspace);
   const size_t r = d->n_req;
