@@ -36,7 +36,6 @@ struct AttnBase {
   int32_t window;
   int32_t n_req;      // of the whole call
   int32_t req0;       // of this launch
-  int32_t n_here;
   int32_t n_pos;
   int32_t kvheads;
   int32_t group;      // query heads per key/value head
@@ -46,11 +45,24 @@ struct AttnBase {
   int32_t page_shift;
   int32_t table_len;
   int32_t tree;
-  int32_t log_blocks; // of the launch's blocks
 };
-// The join does without the trees: every launch copies its arguments.
-struct AttnArgs : AttnBase {
+// Chains and the join do without the trees: every launch copies its arguments.
+struct AttnTree : AttnBase {
   int8_t parent[kGeomBytes];
+};
+
+// What the cut needs to know. These are kernel arguments of their own, at the
+// front, which the hardware has in registers when a wave starts: the lengths'
+// loads, the first of a chain of dependent ones, need not wait for the
+// argument block's.
+struct AttnLens {
+  const int32_t* len;   // of the launch's first request
+  int32_t n;            // requests
+  int32_t heads;        // key/value heads times row blocks
+  int32_t most;         // slots of a table
+  int32_t window;
+  int32_t n_pos;
+  int32_t log_blocks;   // of the launch's blocks
 };
 
 // How a block is built for a type, a head size and a class of row counts
@@ -114,8 +126,8 @@ struct AttnUnits {
   __device__ __forceinline__ int tiles() const { return all - kExtraUnits; }
 };
 
-__device__ __forceinline__ AttnUnits attn_units(const AttnBase& a, int len, unsigned ts) {
-  const bool ok = len >= 0 && len <= (a.table_len << a.page_shift);
+__device__ __forceinline__ AttnUnits attn_units(const AttnLens& a, int len, unsigned ts) {
+  const bool ok = len >= 0 && len <= a.most;
   const unsigned n = ok ? len : 0;
   const unsigned first = a.window > 0 ? static_cast<unsigned>(max(static_cast<int>(n) + 1 - a.window, 0)) / ts : 0;
   const int ctx = static_cast<int>((n + ts - 1) / ts - min(first, (n + ts - 1) / ts));
@@ -135,6 +147,6 @@ struct AttnShape {
   int rows, ts, blocks;
 };
 template <int KIND> AttnShape attn_shape(int d, int cls);
-template <int KIND> void attn_launch(const AttnArgs& args, int d, int cls, hipStream_t s);
+template <int KIND> void attn_launch(const AttnTree& args, const AttnLens& lens, int d, int cls, hipStream_t s);
 
 }  // namespace hrs

@@ -24,22 +24,24 @@ namespace {
 // long request, more loads are on their way (4 heads x 102 rows x 64 parts of
 // 256: 35.7 us with all parts in one thread group per row).
 template <bool F32, int D, int NS>
-__global__ __launch_bounds__(NS > 1 ? 64 * NS : 256) void attn_join_kernel(const AttnBase args, int rows_per_block) {
+__global__ __launch_bounds__(NS > 1 ? 64 * NS : 256) void attn_join_kernel(const int32_t* plan, const f32x4* part,
+                                                                          const float2* part_ml, int n_here, int heads,
+                                                                          int log_blocks, int rows_per_block,
+                                                                          const AttnBase args) {
   constexpr int DT = D / 16;
-  const int heads = args.kvheads * args.row_blocks;
   const int i = blockIdx.x / heads;
   const int seg = blockIdx.x - i * heads;
+  const int total = plan[n_here];
+  const int first = plan[i], end = plan[i + 1];
   const int h = seg / args.row_blocks, rb = seg - h * args.row_blocks;
   const int r = args.req0 + i;
-  const int total = args.plan[args.n_here];
-  const int first = args.plan[i], end = args.plan[i + 1];
   if (end == first) return;
   const int units = (end - first) / heads;
   const int s0 = first + seg * units, s1 = s0 + units;
   // Block of a unit: the last whose run starts at or before it.
   auto block_of = [&](int u) {
-    if (total <= (1 << args.log_blocks)) return u;
-    return static_cast<int>((((static_cast<int64_t>(u) + 1) << args.log_blocks) - 1) / total);
+    if (total <= (1 << log_blocks)) return u;
+    return static_cast<int>((((static_cast<int64_t>(u) + 1) << log_blocks) - 1) / total);
   };
   const int b0 = block_of(s0), b1 = block_of(s1 - 1);
   if (b0 == b1) return;                       // one block had all of it and wrote the result
@@ -63,8 +65,8 @@ __global__ __launch_bounds__(NS > 1 ? 64 * NS : 256) void attn_join_kernel(const
       // The segment's first block left its part as its last, the others theirs
       // as their first.
       const int64_t slot = 2 * bj + (bj == b0 ? 1 : 0);
-      w[j] = args.part_ml[slot * rows_per_block + row];
-      const f32x4* at = reinterpret_cast<const f32x4*>(args.part) + (slot * (rows_per_block / 16) + tile) * (DT * 64) + lane;
+      w[j] = part_ml[slot * rows_per_block + row];
+      const f32x4* at = part + (slot * (rows_per_block / 16) + tile) * (DT * 64) + lane;
       x[j][0] = at[(2 * dp) * 64];
       x[j][1] = at[(2 * dp + 1) * 64];
     }
@@ -133,19 +135,22 @@ __global__ __launch_bounds__(NS > 1 ? 64 * NS : 256) void attn_join_kernel(const
   }
 }
 
-template <bool F32, int D> void launch_join_d(const AttnBase& args, const AttnShape& sh, hipStream_t s) {
-  const int segs = args.n_here * args.kvheads * args.row_blocks;
+template <bool F32, int D> void launch_join_d(const AttnBase& args, const AttnLens& l, const AttnShape& sh, hipStream_t s) {
+  const int segs = l.n * l.heads;
+  const f32x4* const part = reinterpret_cast<const f32x4*>(args.part);
   const int tasks = (std::min(sh.rows, args.rows) + 15) / 16 * (D / 32);
   if (static_cast<int64_t>(segs) * tasks <= 1024)
-    hipLaunchKernelGGL((attn_join_kernel<F32, D, 8>), dim3(segs, tasks), dim3(512), 0, s, args, sh.rows);
+    hipLaunchKernelGGL((attn_join_kernel<F32, D, 8>), dim3(segs, tasks), dim3(512), 0, s, args.plan, part, args.part_ml, l.n,
+                       l.heads, l.log_blocks, sh.rows, args);
   else
-    hipLaunchKernelGGL((attn_join_kernel<F32, D, 1>), dim3(segs, (tasks + 3) / 4), dim3(256), 0, s, args, sh.rows);
+    hipLaunchKernelGGL((attn_join_kernel<F32, D, 1>), dim3(segs, (tasks + 3) / 4), dim3(256), 0, s, args.plan,
+                       part, args.part_ml, l.n, l.heads, l.log_blocks, sh.rows, args);
 }
 
-template <bool F32> void launch_join(const AttnBase& args, int d, const AttnShape& sh, hipStream_t s) {
-  if (d == 64) launch_join_d<F32, 64>(args, sh, s);
-  if (d == 128) launch_join_d<F32, 128>(args, sh, s);
-  if (d == 256) launch_join_d<F32, 256>(args, sh, s);
+template <bool F32> void launch_join(const AttnBase& args, const AttnLens& l, int d, const AttnShape& sh, hipStream_t s) {
+  if (d == 64) launch_join_d<F32, 64>(args, l, sh, s);
+  if (d == 128) launch_join_d<F32, 128>(args, l, sh, s);
+  if (d == 256) launch_join_d<F32, 256>(args, l, sh, s);
 }
 
 bool sizes_ok(const hrs_attn_desc* d) {
@@ -197,7 +202,7 @@ extern "C" int attn_verify_span(const hrs_attn_desc* d, const void* q, const voi
   const int cc = check_cache(d->cache, d->dtype);
   if (cc != HRS_OK) return cc;
   if (d->d != 64 && d->d != 128 && d->d != 256) return HRS_EUNSUPPORTED;
-  AttnArgs args;
+  AttnTree args;
   const int64_t kv_dense = static_cast<int64_t>(d->n_kvheads) * d->d;
   if (!span_stride(d->q_stride, static_cast<int64_t>(d->n_heads) * d->d, &args.q_stride) ||
       !span_stride(d->k_stride, kv_dense, &args.k_stride) || !span_stride(d->v_stride, kv_dense, &args.v_stride))
@@ -242,20 +247,20 @@ extern "C" int attn_verify_span(const hrs_attn_desc* d, const void* q, const voi
   (void)hipGetLastError();
   for (int r0 = 0; r0 < d->n_req; r0 += per_launch) {
     args.req0 = r0;
-    args.n_here = std::min(per_launch, d->n_req - r0);
+    AttnLens lens{seq_len + r0, std::min(per_launch, d->n_req - r0), args.kvheads * args.row_blocks,
+                  args.table_len << args.page_shift, d->window, d->n_pos, 0};
     if (args.tree)
-      for (int i = 0; i < args.n_here * d->n_pos; ++i)
+      for (int i = 0; i < lens.n * d->n_pos; ++i)
         args.parent[i] = static_cast<int8_t>(d->parent[static_cast<size_t>(r0) * d->n_pos + i]);
     // No more blocks than the longest contexts the table could hold have
     // tiles, a power of two.
-    args.log_blocks = 0;
-    while ((1 << args.log_blocks) < sh.blocks && (1 << args.log_blocks) < args.n_here * most) ++args.log_blocks;
-    if (kind == kF32) attn_launch<kF32>(args, d->d, cls, s);
-    else if (kind == kB16) attn_launch<kB16>(args, d->d, cls, s);
-    else attn_launch<kF8>(args, d->d, cls, s);
+    while ((1 << lens.log_blocks) < sh.blocks && (1 << lens.log_blocks) < lens.n * most) ++lens.log_blocks;
+    if (kind == kF32) attn_launch<kF32>(args, lens, d->d, cls, s);
+    else if (kind == kB16) attn_launch<kB16>(args, lens, d->d, cls, s);
+    else attn_launch<kF8>(args, lens, d->d, cls, s);
     if (launch_error() != hipSuccess) return HRS_EDEVICE;
-    if (kind == kF32) launch_join<true>(args, d->d, sh, s);
-    else launch_join<false>(args, d->d, sh, s);
+    if (kind == kF32) launch_join<true>(args, lens, d->d, sh, s);
+    else launch_join<false>(args, lens, d->d, sh, s);
     if (launch_error() != hipSuccess) return HRS_EDEVICE;
   }
   return HRS_OK;

@@ -3,5 +3,5 @@
 
 namespace hrs {
 template AttnShape attn_shape<kB16>(int, int);
-template void attn_launch<kB16>(const AttnArgs&, int, int, hipStream_t);
+template void attn_launch<kB16>(const AttnTree&, const AttnLens&, int, int, hipStream_t);
 }  // namespace hrs

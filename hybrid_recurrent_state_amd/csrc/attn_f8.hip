@@ -3,5 +3,5 @@
 
 namespace hrs {
 template AttnShape attn_shape<kF8>(int, int);
-template void attn_launch<kF8>(const AttnArgs&, int, int, hipStream_t);
+template void attn_launch<kF8>(const AttnTree&, const AttnLens&, int, int, hipStream_t);
 }  // namespace hrs

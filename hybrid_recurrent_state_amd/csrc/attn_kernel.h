@@ -52,6 +52,8 @@
 // long as its read and hides behind it only in part.
 #pragma once
 
+#include <type_traits>
+
 #include "attn.h"
 
 namespace hrs {
@@ -139,7 +141,7 @@ template <int KIND, int D, int CLS> struct AttnBlock {
   static_assert(SB <= 2, "one or two blocks of 16 slots");
   static_assert(LPS >= 1 && LPS * 64 * C::WR == 2 * C::SS * RCPR && (C::NST - 1) * LPS < 64, "whole loads");
 
-  const AttnArgs& a;
+  const AttnBase& a;
   char* lds;
   AttnRows<C::ROWS>* rows;
   int wave, lane, wr, kg, n16, g;
@@ -158,7 +160,7 @@ template <int KIND, int D, int CLS> struct AttnBlock {
   int next;                    // next tile to start
   int pg[SB];                  // pages of the next tile to load
 
-  __device__ __forceinline__ AttnBlock(const AttnArgs& args, char* l_, AttnRows<C::ROWS>* rows_) : a(args), lds(l_), rows(rows_) {
+  __device__ __forceinline__ AttnBlock(const AttnBase& args, char* l_, AttnRows<C::ROWS>* rows_) : a(args), lds(l_), rows(rows_) {
     wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     lane = threadIdx.x & 63;
     wr = wave % C::WR;
@@ -302,7 +304,7 @@ template <int KIND, int D, int CLS> struct AttnBlock {
     vs = uniform(vs);
     c_ctx = uniform(c_ctx);
   }
-  __device__ __forceinline__ void mask_rows(const int8_t* par) {
+  template <bool TREE> __device__ __forceinline__ void mask_rows(const int8_t* par) {
     if (kg != 0) return;
     const int n16 = fresh(this->n16), g = fresh(this->g);
 #pragma unroll
@@ -313,7 +315,7 @@ template <int KIND, int D, int CLS> struct AttnBlock {
       const int t = on ? row / a.group : 0;
       uint64_t path = 0;
       int dep = 0;
-      if (a.tree) {
+      if constexpr (TREE) {
         int up = t;
         for (int i = 0; up >= 0; ++i, up = par[up]) {
           if (a.window == 0 || i < a.window) path |= uint64_t{1} << up;
@@ -842,17 +844,15 @@ struct AttnPlan {
   int before;     // units before the lane's requests
   int total;
 
-  __device__ __forceinline__ AttnPlan(const AttnArgs& a, int ts) {
+  __device__ __forceinline__ AttnPlan(const AttnLens& a, int ts) {
     const int lane = fresh(threadIdx.x) & 63;
-    const int heads = a.kvheads * a.row_blocks;
 #pragma unroll
-    for (int k = 0; k < kAttnReqs / 64; ++k)
-      len[k] = a.seq_len[a.req0 + min(lane * (kAttnReqs / 64) + k, a.n_here - 1)];
+    for (int k = 0; k < kAttnReqs / 64; ++k) len[k] = a.len[min(lane * (kAttnReqs / 64) + k, a.n - 1)];
     int sum = 0;
 #pragma unroll
     for (int k = 0; k < kAttnReqs / 64; ++k) {
-      const int n = attn_units(a, len[k], ts).all * heads;
-      all[k] = lane * (kAttnReqs / 64) + k < a.n_here ? n : 0;
+      const int n = attn_units(a, len[k], ts).all * a.heads;
+      all[k] = lane * (kAttnReqs / 64) + k < a.n ? n : 0;
       sum += all[k];
     }
     // Inclusive sum over the lanes: within rows of 16, then across them.
@@ -868,16 +868,16 @@ struct AttnPlan {
   }
 
   // For the join kernel: units before every request, and the total.
-  __device__ __forceinline__ void write(const AttnArgs& a) const {
+  __device__ __forceinline__ void write(int32_t* plan, int n) const {
     if (threadIdx.x >= 64) return;
     int at = before;
 #pragma unroll
     for (int k = 0; k < kAttnReqs / 64; ++k) {
       const int i = threadIdx.x * (kAttnReqs / 64) + k;
-      if (i <= a.n_here) a.plan[i] = at;
+      if (i <= n) plan[i] = at;
       at += all[k];
     }
-    if (threadIdx.x == 63 && a.n_here == kAttnReqs) a.plan[kAttnReqs] = at;
+    if (threadIdx.x == 63 && n == kAttnReqs) plan[kAttnReqs] = at;
   }
 
   // Request of unit u (uniform, below the total), the unit's number in it and
@@ -911,7 +911,7 @@ struct AttnPlan {
 };
 
 // Refused requests of the whole call: a count per thread, added in order.
-template <int NT> __device__ __forceinline__ void count_refused(const AttnArgs& a, int32_t* sums) {
+template <int NT> __device__ __forceinline__ void count_refused(const AttnBase& a, int32_t* sums) {
   int bad = 0;
   for (int i = threadIdx.x; i < a.n_req; i += NT) {
     const int n = a.seq_len[i];
@@ -927,23 +927,25 @@ template <int NT> __device__ __forceinline__ void count_refused(const AttnArgs& 
   block_barrier();
 }
 
-template <int KIND, int D, int CLS>
+template <int KIND, int D, int CLS, typename Args>
 __global__ __launch_bounds__((AttnCfg<KIND, D, CLS>::NT), (AttnCfg<KIND, D, CLS>::NT * AttnCfg<KIND, D, CLS>::PER_CU + 255) / 256)
-void attn_kernel(const AttnArgs args) {
+void attn_kernel(const int32_t* len, int n, int heads, int most, int window, int n_pos, int log_blocks, const Args args) {
   using C = AttnCfg<KIND, D, CLS>;
+  constexpr bool kTree = std::is_same<Args, AttnTree>::value;
+  const AttnLens lens{len, n, heads, most, window, n_pos, log_blocks};
   extern __shared__ __align__(1024) char lds[];   // rows of a tile start at multiples of their size
-  __shared__ int8_t par[HRS_MAX_POS];
+  __shared__ int8_t par[kTree ? HRS_MAX_POS : 1];
   __shared__ AttnRows<C::ROWS> rows;
   const int tid = threadIdx.x;
   AttnBlock<KIND, D, CLS> blk(args, lds, &rows);
   int u, u1, in_req = 0, i = 0;
   {
-    const AttnPlan plan(args, C::TS);
-    u = attn_cut(blockIdx.x, plan.total, args.log_blocks);
-    u1 = attn_cut(blockIdx.x + 1, plan.total, args.log_blocks);
+    const AttnPlan plan(lens, C::TS);
+    u = attn_cut(blockIdx.x, plan.total, log_blocks);
+    u1 = attn_cut(blockIdx.x + 1, plan.total, log_blocks);
     if (u < u1) i = plan.find(u, &in_req, &blk.len);
     if (blockIdx.x == 0) {
-      plan.write(args);
+      plan.write(args.plan, n);
       if (args.status && args.req0 == 0) count_refused<C::NT>(args, reinterpret_cast<int32_t*>(lds));
     }
   }
@@ -954,12 +956,12 @@ void attn_kernel(const AttnArgs args) {
       // Counted again for every further segment rather than kept in registers
       // over the tiles; everybody is done with the last segment's tiles and
       // masks after the barrier.
-      i = AttnPlan(args, C::TS).find(u, &in_req, &blk.len);
+      i = AttnPlan(lens, C::TS).find(u, &in_req, &blk.len);
       block_barrier();
     }
     again = true;
     blk.r = args.req0 + i;
-    blk.un = attn_units(args, blk.len, C::TS);
+    blk.un = attn_units(lens, blk.len, C::TS);
     const int seg = __builtin_amdgcn_readfirstlane(in_req / blk.un.all);
     const int u0 = in_req - seg * blk.un.all;
     const int ue = min(blk.un.all, u0 + (u1 - u));
@@ -978,11 +980,11 @@ void attn_kernel(const AttnArgs args) {
     // the time that the span's masks and a segment's end take).
     const int last = min(ue, blk.un.tiles());
     blk.start_ring(u0, last);
-    if (args.tree) {
+    if constexpr (kTree) {
       if (tid < args.n_pos) par[tid] = args.parent[i * args.n_pos + tid];
       block_barrier();
     }
-    blk.mask_rows(par);
+    blk.template mask_rows<kTree>(par);
     blk.settle();
     block_barrier();
     blk.run(u0, last);
@@ -996,10 +998,15 @@ void attn_kernel(const AttnArgs args) {
 
 namespace {
 
-template <int KIND, int D, int CLS>
-void launch_one(const AttnArgs& args, hipStream_t s) {
+template <int KIND, int D, int CLS, typename Args>
+void launch_as(const Args& args, const AttnLens& l, hipStream_t s) {
   using C = AttnCfg<KIND, D, CLS>;
-  hipLaunchKernelGGL((attn_kernel<KIND, D, CLS>), dim3(1 << args.log_blocks), dim3(C::NT), C::LDS, s, args);
+  hipLaunchKernelGGL((attn_kernel<KIND, D, CLS, Args>), dim3(1 << l.log_blocks), dim3(C::NT), C::LDS, s, l.len, l.n, l.heads,
+                     l.most, l.window, l.n_pos, l.log_blocks, args);
+}
+template <int KIND, int D, int CLS> void launch_one(const AttnTree& args, const AttnLens& l, hipStream_t s) {
+  if (args.tree) launch_as<KIND, D, CLS>(args, l, s);
+  else launch_as<KIND, D, CLS>(static_cast<const AttnBase&>(args), l, s);
 }
 template <int KIND, int D, int CLS> AttnShape shape_one() {
   using C = AttnCfg<KIND, D, CLS>;
@@ -1029,23 +1036,23 @@ template <int KIND> AttnShape attn_shape(int d, int cls) {
   return {0, 0, 0};
 }
 
-template <int KIND> void attn_launch(const AttnArgs& args, int d, int cls, hipStream_t s) {
+template <int KIND> void attn_launch(const AttnTree& args, const AttnLens& lens, int d, int cls, hipStream_t s) {
   switch (d * 8 + cls) {
-    case 64 * 8 + 0: return launch_one<KIND, 64, 0>(args, s);
-    case 64 * 8 + 1: return launch_one<KIND, 64, 1>(args, s);
-    case 64 * 8 + 2: return launch_one<KIND, 64, 2>(args, s);
-    case 64 * 8 + 3: return launch_one<KIND, 64, 3>(args, s);
-    case 128 * 8 + 0: return launch_one<KIND, 128, 0>(args, s);
-    case 128 * 8 + 1: return launch_one<KIND, 128, 1>(args, s);
-    case 128 * 8 + 2: return launch_one<KIND, 128, 2>(args, s);
-    case 128 * 8 + 3: return launch_one<KIND, 128, 3>(args, s);
-    case 256 * 8 + 0: return launch_one<KIND, 256, 0>(args, s);
-    case 256 * 8 + 1: return launch_one<KIND, 256, 1>(args, s);
-    case 256 * 8 + 2: return launch_one<KIND, 256, 2>(args, s);
-    case 256 * 8 + 3: return launch_one<KIND, 256, 3>(args, s);
+    case 64 * 8 + 0: return launch_one<KIND, 64, 0>(args, lens, s);
+    case 64 * 8 + 1: return launch_one<KIND, 64, 1>(args, lens, s);
+    case 64 * 8 + 2: return launch_one<KIND, 64, 2>(args, lens, s);
+    case 64 * 8 + 3: return launch_one<KIND, 64, 3>(args, lens, s);
+    case 128 * 8 + 0: return launch_one<KIND, 128, 0>(args, lens, s);
+    case 128 * 8 + 1: return launch_one<KIND, 128, 1>(args, lens, s);
+    case 128 * 8 + 2: return launch_one<KIND, 128, 2>(args, lens, s);
+    case 128 * 8 + 3: return launch_one<KIND, 128, 3>(args, lens, s);
+    case 256 * 8 + 0: return launch_one<KIND, 256, 0>(args, lens, s);
+    case 256 * 8 + 1: return launch_one<KIND, 256, 1>(args, lens, s);
+    case 256 * 8 + 2: return launch_one<KIND, 256, 2>(args, lens, s);
+    case 256 * 8 + 3: return launch_one<KIND, 256, 3>(args, lens, s);
   }
   if constexpr (KIND == kF8) {
-    if (cls == 4) return d == 64 ? launch_one<KIND, 64, 4>(args, s) : launch_one<KIND, 128, 4>(args, s);
+    if (cls == 4) return d == 64 ? launch_one<KIND, 64, 4>(args, lens, s) : launch_one<KIND, 128, 4>(args, lens, s);
   }
 }
 

@@ -37,7 +37,10 @@ HIP_FLAGS = ["-x", "hip", f"--offload-arch={ARCH}", "-ffp-contract=off", "-mcode
 # (input pointers and packed shape) are preloaded into SGPRs by the hardware
 # at wave launch (kernel-argument preloading; the compiler emits a prologue
 # that loads them for firmware without it).
-FILE_FLAGS = {"gdn.hip": ["-mllvm", "-amdgpu-kernarg-preload-count=8"]}
+# attn*.hip: likewise what the first loads of attention and its join need.
+PRELOAD = ["-mllvm", "-amdgpu-kernarg-preload-count=8"]
+FILE_FLAGS = {"gdn.hip": PRELOAD, "attn.hip": PRELOAD, "attn_f32.hip": PRELOAD, "attn_bf16.hip": PRELOAD,
+              "attn_f8.hip": PRELOAD}
 
 
 def hipcc() -> str:
