@@ -453,9 +453,12 @@ template <int KIND, int D, int CLS> struct AttnBlock {
     if (__any(more)) {
 #pragma unroll
       for (int rt = 0; rt < C::RT; ++rt) {
-        const float mn = fmaxf(m[rt], row_max(top[rt]));
-        const float keep = m[rt] == mn ? 1.0f : __builtin_amdgcn_exp2f(m[rt] - mn);
-        m[rt] = mn;
+        // Only the rows that ask for it: moved along with its neighbours, a
+        // row's rounding would depend on scores that it does not count.
+        const float mt = row_max(top[rt]);
+        const bool moves = mt > m[rt] + 8.0f;
+        const float keep = moves ? __builtin_amdgcn_exp2f(m[rt] - mt) : 1.0f;
+        m[rt] = moves ? mt : m[rt];
         l[rt] *= keep;
 #pragma unroll
         for (int dt = 0; dt < DT; ++dt) o[rt][dt] *= keep;

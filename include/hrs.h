@@ -54,9 +54,10 @@
  *  - Determinism: results are bit-identical from run to run, and the
  *    arithmetic of one position does not depend on the span length or on the
  *    tree topology (attn_verify_span: bit-identical from run to run of the
- *    same call; where a context is split among blocks depends on every
- *    length in the batch, so the same request in another batch agrees to
- *    rounding only).
+ *    same call, and whatever the keys and values that a query does not count
+ *    hold; where a context is split among blocks depends on every length in
+ *    the batch, and inside a block on T * Hq / Hkv, so the same request in
+ *    another batch or a longer span agrees to rounding only).
  *
  * Sources (the pages this path comes from):
  *  [P1] lucebox PR #533, "feat: DFlash support for tensor-parallel Qwen3.6

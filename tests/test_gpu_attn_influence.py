@@ -1,0 +1,78 @@
+"""attn_verify_span on the GPU: what a query does not count leaves its result
+alone, bit for bit, also where it is finite and large."""
+import numpy as np
+import pytest
+
+from oracle.common import widen
+from tests.test_gpu_attn import KINDS, Attn, cast, host
+from tests.test_gpu_attn_runs import Runs, block_shape
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def hrs():
+    import torch
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    import hybrid_recurrent_state_amd as m
+    return m
+
+
+def toward(q, size, dtype):
+    """A key whose products with the query q are large and positive."""
+    return cast(size * np.sign(widen(q)), dtype)
+
+
+def path_of(parent, t):
+    out = []
+    while t >= 0:
+        out.append(t)
+        t = int(parent[t])
+    return out
+
+
+@pytest.mark.parametrize("group", [1, 3, 7, 8, 12])       # 9 to 108 rows a key head: every class of blocks
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("dtype,cache", KINDS)
+def test_large_keys_off_the_path_change_nothing(hrs, dtype, cache, d, group):
+    """Keys of other branches with scores of a hundred for the positions that
+    count them, in a tile behind tiles of the context that have set every
+    row's reference; a row's own keys in that tile are a little larger than
+    the context's, so that its maximum grows without its reference having to
+    move."""
+    import torch
+    rows, ts, blocks, _ = block_shape(cache, d, 9 * group)
+    n = 5 * blocks * ts // 4
+    a = Runs(2, 9, group, 2, d, 64, [n, n // 2 + 3], dtype, cache, True, 0, seed=d + group)
+    a.scale = 0.3 * d ** -0.5
+    for t in range(9):
+        a.k[:, t] = cast(0.5 * widen(a.q)[:, t, ::group], dtype)
+    clean = a.run(hrs)
+    k0 = a.k.copy()
+    for node in (0, 4, 8):
+        a.k = k0.copy()
+        for r in range(2):
+            off = [t for t in range(9) if t not in path_of(a.parent[r], node)]
+            for t in off:
+                for h in range(2):
+                    a.k[r, t, h] = toward(a.q[r, t, h * group], 40.0, dtype)
+        got = a.run(hrs)
+        assert torch.equal(got[:, node], clean[:, node]), node
+        assert not torch.equal(got, clean)
+
+
+@pytest.mark.parametrize("group", [1, 3, 7, 8, 12])
+@pytest.mark.parametrize("dtype,cache", [("bf16", "bf16"), ("f32", "f32")])
+def test_large_keys_behind_the_window_change_nothing(hrs, dtype, cache, group):
+    """Slots that only the first positions' windows still reach."""
+    import torch
+    T, W, n = 9, 50, 200
+    a = Attn(1, T, 2 * group, 2, 64, 16, [n], dtype, cache, window=W, seed=group)
+    clean = a.run(hrs)
+    for t in (3, 8):                          # the first slot that position t counts is n + t - W + 1
+        for j in range(n - W + 1, n + t - W + 1):
+            for h in range(2):
+                a.kc[a.pages[0][j // 16], h, j % 16] = toward(a.q[0, 0, h * group], 40.0, cache)
+        got = a.run(hrs)
+        assert torch.equal(got[:, t:], clean[:, t:]), t
+        assert not torch.equal(got[:, 0], clean[:, 0])

@@ -5,10 +5,11 @@ between tiles, pages are read a tile ahead, runs are cut inside heads.
 Two checks of every block shape:
   coverage: queries of zero weigh every slot that counts alike, values are
     small whole numbers, so all sums are exact and a result is S / n after a
-    reciprocal, a product and the rounding to the output's type: a slot that is left out or taken
-    twice shows.
-  peaked: scores with a deviation of 6 whose size grows or falls along the context, against the
-    formula in 64 bits under the bound of test_gpu_attn.py.
+    reciprocal, a product and the rounding to the output's type: a slot that
+    is left out or taken twice shows.
+  peaked: scores with a deviation of 6 whose size grows or falls along the
+    context, against the formula in 64 bits under the bound of
+    test_gpu_attn.py.
 """
 import numpy as np
 import pytest
@@ -31,8 +32,8 @@ def hrs():
 
 def block_shape(cache, d, rows):
     """(rows of a block, slots of a tile, blocks, tiles of the ring) of a
-    launch, worked out here for the inputs' sake: that they give a block more tiles than
-    its ring holds is asserted below."""
+    launch, worked out here for the inputs' sake: that they give a block more
+    tiles than its ring holds is asserted below."""
     wide, esz = d == 256, {"f32": 4, "bf16": 2, "f8": 1}[cache]
     cls = 4 if cache == "f8" and not wide and 64 < rows <= 96 else 0 if rows <= 16 else 1 if rows <= 32 else 2 if rows <= 64 else 3
     rt = 3 if cls == 4 else 1 if cls < 3 or wide else 2
