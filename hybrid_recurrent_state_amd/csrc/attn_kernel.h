@@ -417,16 +417,18 @@ template <int KIND, int D, int CLS> struct AttnBlock {
     Values<F8> v;
     if constexpr (KIND != kF32) v.load(vt, n16, g, 0);
     // c S - m is one operation on the raw products; c is positive (a negative
-    // one turns the products' sign).
+    // one turns the products' sign, one that is not a number goes to them: the
+    // scores that do not count must not have it).
     float c = span ? c_span : c_ctx;
-    if (c < 0.0f) {
+    if (!(c >= 0.0f)) {
+      const float turn = c < 0.0f ? -1.0f : c;
       c = -c;
 #pragma unroll
       for (int rt = 0; rt < C::RT; ++rt)
 #pragma unroll
-        for (int sb = 0; sb < SB; ++sb) s[rt][sb] = -s[rt][sb];
+        for (int sb = 0; sb < SB; ++sb) s[rt][sb] *= turn;
     }
-    c = fmaxf(c, 1e-37f);          // masked scores stay below everything at a scale of zero
+    c = fmaxf(c, 1e-37f);          // masked scores stay below everything at a scale of zero (or NaN)
     if (mask) {
 #pragma unroll
       for (int rt = 0; rt < C::RT; ++rt) {

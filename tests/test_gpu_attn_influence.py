@@ -1,5 +1,6 @@
 """attn_verify_span on the GPU: what a query does not count leaves its result
-alone, bit for bit, also where it is finite and large."""
+alone, bit for bit, also where it is finite and large; what it counts is seen,
+also where it is not a number."""
 import numpy as np
 import pytest
 
@@ -76,3 +77,31 @@ def test_large_keys_behind_the_window_change_nothing(hrs, dtype, cache, group):
         got = a.run(hrs)
         assert torch.equal(got[:, t:], clean[:, t:]), t
         assert not torch.equal(got[:, 0], clean[:, 0])
+
+
+@pytest.mark.parametrize("group", [1, 3, 7, 8, 12])
+@pytest.mark.parametrize("dtype,cache", KINDS)
+def test_scale_that_is_not_a_number_is_seen(hrs, dtype, cache, group):
+    a = Attn(2, 9, 2 * group, 2, 64, 16, [100, 0], dtype, cache, scale=float("nan"))
+    assert np.isnan(widen(host(a.run(hrs)))).all()
+
+
+@pytest.mark.parametrize("group", [1, 3, 7, 8, 12])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_key_scale_that_is_not_a_number(hrs, d, group):
+    """Seen by every query that counts a cached slot of its head, by no other:
+    not by the other head's, by a request without a context's, nor by those
+    whose window ends at their own position."""
+    import torch
+    a = Attn(2, 9, 2 * group, 2, d, 16, [100, 0], "bf16", "f8", seed=group)
+    clean = a.run(hrs)
+    keep, bad = a.ks, a.ks.copy()
+    bad[1] = np.nan
+    a.ks = bad
+    got = a.run(hrs)
+    assert bool(torch.isnan(got[0, :, group:]).all())
+    assert torch.equal(got[0, :, :group], clean[0, :, :group]) and torch.equal(got[1], clean[1])
+    a.window, a.ks = 1, keep
+    clean = a.run(hrs)
+    a.ks = bad
+    assert torch.equal(a.run(hrs), clean)
