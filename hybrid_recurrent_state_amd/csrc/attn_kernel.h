@@ -740,11 +740,15 @@ template <int KIND, int D, int CLS> struct AttnBlock {
       mem_fence();
     }
     if constexpr (KIND == kF8) {
-      // The values' scale, once for all tiles of the cache.
+      // The values' scale, once for all tiles of the cache, of the rows that
+      // count a slot of them (the others' sums are zero, the scale may be
+      // anything).
 #pragma unroll
-      for (int rt = 0; rt < C::RT; ++rt)
+      for (int rt = 0; rt < C::RT; ++rt) {
+        const float f = m[rt] == -__builtin_inff() ? 1.0f : vs;
 #pragma unroll
-        for (int dt = 0; dt < DT; ++dt) o[rt][dt] *= vs;
+        for (int dt = 0; dt < DT; ++dt) o[rt][dt] *= f;
+      }
       for (int u = max(i0, un.ctx); u < i1; ++u) {
         block_barrier();
         issue_span(u);

@@ -86,22 +86,24 @@ def test_scale_that_is_not_a_number_is_seen(hrs, dtype, cache, group):
     assert np.isnan(widen(host(a.run(hrs)))).all()
 
 
+@pytest.mark.parametrize("which", ["ks", "vs"])
 @pytest.mark.parametrize("group", [1, 3, 7, 8, 12])
 @pytest.mark.parametrize("d", [64, 128, 256])
-def test_key_scale_that_is_not_a_number(hrs, d, group):
+def test_cache_scale_that_is_not_a_number(hrs, d, group, which):
     """Seen by every query that counts a cached slot of its head, by no other:
     not by the other head's, by a request without a context's, nor by those
     whose window ends at their own position."""
     import torch
     a = Attn(2, 9, 2 * group, 2, d, 16, [100, 0], "bf16", "f8", seed=group)
     clean = a.run(hrs)
-    keep, bad = a.ks, a.ks.copy()
+    keep, bad = getattr(a, which), getattr(a, which).copy()
     bad[1] = np.nan
-    a.ks = bad
+    setattr(a, which, bad)
     got = a.run(hrs)
     assert bool(torch.isnan(got[0, :, group:]).all())
     assert torch.equal(got[0, :, :group], clean[0, :, :group]) and torch.equal(got[1], clean[1])
-    a.window, a.ks = 1, keep
+    a.window = 1
+    setattr(a, which, keep)
     clean = a.run(hrs)
-    a.ks = bad
+    setattr(a, which, bad)
     assert torch.equal(a.run(hrs), clean)
