@@ -118,10 +118,10 @@ __global__ __launch_bounds__(NS > 1 ? 64 * NS : 256) void attn_join_kernel(const
   const int at_row = rb * rows_per_block + row;
   if (at_row >= args.rows) return;
   const int t = at_row / args.group, hq = h * args.group + at_row - t * args.group;
-  const float inv = ls == 0.0f ? 0.0f : 1.0f / ls;
+  const float inv = 1.0f / ls;      // scores of -inf alone: 0 * inf, as the formula's 0 / 0
   const int64_t at = ((static_cast<int64_t>(r) * args.n_pos + t) * (args.kvheads * args.group) + hq) * D;
 #pragma unroll
-  for (int e = 0; e < 2; ++e) sum[e] = ls == 0.0f ? f32x4{} : sum[e] * inv;
+  for (int e = 0; e < 2; ++e) sum[e] *= inv;
   if constexpr (F32) {
     float* const out = static_cast<float*>(args.out) + at + 32 * dp + 4 * g;
     *reinterpret_cast<f32x4*>(out) = sum[0];

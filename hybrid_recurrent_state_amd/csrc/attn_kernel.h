@@ -805,13 +805,13 @@ template <int KIND, int D, int CLS> struct AttnBlock {
         if (rb * C::ROWS + row >= a.rows) continue;
         const int at_row = rb * C::ROWS + row;
         const int t = at_row / a.group, hq = h * a.group + at_row - t * a.group;
-        const float inv = ls == 0.0f ? 0.0f : 1.0f / ls;
+        const float inv = 1.0f / ls;      // scores of -inf alone: 0 * inf, as the formula's 0 / 0
         const int64_t at = ((static_cast<int64_t>(r) * a.n_pos + t) * (a.kvheads * a.group) + hq) * D;
 #pragma unroll
         for (int j = 0; j < D / 16 / kRun * 4; ++j) {
           float y[kRun];
 #pragma unroll
-          for (int e = 0; e < kRun; ++e) y[e] = ls == 0.0f ? 0.0f : run_at(o[rt], j, e) * inv;
+          for (int e = 0; e < kRun; ++e) y[e] = run_at(o[rt], j, e) * inv;
           if constexpr (KIND == kF32) {
             *reinterpret_cast<f32x4*>(static_cast<float*>(a.out) + at + run_column(j, g)) = f32x4{y[0], y[1], y[2], y[3]};
           } else {

@@ -638,9 +638,11 @@ size_t attn_verify_span_workspace_bytes(const hrs_attn_desc* desc);
  * j > n + depth(t) - W and path positions s with depth(t) - depth(s) < W
  * count. Cached e4m3 values stand for k_scale[g], v_scale[g] times themselves
  * (NULL: 1); span rows are taken as they are. What does not count has no
- * influence, whatever it holds (infinities and NaN included); a query that
- * nothing counts for gives zeros. Sums and softmax statistics are float32;
- * bf16 spans round the weights to bf16 for the product with the values.
+ * influence, whatever it holds (infinities and NaN included). Every position
+ * counts itself, so no query is without a score; where all of them are -inf
+ * the result is NaN, as the formula's. Sums and softmax statistics are
+ * float32; bf16 spans round the weights to bf16 for the product with the
+ * values.
  *
  * Layouts:  q [R][T][Hq][d], k, v [R][T][Hkv][d]  dtype, strided as above
  *           k_cache, v_cache [n_pages][Hkv][page_size][d]  cache.dtype

@@ -10,6 +10,8 @@ from tests.test_gpu_attn_runs import Runs, block_shape
 
 pytestmark = pytest.mark.gpu
 
+NEG = {"f32": np.float32(-np.inf), "bf16": np.uint16(0xFF80)}
+
 
 @pytest.fixture(scope="module")
 def hrs():
@@ -107,3 +109,23 @@ def test_cache_scale_that_is_not_a_number(hrs, d, group, which):
     clean = a.run(hrs)
     setattr(a, which, bad)
     assert torch.equal(a.run(hrs), clean)
+
+
+@pytest.mark.parametrize("group", [1, 3, 7, 8, 12])
+@pytest.mark.parametrize("n", [0, 100, 3000])
+@pytest.mark.parametrize("dtype,cache", [("bf16", "bf16"), ("f32", "f32")])
+def test_scores_of_minus_infinity_alone_have_no_softmax(hrs, dtype, cache, n, group):
+    """Every score of one head is -inf: 0 / 0. The other head's are not
+    touched, and one finite score is enough."""
+    import torch
+    a = Attn(1, 9, 2 * group, 2, 64, 16, [n], dtype, cache, seed=group)
+    a.q = np.abs(a.q) if dtype == "f32" else a.q & np.uint16(0x7FFF)
+    clean = a.run(hrs)
+    a.kc[:, 1], a.k[:, :, 1] = NEG[cache], NEG[dtype]
+    got = a.run(hrs)
+    assert bool(torch.isnan(got[:, :, group:]).all())
+    assert torch.equal(got[:, :, :group], clean[:, :, :group])
+    a.k[:, 0, 1] = 0                                       # the root counts for everybody
+    got = widen(host(a.run(hrs)))
+    for t in range(9):
+        assert np.array_equal(got[0, t, group:], np.broadcast_to(widen(a.v[0, 0, 1]), (group, 64))), t
