@@ -120,6 +120,10 @@ class SampleDesc(ctypes.Structure):
                 ("topo", _i32), ("parent", ctypes.POINTER(_i32))]
 
 
+class HoldDesc(ctypes.Structure):
+    _fields_ = [("n_req", _i32), ("n_pos", _i32), ("n_pages", _i32), ("page_size", _i32), ("table_len", _i32)]
+
+
 # Exported symbols and their signatures (every function of include/hrs.h).
 _SIGNATURES = {
     "hrs_validate_tree": (_i32, [ctypes.POINTER(_i32), _i32, _i32, ctypes.POINTER(_i32)]),
@@ -148,6 +152,7 @@ _SIGNATURES = {
     "kv_cache_append": (_i32, [ctypes.POINTER(AppendDesc)] + [_p] * 13),
     "accept_sample_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(SampleDesc)]),
     "accept_sample": (_i32, [ctypes.POINTER(SampleDesc)] + [_p] * 12 + [ctypes.c_size_t, _p]),
+    "accept_hold": (_i32, [ctypes.POINTER(HoldDesc)] + [_p] * 11),
     "hrs_strerror": (ctypes.c_char_p, [_i32]),
     "hrs_abi_version": (_i32, []),
     "hrs_last_hip_error": (_i32, []),
@@ -934,3 +939,35 @@ def accept_sample(logits, tokens, uniforms, token_prob, accept_node, accept_len,
     path [R,T], bonus [R]."""
     accept_sample_call(logits, tokens, uniforms, token_prob, accept_node, accept_len, path, bonus, workspace,
                        draft_probs, temperature, parent, status)(stream)
+
+
+def accept_hold_call(page_table, seq_len, accept_node, accept_len, path, bonus, held, last_node, n_pages: int,
+                     page_size: int, held_node=None, temperature=None) -> PreparedCall:
+    """The PreparedCall of accept_hold (same arguments, without the stream)."""
+    _rank("path", path, 2)
+    _rank("page_table", page_table, 2)
+    R, T = path.shape
+    chk = _SpanChecks()
+    for name, t, shape in (("path", path, (R, T)), ("page_table", page_table, (R, page_table.shape[1])),
+                           ("seq_len", seq_len, (R,)), ("accept_node", accept_node, (R,)),
+                           ("accept_len", accept_len, (R,)), ("bonus", bonus, (R,)), ("held", held, (R,)),
+                           ("last_node", last_node, (R,))):
+        chk(name, t, shape, _i32t())
+    chk("held_node", held_node, (R,), _i32t(), optional=True)
+    chk("temperature", temperature, (R,), _f32(), optional=True)
+    chk.on_gpu()
+    d = HoldDesc(R, T, n_pages, page_size, page_table.shape[1])
+    return chk.call("accept_hold",
+                    (ctypes.byref(d), _data(page_table), _data(seq_len), _data(temperature), _data(accept_node),
+                     _data(accept_len), _data(path), _data(bonus), _data(held), _data(last_node), _data(held_node)), d)
+
+
+def accept_hold(page_table, seq_len, accept_node, accept_len, path, bonus, held, last_node, n_pages: int,
+                page_size: int, held_node=None, temperature=None, stream=None):
+    """Requests that cannot go on taken out of an acceptance (accept_node,
+    accept_len, bonus [R] and path [R,T] become -1, held [R] 1): pages of
+    page_table [R,P] missing or full behind seq_len [R], a temperature [R]
+    that is negative or NaN, or held before. The others' accept_node goes to
+    last_node [R]; a newly held request's last_node to held_node [R]."""
+    accept_hold_call(page_table, seq_len, accept_node, accept_len, path, bonus, held, last_node, n_pages, page_size,
+                     held_node, temperature)(stream)

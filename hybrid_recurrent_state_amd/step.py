@@ -32,7 +32,7 @@ from typing import List, Optional, Sequence
 import numpy as np
 
 from . import (AcceptDesc, ConvAdvanceDesc, ConvDesc, GdnDesc, GdnLayerDesc, HRS_BF16, HRS_CHAIN, HRS_F32, HRS_TREE,
-               HrsError, RingDesc, RingRun, RollbackDesc, SpanSource, accept_greedy_workspace_bytes,
+               HrsError, RingDesc, RingRun, RollbackDesc, SpanSource, accept_greedy_workspace_bytes, accept_hold_call,
                accept_sample_call, accept_sample_workspace_bytes, attn_verify_span_call,
                attn_verify_span_workspace_bytes, kv_cache_append_call, lib, qk_norm_rope_call)
 
@@ -457,7 +457,7 @@ class AttnShape:
     n_heads: int
     n_kvheads: int
     head_dim: int
-    rotary_dim: int            # even, at most head_dim; 0: no rotation
+    rotary_dim: int            # multiple of 16, at most head_dim; 0: no rotation
     n_pages: int               # pages of one layer
     page_size: int             # slots of one page
     table_len: int             # pages one request may hold
@@ -474,7 +474,8 @@ class AttnBuffers:
     qkv [L,R,T,Hq+2Hkv,d] is each layer's projection; q_out, k_out its
     normalised and rotated heads. page_table holds distinct pages per request
     and seq_len [R] the slots that count (the step advances them itself).
-    uniforms [R,T] and temperature [R] are read where acceptance samples."""
+    uniforms [R,T] and temperature [R] are read where acceptance samples.
+    held [R] marks requests that could not go on (see HybridVerifyStep)."""
 
     def __init__(self, shape: AttnShape, step: StepShape, device="cuda"):
         import torch
@@ -510,6 +511,11 @@ class AttnBuffers:
         self.uniforms = z(R, T, dtype=torch.float32)
         self.token_prob = z(R, T, dtype=torch.float32)
         self.temperature = torch.ones(R, device=device)
+        self.held = z(R)
+        self.last_node = z(R)
+        # Where a held request's recurrent state is: a position of checkpoint
+        # buffer 0 or 1, or -1.
+        self.held_node = [z(R), z(R)]
         nbytes = max(attn_verify_span_workspace_bytes(R, T, Hq, Hkv, d),
                      accept_sample_workspace_bytes(R, T, step.vocab) if step.vocab else 0)
         self.workspace = e(max(16, nbytes), dtype=torch.uint8)   # one stream: the calls take turns
@@ -523,6 +529,15 @@ class HybridVerifyStep(FusedVerifyStep):
     with ``sample``: ``uniforms`` and ``temperature`` of the AttnBuffers) the
     accepted rows of all attention layers go into their pages and ``seq_len``
     advances, so replays of the captured step carry on by themselves.
+
+    A request that cannot go on is held (accept_hold): its accepted rows do not
+    fit in its page table, a page for them is not there, or its temperature is
+    negative or NaN. The step then reports -1 as its accepted length and bonus
+    token and leaves its pages, length, conv and recurrent state as they were;
+    so do all later steps. The other requests go on. To take it up again:
+    ``materialize()`` (which writes every request's recurrent state, a held
+    one's from in front of the step that held it), give it what it lacks, and
+    start a new speculation with a new HybridVerifyStep.
     """
 
     def __init__(self, bufs: StepBuffers, attn: AttnBuffers, parent=None, runs: Optional[Sequence[tuple]] = None,
@@ -530,6 +545,9 @@ class HybridVerifyStep(FusedVerifyStep):
         super().__init__(bufs, parent, runs, silu, q_scale, l2_eps)
         s, b, n = attn.shape, attn, bufs.shape.n_layers
         self.attn = attn
+        b.held.zero_()
+        for node in b.held_node:
+            node.fill_(-1)
         after = [(i + 1) * n // s.n_layers - 1 for i in range(s.n_layers)] if s.after is None else list(s.after)
         if len(after) != s.n_layers or any(not 0 <= l < n for l in after) or after != sorted(after):
             raise ValueError(f"after: {after}, expected {s.n_layers} ascending GDN layers of {n}")
@@ -546,6 +564,11 @@ class HybridVerifyStep(FusedVerifyStep):
             bufs.logits, bufs.tokens, b.uniforms, b.token_prob, bufs.accept_node, bufs.accept_len, bufs.path,
             bufs.bonus, b.workspace, temperature=b.temperature, parent=self._parent,
             status=b.status[-2]) if sample else None
+        # By the checkpoint buffer that a step's spans start from; None: from ``state``.
+        self.hold_calls = {c: accept_hold_call(
+            b.page_table, b.seq_len, bufs.accept_node, bufs.accept_len, bufs.path, bufs.bonus, b.held, b.last_node,
+            s.n_pages, s.page_size, held_node=None if c is None else b.held_node[c],
+            temperature=b.temperature if sample else None) for c in (None, 0, 1)}
         self.append_call = kv_cache_append_call(
             b.k_out, b.v, b.k_cache, b.v_cache, b.page_table, b.seq_len, bufs.accept_len, b.seq_len, bufs.path,
             b.k_scale, b.v_scale, b.status[-1])
@@ -560,7 +583,22 @@ class HybridVerifyStep(FusedVerifyStep):
             super().launch_accept(stream)
         else:
             self.sample_call(stream)
+        self.hold_calls[None if self.first else 1 - self.cur](stream)
 
     def launch_rollback(self, stream: int) -> None:
         super().launch_rollback(stream)
         self.append_call(stream)
+
+    def materialize(self, stream=None) -> None:
+        """state <- every request's recurrent state after its last accepted
+        position (held ones': in front of the step that held them)."""
+        import torch
+        if stream is None:
+            stream = torch.cuda.current_stream()
+        h = stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
+        s, b = self.bufs.shape, self.bufs
+        d = RollbackDesc(s.n_layers, s.n_req, s.n_pos, s.n_vheads, s.d_k, s.d_v, 0, 0, HRS_F32)
+        for c in (0, 1):
+            _check(lib.rollback_restore(ctypes.byref(d), self.ckpts[c].data_ptr(), b.state.data_ptr(), None, None,
+                                        self.attn.held_node[c].data_ptr(), b.status.data_ptr(), h), "rollback_restore")
+        super().materialize(stream)

@@ -32,6 +32,8 @@
  *                       pages of every layer, indices read on the device
  *   accept_sample       verification of the drafts against the target's
  *                       probabilities from given random numbers
+ *   accept_hold         requests that cannot go on (pages full or missing, no
+ *                       valid temperature) taken out before the commit
  *
  * Conventions shared by every entry point
  * ----------------------------------------
@@ -782,6 +784,41 @@ int accept_sample(const hrs_sample_desc* desc, const void* logits, const int32_t
                   float* token_prob, int32_t* accept_node, int32_t* accept_len, int32_t* path,
                   int32_t* bonus, int32_t* status, void* workspace, size_t workspace_bytes,
                   void* stream);
+
+typedef struct {
+  int32_t n_req;     /* R                                                  */
+  int32_t n_pos;     /* T of the span, in [1, HRS_MAX_POS]                 */
+  int32_t n_pages;   /* pages, slots of a page and entries of a request's  */
+  int32_t page_size; /* table, as hrs_cache_desc                           */
+  int32_t table_len;
+} hrs_hold_desc;
+
+/*
+ * accept_hold - takes the requests that cannot go on out of an acceptance,
+ * between accept_greedy or accept_sample and the entry points that commit it
+ * ([P3] Safety boundary: rejected before execution). A request goes on if
+ * held[r] is 0, its temperature is not negative or NaN, accept_len[r] and
+ * accept_node[r] are in [0, T), path[r][0..accept_len[r]] too, and slots
+ * seq_len[r] .. seq_len[r] + accept_len[r] lie inside its page table, in
+ * pages that are there. Then last_node[r] = accept_node[r]. Otherwise
+ *     accept_node[r] = accept_len[r] = bonus[r] = -1,  path[r][:] = -1
+ * and, where held[r] was 0, held[r] = 1 and held_node[r] = last_node[r].
+ * rollback_restore, conv_state_advance, kv_cache_append and the next
+ * gdn_verify_span_from or gdn_layer_verify_span all leave a request with
+ * such indices as it is, so none of its state moves, in this step or later
+ * ones, until the caller clears held[r]. Its recurrent state then still is in
+ * the checkpoint buffer that this step's spans started from, at held_node[r].
+ *
+ * Layouts:  page_table [R][table_len], seq_len [R] int32, temperature [R]
+ *           float32 or NULL (1); accept_node, accept_len, bonus, held,
+ *           last_node [R] and path [R][T] int32, read and written; held_node
+ *           [R] int32 or NULL (spans that started from `state`); all device.
+ * Errors: HRS_EINVAL (R > 65535; sizes as hrs_cache_desc), HRS_EALIGN,
+ * HRS_EDEVICE.
+ */
+int accept_hold(const hrs_hold_desc* desc, const int32_t* page_table, const int32_t* seq_len,
+                const float* temperature, int32_t* accept_node, int32_t* accept_len, int32_t* path,
+                int32_t* bonus, int32_t* held, int32_t* last_node, int32_t* held_node, void* stream);
 
 /* ------------------------------------------------------------------------ */
 /* Misc                                                                     */
