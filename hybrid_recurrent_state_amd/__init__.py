@@ -711,6 +711,21 @@ class _SpanChecks(_Checks):
             if a < d and c < b:
                 raise ValueError(f"{name} overlaps {other}")
 
+    def written(self, *names: str) -> None:
+        """The tensors of these names share no byte with any other tensor of
+        the call: blocks write them while others read."""
+        spans = []
+        for name, t in self.seen:
+            last = sum((n - 1) * st for n, st in zip(t.shape, t.stride()))
+            spans.append((t.data_ptr(), t.data_ptr() + (last + 1) * t.element_size(), name))
+        spans.sort()
+        for i, (_, end, name) in enumerate(spans):
+            for start, _, other in spans[i + 1:]:
+                if start >= end:
+                    break
+                if name in names or other in names:
+                    raise ValueError(f"{other} overlaps {name}")
+
     def on_gpu(self) -> None:
         super().on_gpu()
         dev = self.seen[0][1].device
@@ -868,10 +883,14 @@ def kv_cache_append_call(k, v, k_cache, v_cache, page_table, seq_len, accept_len
     chk("page_table", page_table, (R, page_table.shape[1]), _i32t())
     chk("seq_len", seq_len, (R,), _i32t())
     chk("accept_len", accept_len, (R,), _i32t())
-    chk("seq_len_out", seq_len_out, (R,), _i32t(), optional=True)
     chk("path", path, (R, T), _i32t(), optional=True)
     _scales(chk, (L, Hkv), code, k_scale=k_scale, v_scale=v_scale)
     chk.status(status)
+    chk("seq_len_out", seq_len_out, (R,), _i32t(), optional=True)
+    in_place = seq_len_out is not None and seq_len_out.data_ptr() == seq_len.data_ptr()
+    if in_place:
+        chk.seen.pop()
+    chk.written("k_cache", "v_cache", "seq_len" if in_place else "seq_len_out", "status")
     chk.on_gpu()
     d = AppendDesc(L, R, T, Hkv, D, _dtype_code(k), ks, vs, CacheDesc(N, S, page_table.shape[1], code))
     return chk.call("kv_cache_append",
@@ -885,7 +904,7 @@ def kv_cache_append(k, v, k_cache, v_cache, page_table, seq_len, accept_len, seq
     """Rows path[r][0..accept_len[r]] (path None: 0..accept_len[r]) of the
     span's k, v [L,R,T,Hkv,D] into slots seq_len[r] ... of every layer's pages
     (k_cache, v_cache [L,pages,Hkv,slots,D]); seq_len_out [R] (seq_len itself,
-    a buffer apart from it, or None) receives the new lengths."""
+    a buffer apart from all others, or None) receives the new lengths."""
     kv_cache_append_call(k, v, k_cache, v_cache, page_table, seq_len, accept_len, seq_len_out, path, k_scale,
                          v_scale, status)(stream)
 

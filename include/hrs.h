@@ -701,7 +701,8 @@ typedef struct {
  *           k_scale, v_scale [L][Hkv] float32, device (e4m3 caches only;
  *           4-byte aligned)
  *           seq_len_out [R] int32, device: seq_len itself, a buffer apart
- *           from it, or NULL
+ *           from every other one, or NULL
+ * The caches and status must not overlap any other buffer of the call.
  * A request is left untouched (seq_len_out[r] = seq_len[r]) and counted in
  * status (optional device int32) when accept_len is outside [0, T), seq_len
  * is negative, seq_len + accept_len + 1 > table_len * page_size, or one of
