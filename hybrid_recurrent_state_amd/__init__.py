@@ -938,6 +938,7 @@ def accept_sample_call(logits, tokens, uniforms, token_prob, accept_node, accept
         chk("draft_probs", draft_probs, (R, T, V), _in_dtypes("draft_probs", draft_probs))
     chk("temperature", temperature, (R,), _f32(), optional=True)
     chk.status(status)
+    chk.written("token_prob", "accept_node", "accept_len", "path", "bonus", "workspace", "status")
     d, par = sample_desc(R, T, V, _dtype_code(logits), HRS_F32 if draft_probs is None else _dtype_code(draft_probs),
                          parent)
     chk.on_gpu()
@@ -974,6 +975,7 @@ def accept_hold_call(page_table, seq_len, accept_node, accept_len, path, bonus, 
         chk(name, t, shape, _i32t())
     chk("held_node", held_node, (R,), _i32t(), optional=True)
     chk("temperature", temperature, (R,), _f32(), optional=True)
+    chk.written("accept_node", "accept_len", "path", "bonus", "held", "last_node", "held_node")
     chk.on_gpu()
     d = HoldDesc(R, T, n_pages, page_size, page_table.shape[1])
     return chk.call("accept_hold",

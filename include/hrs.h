@@ -776,6 +776,7 @@ size_t accept_sample_workspace_bytes(const hrs_sample_desc* desc);
  *           accept_node, accept_len, bonus [R], path [R][T] int32; all
  *           device. workspace: device scratch of at least
  *           accept_sample_workspace_bytes(desc) bytes, contents ignored.
+ * Outputs and workspace must not overlap each other or any input.
  * Size limits as accept_greedy, R <= 65535 and V <= 2^30. Errors: HRS_EINVAL,
  * HRS_EALIGN, HRS_EGEOMETRY, HRS_EUNSUPPORTED (draft_probs with a tree),
  * HRS_EDEVICE.
@@ -814,6 +815,7 @@ typedef struct {
  *           float32 or NULL (1); accept_node, accept_len, bonus, held,
  *           last_node [R] and path [R][T] int32, read and written; held_node
  *           [R] int32 or NULL (spans that started from `state`); all device.
+ *           No two of them overlap.
  * Errors: HRS_EINVAL (R > 65535; sizes as hrs_cache_desc), HRS_EALIGN,
  * HRS_EDEVICE.
  */

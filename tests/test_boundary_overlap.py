@@ -35,3 +35,34 @@ def test_append_refuses_written_buffers_over_others():
         hrs.kv_cache_append(**{**ok, "accept_len": both[:4], "seq_len_out": both[3:7]})
     with pytest.raises(ValueError, match="GPU"):
         hrs.kv_cache_append(**{**ok, "seq_len": both[:4], "seq_len_out": both[4:8], "accept_len": both[8:]})
+
+
+def test_sample_refuses_outputs_over_inputs_or_each_other():
+    import torch
+    i32, f32 = torch.int32, torch.float32
+    ok = dict(logits=t(2, 4, 64), tokens=t(2, 4, dtype=i32), uniforms=t(2, 4, dtype=f32), token_prob=t(2, 4, dtype=f32),
+              accept_node=t(2, dtype=i32), accept_len=t(2, dtype=i32), path=t(2, 4, dtype=i32), bonus=t(2, dtype=i32),
+              workspace=t(64, dtype=f32), draft_probs=t(2, 4, 64, dtype=f32), temperature=t(2, dtype=f32),
+              status=t(4, dtype=i32))
+    for more in (dict(), dict(draft_probs=None, temperature=None, status=None), dict(draft_probs=ok["logits"])):
+        with pytest.raises(ValueError, match="GPU"):
+            hrs.accept_sample(**{**ok, **more})
+    for bad in (dict(path=ok["tokens"]), dict(token_prob=ok["uniforms"]), dict(accept_node=ok["accept_len"]),
+                dict(bonus=ok["tokens"][1, :2]), dict(status=ok["bonus"]), dict(workspace=ok["draft_probs"].view(-1)),
+                dict(temperature=ok["token_prob"][0, :2])):
+        with pytest.raises(ValueError, match="overlaps"):
+            hrs.accept_sample(**{**ok, **bad})
+
+
+def test_hold_refuses_written_buffers_over_others():
+    import torch
+    i32 = torch.int32
+    ok = dict(page_table=t(2, 3, dtype=i32), seq_len=t(2, dtype=i32), accept_node=t(2, dtype=i32),
+              accept_len=t(2, dtype=i32), path=t(2, 5, dtype=i32), bonus=t(2, dtype=i32), held=t(2, dtype=i32),
+              last_node=t(2, dtype=i32), n_pages=4, page_size=16, held_node=t(2, dtype=i32))
+    with pytest.raises(ValueError, match="GPU"):
+        hrs.accept_hold(**ok)
+    for bad in (dict(held=ok["seq_len"]), dict(held_node=ok["last_node"]), dict(bonus=ok["path"][1, :2]),
+                dict(last_node=ok["page_table"][0, 1:])):
+        with pytest.raises(ValueError, match="overlaps"):
+            hrs.accept_hold(**{**ok, **bad})
