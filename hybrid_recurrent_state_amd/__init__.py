@@ -699,18 +699,6 @@ class _SpanChecks(_Checks):
         self.seen.append((name, t))
         return stride
 
-    def apart(self, name: str, t, **others) -> None:
-        """t shares no byte with the others (from their first to their last
-        element): blocks write their part of it while others still read."""
-        def span(x):
-            last = sum((n - 1) * st for n, st in zip(x.shape, x.stride()))
-            return x.data_ptr(), x.data_ptr() + (last + 1) * x.element_size()
-        a, b = span(t)
-        for other, x in others.items():
-            c, d = span(x)
-            if a < d and c < b:
-                raise ValueError(f"{name} overlaps {other}")
-
     def written(self, *names: str) -> None:
         """The tensors of these names share no byte with any other tensor of
         the call: blocks write them while others read."""
@@ -784,11 +772,14 @@ def qk_norm_rope_call(q, k, q_weight, k_weight, freq, seq_len, q_out, k_out, par
     chk("seq_len", seq_len, (R,), _i32t())
     chk("q_out", q_out, (R, T, Hq, D), dt)
     chk("k_out", k_out, (R, T, Hkv, D), dt)
-    chk.apart("q_out", q_out, k=k, k_out=k_out)
-    chk.apart("k_out", k_out, q=q)
+    # In place where that side is dense; blocks still read everything else.
+    written = []
     for name, out, x in (("q", q_out, q), ("k", k_out, k)):
-        if out.data_ptr() != x.data_ptr() or not x.is_contiguous():
-            chk.apart(f"{name}_out", out, **{name: x})
+        in_place = out.data_ptr() == x.data_ptr() and x.is_contiguous()
+        if in_place:
+            chk.seen = [(n, y) for n, y in chk.seen if n != f"{name}_out"]
+        written.append(name if in_place else f"{name}_out")
+    chk.written(*written)
     par, par_p = _parent_array(parent, R, T)
     chk.on_gpu()
     rot = 0 if freq is None else 2 * freq.shape[0]
@@ -838,10 +829,10 @@ def attn_verify_span_call(q, k, v, k_cache, v_cache, page_table, seq_len, out, w
     chk("page_table", page_table, (R, page_table.shape[1]), _i32t())
     chk("seq_len", seq_len, (R,), _i32t())
     chk("out", out, (R, T, Hq, D), dt)
-    chk.apart("out", out, q=q, k=k, v=v)
     chk("workspace", workspace)
     _scales(chk, (Hkv,), code, k_scale=k_scale, v_scale=v_scale)
     chk.status(status)
+    chk.written("out", "workspace", "status")
     par, par_p = _parent_array(parent, R, T)
     chk.on_gpu()
     cache = CacheDesc(N, S, page_table.shape[1], code)

@@ -586,8 +586,9 @@ typedef struct {
  *           seq_len [R] int32, device           tokens before the root
  *           q_out [R][T][Hq][d], k_out [R][T][Hkv][d]  dtype, dense
  * q_out may be q itself, and k_out k, where that side is dense; any other
- * overlap is not allowed. Errors: HRS_EINVAL (also R * T > 2^24), HRS_EALIGN,
- * HRS_EGEOMETRY, HRS_EUNSUPPORTED (d, rot), HRS_EDEVICE.
+ * overlap of an output with a buffer of the call is not allowed. Errors:
+ * HRS_EINVAL (also R * T > 2^24), HRS_EALIGN, HRS_EGEOMETRY, HRS_EUNSUPPORTED
+ * (d, rot), HRS_EDEVICE.
  */
 int qk_norm_rope(const hrs_qk_desc* desc, const void* q, const void* k, const void* q_weight,
                  const void* k_weight, const double* freq, const int32_t* seq_len, void* q_out,
@@ -654,8 +655,9 @@ size_t attn_verify_span_workspace_bytes(const hrs_attn_desc* desc);
  *           out [R][T][Hq][d] dtype, dense
  *           workspace: device scratch of at least
  *           attn_verify_span_workspace_bytes(desc) bytes, contents ignored
- * out must not overlap q, k or v. A request whose seq_len is outside [0,
- * table_len * page_size] keeps its rows of out as they were; status (optional device int32) receives the
+ * out, status and workspace must not overlap each other or any input. A
+ * request whose seq_len is outside [0, table_len * page_size] keeps its rows
+ * of out as they were; status (optional device int32) receives the
  * number of such requests. Calls that may run at the same time need
  * workspaces of their own. Errors: HRS_EINVAL (sizes, dtype combination,
  * R > 4096, Hkv > 1024, Hq / Hkv > 64; also where one request's longest table

@@ -66,3 +66,27 @@ def test_hold_refuses_written_buffers_over_others():
                 dict(last_node=ok["page_table"][0, 1:])):
         with pytest.raises(ValueError, match="overlaps"):
             hrs.accept_hold(**{**ok, **bad})
+
+
+def test_attention_layer_calls_refuse_outputs_over_any_input():
+    import torch
+    i32, f32, f64 = torch.int32, torch.float32, torch.float64
+    ok = dict(q=t(2, 3, 4, 64), k=t(2, 3, 2, 64), q_weight=t(64), k_weight=t(64), freq=t(16, dtype=f64), seq_len=t(2, dtype=i32),
+              q_out=t(2, 3, 4, 64), k_out=t(2, 3, 2, 64))
+    for more in (dict(), dict(q_out=ok["q"]), dict(q_out=ok["q"], k_out=ok["k"]), dict(k_weight=ok["q_weight"])):
+        with pytest.raises(ValueError, match="GPU"):
+            hrs.qk_norm_rope(**{**ok, **more})
+    for bad in (dict(q_weight=ok["q_out"].view(-1)[64:128]), dict(freq=ok["k_out"].view(f64).view(-1)[:16]),
+                dict(q_out=ok["q"], q_weight=ok["q"].view(-1)[64:128]), dict(seq_len=ok["q_out"].view(i32).view(-1)[:2])):
+        with pytest.raises(ValueError, match="overlaps"):
+            hrs.qk_norm_rope(**{**ok, **bad})
+    ok = dict(q=t(2, 3, 4, 64), k=t(2, 3, 2, 64), v=t(2, 3, 2, 64), k_cache=t(5, 2, 16, 64), v_cache=t(5, 2, 16, 64),
+              page_table=t(2, 3, dtype=i32), seq_len=t(4, dtype=i32)[:2], out=t(2, 3, 4, 64), workspace=t(64, dtype=f32),
+              status=t(4, dtype=i32))
+    for more in (dict(), dict(status=None), dict(v=ok["k"], v_cache=ok["k_cache"])):
+        with pytest.raises(ValueError, match="GPU"):
+            hrs.attn_verify_span(**{**ok, **more})
+    for bad in (dict(status=ok["seq_len"]), dict(workspace=ok["out"].view(-1)), dict(page_table=ok["out"].view(i32).view(-1)[:6].view(2, 3)),
+                dict(out=ok["v_cache"].view(-1)[:1536].view(2, 3, 4, 64)), dict(status=ok["workspace"].view(i32))):
+        with pytest.raises(ValueError, match="overlaps"):
+            hrs.attn_verify_span(**{**ok, **bad})
