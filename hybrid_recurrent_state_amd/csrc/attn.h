@@ -141,11 +141,6 @@ __device__ __forceinline__ int attn_cut(int b, int total, int log_blocks) {
   return static_cast<int>((static_cast<int64_t>(b) * total) >> log_blocks);
 }
 
-// A cut inside a head's units without a tile moves to the head's end, one
-// within this many tiles of its start to the start: a part is written and read
-// again, which is more than a few tiles' time where heads are short.
-__device__ __forceinline__ int attn_near(int total, int log_blocks) { return min(2, total >> (log_blocks + 1)); }
-
 // Launches of one type (rows class cls, head size d); the number of rows a
 // block holds and the slots of its tile for it.
 struct AttnShape {

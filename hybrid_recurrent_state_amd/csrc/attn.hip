@@ -37,16 +37,14 @@ __global__ __launch_bounds__(NS > 1 ? 64 * NS : 256) void attn_join_kernel(const
   const int r = args.req0 + i;
   if (end == first) return;
   const int units = (end - first) / heads;
-  const int s0 = first + seg * units;
+  const int s0 = first + seg * units, s1 = s0 + units;
   // Block of a unit: the last whose run starts at or before it.
   auto block_of = [&](int u) {
     if (total <= (1 << log_blocks)) return u;
     return static_cast<int>((((static_cast<int64_t>(u) + 1) << log_blocks) - 1) / total);
   };
-  // The segment's cuts are those past the tiles near its start and ahead of its
-  // units without a tile.
-  const int b0 = block_of(s0 + attn_near(total, log_blocks)), b1 = block_of(s0 + units - kExtraUnits - 1);
-  if (b0 >= b1) return;                       // one block had all of it and wrote the result
+  const int b0 = block_of(s0), b1 = block_of(s1 - 1);
+  if (b0 == b1) return;                       // one block had all of it and wrote the result
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int task = NS > 1 ? blockIdx.y : blockIdx.y * 4 + wave;
   const int tiles = (min(rows_per_block, args.rows - rb * rows_per_block) + 15) / 16;

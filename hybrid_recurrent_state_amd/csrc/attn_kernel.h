@@ -917,16 +917,6 @@ struct AttnPlan {
     *n = at;
     return i;
   }
-
-  // Cut u, moved to a head's border where it is near one.
-  __device__ __forceinline__ int snap(const AttnLens& a, int ts, int u) const {
-    if (u >= total) return total;
-    int in_req, n;
-    find(u, &in_req, &n);
-    const AttnUnits un = attn_units(a, n, ts);
-    const int pos = in_req - __builtin_amdgcn_readfirstlane(in_req / un.all) * un.all;
-    return pos >= un.tiles() ? u + un.all - pos : pos <= attn_near(total, a.log_blocks) ? u - pos : u;
-  }
 };
 
 // Refused requests of the whole call: a count per thread, added in order.
@@ -960,8 +950,8 @@ void attn_kernel(const int32_t* len, int n, int heads, int most, int window, int
   int u, u1, in_req = 0, i = 0;
   {
     const AttnPlan plan(lens, C::TS);
-    u = plan.snap(lens, C::TS, attn_cut(blockIdx.x, plan.total, log_blocks));
-    u1 = plan.snap(lens, C::TS, attn_cut(blockIdx.x + 1, plan.total, log_blocks));
+    u = attn_cut(blockIdx.x, plan.total, log_blocks);
+    u1 = attn_cut(blockIdx.x + 1, plan.total, log_blocks);
     if (u < u1) i = plan.find(u, &in_req, &blk.len);
     if (blockIdx.x == 0) {
       plan.write(args.plan, n);

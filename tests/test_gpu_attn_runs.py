@@ -164,8 +164,8 @@ MANY = [(d, rows, ratio) for d in (64, 128, 256) for rows in ROWS for ratio in (
 @pytest.mark.parametrize("dtype,cache", KINDS)
 def test_runs_of_many_tiles(hrs, dtype, cache, d, rows, ratio):
     """Four ragged requests, one of them without a context, three key heads:
-    1.5, 3 and 8 units a block (a cut moves to a head's border over up to 0, 1
-    and 2 units). Chains and trees, with and without a window, absent pages."""
+    1.5, 3 and 8 units a block. Chains and trees, with and without a window,
+    absent pages."""
     T, G = rows
     tree, windowed = (ROWS.index(rows) // 2 + d // 128) % 2 == 1, (ROWS.index(rows) + d // 128) % 2 == 1
     Hkv, S = 3, 32 if d == 128 else 64
@@ -176,7 +176,7 @@ def test_runs_of_many_tiles(hrs, dtype, cache, d, rows, ratio):
     if windowed:
         lens[0] += lens[3] // 3
     units, blocks, ring = total_units(cache, d, T, G, Hkv, lens, window)
-    assert min(2, units // blocks // 2) == {1.5: 0, 3: 1, 8: 2}[ratio], (units, blocks)
+    assert 0.85 * ratio < units / blocks < 1.4 * ratio, (units, blocks)
     if ratio == 8:
         assert units / blocks > ring + 1
     a = Runs(4, T, G, Hkv, d, S, lens, dtype, cache, tree, window, seed=T * G + d)
