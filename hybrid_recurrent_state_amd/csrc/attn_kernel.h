@@ -31,10 +31,19 @@
 //    rescaling of O are per-lane numbers.
 //  - The reference m moves only when a row's maximum exceeds it by more than
 //    8 (in log2), so most tiles neither reduce across lanes nor rescale; P is
-//    at most 2^8 and l and O are f32, which loses nothing. P is rounded to the
-//    span's type for the product with V, once, relative to itself.
-//  - e4m3 tiles stay e4m3 in LDS and are widened (exactly) to bf16 between LDS
-//    and the products; the scales are factors of c and of O. (Widened once per
+//    at most 2^8 and l and O are f32, which loses nothing.
+//  - P for the product with bf16 values is the sum of two bf16 parts, the upper
+//    bits and what they leave: 2^-15 of a weight at most is lost. One part
+//    alone (2^-9) made the result's error 0.0023 instead of 0.0017, which is
+//    what rounding the result costs, and took 6% less time (26,758 slots: 41.5
+//    / 44.1 us; 16 trees: 109.9 / 113.7; 1000 slots: no difference, since 16
+//    slots fill half of a matrix instruction and the second part the other).
+//    Beside e4m3 values P is float16 (2^-11 of a weight, or 2^-32 of the row's
+//    largest where that is more), which the values are widened to as well: the
+//    same matrix rate, no second part (two bf16 parts took 190 instead of 160
+//    us at 262,144 slots).
+//  - e4m3 tiles stay e4m3 in LDS and are widened (exactly) to 16 bits between
+//    LDS and the products; the scales are factors of c and of O. (Widened once per
 //    block into a second LDS tile: 215 us instead of 160 at 262,144 slots: the
 //    extra pass and its barrier were not hidden.) The span's own tile is of
 //    the span's type and takes the ring's place after the cache's tiles.
@@ -60,7 +69,9 @@ namespace hrs {
 namespace {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef __attribute__((address_space(3))) char lds_char;
 
 // The same number, but what is computed from it is computed after this point:
@@ -139,6 +150,10 @@ template <int KIND, int D, int CLS> struct AttnBlock {
   static constexpr int DT = D / 16;
   static constexpr int QC = D * ESZ / 64;                                 // pieces of a query row per lane
   static_assert(SB <= 2, "one or two blocks of 16 slots");
+  // P's exponent is lifted beside an e4m3 cache: at most 8 + 7, so that the
+  // small weights of many slots are not lost below float16's range (2^-24:
+  // 2^-31 of the reference's weight).
+  static constexpr float kLift = KIND == kF8 ? 7.0f : 0.0f;
   static_assert(LPS >= 1 && LPS * 64 * C::WR == 2 * C::SS * RCPR && (C::NST - 1) * LPS < 64, "whole loads");
 
   const AttnBase& a;
@@ -371,7 +386,8 @@ template <int KIND, int D, int CLS> struct AttnBlock {
   }
 
   // One tile: its scores, weights and the product with the values. F8: the
-  // tile is e4m3, widened to bf16 (exactly) on the way to the products.
+  // tile is e4m3, widened (exactly) on the way to the products, keys to bf16,
+  // values to float16.
   template <bool F8> __device__ __forceinline__ void tile(int u, const char* base, bool span, bool mask, uint32_t there) {
     constexpr int EB = F8 ? 1 : ESZ, ROW = D * EB, PIECES = ROW / 16;
     constexpr bool kRare = KIND == kF8 && !F8;       // a span tile after the loop over the cache's
@@ -466,10 +482,14 @@ template <int KIND, int D, int CLS> struct AttnBlock {
         for (int dt = 0; dt < DT; ++dt) o[rt][dt] *= keep;
       }
     }
-    u32x2 pb[C::RT][SB];       // P^T as the products' second operand (bf16)
+    // P^T as the products' second operand. float16 beside e4m3 values, which
+    // it holds exactly as well; beside bf16 values two bf16 parts, the upper
+    // bits and what they leave (and 2^-40 of P, so that it is positive where P
+    // is: infinite values must not meet a zero).
+    u32x2 pb[C::RT][F8 ? 1 : 2][SB];
 #pragma unroll
     for (int rt = 0; rt < C::RT; ++rt) {
-      const float mb = m[rt] == -__builtin_inff() ? 0.0f : m[rt];
+      const float mb = m[rt] == -__builtin_inff() ? 0.0f : m[rt] - kLift;
       float sum = 0.0f;
 #pragma unroll
       for (int sb = 0; sb < SB; ++sb) {
@@ -479,8 +499,17 @@ template <int KIND, int D, int CLS> struct AttnBlock {
           sum += p;
           s[rt][sb][i] = p;
         }
-        if constexpr (KIND != kF32)
-          pb[rt][sb] = u32x2{pack_bf16(s[rt][sb][0], s[rt][sb][1]), pack_bf16(s[rt][sb][2], s[rt][sb][3])};
+        const f32x4 p = s[rt][sb];
+        if constexpr (F8) {
+          pb[rt][0][sb] = u32x2{pack_f16(p[0], p[1]), pack_f16(p[2], p[3])};
+        } else if constexpr (KIND != kF32) {
+          auto rest = [&](int i) {
+            return fmaf(p[i], 0x1p-40f, p[i] - __uint_as_float(__float_as_uint(p[i]) & 0xFFFF0000u));
+          };
+          auto upper = [&](int i) { return __builtin_amdgcn_perm(__float_as_uint(p[i + 1]), __float_as_uint(p[i]), 0x07060302u); };
+          pb[rt][0][sb] = u32x2{upper(0), upper(2)};
+          pb[rt][1][sb] = u32x2{pack_bf16(rest(0), rest(1)), pack_bf16(rest(2), rest(3))};
+        }
       }
       l[rt] += sum;
     }
@@ -491,7 +520,7 @@ template <int KIND, int D, int CLS> struct AttnBlock {
       for (int half = 0; half < kHalves; ++half) {
         if (half > 0) v.load(vt, n16, g, half);
         if (mask) odd_seen = __any(v.drop_odd()) || odd_seen;
-        values_bf16<F8>(v, half, pb);
+        values_16<F8>(v, half, pb);
       }
     }
   }
@@ -500,6 +529,15 @@ template <int KIND, int D, int CLS> struct AttnBlock {
   static __device__ __forceinline__ uint32_t widen2(uint32_t w, bool high) {
     return __builtin_bit_cast(uint32_t, high ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, true)
                                              : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, false));
+  }
+  // Two of them as float16.
+  static __device__ __forceinline__ uint32_t widen2_f16(uint32_t w, bool high) {
+    return __builtin_bit_cast(uint32_t, high ? __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, true)
+                                             : __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, false));
+  }
+  // Two float32 rounded to float16 (nearest), the first in the low half.
+  static __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+    return __builtin_bit_cast(uint32_t, f16x2{static_cast<_Float16>(lo), static_cast<_Float16>(hi)});
   }
   static __device__ __forceinline__ u32x4 widen8(uint32_t a, uint32_t b) {
     return u32x4{widen2(a, false), widen2(a, true), widen2(b, false), widen2(b, true)};
@@ -569,8 +607,8 @@ template <int KIND, int D, int CLS> struct AttnBlock {
     __device__ __forceinline__ u32x2 operand(int sb, int x) const {
       if constexpr (F8) {
         const uint32_t sel = x & 2 ? 0x07030602u : 0x05010400u;
-        return u32x2{widen2(__builtin_amdgcn_perm(w[sb][1][x >> 2], w[sb][0][x >> 2], sel), x & 1),
-                     widen2(__builtin_amdgcn_perm(w[sb][3][x >> 2], w[sb][2][x >> 2], sel), x & 1)};
+        return u32x2{widen2_f16(__builtin_amdgcn_perm(w[sb][1][x >> 2], w[sb][0][x >> 2], sel), x & 1),
+                     widen2_f16(__builtin_amdgcn_perm(w[sb][3][x >> 2], w[sb][2][x >> 2], sel), x & 1)};
       } else {
         const uint32_t sel = x & 1 ? 0x07060302u : 0x05040100u;
         return u32x2{__builtin_amdgcn_perm(w[sb][1][x >> 1], w[sb][0][x >> 1], sel),
@@ -579,28 +617,43 @@ template <int KIND, int D, int CLS> struct AttnBlock {
     }
   };
 
-  // O^T += V^T P^T.
-  template <bool F8> __device__ __forceinline__ void values_bf16(const Values<F8>& v, int half, const u32x2 (&pb)[C::RT][SB]) {
+  // O^T += V^T P^T. P in two parts: both in one product where a tile has 16
+  // slots of a wave, otherwise the second ones behind all columns' first.
+  template <bool F8>
+  __device__ __forceinline__ void values_16(const Values<F8>& v, int half, const u32x2 (&pb)[C::RT][F8 ? 1 : 2][SB]) {
+    constexpr int STEPS = F8 ? 1 : SB, AT = STEPS == 1 ? 1 : kCols;
 #pragma unroll
-    for (int x = 0; x < kCols; ++x) {
-      u32x2 w[SB];
+    for (int x0 = 0; x0 < kCols; x0 += AT) {
+      u32x2 w[AT][SB];
 #pragma unroll
-      for (int sb = 0; sb < SB; ++sb) w[sb] = v.operand(sb, x);
+      for (int x = 0; x < AT; ++x)
 #pragma unroll
-      for (int rt = 0; rt < C::RT; ++rt) {
-        f32x4& acc = o[rt][half * kCols + x];
-        acc = product(w, pb[rt], acc);
-      }
+        for (int sb = 0; sb < SB; ++sb) w[x][sb] = v.operand(sb, x0 + x);
+#pragma unroll
+      for (int part = 0; part < STEPS; ++part)
+#pragma unroll
+        for (int x = 0; x < AT; ++x)
+#pragma unroll
+          for (int rt = 0; rt < C::RT; ++rt) {
+            f32x4& acc = o[rt][half * kCols + x0 + x];
+            if constexpr (F8) acc = product_f16(w[x], pb[rt][0], acc);
+            else if constexpr (SB == 1) acc = product_bf16(w[x][0], w[x][0], pb[rt][0][0], pb[rt][1][0], acc);
+            else acc = product_bf16(w[x][0], w[x][1], pb[rt][part][0], pb[rt][part][1], acc);
+          }
     }
   }
-  static __device__ __forceinline__ f32x4 product(const u32x2 (&w)[SB], const u32x2 (&p)[SB], f32x4 acc) {
+  static __device__ __forceinline__ f32x4 product_bf16(u32x2 w0, u32x2 w1, u32x2 p0, u32x2 p1, f32x4 acc) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, u32x4{w0.x, w0.y, w1.x, w1.y}),
+                                                   __builtin_bit_cast(bf16x8, u32x4{p0.x, p0.y, p1.x, p1.y}), acc, 0, 0, 0);
+  }
+  static __device__ __forceinline__ f32x4 product_f16(const u32x2 (&w)[SB], const u32x2 (&p)[SB], f32x4 acc) {
     if constexpr (SB == 1)
-      return __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(__builtin_bit_cast(s16x4, w[0]), __builtin_bit_cast(s16x4, p[0]),
-                                                      acc, 0, 0, 0);
+      return __builtin_amdgcn_mfma_f32_16x16x16f16(__builtin_bit_cast(f16x4, w[0]), __builtin_bit_cast(f16x4, p[0]), acc, 0,
+                                                   0, 0);
     else
-      return __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-          __builtin_bit_cast(bf16x8, u32x4{w[0].x, w[0].y, w[SB - 1].x, w[SB - 1].y}),
-          __builtin_bit_cast(bf16x8, u32x4{p[0].x, p[0].y, p[SB - 1].x, p[SB - 1].y}), acc, 0, 0, 0);
+      return __builtin_amdgcn_mfma_f32_16x16x32_f16(
+          __builtin_bit_cast(f16x8, u32x4{w[0].x, w[0].y, w[SB - 1].x, w[SB - 1].y}),
+          __builtin_bit_cast(f16x8, u32x4{p[0].x, p[0].y, p[SB - 1].x, p[SB - 1].y}), acc, 0, 0, 0);
   }
 
   // The same for float32: row 16 sb + 4 g + i, column 16 dt + n16.

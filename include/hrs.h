@@ -644,8 +644,9 @@ size_t attn_verify_span_workspace_bytes(const hrs_attn_desc* desc);
  * influence, whatever it holds (infinities and NaN included). Every position
  * counts itself, so no query is without a score; where all of them are -inf
  * the result is NaN, as the formula's. Sums and softmax statistics are
- * float32; bf16 spans round the weights to bf16 for the product with the
- * values.
+ * float32. For the product with bf16 values a weight keeps 16 bits, beside
+ * e4m3 values it is rounded to float16 (11 bits, and 2^-32 of the row's
+ * largest weight at least).
  *
  * Layouts:  q [R][T][Hq][d], k, v [R][T][Hkv][d]  dtype, strided as above
  *           k_cache, v_cache [n_pages][Hkv][page_size][d]  cache.dtype

@@ -125,7 +125,10 @@ class Runs(Attn):
         assert not np.isnan(out).any(), (r, g)
         if flat:
             want = ((mask @ v) / mask.sum(1)[:, None])[:, None, :]
-            tol = (3 * U + OUT[self.dtype] * (1 + 3 * U)) * np.abs(want)
+            # A weight's lower part is 2^-40 of it where the upper one is all
+            # of it: lost beside a sum that is not zero, 2^-40 of values up to
+            # 8 where it is.
+            tol = (3 * U + OUT[self.dtype] * (1 + 3 * U)) * np.abs(want) + 2.0 ** -37
             assert np.all(np.abs(out - want) <= tol), (r, g, float(np.max(np.abs(out - want) / (tol + 1e-300))))
             return
         q = widen(self.q)[r, :, g * G:(g + 1) * G].reshape(T * G, d)
@@ -136,7 +139,12 @@ class Runs(Attn):
         reach = np.max(np.where(m, self.scale * (np.abs(q) @ np.abs(k).T), 0), 1)
         rel = (2 * (2 * (d + 4) * U) * reach + (2 * m.sum(1) + 16) * U + (2.0 ** -8 if self.dtype == "bf16" else 0))[:, None]
         want, absv = w @ v, w @ np.abs(v)
-        tol = rel * absv + OUT[self.dtype] * (np.abs(want) + rel * absv)
+        e = rel * absv
+        if self.cache == "f8":
+            # float16 weights end at 2^-25 beside a largest one of 2^7 at
+            # least: 2^-32 of it for every slot, of values up to the largest.
+            e = e + (m.sum(1) * 2.0 ** -32)[:, None] * np.abs(v).max()
+        tol = e + OUT[self.dtype] * (np.abs(want) + e)
         err = np.abs(out.reshape(T * G, d) - want)
         assert np.all(err <= tol), (r, g, float(np.max(err / (tol + 1e-300))))
 
