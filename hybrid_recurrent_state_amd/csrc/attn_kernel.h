@@ -466,7 +466,7 @@ template <int KIND, int D, int CLS> struct AttnBlock {
 #pragma unroll
         for (int i = 0; i < 4; ++i) top[rt] = fmaxf(top[rt], s[rt][sb][i]);
       top[rt] *= c;
-      more = more || top[rt] > m[rt] + 8.0f;
+      more = more || top[rt] - m[rt] > 8.0f;
     }
     if (__any(more)) {
 #pragma unroll
@@ -474,13 +474,33 @@ template <int KIND, int D, int CLS> struct AttnBlock {
         // Only the rows that ask for it: moved along with its neighbours, a
         // row's rounding would depend on scores that it does not count.
         const float mt = row_max(top[rt]);
-        const bool moves = mt > m[rt] + 8.0f;
+        const bool moves = mt - m[rt] > 8.0f;
         const float keep = moves ? __builtin_amdgcn_exp2f(m[rt] - mt) : 1.0f;
         m[rt] = moves ? mt : m[rt];
         l[rt] *= keep;
 #pragma unroll
         for (int dt = 0; dt < DT; ++dt) o[rt][dt] *= keep;
       }
+    }
+    // Far out the rounding of c S in m is whole powers of two beside the
+    // unrounded one: rounded alike, and lifted afterwards, P stays within its
+    // range.
+    float mb[C::RT];
+    bool far = false;
+#pragma unroll
+    for (int rt = 0; rt < C::RT; ++rt) {
+      mb[rt] = m[rt] == -__builtin_inff() ? 0.0f : m[rt];
+      far = far || fabsf(mb[rt]) >= 0x1p22f;
+      mb[rt] -= kLift;
+    }
+    if (__any(far)) {
+#pragma unroll
+      for (int rt = 0; rt < C::RT; ++rt) {
+#pragma unroll
+        for (int sb = 0; sb < SB; ++sb) s[rt][sb] = s[rt][sb] * c - (m[rt] == -__builtin_inff() ? 0.0f : m[rt]);
+        mb[rt] = -kLift;
+      }
+      c = 1.0f;
     }
     // P^T as the products' second operand. float16 beside e4m3 values, which
     // it holds exactly as well; beside bf16 values two bf16 parts, the upper
@@ -489,13 +509,12 @@ template <int KIND, int D, int CLS> struct AttnBlock {
     u32x2 pb[C::RT][F8 ? 1 : 2][SB];
 #pragma unroll
     for (int rt = 0; rt < C::RT; ++rt) {
-      const float mb = m[rt] == -__builtin_inff() ? 0.0f : m[rt] - kLift;
       float sum = 0.0f;
 #pragma unroll
       for (int sb = 0; sb < SB; ++sb) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          float p = __builtin_amdgcn_exp2f(fmaf(s[rt][sb][i], c, -mb));
+          const float p = __builtin_amdgcn_exp2f(fmaf(s[rt][sb][i], c, -mb[rt]));
           sum += p;
           s[rt][sb][i] = p;
         }

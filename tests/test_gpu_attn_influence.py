@@ -4,6 +4,7 @@ also where it is not a number."""
 import numpy as np
 import pytest
 
+from oracle import attn as oa
 from oracle.common import widen
 from tests.test_gpu_attn import KINDS, Attn, cast, host
 from tests.test_gpu_attn_runs import Runs, block_shape
@@ -129,3 +130,66 @@ def test_scores_of_minus_infinity_alone_have_no_softmax(hrs, dtype, cache, n, gr
     got = widen(host(a.run(hrs)))
     for t in range(9):
         assert np.array_equal(got[0, t, group:], np.broadcast_to(widen(a.v[0, 0, 1]), (group, 64))), t
+
+
+@pytest.mark.parametrize("power", [20, 24, 27, 33, 60, 100])
+@pytest.mark.parametrize("group", [1, 3, 7, 8, 12])
+@pytest.mark.parametrize("dtype,cache", KINDS)
+def test_scores_far_out_leave_the_largest(hrs, dtype, cache, group, power):
+    """Scores of about 2^power, the largest twice the second: the result is
+    that slot's value, however the scores are rounded. The slot lies in the
+    context or is the root of the span."""
+    n = 3000
+    for where in (5, 2500, n):
+        a = Attn(1, 9, 2 * group, 2, 64, 16, [n], dtype, cache, seed=group, scale=1.0)
+        rng = np.random.default_rng(power)
+        a.q, a.k = cast(np.zeros(a.q.shape), dtype), cast(np.zeros(a.k.shape), dtype)
+        # One product a score, whose rounding with the scale is not exact.
+        a.q[..., 3] = cast(np.full(1, 1.4140625 * 2.0 ** (power // 2)), dtype)
+        size = 2.0 ** (power - power // 2)
+        a.scale = 1.37
+        if cache == "f8":
+            a.kc[:] = 0
+            a.kc[..., 3] = rng.integers(0x28, 0x31, a.kc.shape[:3]).astype(np.uint8)      # 0.25 to 0.5
+            a.ks = np.full(2, 1.1 * size, dtype=np.float32)
+            one = np.uint8(0x39)                                                          # 1.125
+        else:
+            a.kc[:] = cast(np.zeros(a.kc.shape), cache)
+            a.kc[..., 3] = cast(rng.uniform(0.25, 0.5, a.kc.shape[:3]) * size, cache)
+            one = cast(np.full(1, 1.1328125 * size), cache)
+        if where < n:
+            a.kc[a.pages[0][where // 16], :, where % 16, 3] = one
+            page = a.vc[a.pages[0][where // 16], :, where % 16]
+            want = oa.widen_cache(page) * (1.0 if a.vs is None else a.vs.astype(np.float64)[:, None])
+        else:
+            a.k[0, 0, :, 3] = cast(np.full(1, 1.1328125 * size), dtype)
+            want = widen(a.v)[0, 0]
+        got = widen(host(a.run(hrs)))[0].reshape(9, 2, group, 64)
+        tol = (2.0 ** -8 if dtype == "bf16" else 2.0 ** -22) * np.abs(want[None, :, None]) * 1.01 + (2.0 ** -11 if cache == "f8" else 2.0 ** -15 if dtype == "bf16" else 0) * np.abs(want[None, :, None])
+        assert np.all(np.abs(got - want[None, :, None]) <= tol), where
+
+
+@pytest.mark.parametrize("power", [22, 24, 25, 26, 27, 28, 31, 34])
+@pytest.mark.parametrize("group", [1, 3, 7, 8, 12])
+@pytest.mark.parametrize("dtype,cache", KINDS)
+def test_scores_far_out_in_small_steps(hrs, dtype, cache, group, power):
+    """Scores of 2^power that grow along the context in steps of an ulp or a
+    few: whatever their rounding makes of the differences, weights are
+    positive and add up to one, so results lie within the values."""
+    n = 3000
+    a = Attn(1, 3, 2 * group, 2, 64, 16, [n], dtype, cache, seed=group, scale=float(np.log(2.0)))
+    a.q, a.k = cast(np.zeros(a.q.shape), dtype), cast(np.zeros(a.k.shape), dtype)
+    a.q[..., 0] = cast(np.full(1, 2.0 ** power), dtype)
+    a.q[..., 1] = cast(np.full(1, 2.0 ** max(power - 23, 1)), dtype)
+    step = np.minimum(np.arange(n) // 150, 15)
+    one = {"f8": np.uint8(0x38), "bf16": np.uint16(0x3F80), "f32": np.float32(1)}[cache]
+    small = oa.quantize_e4m3(np.arange(16.0), None) if cache == "f8" else cast(np.arange(16.0), cache)
+    a.kc[:] = 0
+    a.kc[..., 0] = one
+    for j in range(n):
+        a.kc[a.pages[0][j // 16], :, j % 16, 1] = small[step[j]]
+    if cache == "f8":
+        a.ks = np.full(2, 1.0, dtype=np.float32)
+    got = widen(host(a.run(hrs)))
+    v = oa.widen_cache(a.vc) * (1.0 if a.vs is None else a.vs.astype(np.float64)[None, :, None, None])
+    assert np.isfinite(got).all() and np.abs(got).max() <= np.abs(v).max() * (1 + 2.0 ** -7)
