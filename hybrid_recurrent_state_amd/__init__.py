@@ -704,15 +704,20 @@ class _SpanChecks(_Checks):
         the call: blocks write them while others read."""
         spans = []
         for name, t in self.seen:
-            last = sum((n - 1) * st for n, st in zip(t.shape, t.stride()))
-            spans.append((t.data_ptr(), t.data_ptr() + (last + 1) * t.element_size(), name))
+            at = t.data_ptr()
+            if t.is_contiguous():
+                spans.append((at, at + t.nbytes, name))
+            else:
+                last = sum((n - 1) * st for n, st in zip(t.shape, t.stride()))
+                spans.append((at, at + (last + 1) * t.element_size(), name))
         spans.sort()
-        for i, (_, end, name) in enumerate(spans):
-            for start, _, other in spans[i + 1:]:
-                if start >= end:
-                    break
-                if name in names or other in names:
-                    raise ValueError(f"{other} overlaps {name}")
+        top = 0        # where the last of the spans before ends
+        for i, (start, end, name) in enumerate(spans):
+            if start < top:
+                for _, e, other in spans[:i]:
+                    if start < e and (name in names or other in names):
+                        raise ValueError(f"{name} overlaps {other}")
+            top = max(top, end)
 
     def on_gpu(self) -> None:
         super().on_gpu()
