@@ -76,8 +76,10 @@ struct AttnLens {
 //    (26,758 slots, bf16), 37.6 / 34.3 (48 rows, 30,000 slots of 8 heads of
 //    128, bf16), 34.3 / 30.5 (the same, e4m3).
 //  - class 4: an e4m3 tile is widened by every wave that reads it, so two
-//    waves of 48 rows (160 us at 262,144 slots of 8 heads of 128, 68 rows)
-//    instead of four of 32 (200 us); bf16 is bound by the read either way.
+//    waves of 48 rows instead of four of 32 (8 heads of 128, the same at 65,
+//    68, 80 and 96 rows: 154 / 197 us at 262,144 slots, 37.5 / 38 at 30,000, 22
+//    / 20 at 3000; lengths are not known where the class is chosen); bf16 is
+//    bound by the read either way.
 //  - 32 slots a wave in class 1 where a row is at most 128 bytes (24.7 / 26.5
 //    us, 28 rows, e4m3); 16 for longer ones (34.0 / 35.4 us, bf16).
 //  - four waves with slots of their own in class 0: eight, or 32 slots each,

@@ -6,7 +6,8 @@
 //
 // MI355X design. The rows of a key/value head are all query heads of its
 // group at all span positions (17 positions x 6 heads = 102), so its keys and
-// values are read from memory once for all of them. That read is the bound of
+// values are read once for up to 128 of them (every further block of rows
+// reads them again). That read is the bound of
 // every long context; short ones are bound by latency (lengths, page numbers,
 // tiles, the parts' join: four dependent reads and two launches). The tiles of
 // all requests and heads form one list that is cut into equal runs, one per
@@ -43,22 +44,23 @@
 //    same matrix rate, no second part (two bf16 parts took 190 instead of 160
 //    us at 262,144 slots).
 //  - e4m3 tiles stay e4m3 in LDS and are widened (exactly) to 16 bits between
-//    LDS and the products; the scales are factors of c and of O. (Widened once per
-//    block into a second LDS tile: 215 us instead of 160 at 262,144 slots: the
-//    extra pass and its barrier were not hidden.) The span's own tile is of
+//    LDS and the products; the scales are factors of c and of O. (Widened once
+//    per block into a second LDS tile: 215 us instead of 160 at 262,144 slots:
+//    the extra pass and its barrier were not hidden.) The span's own tile is of
 //    the span's type and takes the ring's place after the cache's tiles.
 //  - Tiles with a mask (the span, the context's end, a window's border,
 //    absent pages) drop scores that do not count; values that are not finite
 //    leave the product (0 * NaN) and are added after the segment for the rows
 //    that count them (add_odd).
 //
-// Measured (bf16 unless noted, whole call with the join): 1 position, 1000
-// slots of 4 heads of 256: 15 us (main kernel 9.3, join 5.3); chain of 17 over
-// 26,758 slots of 4 heads of 256 (110 MB): 46 us (35 and 8.8); 16 trees of 23
-// over 2000 to 8191 slots of 8 heads of 128: 111 us, 4.4 TB/s; chain of 17
-// over 262,144 e4m3 slots of 8 heads of 128 (537 MB): 160 us, 3.4 TB/s, where
-// the vector units' work per tile (widening, exponentials, permutations) is as
-// long as its read and hides behind it only in part.
+// Measured (bf16 unless noted, whole call with the join; other cards gave up
+// to 10% more): 1 position, 1000 slots of 4 heads of 256: 13.4 us (main kernel
+// 8.8, join 5.2); chain of 17 over 26,758 slots of 4 heads of 256 (110 MB): 44
+// us; 16 trees of 23 over 4368 to 8191 slots of 8 heads of 128 (427 MB): 114
+// us, 3.8 TB/s; chain of 17 over 262,144 e4m3 slots of 8 heads of 128 (537 MB):
+// 146 us, 3.7 TB/s, where the vector units' work per tile (widening,
+// exponentials, permutations) is as long as its read and hides behind it only
+// in part.
 #pragma once
 
 #include <type_traits>

