@@ -41,8 +41,8 @@
 //    slots fill half of a matrix instruction and the second part the other).
 //    Beside e4m3 values P is float16 (2^-11 of a weight, or 2^-32 of the row's
 //    largest where that is more), which the values are widened to as well: the
-//    same matrix rate, no second part (two bf16 parts took 190 instead of 160
-//    us at 262,144 slots).
+//    same matrix rate, no second part (two parts took 190 instead of 160 us at
+//    262,144 slots in bf16, 206 instead of 167 in float16).
 //  - e4m3 tiles stay e4m3 in LDS and are widened (exactly) to 16 bits between
 //    LDS and the products; the scales are factors of c and of O. (Widened once
 //    per block into a second LDS tile: 215 us instead of 160 at 262,144 slots:
@@ -486,7 +486,7 @@ template <int KIND, int D, int CLS> struct AttnBlock {
     }
     // Far out the rounding of c S in m is whole powers of two beside the
     // unrounded one: rounded alike, and lifted afterwards, P stays within its
-    // range.
+    // range. The other rows' arguments are what they would be.
     float mb[C::RT];
     bool far = false;
 #pragma unroll
@@ -498,9 +498,15 @@ template <int KIND, int D, int CLS> struct AttnBlock {
     if (__any(far)) {
 #pragma unroll
       for (int rt = 0; rt < C::RT; ++rt) {
+        const bool own = fabsf(m[rt]) >= 0x1p22f && m[rt] != -__builtin_inff();
 #pragma unroll
-        for (int sb = 0; sb < SB; ++sb) s[rt][sb] = s[rt][sb] * c - (m[rt] == -__builtin_inff() ? 0.0f : m[rt]);
-        mb[rt] = -kLift;
+        for (int sb = 0; sb < SB; ++sb)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float x = s[rt][sb][i];
+            s[rt][sb][i] = own ? (x * c - m[rt]) + kLift : fmaf(x, c, -mb[rt]);
+          }
+        mb[rt] = 0.0f;
       }
       c = 1.0f;
     }

@@ -35,12 +35,13 @@ def path_of(parent, t):
     return out
 
 
+@pytest.mark.parametrize("size", [40.0, 1e8])
 @pytest.mark.parametrize("group", [1, 3, 7, 8, 12])       # 9 to 108 rows a key head: every class of blocks
 @pytest.mark.parametrize("d", [64, 128, 256])
 @pytest.mark.parametrize("dtype,cache", KINDS)
-def test_large_keys_off_the_path_change_nothing(hrs, dtype, cache, d, group):
-    """Keys of other branches with scores of a hundred for the positions that
-    count them, in a tile behind tiles of the context that have set every
+def test_large_keys_off_the_path_change_nothing(hrs, dtype, cache, d, group, size):
+    """Keys of other branches with scores of a hundred (a hundred million) for
+    the positions that count them, in a tile behind tiles of the context that have set every
     row's reference; a row's own keys in that tile are a little larger than
     the context's, so that its maximum grows without its reference having to
     move."""
@@ -59,7 +60,7 @@ def test_large_keys_off_the_path_change_nothing(hrs, dtype, cache, d, group):
             off = [t for t in range(9) if t not in path_of(a.parent[r], node)]
             for t in off:
                 for h in range(2):
-                    a.k[r, t, h] = toward(a.q[r, t, h * group], 40.0, dtype)
+                    a.k[r, t, h] = toward(a.q[r, t, h * group], size, dtype)
         got = a.run(hrs)
         assert torch.equal(got[:, node], clean[:, node]), node
         assert not torch.equal(got, clean)
