@@ -10,9 +10,9 @@ from tests.test_boundary_host import hrs
 def append_args():
     import torch
     i32 = torch.int32
-    return dict(k=t(2, 4, 3, 2, 64), v=t(2, 4, 3, 2, 64), k_cache=t(2, 5, 2, 16, 64), v_cache=t(2, 5, 2, 16, 64),
+    return dict(k=t(2, 4, 5, 2, 64), v=t(2, 4, 5, 2, 64), k_cache=t(2, 5, 2, 16, 64), v_cache=t(2, 5, 2, 16, 64),
                 page_table=t(4, 4, dtype=i32), seq_len=t(4, dtype=i32), accept_len=t(4, dtype=i32),
-                seq_len_out=t(4, dtype=i32), path=t(4, 3, dtype=i32), status=t(4, dtype=i32))
+                seq_len_out=t(4, dtype=i32), path=t(4, 5, dtype=i32), status=t(4, dtype=i32))
 
 
 def test_append_refuses_written_buffers_over_others():
@@ -24,8 +24,8 @@ def test_append_refuses_written_buffers_over_others():
     for bad in (dict(seq_len_out=ok["accept_len"]), dict(seq_len_out=ok["path"].view(-1)[4:8]),
                 dict(seq_len_out=ok["page_table"][1]), dict(status=ok["accept_len"]), dict(status=n),
                 dict(status=ok["seq_len_out"]), dict(status=n, seq_len_out=n), dict(v_cache=ok["k_cache"]),
-                dict(k=ok["k_cache"].view(-1)[:3072].view(2, 4, 3, 2, 64)),
-                dict(v=ok["k_cache"].view(-1)[512:3584].view(2, 4, 3, 2, 64))):
+                dict(k=ok["k_cache"].view(-1)[:5120].view(2, 4, 5, 2, 64)),
+                dict(v=ok["k_cache"].view(-1)[512:5632].view(2, 4, 5, 2, 64))):
         with pytest.raises(ValueError, match="overlaps"):
             hrs.kv_cache_append(**{**ok, **bad})
     both = t(12, dtype=n.dtype)
