@@ -124,6 +124,11 @@ class HoldDesc(ctypes.Structure):
     _fields_ = [("n_req", _i32), ("n_pos", _i32), ("n_pages", _i32), ("page_size", _i32), ("table_len", _i32)]
 
 
+class PagesDesc(ctypes.Structure):
+    _fields_ = [("n_req", _i32), ("n_pos", _i32), ("n_pages", _i32), ("page_size", _i32), ("table_len", _i32),
+                ("n_prefix", _i32)]
+
+
 # Exported symbols and their signatures (every function of include/hrs.h).
 _SIGNATURES = {
     "hrs_validate_tree": (_i32, [ctypes.POINTER(_i32), _i32, _i32, ctypes.POINTER(_i32)]),
@@ -153,6 +158,9 @@ _SIGNATURES = {
     "accept_sample_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(SampleDesc)]),
     "accept_sample": (_i32, [ctypes.POINTER(SampleDesc)] + [_p] * 12 + [ctypes.c_size_t, _p]),
     "accept_hold": (_i32, [ctypes.POINTER(HoldDesc)] + [_p] * 11),
+    "kv_pages_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(PagesDesc)]),
+    "kv_pages_reserve": (_i32, [ctypes.POINTER(PagesDesc)] + [_p] * 10 + [ctypes.c_size_t, _p]),
+    "kv_pages_release": (_i32, [ctypes.POINTER(PagesDesc)] + [_p] * 7 + [ctypes.c_size_t, _p]),
     "hrs_strerror": (ctypes.c_char_p, [_i32]),
     "hrs_abi_version": (_i32, []),
     "hrs_last_hip_error": (_i32, []),
@@ -988,3 +996,79 @@ def accept_hold(page_table, seq_len, accept_node, accept_len, path, bonus, held,
     last_node [R]; a newly held request's last_node to held_node [R]."""
     accept_hold_call(page_table, seq_len, accept_node, accept_len, path, bonus, held, last_node, n_pages, page_size,
                      held_node, temperature)(stream)
+
+
+# --- page lists -----------------------------------------------------------------
+
+def kv_pages_workspace_bytes(n_req: int) -> int:
+    """Device workspace bytes kv_pages_reserve and kv_pages_release need."""
+    return int(lib.kv_pages_workspace_bytes(ctypes.byref(PagesDesc(n_req, 1, 1, 16, 1, 0))))
+
+
+def _pages_checks(page_table, n_held, free_pages, n_free, workspace, status, **lens):
+    _rank("page_table", page_table, 2)
+    _rank("free_pages", free_pages, 1)
+    R, P = page_table.shape
+    chk = _SpanChecks()
+    for name, t in lens.items():
+        chk(name, t, (R,), _i32t(), optional=name == "n_new")
+    for name, t, shape in (("page_table", page_table, (R, P)), ("n_held", n_held, (R,)),
+                           ("free_pages", free_pages, None), ("n_free", n_free, (1,))):
+        chk(name, t, shape, _i32t())
+    chk("workspace", workspace)
+    chk.status(status)
+    return chk, R, P
+
+
+def kv_pages_reserve_call(seq_len, page_table, n_held, free_pages, n_free, workspace, page_size: int, n_pos: int = 0,
+                          n_new=None, prefix_table=None, slot_map=None, status=None) -> PreparedCall:
+    """The PreparedCall of kv_pages_reserve (same arguments, without the stream)."""
+    chk, R, P = _pages_checks(page_table, n_held, free_pages, n_free, workspace, status, seq_len=seq_len, n_new=n_new)
+    if prefix_table is not None:
+        _rank("prefix_table", prefix_table, 1)
+    chk("prefix_table", prefix_table, None, _i32t(), optional=True)
+    if slot_map is not None:
+        _rank("slot_map", slot_map, 2)
+        n_pos = n_pos or slot_map.shape[1]
+    chk("slot_map", slot_map, (R, n_pos), (_torch().int64,), optional=True)
+    chk.written("page_table", "n_held", "n_free", "slot_map", "workspace", "status")
+    chk.on_gpu()
+    d = PagesDesc(R, n_pos, free_pages.shape[0], page_size, P, 0 if prefix_table is None else prefix_table.shape[0])
+    nbytes = workspace.numel() * workspace.element_size()
+    return chk.call("kv_pages_reserve",
+                    (ctypes.byref(d), _data(seq_len), _data(n_new), _data(prefix_table) if d.n_prefix else None,
+                     _data(page_table), _data(n_held), _data(free_pages), _data(n_free), _data(slot_map), _data(status),
+                     _data(workspace), nbytes), d)
+
+
+def kv_pages_reserve(seq_len, page_table, n_held, free_pages, n_free, workspace, page_size: int, n_pos: int = 0,
+                     n_new=None, prefix_table=None, slot_map=None, status=None, stream=None):
+    """Pages for slots up to seq_len[r] + n_new[r] (None: n_pos) of every
+    request, from the stack free_pages [n_pages], n_free [1] into page_table
+    [R,P], n_held [R]; prefix_table: the shared leading entries of every table.
+    slot_map [R,n_pos] int64: where the new positions lie. int32 device tensors
+    but for slot_map; workspace of at least kv_pages_workspace_bytes."""
+    kv_pages_reserve_call(seq_len, page_table, n_held, free_pages, n_free, workspace, page_size, n_pos, n_new,
+                          prefix_table, slot_map, status)(stream)
+
+
+def kv_pages_release_call(keep_len, page_table, n_held, free_pages, n_free, workspace, page_size: int,
+                          n_prefix: int = 0, status=None) -> PreparedCall:
+    """The PreparedCall of kv_pages_release (same arguments, without the stream)."""
+    chk, R, P = _pages_checks(page_table, n_held, free_pages, n_free, workspace, status, keep_len=keep_len)
+    chk.written("page_table", "n_held", "free_pages", "n_free", "workspace", "status")
+    chk.on_gpu()
+    d = PagesDesc(R, 1, free_pages.shape[0], page_size, P, n_prefix)
+    nbytes = workspace.numel() * workspace.element_size()
+    return chk.call("kv_pages_release",
+                    (ctypes.byref(d), _data(keep_len), _data(page_table), _data(n_held), _data(free_pages),
+                     _data(n_free), _data(status), _data(workspace), nbytes), d)
+
+
+def kv_pages_release(keep_len, page_table, n_held, free_pages, n_free, workspace, page_size: int, n_prefix: int = 0,
+                     status=None, stream=None):
+    """Pages behind slot keep_len[r] of every request (and the n_prefix
+    leading ones) back from page_table [R,P], n_held [R] onto the stack
+    free_pages [n_pages], n_free [1]; their entries become -1."""
+    kv_pages_release_call(keep_len, page_table, n_held, free_pages, n_free, workspace, page_size, n_prefix,
+                          status)(stream)

@@ -34,6 +34,9 @@
  *                       probabilities from given random numbers
  *   accept_hold         requests that cannot go on (pages full or missing, no
  *                       valid temperature) taken out before the commit
+ *   kv_pages_reserve / kv_pages_release
+ *                       page tables that grow from a free list and shrink back
+ *                       into it, and the slots of new positions
  *
  * Conventions shared by every entry point
  * ----------------------------------------
@@ -825,6 +828,80 @@ typedef struct {
 int accept_hold(const hrs_hold_desc* desc, const int32_t* page_table, const int32_t* seq_len,
                 const float* temperature, int32_t* accept_node, int32_t* accept_len, int32_t* path,
                 int32_t* bonus, int32_t* held, int32_t* last_node, int32_t* held_node, void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* Page lists                                                               */
+/* ------------------------------------------------------------------------ */
+
+typedef struct {
+  int32_t n_req;     /* R in [1, 4096]                                     */
+  int32_t n_pos;     /* new positions of a request at most, in
+                        [1, HRS_MAX_CHUNKED_POS] (release: ignored but for
+                        that range)                                        */
+  int32_t n_pages;   /* pages, slots of a page and entries of a request's  */
+  int32_t page_size; /* table, as hrs_cache_desc                           */
+  int32_t table_len;
+  int32_t n_prefix;  /* leading entries of every table that hold the pages
+                        of a prefix shared by all requests; 0 = none       */
+} hrs_pages_desc;
+
+/* Bytes of device workspace the two calls need for this descriptor (0 if it
+ * is invalid). */
+size_t kv_pages_workspace_bytes(const hrs_pages_desc* desc);
+
+/*
+ * kv_pages_reserve - pages for the new positions of every request, from a
+ * free list on the device, and their slots ([P2] What Changed: the hybrid
+ * state includes the KV cache; [P1] Changes: nothing through the host). The
+ * list is a stack free_pages[0 .. n_free). With S = page_size,
+ * m = n_new[r] (NULL: n_pos), request r needs
+ *     need_r = max(0, ceil((seq_len[r] + m) / S) - max(n_held[r], n_prefix))
+ * pages beyond those it holds (table entries [0, n_held[r])) and the prefix's.
+ * It is served where need_0 + ... + need_r <= n_free: in request order until
+ * the list is used up. Requests that need nothing are always served. The
+ * pages of all served requests are the last ones of the list, in request
+ * order, each request's in the order of its entries. Then
+ *     page_table[r][n_held[r] .. n_prefix) = prefix_table[same]
+ *     page_table[r][max(n_held[r], n_prefix) + i] = its i-th page
+ *     n_held[r] = max(n_held[r], n_prefix) + (its pages), n_free -= all pages
+ *     slot_map[r][t] = page * S + j % S of j = seq_len[r] + t, t < m, in
+ *         entry j / S of the table as it is then; -1 where that entry is not
+ *         held or names no page, and for t >= m
+ * A request that is not served gets no page (the prefix's excepted). One
+ * whose seq_len is negative, n_new outside [0, n_pos], n_held outside
+ * [0, table_len] or that would need more than table_len entries is left as it
+ * is, with a slot map of -1. status (optional device int32) receives the
+ * number of both. n_free outside [0, n_pages] counts as the nearest of these.
+ *
+ * Layouts: seq_len, n_new, n_held [R], prefix_table [n_prefix] (NULL with
+ *          n_prefix 0), page_table [R][table_len], free_pages [n_pages],
+ *          n_free [1] int32; slot_map [R][n_pos] int64 or NULL; all device.
+ *          workspace: device scratch of at least kv_pages_workspace_bytes(desc)
+ *          bytes, contents ignored.
+ * page_table, n_held, n_free, slot_map, status and workspace overlap nothing
+ * else of the call. Errors: HRS_EINVAL, HRS_EALIGN, HRS_EDEVICE.
+ */
+int kv_pages_reserve(const hrs_pages_desc* desc, const int32_t* seq_len, const int32_t* n_new,
+                     const int32_t* prefix_table, int32_t* page_table, int32_t* n_held,
+                     const int32_t* free_pages, int32_t* n_free, int64_t* slot_map, int32_t* status,
+                     void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * kv_pages_release - the counterpart: every request keeps the pages of its
+ * first keep_len[r] slots (0: a request that has ended) and the prefix's.
+ * Entries [max(ceil(keep_len[r] / S), n_prefix), n_held[r]) go back on top of
+ * the list, in request order and the order of the entries, and become -1;
+ * n_held[r] becomes their start. Entries that name no page are dropped, and so
+ * is what the list has no place for. What kv_pages_reserve gave, given back by
+ * the next call, restores list and tables. The same page must not be in two
+ * tables behind the prefix. A request whose keep_len is negative or n_held
+ * outside [0, table_len] is left as it is; status (optional device int32)
+ * receives their number. Layouts, overlaps and errors as kv_pages_reserve
+ * (free_pages is written).
+ */
+int kv_pages_release(const hrs_pages_desc* desc, const int32_t* keep_len, int32_t* page_table,
+                     int32_t* n_held, int32_t* free_pages, int32_t* n_free, int32_t* status,
+                     void* workspace, size_t workspace_bytes, void* stream);
 
 /* ------------------------------------------------------------------------ */
 /* Misc                                                                     */
