@@ -157,6 +157,8 @@ _SIGNATURES = {
     "kv_cache_append": (_i32, [ctypes.POINTER(AppendDesc)] + [_p] * 13),
     "accept_sample_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(SampleDesc)]),
     "accept_sample": (_i32, [ctypes.POINTER(SampleDesc)] + [_p] * 12 + [ctypes.c_size_t, _p]),
+    "accept_sample_filtered_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(SampleDesc)]),
+    "accept_sample_filtered": (_i32, [ctypes.POINTER(SampleDesc)] + [_p] * 15 + [ctypes.c_size_t, _p]),
     "accept_hold": (_i32, [ctypes.POINTER(HoldDesc)] + [_p] * 11),
     "kv_pages_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(PagesDesc)]),
     "kv_pages_reserve": (_i32, [ctypes.POINTER(PagesDesc)] + [_p] * 10 + [ctypes.c_size_t, _p]),
@@ -924,9 +926,8 @@ def accept_sample_workspace_bytes(n_req: int, n_pos: int, vocab: int) -> int:
     return int(lib.accept_sample_workspace_bytes(ctypes.byref(d)))
 
 
-def accept_sample_call(logits, tokens, uniforms, token_prob, accept_node, accept_len, path, bonus, workspace,
-                       draft_probs=None, temperature=None, parent=None, status=None) -> PreparedCall:
-    """The PreparedCall of accept_sample (same arguments, without the stream)."""
+def _sample_checks(logits, tokens, uniforms, token_prob, accept_node, accept_len, path, bonus, workspace, draft_probs,
+                   temperature, status, **limits):
     _rank("logits", logits, 3)
     R, T, V = logits.shape
     chk = _SpanChecks()
@@ -941,8 +942,19 @@ def accept_sample_call(logits, tokens, uniforms, token_prob, accept_node, accept
     if draft_probs is not None:
         chk("draft_probs", draft_probs, (R, T, V), _in_dtypes("draft_probs", draft_probs))
     chk("temperature", temperature, (R,), _f32(), optional=True)
+    for name, t in limits.items():
+        chk(name, t, (R,), _i32t() if name == "top_k" else _f32(), optional=True)
     chk.status(status)
     chk.written("token_prob", "accept_node", "accept_len", "path", "bonus", "workspace", "status")
+    return chk
+
+
+def accept_sample_call(logits, tokens, uniforms, token_prob, accept_node, accept_len, path, bonus, workspace,
+                       draft_probs=None, temperature=None, parent=None, status=None) -> PreparedCall:
+    """The PreparedCall of accept_sample (same arguments, without the stream)."""
+    chk = _sample_checks(logits, tokens, uniforms, token_prob, accept_node, accept_len, path, bonus, workspace,
+                         draft_probs, temperature, status)
+    R, T, V = logits.shape
     d, par = sample_desc(R, T, V, _dtype_code(logits), HRS_F32 if draft_probs is None else _dtype_code(draft_probs),
                          parent)
     chk.on_gpu()
@@ -963,6 +975,41 @@ def accept_sample(logits, tokens, uniforms, token_prob, accept_node, accept_len,
     path [R,T], bonus [R]."""
     accept_sample_call(logits, tokens, uniforms, token_prob, accept_node, accept_len, path, bonus, workspace,
                        draft_probs, temperature, parent, status)(stream)
+
+
+def accept_sample_filtered_workspace_bytes(n_req: int, n_pos: int, vocab: int) -> int:
+    """Device workspace bytes accept_sample_filtered needs for these sizes."""
+    d, _keep = sample_desc(n_req, n_pos, vocab, HRS_BF16)
+    return int(lib.accept_sample_filtered_workspace_bytes(ctypes.byref(d)))
+
+
+def accept_sample_filtered_call(logits, tokens, uniforms, token_prob, accept_node, accept_len, path, bonus, workspace,
+                                top_k=None, top_p=None, min_p=None, draft_probs=None, temperature=None, parent=None,
+                                status=None) -> PreparedCall:
+    """The PreparedCall of accept_sample_filtered (same arguments, without the stream)."""
+    chk = _sample_checks(logits, tokens, uniforms, token_prob, accept_node, accept_len, path, bonus, workspace,
+                         draft_probs, temperature, status, top_k=top_k, top_p=top_p, min_p=min_p)
+    R, T, V = logits.shape
+    d, par = sample_desc(R, T, V, _dtype_code(logits), HRS_F32 if draft_probs is None else _dtype_code(draft_probs),
+                         parent)
+    chk.on_gpu()
+    nbytes = workspace.numel() * workspace.element_size()
+    return chk.call("accept_sample_filtered",
+                    (ctypes.byref(d), _data(logits), _data(tokens), _data(uniforms), _data(draft_probs),
+                     _data(temperature), _data(top_k), _data(top_p), _data(min_p), _data(token_prob),
+                     _data(accept_node), _data(accept_len), _data(path), _data(bonus), _data(status),
+                     _data(workspace), nbytes), d, par)
+
+
+def accept_sample_filtered(logits, tokens, uniforms, token_prob, accept_node, accept_len, path, bonus, workspace,
+                           top_k=None, top_p=None, min_p=None, draft_probs=None, temperature=None, parent=None,
+                           status=None, stream=None):
+    """accept_sample from the target's probabilities after top_k [R] int32 (0:
+    none), top_p [R] f32 (1: none) and min_p [R] f32 (0: none), each or None;
+    workspace of at least accept_sample_filtered_workspace_bytes. One position
+    a request (T = 1): plain sampling, the token in bonus."""
+    accept_sample_filtered_call(logits, tokens, uniforms, token_prob, accept_node, accept_len, path, bonus, workspace,
+                                top_k, top_p, min_p, draft_probs, temperature, parent, status)(stream)
 
 
 def accept_hold_call(page_table, seq_len, accept_node, accept_len, path, bonus, held, last_node, n_pages: int,

@@ -26,7 +26,7 @@ LIB = os.path.join(PKG, "libhrs.so")
 
 HIP_SOURCES = ["gdn.hip", "chunked.hip", "conv.hip", "accept.hip", "rollback.hip", "ring.hip",
                "rope.hip", "attn.hip", "attn_f32.hip", "attn_bf16.hip", "attn_f8.hip",
-               "kvcache.hip", "sample.hip", "hold.hip", "pages.hip"]
+               "kvcache.hip", "sample.hip", "hold.hip", "pages.hip", "filter.hip"]
 HOST_SOURCES = ["validate.cpp"]
 
 ARCH = "gfx950"

@@ -32,6 +32,8 @@
  *                       pages of every layer, indices read on the device
  *   accept_sample       verification of the drafts against the target's
  *                       probabilities from given random numbers
+ *   accept_sample_filtered
+ *                       the same after top-k, top-p and min-p
  *   accept_hold         requests that cannot go on (pages full or missing, no
  *                       valid temperature) taken out before the commit
  *   kv_pages_reserve / kv_pages_release
@@ -792,6 +794,43 @@ int accept_sample(const hrs_sample_desc* desc, const void* logits, const int32_t
                   float* token_prob, int32_t* accept_node, int32_t* accept_len, int32_t* path,
                   int32_t* bonus, int32_t* status, void* workspace, size_t workspace_bytes,
                   void* stream);
+
+/* Bytes of device workspace accept_sample_filtered needs for this descriptor
+ * (0 if the descriptor is invalid): about 2 KiB for every 8192 logits and
+ * 8 KiB a row. */
+size_t accept_sample_filtered_workspace_bytes(const hrs_sample_desc* desc);
+
+/*
+ * accept_sample_filtered - accept_sample for requests that sample from the
+ * target's probabilities after top-k, top-p and min-p. The tokens of row
+ * (r, t) stand in the order of their logits, largest first, equal ones by
+ * index, NaN left out; w_i = e^((z_i - z_0) / temperature[r]) is the weight of
+ * the i-th. The first n = min(n_k, n_p, n_m) of them stay:
+ *     n_k = top_k[r] (all where it is outside [1, V], or without top_k)
+ *     n_p = the smallest n with w_0 + ... + w_{n-1} >= top_p[r] (w_0 + ... +
+ *           w_{n_k - 1}), at least 1 (all from top_p[r] = 1 on, for NaN, or
+ *           without top_p)
+ *     n_m = how many have w_i >= min(min_p[r], 1) (all up to min_p[r] = 0,
+ *           for NaN, or without min_p)
+ * and p_t is their weights divided by their sum, zero elsewhere. Everything
+ * else as accept_sample, whose results it gives without limits; n_pos = 1 is
+ * plain sampling (bonus). Weights below e^-48 of the largest count as none.
+ * Borders are decided on 64-bit sums of weights in 64 bits where a row is
+ * settled by its largest few hundred logits, otherwise of weights good to a
+ * few units of 2^-24; the draw is in 64 bits.
+ *
+ * Layouts: as accept_sample; top_k [R] int32, top_p, min_p [R] float32, device,
+ *          each or NULL; workspace of at least
+ *          accept_sample_filtered_workspace_bytes(desc) bytes.
+ * Overlaps, refused requests (by their temperature), status, size limits and
+ * errors as accept_sample.
+ */
+int accept_sample_filtered(const hrs_sample_desc* desc, const void* logits, const int32_t* tokens,
+                           const float* uniforms, const void* draft_probs, const float* temperature,
+                           const int32_t* top_k, const float* top_p, const float* min_p,
+                           float* token_prob, int32_t* accept_node, int32_t* accept_len,
+                           int32_t* path, int32_t* bonus, int32_t* status, void* workspace,
+                           size_t workspace_bytes, void* stream);
 
 typedef struct {
   int32_t n_req;     /* R                                                  */

@@ -64,11 +64,15 @@ def draw(weights: np.ndarray, u: float):
 
 
 def accept(logits, tokens, uniforms, draft=None, tau: float = 1.0, parent: Optional[np.ndarray] = None) -> SampleResult:
-    T, V = np.asarray(logits).shape
+    return accept_from(np.stack([probabilities(row, tau) for row in np.asarray(logits)]), tokens, uniforms, draft, parent)
+
+
+def accept_from(p, tokens, uniforms, draft=None, parent: Optional[np.ndarray] = None) -> SampleResult:
+    """The same from the target's probabilities p [T, V]."""
+    T, V = p.shape
     parent = np.arange(-1, T - 1) if parent is None else np.asarray(parent)
     tokens = np.asarray(tokens)
     u = np.asarray(uniforms, dtype=np.float64)
-    p = np.stack([probabilities(logits[t], tau) for t in range(T)])
     prob = np.ones(T)
     for t in range(1, T):
         x = int(tokens[t])
