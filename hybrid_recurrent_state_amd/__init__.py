@@ -154,6 +154,8 @@ _SIGNATURES = {
     "qk_norm_rope": (_i32, [ctypes.POINTER(QkDesc)] + [_p] * 9),
     "attn_verify_span_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(AttnDesc)]),
     "attn_verify_span": (_i32, [ctypes.POINTER(AttnDesc)] + [_p] * 12 + [ctypes.c_size_t, _p]),
+    "attn_verify_shared_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(AttnDesc)]),
+    "attn_verify_shared": (_i32, [ctypes.POINTER(AttnDesc), _i32] + [_p] * 14 + [ctypes.c_size_t, _p]),
     "kv_cache_append": (_i32, [ctypes.POINTER(AppendDesc)] + [_p] * 13),
     "accept_sample_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(SampleDesc)]),
     "accept_sample": (_i32, [ctypes.POINTER(SampleDesc)] + [_p] * 12 + [ctypes.c_size_t, _p]),
@@ -823,9 +825,9 @@ def attn_verify_span_workspace_bytes(n_req: int, n_pos: int, n_heads: int, n_kvh
     return int(lib.attn_verify_span_workspace_bytes(ctypes.byref(a)))
 
 
-def attn_verify_span_call(q, k, v, k_cache, v_cache, page_table, seq_len, out, workspace, parent=None, scale=None,
-                          window: int = 0, k_scale=None, v_scale=None, status=None) -> PreparedCall:
-    """The PreparedCall of attn_verify_span (same arguments, without the stream)."""
+def _attn_checks(q, k, v, k_cache, v_cache, page_table, seq_len, out, workspace, parent, scale, window, k_scale,
+                 v_scale, status):
+    """Checks and descriptor of the attention calls: (checks, AttnDesc, what it points to)."""
     _rank("q", q, 4)
     _rank("k", k, 4)
     _rank("k_cache", k_cache, 4)
@@ -847,12 +849,20 @@ def attn_verify_span_call(q, k, v, k_cache, v_cache, page_table, seq_len, out, w
     chk("workspace", workspace)
     _scales(chk, (Hkv,), code, k_scale=k_scale, v_scale=v_scale)
     chk.status(status)
-    chk.written("out", "workspace", "status")
     par, par_p = _parent_array(parent, R, T)
-    chk.on_gpu()
     cache = CacheDesc(N, S, page_table.shape[1], code)
     d = AttnDesc(R, T, Hq, Hkv, D, _dtype_code(q), qs, ks, vs, float(D ** -0.5 if scale is None else scale),
                  int(window), cache, _topo(parent), par_p)
+    return chk, d, par
+
+
+def attn_verify_span_call(q, k, v, k_cache, v_cache, page_table, seq_len, out, workspace, parent=None, scale=None,
+                          window: int = 0, k_scale=None, v_scale=None, status=None) -> PreparedCall:
+    """The PreparedCall of attn_verify_span (same arguments, without the stream)."""
+    chk, d, par = _attn_checks(q, k, v, k_cache, v_cache, page_table, seq_len, out, workspace, parent, scale, window,
+                               k_scale, v_scale, status)
+    chk.written("out", "workspace", "status")
+    chk.on_gpu()
     nbytes = workspace.numel() * workspace.element_size()
     return chk.call("attn_verify_span",
                     (ctypes.byref(d), _data(q), _data(k), _data(v), _data(k_cache), _data(v_cache), _data(page_table),
@@ -869,6 +879,41 @@ def attn_verify_span(q, k, v, k_cache, v_cache, page_table, seq_len, out, worksp
     0 = everything. k_scale, v_scale [Hkv] f32: float8_e4m3fn caches."""
     attn_verify_span_call(q, k, v, k_cache, v_cache, page_table, seq_len, out, workspace, parent, scale, window,
                           k_scale, v_scale, status)(stream)
+
+
+def attn_verify_shared_workspace_bytes(n_req: int, n_pos: int, n_heads: int, n_kvheads: int, d: int) -> int:
+    """Device workspace bytes attn_verify_shared needs for these sizes."""
+    a = AttnDesc(n_req, n_pos, n_heads, n_kvheads, d, HRS_BF16, 0, 0, 0, 1.0, 0, CacheDesc(1, 16, 1, HRS_BF16),
+                 HRS_CHAIN, None)
+    return int(lib.attn_verify_shared_workspace_bytes(ctypes.byref(a)))
+
+
+def attn_verify_shared_call(q, k, v, k_cache, v_cache, prefix_table, prefix_len, page_table, seq_len, out, workspace,
+                            parent=None, scale=None, window: int = 0, k_scale=None, v_scale=None,
+                            status=None) -> PreparedCall:
+    """The PreparedCall of attn_verify_shared (same arguments, without the stream)."""
+    chk, d, par = _attn_checks(q, k, v, k_cache, v_cache, page_table, seq_len, out, workspace, parent, scale, window,
+                               k_scale, v_scale, status)
+    _rank("prefix_table", prefix_table, 1)
+    chk("prefix_table", prefix_table, None, _i32t())
+    chk("prefix_len", prefix_len, (1,), _i32t())
+    chk.written("out", "workspace", "status")
+    chk.on_gpu()
+    nbytes = workspace.numel() * workspace.element_size()
+    return chk.call("attn_verify_shared",
+                    (ctypes.byref(d), prefix_table.shape[0], _data(q), _data(k), _data(v), _data(k_cache),
+                     _data(v_cache), _data(prefix_table), _data(prefix_len), _data(page_table), _data(seq_len),
+                     _data(k_scale), _data(v_scale), _data(out), _data(status), _data(workspace), nbytes), d, par)
+
+
+def attn_verify_shared(q, k, v, k_cache, v_cache, prefix_table, prefix_len, page_table, seq_len, out, workspace,
+                       parent=None, scale=None, window: int = 0, k_scale=None, v_scale=None, status=None, stream=None):
+    """attn_verify_span of requests that share a prefix: slots below
+    prefix_len [1] are read through prefix_table [n], once for all requests,
+    the others through each one's page_table row (seq_len counts both).
+    workspace of at least attn_verify_shared_workspace_bytes."""
+    attn_verify_shared_call(q, k, v, k_cache, v_cache, prefix_table, prefix_len, page_table, seq_len, out, workspace,
+                            parent, scale, window, k_scale, v_scale, status)(stream)
 
 
 def kv_cache_append_call(k, v, k_cache, v_cache, page_table, seq_len, accept_len, seq_len_out=None, path=None,

@@ -51,6 +51,21 @@ struct AttnTree : AttnBase {
   int8_t parent[kGeomBytes];
 };
 
+// attn_verify_shared: a prefix that all requests of a launch share.
+struct AttnShared : AttnBase {
+  const int32_t* prefix_table;
+  const int32_t* prefix_len;
+  int32_t prefix_pages;
+  int32_t pad;
+};
+struct AttnSharedTree : AttnShared {
+  int8_t parent[kGeomBytes];
+};
+// What a launch computes: attn_verify_span; the same without the slots that
+// attn_verify_shared takes for all requests at once; those slots, for the rows
+// of all requests.
+constexpr int kSpan = 0, kOwn = 1, kPrefix = 2;
+
 // What the cut needs to know. These are kernel arguments of their own, at the
 // front, which the hardware has in registers when a wave starts: the lengths'
 // loads, the first of a chain of dependent ones, need not wait for the
@@ -136,6 +151,41 @@ __device__ __forceinline__ AttnUnits attn_units(const AttnLens& a, int len, unsi
   return {static_cast<int>(first), ctx, ok ? ctx + static_cast<int>((a.n_pos + ts - 1) / ts) + kExtraUnits : 0};
 }
 
+// The slots that all requests of a launch count at every position, in the
+// prefix's pages: whole tiles of every block shape. What is left of the prefix
+// at either end (a window's start, a length that is no multiple) is read by
+// each request for itself.
+constexpr int kHoleStep = 128;
+struct AttnHole {
+  int first, end;    // slots; equal: none
+  int prefix;        // slots of the prefix, -1: not a length
+};
+
+// Units of a request that leaves out the hole: its own tiles of the prefix
+// (`before` of them), then those of its own pages. The tile that the prefix
+// ends in is of both kinds.
+struct AttnSharedUnits : AttnUnits {
+  int before;
+  int hole, skip;    // first tile of the hole, and its tiles
+  int own;           // first tile of its own pages
+};
+__device__ __forceinline__ AttnSharedUnits attn_shared_units(const AttnLens& a, const AttnHole& hole, int len, int ts) {
+  AttnSharedUnits un{};
+  const bool ok = len >= 0 && len <= a.most && hole.prefix >= 0;
+  if (!ok) return un;
+  const int reach = a.window > 0 ? max(len + 1 - a.window, 0) : 0;     // first slot that counts for anyone
+  const int shared = min(len, hole.prefix);
+  un.first = reach / ts;
+  un.hole = hole.first / ts;
+  un.skip = (hole.end - hole.first) / ts;
+  un.before = reach < shared ? (shared + ts - 1) / ts - un.first - un.skip : 0;
+  un.own = max(hole.prefix, reach) / ts;
+  const int mine = len > hole.prefix && len > reach ? (len + ts - 1) / ts - un.own : 0;
+  un.ctx = un.before + mine;
+  un.all = un.ctx + (a.n_pos + ts - 1) / ts + kExtraUnits;
+  return un;
+}
+
 // Where block b's run of units starts: an even cut where there are at least
 // as many units as blocks (a power of two), one unit a block otherwise.
 __device__ __forceinline__ int attn_cut(int b, int total, int log_blocks) {
@@ -150,5 +200,28 @@ struct AttnShape {
 };
 template <int KIND> AttnShape attn_shape(int d, int cls);
 template <int KIND> void attn_launch(const AttnTree& args, const AttnLens& lens, int d, int cls, hipStream_t s);
+// Launches of attn_verify_shared: the requests' own part, the prefix.
+template <int KIND> void attn_own_launch(const AttnSharedTree& args, const AttnLens& lens, int d, int cls, hipStream_t s);
+template <int KIND> void attn_prefix_launch(const AttnShared& args, const AttnLens& lens, int d, int cls, hipStream_t s);
+
+inline bool sizes_ok(const hrs_attn_desc* d) {
+  return d && d->n_req >= 1 && d->n_req <= 4096 && d->n_pos >= 1 && d->n_pos <= HRS_MAX_POS && d->n_heads >= 1 &&
+         d->n_kvheads >= 1 && d->n_kvheads <= 1024 && d->n_heads % d->n_kvheads == 0 &&
+         d->n_heads / d->n_kvheads <= 64;
+}
+
+// The class of AttnCfg; its comment has both sides of each border.
+inline int rows_class(int kind, int d, int64_t rows) {
+  if (kind == kF8 && d <= 128 && rows > 64 && rows <= 96) return 4;
+  return rows <= 16 ? 0 : rows <= 32 ? 1 : rows <= 64 ? 2 : 3;
+}
+
+inline AttnShape shape_of(int kind, int d, int64_t rows) {
+  const int cls = rows_class(kind, d, rows);
+  return kind == kF32 ? attn_shape<kF32>(d, cls) : kind == kB16 ? attn_shape<kB16>(d, cls) : attn_shape<kF8>(d, cls);
+}
+inline AttnShape shape_of(const hrs_attn_desc* d, int kind) {
+  return shape_of(kind, d->d, static_cast<int64_t>(d->n_pos) * (d->n_heads / d->n_kvheads));
+}
 
 }  // namespace hrs

@@ -153,24 +153,6 @@ template <bool F32> void launch_join(const AttnBase& args, const AttnLens& l, in
   if (d == 256) launch_join_d<F32, 256>(args, l, sh, s);
 }
 
-bool sizes_ok(const hrs_attn_desc* d) {
-  return d && d->n_req >= 1 && d->n_req <= 4096 && d->n_pos >= 1 && d->n_pos <= HRS_MAX_POS && d->n_heads >= 1 &&
-         d->n_kvheads >= 1 && d->n_kvheads <= 1024 && d->n_heads % d->n_kvheads == 0 &&
-         d->n_heads / d->n_kvheads <= 64;
-}
-
-// The class of AttnCfg; its comment has both sides of each border.
-int rows_class(int kind, int d, int rows) {
-  if (kind == kF8 && d <= 128 && rows > 64 && rows <= 96) return 4;
-  return rows <= 16 ? 0 : rows <= 32 ? 1 : rows <= 64 ? 2 : 3;
-}
-
-AttnShape shape_of(const hrs_attn_desc* d, int kind) {
-  const int cls = rows_class(kind, d->d, d->n_pos * (d->n_heads / d->n_kvheads));
-  return kind == kF32 ? attn_shape<kF32>(d->d, cls) : kind == kB16 ? attn_shape<kB16>(d->d, cls)
-                                                                   : attn_shape<kF8>(d->d, cls);
-}
-
 constexpr size_t kPlanBytes = ((kAttnReqs + 1) * sizeof(int32_t) + 255) / 256 * 256;
 
 }  // namespace

@@ -1,5 +1,5 @@
 // attn_verify_span for one span and cache type (attn_kernel.h).
-#include "attn_kernel.h"
+#include "attn_launch.h"
 
 namespace hrs {
 template AttnShape attn_shape<kF8>(int, int);

@@ -142,8 +142,12 @@ template <int ROWS> struct AttnRows {
   int32_t first[ROWS];    // first context slot that counts; no row: past all
 };
 
-template <int KIND, int D, int CLS> struct AttnBlock {
+template <int MODE> using AttnBlockArgs = std::conditional_t<MODE == kSpan, AttnBase, AttnShared>;
+
+template <int KIND, int D, int CLS, int MODE> struct AttnBlock {
   using C = AttnCfg<KIND, D, CLS>;
+  using Args = AttnBlockArgs<MODE>;
+  using Units = std::conditional_t<MODE == kOwn, AttnSharedUnits, AttnUnits>;
   static constexpr int ESZ = C::ESZ, CPR = D * ESZ / 16, SB = C::SS / 16;
   static constexpr int CSZ = KIND == kF32 ? 4 : KIND == kB16 ? 2 : 1;      // bytes of a cached element
   static constexpr int RCPR = D * CSZ / 16;                               // pieces of a cached row
@@ -158,13 +162,14 @@ template <int KIND, int D, int CLS> struct AttnBlock {
   static constexpr float kLift = KIND == kF8 ? 7.0f : 0.0f;
   static_assert(LPS >= 1 && LPS * 64 * C::WR == 2 * C::SS * RCPR && (C::NST - 1) * LPS < 64, "whole loads");
 
-  const AttnBase& a;
+  const Args& a;
   char* lds;
   AttnRows<C::ROWS>* rows;
   int wave, lane, wr, kg, n16, g;
   // the segment
   int r, h, len, n_units, rb;
-  AttnUnits un;
+  Units un;
+  int prefix;                  // kOwn: slots of the prefix
   bool idle;                   // no row of the wave exists
   bool odd_seen;               // a masked tile held values that are not finite
   u32x4 q[C::RT][QC];
@@ -177,7 +182,7 @@ template <int KIND, int D, int CLS> struct AttnBlock {
   int next;                    // next tile to start
   int pg[SB];                  // pages of the next tile to load
 
-  __device__ __forceinline__ AttnBlock(const AttnBase& args, char* l_, AttnRows<C::ROWS>* rows_) : a(args), lds(l_), rows(rows_) {
+  __device__ __forceinline__ AttnBlock(const Args& args, char* l_, AttnRows<C::ROWS>* rows_) : a(args), lds(l_), rows(rows_) {
     wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     lane = threadIdx.x & 63;
     wr = wave % C::WR;
@@ -187,7 +192,18 @@ template <int KIND, int D, int CLS> struct AttnBlock {
   }
 
   // Slot of tile u where this wave group starts.
-  __device__ __forceinline__ int slot0(int u) const { return (un.first + u) * C::TS + kg * C::SS; }
+  __device__ __forceinline__ int slot0(int u) const {
+    int n = un.first + u;
+    if constexpr (MODE == kOwn) n = u >= un.before ? un.own + (u - un.before) : n >= un.hole ? n + un.skip : n;
+    return n * C::TS + kg * C::SS;
+  }
+  // Whether context tile u is read through the prefix's table, and the end of
+  // its slots.
+  __device__ __forceinline__ bool of_prefix(int u) const {
+    if constexpr (MODE == kOwn) return u < un.before;
+    else return MODE == kPrefix;
+  }
+  __device__ __forceinline__ int slots_end(int u) const { return MODE == kOwn && of_prefix(u) ? min(len, prefix) : len; }
 
   // In a scalar register: the compiler keeps some uniform numbers in vector
   // ones, with the arithmetic on them.
@@ -196,11 +212,18 @@ template <int KIND, int D, int CLS> struct AttnBlock {
   // Page numbers of context tile u: scalar loads, nothing waits for them here.
   __device__ __forceinline__ void fetch_pages(int u) {
     typedef const __attribute__((address_space(4))) int32_t* cptr;
-    const cptr table = (cptr)(a.page_table + static_cast<int64_t>(r) * a.table_len);
+    cptr table = (cptr)(a.page_table + static_cast<int64_t>(r) * a.table_len);
+    int entries = a.table_len;
+    if constexpr (MODE != kSpan) {
+      if (of_prefix(u)) {
+        table = (cptr)a.prefix_table;
+        entries = a.prefix_pages;
+      }
+    }
 #pragma unroll
     for (int i = 0; i < SB; ++i) {
       const int j = slot0(u) + 16 * i;
-      pg[i] = table[min(j >> a.page_shift, a.table_len - 1)];
+      pg[i] = table[min(j >> a.page_shift, entries - 1)];
     }
   }
 
@@ -212,7 +235,7 @@ template <int KIND, int D, int CLS> struct AttnBlock {
     uint32_t there = 0;
 #pragma unroll
     for (int i = 0; i < SB; ++i) {
-      const bool ok = static_cast<uint32_t>(pg[i]) < static_cast<uint32_t>(a.n_pages) && slot0(u) + 16 * i < len;
+      const bool ok = static_cast<uint32_t>(pg[i]) < static_cast<uint32_t>(a.n_pages) && slot0(u) + 16 * i < slots_end(u);
       there |= ok ? 1u << i : 0u;
       const uint32_t in_page = ((slot0(u) >> 4) + i) & ((1u << (a.page_shift - 4)) - 1);
       const uint32_t group = uniform_int((ok ? pg[i] : 0) * uniform_int(head_groups) + uniform_int(h_groups) + in_page);
@@ -366,15 +389,21 @@ template <int KIND, int D, int CLS> struct AttnBlock {
         if (s0 + 16 * sb < 64) bits |= static_cast<uint32_t>((anc >> (s0 + 16 * sb)) & 15) << (4 * sb);
       return bits;
     }
+    if constexpr (MODE == kPrefix) {     // every row counts what is there
+#pragma unroll
+      for (int sb = 0; sb < SB; ++sb) bits |= (there >> sb) & 1 ? 15u << (4 * sb) : 0u;
+      return bits;
+    }
     const int j0 = slot0(u) + 4 * g;
-    const int first = rows->first[lrow];
+    const int first = MODE == kOwn && !of_prefix(u) ? max(rows->first[lrow], prefix) : rows->first[lrow];
+    const int end = slots_end(u);
 #pragma unroll
     for (int sb = 0; sb < SB; ++sb) {
       if (!((there >> sb) & 1)) continue;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int j = j0 + 16 * sb + i;
-        bits |= j >= first && j < len ? 1u << (4 * sb + i) : 0u;
+        bits |= j >= first && j < end ? 1u << (4 * sb + i) : 0u;
       }
     }
     return bits;
@@ -771,8 +800,10 @@ template <int KIND, int D, int CLS> struct AttnBlock {
 
   // Whether some row of the block does not count some slot of context tile u.
   __device__ __forceinline__ bool masked(int u, uint32_t there) const {
+    if constexpr (MODE == kPrefix) return there != (1u << SB) - 1;
     const int j0 = slot0(u);
-    return j0 + C::SS > len || (a.window > 0 && j0 <= len + a.n_pos - 1 - a.window) || there != (1u << SB) - 1;
+    return j0 + C::SS > slots_end(u) || (a.window > 0 && j0 <= len + a.n_pos - 1 - a.window) ||
+           there != (1u << SB) - 1 || (MODE == kOwn && !of_prefix(u) && j0 < prefix);
   }
 
   // Tile u of the ring (an e4m3 cache's span tiles do not pass through it).
@@ -928,19 +959,59 @@ template <int KIND, int D, int CLS> struct AttnBlock {
 
 // The units of up to 256 requests, four consecutive ones a lane, the same in
 // every wave: no barrier and one round of loads.
-struct AttnPlan {
+template <int MODE> struct AttnPlan {
   int len[kAttnReqs / 64], all[kAttnReqs / 64];
+  AttnHole hole;
   int before;     // units before the lane's requests
   int total;
 
-  __device__ __forceinline__ AttnPlan(const AttnLens& a, int ts) {
+  // What the shared launches count a request's units with.
+  __device__ __forceinline__ auto units(const AttnLens& a, int n, int ts) const {
+    if constexpr (MODE == kOwn) return attn_shared_units(a, hole, n, ts);
+    else return attn_units(a, n, ts);
+  }
+
+  // The slots that all requests count at every position.
+  __device__ __forceinline__ void find_hole(const AttnLens& a, const AttnShared& args) {
+    const int32_t given = *args.prefix_len;
+    const bool ok = given >= 0 && given <= args.prefix_pages << args.page_shift;
+    int lo = 0, hi = ok ? given : 0;
+#pragma unroll
+    for (int k = 0; k < kAttnReqs / 64; ++k) {
+      if (len[k] < 0 || len[k] > a.most) continue;
+      hi = min(hi, len[k]);
+      if (a.window > 0) lo = max(lo, len[k] + a.n_pos - a.window);
+    }
+#pragma unroll
+    for (int d = 32; d; d >>= 1) {
+      lo = max(lo, __shfl_xor(lo, d));
+      hi = min(hi, __shfl_xor(hi, d));
+    }
+    lo = __builtin_amdgcn_readfirstlane((lo + kHoleStep - 1) & ~(kHoleStep - 1));
+    hi = __builtin_amdgcn_readfirstlane(hi & ~(kHoleStep - 1));
+    hole = AttnHole{lo < hi ? lo : 0, lo < hi ? hi : 0, ok ? given : -1};
+  }
+
+  __device__ __forceinline__ AttnPlan(const AttnLens& a, const AttnBlockArgs<MODE>& args, int ts) {
     const int lane = fresh(threadIdx.x) & 63;
 #pragma unroll
     for (int k = 0; k < kAttnReqs / 64; ++k) len[k] = a.len[min(lane * (kAttnReqs / 64) + k, a.n - 1)];
+    if constexpr (MODE != kSpan) find_hole(a, args);
+    if constexpr (MODE == kPrefix) {     // one request of the rows of all, every head the hole's tiles
+      const int tiles = (hole.end - hole.first) / ts;
+#pragma unroll
+      for (int k = 0; k < kAttnReqs / 64; ++k) {
+        len[k] = hole.end;
+        all[k] = threadIdx.x % 64 == 0 && k == 0 && tiles > 0 ? (tiles + kExtraUnits) * a.heads : 0;
+      }
+      before = threadIdx.x % 64 == 0 ? 0 : __builtin_amdgcn_readfirstlane(all[0]);
+      total = __builtin_amdgcn_readfirstlane(all[0]);
+      return;
+    }
     int sum = 0;
 #pragma unroll
     for (int k = 0; k < kAttnReqs / 64; ++k) {
-      const int n = attn_units(a, len[k], ts).all * a.heads;
+      const int n = units(a, len[k], ts).all * a.heads;
       all[k] = lane * (kAttnReqs / 64) + k < a.n ? n : 0;
       sum += all[k];
     }
@@ -1000,11 +1071,11 @@ struct AttnPlan {
 };
 
 // Refused requests of the whole call: a count per thread, added in order.
-template <int NT> __device__ __forceinline__ void count_refused(const AttnBase& a, int32_t* sums) {
+template <int NT> __device__ __forceinline__ void count_refused(const AttnBase& a, bool all, int32_t* sums) {
   int bad = 0;
   for (int i = threadIdx.x; i < a.n_req; i += NT) {
     const int n = a.seq_len[i];
-    bad += n < 0 || n > (a.table_len << a.page_shift);
+    bad += all || n < 0 || n > (a.table_len << a.page_shift);
   }
   sums[threadIdx.x] = bad;
   block_barrier();
@@ -1016,26 +1087,28 @@ template <int NT> __device__ __forceinline__ void count_refused(const AttnBase& 
   block_barrier();
 }
 
-template <int KIND, int D, int CLS, typename Args>
-__global__ __launch_bounds__((AttnCfg<KIND, D, CLS>::NT), (AttnCfg<KIND, D, CLS>::NT * AttnCfg<KIND, D, CLS>::PER_CU + 255) / 256)
-void attn_kernel(const int32_t* len, int n, int heads, int most, int window, int n_pos, int log_blocks, const Args args) {
+template <int KIND, int D, int CLS, int MODE, typename Args>
+__device__ __forceinline__ void attn_blocks(const AttnLens& lens, const Args& args) {
   using C = AttnCfg<KIND, D, CLS>;
-  constexpr bool kTree = std::is_same<Args, AttnTree>::value;
-  const AttnLens lens{len, n, heads, most, window, n_pos, log_blocks};
+  constexpr bool kTree = std::is_same<Args, AttnTree>::value || std::is_same<Args, AttnSharedTree>::value;
+  const int log_blocks = lens.log_blocks;
   extern __shared__ __align__(1024) char lds[];   // rows of a tile start at multiples of their size
   __shared__ int8_t par[kTree ? HRS_MAX_POS : 1];
   __shared__ AttnRows<C::ROWS> rows;
   const int tid = threadIdx.x;
-  AttnBlock<KIND, D, CLS> blk(args, lds, &rows);
+  AttnBlock<KIND, D, CLS, MODE> blk(args, lds, &rows);
   int u, u1, in_req = 0, i = 0;
+  AttnHole hole{};
   {
-    const AttnPlan plan(lens, C::TS);
+    const AttnPlan<MODE> plan(lens, args, C::TS);
     u = attn_cut(blockIdx.x, plan.total, log_blocks);
     u1 = attn_cut(blockIdx.x + 1, plan.total, log_blocks);
     if (u < u1) i = plan.find(u, &in_req, &blk.len);
+    if constexpr (MODE != kSpan) hole = plan.hole;
     if (blockIdx.x == 0) {
-      plan.write(args.plan, n);
-      if (args.status && args.req0 == 0) count_refused<C::NT>(args, reinterpret_cast<int32_t*>(lds));
+      plan.write(args.plan, MODE == kPrefix ? 1 : lens.n);
+      if (MODE != kPrefix && args.status && args.req0 == 0)
+        count_refused<C::NT>(args, MODE == kOwn && hole.prefix < 0, reinterpret_cast<int32_t*>(lds));
     }
   }
 
@@ -1045,12 +1118,20 @@ void attn_kernel(const int32_t* len, int n, int heads, int most, int window, int
       // Counted again for every further segment rather than kept in registers
       // over the tiles; everybody is done with the last segment's tiles and
       // masks after the barrier.
-      i = AttnPlan(lens, C::TS).find(u, &in_req, &blk.len);
+      i = AttnPlan<MODE>(lens, args, C::TS).find(u, &in_req, &blk.len);
       block_barrier();
     }
     again = true;
     blk.r = args.req0 + i;
-    blk.un = attn_units(lens, blk.len, C::TS);
+    if constexpr (MODE == kOwn) {
+      blk.un = attn_shared_units(lens, hole, blk.len, C::TS);
+      blk.prefix = hole.prefix;
+    } else if constexpr (MODE == kPrefix) {
+      const int tiles = (hole.end - hole.first) / C::TS;
+      blk.un = AttnUnits{hole.first / C::TS, tiles, tiles + kExtraUnits};
+    } else {
+      blk.un = attn_units(lens, blk.len, C::TS);
+    }
     const int seg = __builtin_amdgcn_readfirstlane(in_req / blk.un.all);
     const int u0 = in_req - seg * blk.un.all;
     const int ue = min(blk.un.all, u0 + (u1 - u));
@@ -1073,76 +1154,26 @@ void attn_kernel(const int32_t* len, int n, int heads, int most, int window, int
       if (tid < args.n_pos) par[tid] = args.parent[i * args.n_pos + tid];
       block_barrier();
     }
-    blk.template mask_rows<kTree>(par);
+    if constexpr (MODE != kPrefix) blk.template mask_rows<kTree>(par);
     blk.settle();
     block_barrier();
     blk.run(u0, last);
     if (blk.odd_seen) blk.add_odd(u0, last);
-    blk.finish(u0 == 0 && ue == blk.un.all, 2 * static_cast<int>(blockIdx.x) + (u0 == 0 ? 1 : 0));
+    // Parts of the shared launches lie in the order of their segments and
+    // blocks: one of the two numbers goes up from part to part.
+    if constexpr (MODE == kSpan)
+      blk.finish(u0 == 0 && ue == blk.un.all, 2 * static_cast<int>(blockIdx.x) + (u0 == 0 ? 1 : 0));
+    else
+      blk.finish(false, i * lens.heads + seg + static_cast<int>(blockIdx.x));
     u += ue - u0;
   }
 }
 
-}  // namespace
-
-namespace {
-
 template <int KIND, int D, int CLS, typename Args>
-void launch_as(const Args& args, const AttnLens& l, hipStream_t s) {
-  using C = AttnCfg<KIND, D, CLS>;
-  hipLaunchKernelGGL((attn_kernel<KIND, D, CLS, Args>), dim3(1 << l.log_blocks), dim3(C::NT), C::LDS, s, l.len, l.n, l.heads,
-                     l.most, l.window, l.n_pos, l.log_blocks, args);
-}
-template <int KIND, int D, int CLS> void launch_one(const AttnTree& args, const AttnLens& l, hipStream_t s) {
-  if (args.tree) launch_as<KIND, D, CLS>(args, l, s);
-  else launch_as<KIND, D, CLS>(static_cast<const AttnBase&>(args), l, s);
-}
-template <int KIND, int D, int CLS> AttnShape shape_one() {
-  using C = AttnCfg<KIND, D, CLS>;
-  return {C::ROWS, C::TS, kAttnCus * C::PER_CU};
+__global__ __launch_bounds__((AttnCfg<KIND, D, CLS>::NT), (AttnCfg<KIND, D, CLS>::NT * AttnCfg<KIND, D, CLS>::PER_CU + 255) / 256)
+void attn_kernel(const int32_t* len, int n, int heads, int most, int window, int n_pos, int log_blocks, const Args args) {
+  attn_blocks<KIND, D, CLS, kSpan>(AttnLens{len, n, heads, most, window, n_pos, log_blocks}, args);
 }
 
 }  // namespace
-
-template <int KIND> AttnShape attn_shape(int d, int cls) {
-  switch (d * 8 + cls) {
-    case 64 * 8 + 0: return shape_one<KIND, 64, 0>();
-    case 64 * 8 + 1: return shape_one<KIND, 64, 1>();
-    case 64 * 8 + 2: return shape_one<KIND, 64, 2>();
-    case 64 * 8 + 3: return shape_one<KIND, 64, 3>();
-    case 128 * 8 + 0: return shape_one<KIND, 128, 0>();
-    case 128 * 8 + 1: return shape_one<KIND, 128, 1>();
-    case 128 * 8 + 2: return shape_one<KIND, 128, 2>();
-    case 128 * 8 + 3: return shape_one<KIND, 128, 3>();
-    case 256 * 8 + 0: return shape_one<KIND, 256, 0>();
-    case 256 * 8 + 1: return shape_one<KIND, 256, 1>();
-    case 256 * 8 + 2: return shape_one<KIND, 256, 2>();
-    case 256 * 8 + 3: return shape_one<KIND, 256, 3>();
-  }
-  if constexpr (KIND == kF8) {
-    if (cls == 4) return d == 64 ? shape_one<KIND, 64, 4>() : shape_one<KIND, 128, 4>();
-  }
-  return {0, 0, 0};
-}
-
-template <int KIND> void attn_launch(const AttnTree& args, const AttnLens& lens, int d, int cls, hipStream_t s) {
-  switch (d * 8 + cls) {
-    case 64 * 8 + 0: return launch_one<KIND, 64, 0>(args, lens, s);
-    case 64 * 8 + 1: return launch_one<KIND, 64, 1>(args, lens, s);
-    case 64 * 8 + 2: return launch_one<KIND, 64, 2>(args, lens, s);
-    case 64 * 8 + 3: return launch_one<KIND, 64, 3>(args, lens, s);
-    case 128 * 8 + 0: return launch_one<KIND, 128, 0>(args, lens, s);
-    case 128 * 8 + 1: return launch_one<KIND, 128, 1>(args, lens, s);
-    case 128 * 8 + 2: return launch_one<KIND, 128, 2>(args, lens, s);
-    case 128 * 8 + 3: return launch_one<KIND, 128, 3>(args, lens, s);
-    case 256 * 8 + 0: return launch_one<KIND, 256, 0>(args, lens, s);
-    case 256 * 8 + 1: return launch_one<KIND, 256, 1>(args, lens, s);
-    case 256 * 8 + 2: return launch_one<KIND, 256, 2>(args, lens, s);
-    case 256 * 8 + 3: return launch_one<KIND, 256, 3>(args, lens, s);
-  }
-  if constexpr (KIND == kF8) {
-    if (cls == 4) return d == 64 ? launch_one<KIND, 64, 4>(args, lens, s) : launch_one<KIND, 128, 4>(args, lens, s);
-  }
-}
-
 }  // namespace hrs

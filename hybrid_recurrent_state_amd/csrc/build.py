@@ -25,7 +25,8 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libhrs.so")
 
 HIP_SOURCES = ["gdn.hip", "chunked.hip", "conv.hip", "accept.hip", "rollback.hip", "ring.hip",
-               "rope.hip", "attn.hip", "attn_f32.hip", "attn_bf16.hip", "attn_f8.hip",
+               "rope.hip", "attn.hip", "attn_f32.hip", "attn_bf16.hip", "attn_f8.hip", "attn_shared.hip",
+               "attn_shared_f32.hip", "attn_shared_bf16.hip", "attn_shared_f8.hip",
                "kvcache.hip", "sample.hip", "hold.hip", "pages.hip", "filter.hip"]
 HOST_SOURCES = ["validate.cpp"]
 

@@ -28,6 +28,8 @@
  *                       rotation, in one pass
  *   attn_verify_span    attention of the span (chain or draft tree) over a
  *                       paged cache and the span's own root paths
+ *   attn_verify_shared  the same for requests that share a prefix, which is read
+ *                       once for all of them
  *   kv_cache_append     the accepted path's keys and values into the cache
  *                       pages of every layer, indices read on the device
  *   accept_sample       verification of the drafts against the target's
@@ -675,6 +677,41 @@ int attn_verify_span(const hrs_attn_desc* desc, const void* q, const void* k, co
                      const void* k_cache, const void* v_cache, const int32_t* page_table,
                      const int32_t* seq_len, const float* k_scale, const float* v_scale, void* out,
                      int32_t* status, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of device workspace attn_verify_shared needs for these sizes (0 for a
+ * NULL descriptor or sizes out of range). It does not depend on lengths, nor on
+ * the cache. About twice the bytes of R * T * Hq results in float32, and those
+ * of the parts of up to 512 blocks. */
+size_t attn_verify_shared_workspace_bytes(const hrs_attn_desc* desc);
+
+/*
+ * attn_verify_shared - attn_verify_span of requests that share a prefix, whose
+ * keys and values are read once for all of them: the rows of all requests are
+ * one operand of its products. Slots j < P = prefix_len[0] of every request are
+ * those of prefix_table (row j % page_size of page prefix_table[j /
+ * page_size]), the others those of the request's own table, at the same place
+ * as ever (a request's own entries are not read where all of their slots are
+ * below P). seq_len counts both: a request with seq_len[r] < P counts the first
+ * seq_len[r] slots of the prefix. Otherwise arguments, layouts, masks, results
+ * and refusals are those of attn_verify_span, up to rounding.
+ *
+ * What is computed for all requests at once are the slots that every one of
+ * them counts at every position: from the latest window's start to the shortest
+ * context's end within the prefix, in whole groups of 128. Batches of up to 256
+ * requests (trees: 3072 positions) are one unit, larger ones several.
+ *
+ * prefix_table [prefix_pages] int32, prefix_len [1] int32, device;
+ * prefix_pages >= 1. A prefix_len outside [0, prefix_pages * page_size] refuses
+ * all requests (status: R). prefix_table may be part of page_table. workspace:
+ * at least attn_verify_shared_workspace_bytes(desc) bytes. Errors as
+ * attn_verify_span.
+ */
+int attn_verify_shared(const hrs_attn_desc* desc, int32_t prefix_pages, const void* q, const void* k,
+                       const void* v, const void* k_cache, const void* v_cache,
+                       const int32_t* prefix_table, const int32_t* prefix_len,
+                       const int32_t* page_table, const int32_t* seq_len, const float* k_scale,
+                       const float* v_scale, void* out, int32_t* status, void* workspace,
+                       size_t workspace_bytes, void* stream);
 
 typedef struct {
   int32_t n_layers;   /* L                                                 */
