@@ -21,7 +21,9 @@ copy, conv state rebuilt from the accepted path) and ``FusedVerifyStep`` adds
 one fused kernel per layer (conv, SiLU, q/k/v split, q/k L2 norm and the
 gated delta rule) to it. ``HybridVerifyStep`` adds the model's attention
 layers between the GDN layers (norm and rotation, attention over a paged
-cache, accepted rows into the pages) and acceptance by sampling.
+cache, accepted rows into the pages) and acceptance by sampling; also for
+requests that share a prefix, whose page tables grow from a free list and that
+sample after top-k, top-p and min-p.
 """
 from __future__ import annotations
 
@@ -33,8 +35,10 @@ import numpy as np
 
 from . import (AcceptDesc, ConvAdvanceDesc, ConvDesc, GdnDesc, GdnLayerDesc, HRS_BF16, HRS_CHAIN, HRS_F32, HRS_TREE,
                HrsError, RingDesc, RingRun, RollbackDesc, SpanSource, accept_greedy_workspace_bytes, accept_hold_call,
-               accept_sample_call, accept_sample_workspace_bytes, attn_verify_span_call,
-               attn_verify_span_workspace_bytes, kv_cache_append_call, lib, qk_norm_rope_call)
+               accept_sample_call, accept_sample_filtered_call, accept_sample_filtered_workspace_bytes,
+               accept_sample_workspace_bytes, attn_verify_shared_call, attn_verify_shared_workspace_bytes,
+               attn_verify_span_call, attn_verify_span_workspace_bytes, kv_cache_append_call, kv_pages_release_call,
+               kv_pages_reserve_call, kv_pages_workspace_bytes, lib, qk_norm_rope_call)
 
 
 @dataclasses.dataclass(frozen=True)
@@ -466,6 +470,8 @@ class AttnShape:
     weight_offset: float = 0.0
     f8_cache: bool = False     # float8_e4m3fn pages with a scale per layer and key head
     after: Optional[Sequence[int]] = None   # the GDN layer each attention layer follows; default: evenly spread
+    prefix_len: int = 0        # leading slots that all requests share (read once for all of them); seq_len counts them
+    page_list: bool = False    # tables grow from and shrink into a free list on the device, step by step
 
 
 class AttnBuffers:
@@ -474,8 +480,15 @@ class AttnBuffers:
     qkv [L,R,T,Hq+2Hkv,d] is each layer's projection; q_out, k_out its
     normalised and rotated heads. page_table holds distinct pages per request
     and seq_len [R] the slots that count (the step advances them itself).
-    uniforms [R,T] and temperature [R] are read where acceptance samples.
-    held [R] marks requests that could not go on (see HybridVerifyStep)."""
+    uniforms [R,T] and temperature [R] are read where acceptance samples,
+    top_k, top_p and min_p [R] (none to start with) where it is filtered.
+    held [R] marks requests that could not go on (see HybridVerifyStep).
+
+    With a prefix, prefix_table names its pages, the last one possibly in part:
+    that one is of no request's table, each has a page of its own in its place.
+    With a page list, free_pages [n_pages] and n_free [1] start with every page
+    behind the prefix's, which are pages 0, 1, ... then, and n_held [R] with
+    none: the step fills and cuts page_table itself."""
 
     def __init__(self, shape: AttnShape, step: StepShape, device="cuda"):
         import torch
@@ -505,19 +518,37 @@ class AttnBuffers:
             self.k_scale = self.v_scale = None
         self.page_table = z(R, s.table_len)
         self.seq_len = z(R)
+        whole, pages = s.prefix_len // s.page_size, -(-s.prefix_len // s.page_size)
+        self.prefix_table = torch.arange(pages, dtype=torch.int32, device=device) if s.prefix_len else None
+        self.prefix_len = torch.full((1,), s.prefix_len, dtype=torch.int32, device=device) if s.prefix_len else None
+        self.free_pages = None
+        if s.page_list:
+            if whole > s.table_len or pages > s.n_pages:
+                raise ValueError(f"a prefix of {pages} pages, {s.table_len} entries a table, {s.n_pages} pages")
+            self.free_pages = torch.arange(s.n_pages, dtype=torch.int32, device=device).roll(-pages)
+            self.n_free = torch.full((1,), s.n_pages - pages, dtype=torch.int32, device=device)
+            self.n_held = z(R)
+            self.page_table.fill_(-1)
+            self.whole_prefix = self.prefix_table[:whole] if whole else None
         # Refused requests, one row per call (its first word counts): attention
-        # layers 0..L-1, then acceptance, then the append.
+        # layers 0..L-1, then acceptance, then the append; with a page list
+        # the requests whose next span finds no pages, and the release.
         self.status = z(L + 2, 4)
+        self.page_status = z(2, 4)
         self.uniforms = z(R, T, dtype=torch.float32)
         self.token_prob = z(R, T, dtype=torch.float32)
         self.temperature = torch.ones(R, device=device)
+        self.top_k, self.top_p, self.min_p = z(R), torch.ones(R, device=device), torch.zeros(R, device=device)
         self.held = z(R)
         self.last_node = z(R)
         # Where a held request's recurrent state is: a position of checkpoint
         # buffer 0 or 1, or -1.
         self.held_node = [z(R), z(R)]
         nbytes = max(attn_verify_span_workspace_bytes(R, T, Hq, Hkv, d),
-                     accept_sample_workspace_bytes(R, T, step.vocab) if step.vocab else 0)
+                     attn_verify_shared_workspace_bytes(R, T, Hq, Hkv, d) if s.prefix_len else 0,
+                     kv_pages_workspace_bytes(R) if s.page_list else 0,
+                     accept_sample_workspace_bytes(R, T, step.vocab) if step.vocab else 0,
+                     accept_sample_filtered_workspace_bytes(R, T, step.vocab) if step.vocab else 0)
         self.workspace = e(max(16, nbytes), dtype=torch.uint8)   # one stream: the calls take turns
 
 
@@ -538,10 +569,19 @@ class HybridVerifyStep(FusedVerifyStep):
     ``materialize()`` (which writes every request's recurrent state, a held
     one's from in front of the step that held it), give it what it lacks, and
     start a new speculation with a new HybridVerifyStep.
+
+    ``filtered`` samples after top-k, top-p and min-p (accept_sample_filtered:
+    ``top_k``, ``top_p``, ``min_p`` of the AttnBuffers). A shape with a prefix
+    reads its slots once for all requests (attn_verify_shared). With a page list
+    a step takes the pages of its span's slots before its layers and gives
+    those that the accepted rows leave empty back behind the append, so a
+    request is held for want of pages only where the list has none; a request
+    that ends gives its own back through kv_pages_release.
     """
 
     def __init__(self, bufs: StepBuffers, attn: AttnBuffers, parent=None, runs: Optional[Sequence[tuple]] = None,
-                 silu: bool = True, q_scale: float = 1.0, l2_eps: float = 1e-6, sample: bool = False):
+                 silu: bool = True, q_scale: float = 1.0, l2_eps: float = 1e-6, sample: bool = False,
+                 filtered: bool = False):
         super().__init__(bufs, parent, runs, silu, q_scale, l2_eps)
         s, b, n = attn.shape, attn, bufs.shape.n_layers
         self.attn = attn
@@ -557,13 +597,23 @@ class HybridVerifyStep(FusedVerifyStep):
             self.attn_calls[l] += [
                 qk_norm_rope_call(b.q[i], b.k[i], b.q_weight[i], b.k_weight[i], b.freq, b.seq_len, b.q_out[i],
                                   b.k_out[i], self._parent, s.eps, s.weight_offset),
+                attn_verify_shared_call(b.q_out[i], b.k_out[i], b.v[i], b.k_cache[i], b.v_cache[i], b.prefix_table,
+                                        b.prefix_len, b.page_table, b.seq_len, b.out[i], b.workspace, self._parent,
+                                        k_scale=scale(b.k_scale, i), v_scale=scale(b.v_scale, i), status=b.status[i])
+                if s.prefix_len else
                 attn_verify_span_call(b.q_out[i], b.k_out[i], b.v[i], b.k_cache[i], b.v_cache[i], b.page_table,
                                       b.seq_len, b.out[i], b.workspace, self._parent,
                                       k_scale=scale(b.k_scale, i), v_scale=scale(b.v_scale, i), status=b.status[i])]
-        self.sample_call = accept_sample_call(
-            bufs.logits, bufs.tokens, b.uniforms, b.token_prob, bufs.accept_node, bufs.accept_len, bufs.path,
-            bufs.bonus, b.workspace, temperature=b.temperature, parent=self._parent,
-            status=b.status[-2]) if sample else None
+        sample_args = (bufs.logits, bufs.tokens, b.uniforms, b.token_prob, bufs.accept_node, bufs.accept_len,
+                       bufs.path, bufs.bonus, b.workspace)
+        more = dict(temperature=b.temperature, parent=self._parent, status=b.status[-2])
+        self.sample_call = None
+        if filtered:
+            self.sample_call = accept_sample_filtered_call(*sample_args, top_k=b.top_k, top_p=b.top_p, min_p=b.min_p,
+                                                           **more)
+        elif sample:
+            self.sample_call = accept_sample_call(*sample_args, **more)
+        sample = sample or filtered
         # By the checkpoint buffer that a step's spans start from; None: from ``state``.
         self.hold_calls = {c: accept_hold_call(
             b.page_table, b.seq_len, bufs.accept_node, bufs.accept_len, bufs.path, bufs.bonus, b.held, b.last_node,
@@ -572,8 +622,18 @@ class HybridVerifyStep(FusedVerifyStep):
         self.append_call = kv_cache_append_call(
             b.k_out, b.v, b.k_cache, b.v_cache, b.page_table, b.seq_len, bufs.accept_len, b.seq_len, bufs.path,
             b.k_scale, b.v_scale, b.status[-1])
+        self.reserve_call = self.release_call = None
+        if s.page_list:
+            lists = (b.page_table, b.n_held, b.free_pages, b.n_free, b.workspace)
+            whole = 0 if b.whole_prefix is None else b.whole_prefix.shape[0]
+            self.reserve_call = kv_pages_reserve_call(b.seq_len, *lists, page_size=s.page_size, n_pos=bufs.shape.n_pos,
+                                                      prefix_table=b.whole_prefix, status=b.page_status[0])
+            self.release_call = kv_pages_release_call(b.seq_len, *lists, page_size=s.page_size, n_prefix=whole,
+                                                      status=b.page_status[1])
 
     def launch_layer(self, l: int, stream: int, events=None) -> None:
+        if l == 0 and self.reserve_call is not None:
+            self.reserve_call(stream)
         super().launch_layer(l, stream, events)
         for call in self.attn_calls[l]:
             call(stream)
@@ -588,6 +648,8 @@ class HybridVerifyStep(FusedVerifyStep):
     def launch_rollback(self, stream: int) -> None:
         super().launch_rollback(stream)
         self.append_call(stream)
+        if self.release_call is not None:
+            self.release_call(stream)
 
     def materialize(self, stream=None) -> None:
         """state <- every request's recurrent state after its last accepted

@@ -918,7 +918,8 @@ typedef struct {
   int32_t page_size; /* table, as hrs_cache_desc                           */
   int32_t table_len;
   int32_t n_prefix;  /* leading entries of every table that hold the pages
-                        of a prefix shared by all requests; 0 = none       */
+                        of a prefix shared by all requests; 0 = none. Whole
+                        pages of it: new positions are written behind them */
 } hrs_pages_desc;
 
 /* Bytes of device workspace the two calls need for this descriptor (0 if it
