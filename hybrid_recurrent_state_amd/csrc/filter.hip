@@ -32,6 +32,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "sample.h"
 
@@ -40,17 +41,22 @@ namespace {
 
 template <typename T> constexpr int kChunk = 32768 / sizeof(T);
 constexpr int kList = 256;             // candidates that a chunk leaves at most
-constexpr int kRow = 1024;             // threads of a row's block, and tokens of its list
+constexpr int kRow = 512;              // threads of a row's block
+constexpr int kTokens = 1024;          // tokens of a row's list at most
+constexpr int kPool = 2048;            // candidates that a block sorts at most
+constexpr int kFew = 256;              // candidates that one wave settles
 constexpr int kBins = 2048;
+constexpr int kValues = 15360;         // values of a bf16 row that are counted one by one
 constexpr int kSmallK = 64;            // a top-k up to this needs no row sums
 constexpr double kCut = 48.0;          // e^-48 of the largest weight: no weight
+constexpr uint32_t kLeastKey = 0x00800000u;   // of the lowest finite logit
 
 struct ChunkInfo {
   double sum;        // of the weights beside the chunk's own maximum (not for a small top-k)
   float top;         // largest logit
-  float low;         // smallest finite one
   uint32_t bound;    // everything with a key from here on is in the list
   int32_t n;         // how many that are; more than kList: the list is not whole
+  int32_t pad;
 };
 
 struct RowInfo {
@@ -67,7 +73,7 @@ struct FilterArgs : SampleArgs {
   ChunkInfo* chunks;   // workspace [rows][n_chunks]
   uint64_t* lists;     // workspace [rows][n_chunks][kList]: order numbers
   RowInfo* rows;       // workspace [rows]
-  uint64_t* kept;      // workspace [rows][kRow]: complemented index above key, by index
+  uint64_t* kept;      // workspace [rows][kTokens]: complemented index above key, by index
 };
 using FilterTree = WithTree<FilterArgs>;
 
@@ -102,11 +108,11 @@ struct Limits {
   }
 };
 
-// A logit below this beside the largest one has no weight.
+// A logit below this key's beside the largest one has no weight.
 __device__ __forceinline__ uint32_t cut_key(float top, float tau) {
-  if (top == -__builtin_inff()) return 1;
-  const float z = static_cast<float>(static_cast<double>(top) - kCut * fmax(static_cast<double>(tau), 0.0));
-  return max(key_of(z), 1u);          // (+inf - inf, a NaN, gives 1; see below)
+  if (top == __builtin_inff()) return key_of(top);
+  if (top == -__builtin_inff()) return kLeastKey;
+  return max(key_of(static_cast<float>(static_cast<double>(top) - kCut * fmax(static_cast<double>(tau), 0.0))), kLeastKey);
 }
 
 // e^((z - top) / tau) in float32 with the argument good to 2^-40 or so: its
@@ -131,6 +137,21 @@ struct FastWeigher {
   }
 };
 
+// Largest number over the wave, the same in every lane.
+__device__ __forceinline__ uint32_t wave_max(uint32_t x) {
+  auto dpp = [&](auto ctrl) {
+    x = max(x, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(x), decltype(ctrl)::value, 0xF, 0xF, false)));
+  };
+  dpp(std::integral_constant<int, 0xB1>{});
+  dpp(std::integral_constant<int, 0x4E>{});
+  dpp(std::integral_constant<int, 0x141>{});
+  dpp(std::integral_constant<int, 0x140>{});
+  const auto a = __builtin_amdgcn_permlane16_swap(x, x, false, false);
+  x = max(a[0], a[1]);
+  const auto b = __builtin_amdgcn_permlane32_swap(x, x, false, false);
+  return max(b[0], b[1]);
+}
+
 // 1. Grid: (row, chunk).
 template <typename T> __global__ __launch_bounds__(kThreads) void candidate_kernel(const FilterArgs args) {
   const int chunk = blockIdx.x % args.n_chunks;
@@ -149,7 +170,7 @@ template <typename T> __global__ __launch_bounds__(kThreads) void candidate_kern
   }
   const Limits lim(args, r);
   // Slices past the row's end count as NaN.
-  float m = -__builtin_inff(), low = __builtin_inff();
+  float m = -__builtin_inff();
 #pragma unroll
   for (int it = 0; it < kIter; ++it) {
     const bool on = begin + (it * kThreads + static_cast<int>(threadIdx.x)) * 8 < end;
@@ -157,7 +178,6 @@ template <typename T> __global__ __launch_bounds__(kThreads) void candidate_kern
     for (int i = 0; i < 8; ++i) {
       v[it][i] = on ? __builtin_canonicalizef(v[it][i]) : __builtin_nanf("");
       m = fmaxf(m, v[it][i]);
-      low = fminf(low, v[it][i] > -__builtin_inff() ? v[it][i] : __builtin_inff());
     }
   }
   // The wave's j-th largest of the lanes' maxima, a bit at a time; the bits that
@@ -171,46 +191,38 @@ template <typename T> __global__ __launch_bounds__(kThreads) void candidate_kern
     const uint32_t up = bound | 1u << b;
     if (__popcll(__ballot(mine >= up)) >= j) bound = up;
   }
-  float top = m;
-#pragma unroll
-  for (int d = 32; d; d >>= 1) {
-    top = fmaxf(top, __shfl_xor(top, d));
-    low = fminf(low, __shfl_xor(low, d));
-  }
-  __shared__ float tops[kThreads / 64], lows[kThreads / 64];
-  __shared__ uint32_t bounds[kThreads / 64];
+  __shared__ uint32_t tops[kThreads / 64], bounds[kThreads / 64];
   __shared__ int32_t count;
   __shared__ double lds[kThreads / 64];
+  uint32_t top_key = wave_max(mine);
   if (lane == 0) {
-    tops[wave] = top;
-    lows[wave] = low;
+    tops[wave] = top_key;
     bounds[wave] = bound;
   }
   if (threadIdx.x == 0) count = 0;
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < kThreads / 64; ++i) {
-    top = fmaxf(top, tops[i]);
-    low = fminf(low, lows[i]);
+    top_key = max(top_key, tops[i]);
     bound = min(bound, bounds[i]);
   }
+  const float top = top_key ? logit_of(top_key) : -__builtin_inff();
   bound = max(bound, cut_key(top, lim.tau));
-  if (top == __builtin_inff()) bound = key_of(top);
+  const float least = logit_of(bound);
   uint64_t* const list = args.lists + (row * args.n_chunks + chunk) * kList;
-  if (mine >= bound) {
+  if (m >= least) {
 #pragma unroll
     for (int it = 0; it < kIter; ++it)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint32_t k = key_of(v[it][i]);
-        if (k >= bound) {
+      for (int i = 0; i < 8; ++i)
+        if (v[it][i] >= least) {
           const int at = atomicAdd(&count, 1);
-          if (at < kList) list[at] = order_of(k, begin + (it * kThreads + static_cast<int>(threadIdx.x)) * 8 + i);
+          if (at < kList)
+            list[at] = order_of(key_of(v[it][i]), begin + (it * kThreads + static_cast<int>(threadIdx.x)) * 8 + i);
         }
-      }
   }
   double sum = 0.0;
-  if (!small && top > -__builtin_inff()) {
+  if (!small && top_key) {
     const FastWeigher weigh(top, lim.tau);
     float s = 0.0f;
 #pragma unroll
@@ -224,10 +236,10 @@ template <typename T> __global__ __launch_bounds__(kThreads) void candidate_kern
   }
   if (!small) sum = block_reduce(sum, add, lds);
   else __syncthreads();
-  if (threadIdx.x == 0) args.chunks[row * args.n_chunks + chunk] = ChunkInfo{sum, top, low, bound, count};
+  if (threadIdx.x == 0) args.chunks[row * args.n_chunks + chunk] = ChunkInfo{sum, top, bound, count, 0};
 }
 
-// Sums over the first n threads' values, in order, over a block of kRow threads.
+// Sum over the block's threads up to and with this one, in order.
 template <typename V> __device__ __forceinline__ V row_scan(V x, V* lds, V* total) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
 #pragma unroll
@@ -260,31 +272,46 @@ __device__ __forceinline__ int row_min(int x, int* lds) {
   return x;
 }
 
-// a[0 .. n) (n a power of two, at most 2 kRow) in descending order. Up to 128
-// numbers are one wave's work and need no barrier of the block.
-__device__ __forceinline__ void sort_step(uint64_t* a, int i, int size, int apart) {
-  const int lo = 2 * apart * (i / apart) + i % apart, hi = lo + apart;
-  const uint64_t x = a[lo], y = a[hi];
-  if (((lo & size) == 0) == (x < y)) {
-    a[lo] = y;
-    a[hi] = x;
-  }
+// Sum over the lanes up to and with this one.
+__device__ __forceinline__ double lane_scan(double x) {
+  auto dpp = [&](auto ctrl, auto rows) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, x);
+    constexpr int C = decltype(ctrl)::value, M = decltype(rows)::value;
+    const uint32_t lo = __builtin_amdgcn_update_dpp(0, static_cast<int>(b), C, M, 0xF, false);
+    const uint32_t hi = __builtin_amdgcn_update_dpp(0, static_cast<int>(b >> 32), C, M, 0xF, false);
+    x += __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
+  };
+  using std::integral_constant;
+  dpp(integral_constant<int, 0x111>{}, integral_constant<int, 0xF>{});
+  dpp(integral_constant<int, 0x112>{}, integral_constant<int, 0xF>{});
+  dpp(integral_constant<int, 0x114>{}, integral_constant<int, 0xF>{});
+  dpp(integral_constant<int, 0x118>{}, integral_constant<int, 0xF>{});
+  dpp(integral_constant<int, 0x142>{}, integral_constant<int, 0xA>{});
+  dpp(integral_constant<int, 0x143>{}, integral_constant<int, 0xC>{});
+  return x;
 }
+__device__ __forceinline__ double lane_of(double x, int lane) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, x);
+  const uint32_t lo = __builtin_amdgcn_readlane(static_cast<int>(b), lane);
+  const uint32_t hi = __builtin_amdgcn_readlane(static_cast<int>(b >> 32), lane);
+  return __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
+}
+
+// a[0 .. n) (n a power of two) in descending order.
 __device__ __forceinline__ void sort_down(uint64_t* a, int n) {
-  const int tid = threadIdx.x;
   __syncthreads();
   for (int size = 2; size <= n; size <<= 1)
     for (int apart = size >> 1; apart > 0; apart >>= 1) {
-      if (n > 128) {
-        if (tid < n / 2) sort_step(a, tid, size, apart);
-        __syncthreads();
-      } else {
-        if (tid < n / 2) sort_step(a, tid, size, apart);
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        __builtin_amdgcn_wave_barrier();
+      for (int i = threadIdx.x; i < n / 2; i += kRow) {
+        const int lo = 2 * apart * (i / apart) + i % apart, hi = lo + apart;
+        const uint64_t x = a[lo], y = a[hi];
+        if (((lo & size) == 0) == (x < y)) {
+          a[lo] = y;
+          a[hi] = x;
+        }
       }
+      __syncthreads();
     }
-  __syncthreads();
 }
 __device__ __forceinline__ int padded(int n) {
   int p = 2;
@@ -293,8 +320,16 @@ __device__ __forceinline__ int padded(int n) {
 }
 
 struct RowLds {
-  uint64_t list[2 * kRow];
-  uint64_t hist[kBins];
+  alignas(16) uint64_t list[kPool];
+  union {
+    uint64_t hist[kBins];                // of whole-number weights
+    uint32_t count[kValues];             // of values
+    struct {
+      alignas(16) uint64_t few[kFew];    // the largest candidates
+      alignas(16) uint64_t sorted[kFew];
+      uint32_t bins[kFew];
+    };
+  };
   union {
     double d[kRow / 64];
     uint64_t u[kRow / 64];
@@ -302,20 +337,50 @@ struct RowLds {
   } sums;
   uint64_t found;        // hand-over from one thread to all
   uint64_t above;
+  double weight;
   uint32_t least, most;
-  int32_t n;
+  int32_t n, m;
 };
+static_assert(sizeof(RowLds) <= 80 * 1024, "two blocks a CU");
 
-// A row's logits, eight a thread, four slices on their way at once; f(index of
-// the first, eight logits).
+// A row's logits, eight a thread; f(index of the first, eight logits). The next
+// 256 bytes of a thread are on their way while it goes through the last: one
+// block has a row to itself and nothing else hides the reads.
+template <typename T> struct Slice {
+  u32x4 w[sizeof(T) / 2];
+  __device__ __forceinline__ void load(const T* p) {
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) w[i] = reinterpret_cast<const u32x4*>(p)[i];
+  }
+  __device__ __forceinline__ void widen(float* z) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      z[i] = sizeof(T) == 4 ? __uint_as_float(w[i / 4 * (sizeof(T) / 4)][i % 4]) : i % 2 ? bf16_hi(w[0][i / 2]) : bf16_lo(w[0][i / 2]);
+  }
+};
 template <typename T, typename F> __device__ __forceinline__ void each_slice(const T* row, int V, F f) {
-  for (int e0 = threadIdx.x * 8; e0 < V; e0 += 4 * 8 * kRow) {
-    float z[4][8];
+  constexpr int kAhead = 16 / sizeof(T);
+  constexpr int64_t kStep = static_cast<int64_t>(kAhead) * 8 * kRow;
+  Slice<T> x[2][kAhead];
+  const int64_t e0 = threadIdx.x * 8;
+  auto load = [&](Slice<T>(&y)[kAhead], int64_t e) {
 #pragma unroll
-    for (int u = 0; u < 4; ++u) load8<T>(row + min(e0 + u * 8 * kRow, V - 8), z[u]);
+    for (int u = 0; u < kAhead; ++u) y[u].load(row + min(e + u * 8 * kRow, static_cast<int64_t>(V - 8)));
+  };
+  auto use = [&](const Slice<T>(&y)[kAhead], int64_t e) {
 #pragma unroll
-    for (int u = 0; u < 4; ++u)
-      if (e0 + u * 8 * kRow < V) f(e0 + u * 8 * kRow, z[u]);
+    for (int u = 0; u < kAhead; ++u) {
+      float z[8];
+      y[u].widen(z);
+      if (e + u * 8 * kRow < V) f(static_cast<int>(e + u * 8 * kRow), z);
+    }
+  };
+  load(x[0], e0);
+  for (int64_t e = e0; e < V; e += 2 * kStep) {
+    load(x[1], e + kStep);
+    use(x[0], e);
+    load(x[0], e + 2 * kStep);
+    use(x[1], e + kStep);
   }
 }
 
@@ -330,24 +395,103 @@ struct WholeWeigher {
   }
 };
 
-// Order number of the first token, of those that `in` admits, at which the sum
-// of amount(logit) over the order reaches `target`; zero if it is not reached.
-// Everything from `ceiling` on is before the row's first token. Several reads of
-// the row.
+// The index of the nth (from 1) token with this key, by the whole block. Waves
+// count their slices of 64 rounds at a time; the slice where the count is
+// reached is looked through again.
+template <typename T> __device__ int nth_of_key(const T* row, int V, uint32_t key, uint64_t nth, RowLds& s) {
+  constexpr int kRounds = 64;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  uint32_t* const counts = reinterpret_cast<uint32_t*>(s.list);          // [rounds][waves]
+  uint64_t left = nth;
+  for (int64_t base = 0; base < V; base += static_cast<int64_t>(kRounds) * 8 * kRow) {
+    auto hits_of = [&](int64_t e) {
+      uint32_t hits = 0;
+      if (e < V) {
+        float z[8];
+        load8<T>(row + e, z);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) hits |= key_of(z[i]) == key ? 1u << i : 0;
+      }
+      return hits;
+    };
+    __syncthreads();
+#pragma unroll 4
+    for (int it = 0; it < kRounds; ++it) {
+      const int64_t e = base + (static_cast<int64_t>(it) * kRow + tid) * 8;
+      if (base + static_cast<int64_t>(it) * kRow * 8 >= V) {
+        if (lane == 0) counts[it * (kRow / 64) + wave] = 0;
+        continue;
+      }
+      int n = __popc(hits_of(e));
+      n = static_cast<int>(group_sum<16>(static_cast<float>(n)));        // at most 128
+      n = __builtin_amdgcn_readlane(n, 0) + __builtin_amdgcn_readlane(n, 16) + __builtin_amdgcn_readlane(n, 32) +
+          __builtin_amdgcn_readlane(n, 48);
+      if (lane == 0) counts[it * (kRow / 64) + wave] = n;
+    }
+    __syncthreads();
+    uint64_t all;
+    const uint32_t mine = counts[tid];
+    const uint64_t upto = row_scan(static_cast<uint64_t>(mine), s.sums.u, &all);
+    if (all >= left) {
+      if (upto >= left && upto - mine < left) {
+        s.found = tid;
+        s.above = upto - mine;
+      }
+      __syncthreads();
+      const int slice = static_cast<int>(s.found);
+      left -= s.above;
+      __syncthreads();
+      if (wave == 0) {
+        const int64_t e = base + (static_cast<int64_t>(slice / (kRow / 64)) * kRow + slice % (kRow / 64) * 64 + lane) * 8;
+        uint32_t hits = hits_of(e);
+        int c = __popc(hits);
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+          const int y = __shfl_up(c, d);
+          c += lane >= d ? y : 0;
+        }
+        const int before = c - __popc(hits);
+        if (static_cast<uint64_t>(c) >= left && static_cast<uint64_t>(before) < left) {
+          for (int i = before + 1; i < static_cast<int>(left); ++i) hits &= hits - 1;
+          s.found = static_cast<uint64_t>(e) + __ffs(hits) - 1;
+        }
+      }
+      __syncthreads();
+      const int index = static_cast<int>(s.found);
+      __syncthreads();
+      return index;
+    }
+    left -= all;
+  }
+  return 0;
+}
+
+struct Border {
+  uint64_t order;    // zero: the target was not reached
+  uint64_t sum;      // of the amounts up to and with it
+};
+
+// The first token, of those that `in` admits, at which the sum of
+// amount(logit) over the order reaches the target: a share of the sum of all of
+// them (share >= 0, rounded up, at least 1) or `target`. Bins divide the logits
+// from `least` to `top`; what is below is in the last one. Two reads of the row,
+// as a rule.
 template <typename T, typename In, typename Amount>
-__device__ uint64_t select_border(const T* row, int V, float top, float low, uint64_t target, In in, Amount amount, RowLds& s) {
+__device__ Border select_border(const T* row, int V, float top, float least, double share, uint64_t target, In in, Amount amount,
+                                RowLds& s) {
   const int tid = threadIdx.x;
   // First by equal steps of the logits: neighbours in memory then seldom meet
   // in a bin (keys crowd around powers of two).
-  const float step = top > low && top < __builtin_inff() ? fminf((kBins - 1) / (top - low), 3.0e38f) : 0.0f;
+  const float step = top > least && top < __builtin_inff() ? fminf((kBins - 1) / (top - least), 3.0e38f) : 0.0f;
+  const bool steps = step > 0.0f;
   auto bin_of = [&](float z) {
-    if (!(step > 0.0f)) return z == top ? 0 : kBins - 1;
-    return static_cast<int>(fminf((top - z) * step, static_cast<float>(kBins - 1)));
+    return steps ? static_cast<int>(fminf((top - z) * step, static_cast<float>(kBins - 1))) : z == top ? 0 : kBins - 1;
   };
-  uint32_t from = 1, to = 0xFFFFFFFFu;   // keys of the border's bin
-  int shift = -1;                        // -1: bins by steps
-  uint64_t above = 0;                    // amount in front of the bin
+  uint32_t from = kLeastKey, to = 0xFFFFFFFFu;   // keys of the border's bin
+  int shift = -1;                                // -1: bins by steps
+  uint64_t above = 0;                            // amount in front of the bin
   for (;;) {
+    __syncthreads();
     for (int i = tid; i < kBins; i += kRow) s.hist[i] = 0;
     __syncthreads();
     each_slice(row, V, [&](int e, const float* z) {
@@ -362,35 +506,44 @@ __device__ uint64_t select_border(const T* row, int V, float top, float low, uin
       }
     });
     __syncthreads();
-    const uint64_t h0 = s.hist[2 * tid], h1 = s.hist[2 * tid + 1];
-    uint64_t total;
-    const uint64_t upto = row_scan(h0 + h1, s.sums.u, &total);
-    if (above + total < target) return 0;
-    const uint64_t before = above + upto - h0 - h1;
-    if (before < target && above + upto >= target) {
-      const bool second = before + h0 < target;
-      s.found = 2 * tid + second;
-      s.above = before + (second ? h0 : 0);
+    constexpr int kPer = kBins / kRow;
+    uint64_t h[kPer], sum = 0, total;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) sum += h[i] = s.hist[kPer * tid + i];
+    const uint64_t upto = row_scan(sum, s.sums.u, &total);
+    if (share >= 0.0) {
+      target = max(uint64_t{1}, static_cast<uint64_t>(ceil(share * static_cast<double>(total))));
+      share = -1.0;
     }
-    __syncthreads();
-    const int bin = static_cast<int>(s.found);
-    above = s.above;
-    // The bin's members.
-    __syncthreads();
-    if (tid == 0) {
+    if (above + total < target) return Border{0, above + total};
+    uint64_t before = above + upto - sum;
+    if (before < target && above + upto >= target) {
+      int at = 0;
+#pragma unroll
+      for (int i = 0; i + 1 < kPer; ++i)
+        if (at == i && before + h[i] < target) {
+          before += h[i];
+          ++at;
+        }
+      s.found = kPer * tid + at;
+      s.above = before;
       s.n = 0;
       s.least = 0xFFFFFFFFu;
       s.most = 0;
     }
     __syncthreads();
+    const int bin = static_cast<int>(s.found);
+    above = s.above;
+    // The bin's members.
     each_slice(row, V, [&](int e, const float* z) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
+        if (shift < 0 && bin_of(z[i]) != bin) continue;                  // (a NaN is in some bin)
         const uint32_t k = key_of(z[i]);
         if (k < from || k > to || !in(k, e + i) || amount(z[i]) == 0) continue;
-        if ((shift < 0 ? bin_of(z[i]) : static_cast<int>((to - k) >> shift)) != bin) continue;
+        if (shift >= 0 && static_cast<int>((to - k) >> shift) != bin) continue;
         const int at = atomicAdd(&s.n, 1);
-        if (at < 2 * kRow) s.list[at] = order_of(k, e + i);
+        if (at < kPool) s.list[at] = order_of(k, e + i);
         atomicMin(&s.least, k);
         atomicMax(&s.most, k);
       }
@@ -399,44 +552,40 @@ __device__ uint64_t select_border(const T* row, int V, float top, float low, uin
     const int n = s.n;
     from = s.least;
     to = s.most;
-    if (n <= 2 * kRow) {
+    if (n <= kPool) {
       const int size = padded(n);
       for (int i = tid; i < size; i += kRow)
         if (i >= n) s.list[i] = 0;
       sort_down(s.list, size);
-      uint64_t x[2];
+      constexpr int kMine = kPool / kRow;
+      uint64_t x[kMine], part = 0, all;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) x[i] = 2 * tid + i < n ? amount(logit_of(s.list[2 * tid + i] >> 32)) : 0;
-      uint64_t all;
-      const uint64_t c = above + row_scan(x[0] + x[1], s.sums.u, &all);
-      const uint64_t b = c - x[0] - x[1];
-      if (b < target && c >= target) s.found = s.list[2 * tid + (b + x[0] < target)];
-      __syncthreads();
-      return s.found;
-    }
-    if (from == to) {
-      // Ties: the border is the one with so many of the same in front of it.
-      const uint64_t each = amount(logit_of(from));
-      uint64_t left = (target - above + each - 1) / each;
-      for (int e0 = 0; e0 < V; e0 += 8 * kRow) {
-        const int e = e0 + tid * 8;
-        float z[8];
-        load8<T>(row + min(e, V - 8), z);
-        uint32_t hits = 0;
+      for (int i = 0; i < kMine; ++i)
+        part += x[i] = kMine * tid + i < n ? amount(logit_of(s.list[kMine * tid + i] >> 32)) : 0;
+      const uint64_t c = above + row_scan(part, s.sums.u, &all);
+      uint64_t b = c - part;
+      if (b < target && c >= target) {
+        int at = 0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) hits |= e < V && key_of(z[i]) == from && in(from, e + i) ? 1u << i : 0;
-        uint64_t all;
-        const uint64_t c = row_scan(static_cast<uint64_t>(__popc(hits)), s.sums.u, &all);
-        if (c >= left && c - __popc(hits) < left) {
-          uint32_t h = hits;
-          for (uint64_t i = c - __popc(hits) + 1; i < left; ++i) h &= h - 1;
-          s.found = order_of(from, e + __ffs(h) - 1);
-        }
-        if (all >= left) break;
-        left -= all;
+        for (int i = 0; i + 1 < kMine; ++i)
+          if (at == i && b + x[i] < target) {
+            b += x[i];
+            ++at;
+          }
+        s.found = s.list[kMine * tid + at];
+        s.above = b + amount(logit_of(s.found >> 32));
       }
       __syncthreads();
-      return s.found;
+      const Border found{s.found, s.above};
+      __syncthreads();
+      return found;
+    }
+    if (from == to) {
+      // Ties: the border is the one with so many of the same in front of it
+      // (`in` admits whole rows or, by index, a beginning of each key's).
+      const uint64_t each = amount(logit_of(from));
+      const uint64_t nth = (target - above + each - 1) / each;
+      return Border{order_of(from, nth_of_key(row, V, from, nth, s)), above + nth * each};
     }
     // Bins of equal numbers of keys.
     shift = 0;
@@ -445,40 +594,38 @@ __device__ uint64_t select_border(const T* row, int V, float top, float low, uin
 }
 
 // 2. Grid: row.
-template <typename T> __global__ __launch_bounds__(kRow) void border_kernel(const FilterArgs args) {
+template <typename T> __global__ __launch_bounds__(kRow, 4) void border_kernel(const FilterArgs args) {
   __shared__ RowLds s;
   const int64_t row = static_cast<int64_t>(args.req0) * args.n_pos + blockIdx.x;
   const int r = static_cast<int>(row / args.n_pos);
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int V = args.vocab;
   const ChunkInfo* const chunks = args.chunks + row * args.n_chunks;
+  const ChunkInfo mine = chunks[min(lane, args.n_chunks - 1)];
   const Limits lim(args, r);
+  if (tid < kFew) s.bins[tid] = 0;
+  if (tid == 0) s.n = s.m = 0;
   // The chunks' maxima and the largest bound, by every wave for itself.
-  float top = -__builtin_inff(), low = __builtin_inff();
-  uint32_t bound = 1;
-  for (int c = lane; c < args.n_chunks; c += 64) {
-    const ChunkInfo x = chunks[c];
-    top = fmaxf(top, x.top);
-    low = fminf(low, x.low);
-    bound = max(bound, x.bound);
+  uint32_t top_key = key_of(mine.top), bound = max(mine.bound, kLeastKey);
+  for (int c = lane + 64; c < args.n_chunks; c += 64) {
+    top_key = max(top_key, key_of(chunks[c].top));
+    bound = max(bound, chunks[c].bound);
   }
-#pragma unroll
-  for (int d = 32; d; d >>= 1) {
-    top = fmaxf(top, __shfl_xor(top, d));
-    low = fminf(low, __shfl_xor(low, d));
-    bound = max(bound, static_cast<uint32_t>(__shfl_xor(static_cast<int>(bound), d)));
-  }
+  top_key = wave_max(top_key);
+  bound = wave_max(bound);
   RowInfo* const out = args.rows + row;
-  if (top == -__builtin_inff() || bad_temperature(lim.tau)) {
-    if (tid == 0) *out = RowInfo{top, 0.0, 0, 0, 0};
+  if (top_key == 0 || bad_temperature(lim.tau)) {
+    if (tid == 0) *out = RowInfo{-__builtin_inf(), 0.0, 0, 0, 0};
     return;
   }
+  const float top = logit_of(top_key);
   const Weigher weigh(top, lim.tau);
+  const bool hard = lim.tau == 0.0f || top == __builtin_inff();
   const bool small = lim.k <= kSmallK && lim.k < V;
   double all = 0.0;                      // sum of the row's weights
   if (!small) {
     for (int c = lane; c < args.n_chunks; c += 64) {
-      const ChunkInfo x = chunks[c];
+      const ChunkInfo x = c < 64 ? mine : chunks[c];
       all += x.top > -__builtin_inff() ? x.sum * weigh(x.top) : 0.0;
     }
     all = wave_reduce(all, add);
@@ -487,9 +634,13 @@ template <typename T> __global__ __launch_bounds__(kRow) void border_kernel(cons
     if (tid == 0) *out = RowInfo{top, all, 0, -1, 0};
     return;
   }
-  // Everything from the bound on, from the chunks' lists.
-  if (tid == 0) s.n = 0;
+  const uint32_t cut = cut_key(top, lim.tau);
   __syncthreads();
+  // Everything from the bound on, from the chunks' lists, and how it is spread
+  // from there to the largest logit.
+  const float low = logit_of(bound);
+  const float per = top > low && top < __builtin_inff() ? fminf((kFew - 1) / (top - low), 3.0e38f) : 0.0f;
+  auto bin_of = [&](float z) { return per > 0.0f ? static_cast<int>(fminf((top - z) * per, static_cast<float>(kFew - 1))) : 0; };
   bool whole = true;
   for (int c = wave; c < args.n_chunks; c += kRow / 64) {
     const ChunkInfo x = chunks[c];
@@ -499,79 +650,341 @@ template <typename T> __global__ __launch_bounds__(kRow) void border_kernel(cons
       const uint64_t o = args.lists[(row * args.n_chunks + c) * kList + i];
       if (o >> 32 < bound) continue;
       const int at = atomicAdd(&s.n, 1);
-      if (at < kRow) s.list[at] = o;
+      if (at < kPool) s.list[at] = o;
+      atomicAdd(&s.bins[bin_of(logit_of(o >> 32))], 1u);
     }
   }
   whole = __syncthreads_and(whole);
   const int n = s.n;
-  if (whole && n <= kRow) {
-    const int size = padded(n);
-    if (tid >= n && tid < size) s.list[tid] = 0;
-    sort_down(s.list, size);
-    const uint64_t mine = tid < n ? s.list[tid] : 0;
-    const double w = tid < n ? weigh(logit_of(mine >> 32)) : 0.0;
-    double listed;
-    const double c = row_scan(w, s.sums.d, &listed);
-    // Below the bound is nothing that counts, or nothing of the first k.
-    const bool ends = bound <= cut_key(top, lim.tau) || top == __builtin_inff() || lim.tau == 0.0f || lim.k <= n;
-    const int nk = min(lim.k, n);
-    if (tid == nk - 1) s.found = __builtin_bit_cast(uint64_t, c);
+  whole = whole && n <= kPool;
+  // Language models' rows: the first few dozen settle it, by one wave. A bin's
+  // end that leaves as many as top-k asks for, 64 at least.
+  if (whole) {
+    const int wanted = lim.k <= kFew / 2 ? max(lim.k, 64) : 64;
+    int last = kFew - 1;                 // last bin that is taken
+    {
+      uint32_t c[kFew / 64], sum = 0;
+#pragma unroll
+      for (int i = 0; i < kFew / 64; ++i) sum += c[i] = s.bins[lane * (kFew / 64) + i];
+      uint32_t upto = sum;
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1) {
+        const uint32_t y = __shfl_up(static_cast<int>(upto), d);
+        upto += lane >= d ? y : 0;
+      }
+      const uint64_t hit = __ballot(upto >= static_cast<uint32_t>(wanted));
+      if (hit) {
+        const int L = __builtin_ctzll(hit);
+        uint32_t run = upto - sum;
+        int at = kFew / 64 - 1;
+        for (int i = kFew / 64 - 1; i >= 0; --i) {
+          uint32_t x = run;
+          for (int k = 0; k <= i; ++k) x += c[k];
+          if (x >= static_cast<uint32_t>(wanted)) at = i;
+        }
+        last = L * (kFew / 64) + __builtin_amdgcn_readlane(at, L);
+      }
+    }
+    for (int i = tid; i < n; i += kRow) {
+      const uint64_t o = s.list[i];
+      if (bin_of(logit_of(o >> 32)) > last) continue;
+      const int at = atomicAdd(&s.m, 1);
+      if (at < kFew) s.few[at] = o;
+    }
     __syncthreads();
-    const double of_k = ends ? __builtin_bit_cast(double, s.found) : all;
-    const bool known = ends || lim.k == V;               // the sum that top-p is a share of
-    const int np = lim.p < 1.0 ? row_min(tid < nk && c >= lim.p * of_k ? tid + 1 : kRow + 1, s.sums.i) : kRow + 1;
-    const int nm = lim.m > 0.0 ? row_min(tid < n && w < lim.m ? tid : kRow + 1, s.sums.i) : kRow + 1;
-    if ((lim.p >= 1.0 || known) && (ends || np <= n || nm < n)) {
+    const int m = s.m;
+    if (m <= kFew) {
+      // Places by counting what is larger.
+      if (tid == 0 && (m & 1)) s.few[m] = 0;            // (kFew is even)
+      __syncthreads();
+      if (tid < m) {
+        const uint64_t o = s.few[tid];
+        int place = 0;
+        for (int i = 0; i < m; i += 2) {
+          const u32x4 x = *reinterpret_cast<const u32x4*>(&s.few[i]);
+          place += (static_cast<uint64_t>(x.y) << 32 | x.x) > o;
+          place += (static_cast<uint64_t>(x.w) << 32 | x.z) > o;
+        }
+        s.sorted[place] = o;
+      }
+      __syncthreads();
+      if (wave == 0) {
+        constexpr int kPer = kFew / 64;
+        double w[kPer], c[kPer], sum = 0.0;
+        uint64_t o[kPer];
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+          const int at = lane * kPer + i;
+          o[i] = at < m ? s.sorted[at] : 0;
+          w[i] = at < m ? weigh(logit_of(o[i] >> 32)) : 0.0;
+          sum += w[i];
+          c[i] = sum;
+        }
+        const double before = lane_scan(sum) - sum;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) c[i] += before;
+        auto at_place = [&](const double* x, int place) {
+          const int L = place / kPer, k = place % kPer;
+          double y = x[0];
+#pragma unroll
+          for (int i = 1; i < kPer; ++i) y = k == i ? x[i] : y;
+          return lane_of(y, L);
+        };
+        // The first place where a condition holds, or kTokens.
+        auto first = [&](auto holds) {
+          int at = kTokens;
+#pragma unroll
+          for (int i = kPer - 1; i >= 0; --i) at = holds(lane * kPer + i, i) ? lane * kPer + i : at;
+          const uint64_t hit = __ballot(at < kTokens);
+          return hit ? __builtin_amdgcn_readlane(at, __builtin_ctzll(hit)) : kTokens;
+        };
+        // What is not here has no weight, or is none of the first k.
+        const bool ends = (m == n && bound <= cut) || hard || lim.k <= m;
+        const int nk = min(lim.k, m);
+        const double of_k = ends ? at_place(c, nk - 1) : all;
+        const bool known = lim.p >= 1.0 || ends || lim.k == V;
+        const int np = lim.p < 1.0 ? first([&](int at, int i) { return at < nk && c[i] >= lim.p * of_k; }) + 1 : kTokens + 1;
+        const int nm = lim.m > 0.0 ? first([&](int at, int i) { return at < m && w[i] < lim.m; }) : kTokens + 1;
+        const bool settled = known && (ends || np <= m || nm < m);
+        if (settled) {
+          const int stay = min(nk, min(np, nm));
+          const double kept = at_place(c, stay - 1);
+          if (lane == 0) {
+            *out = RowInfo{top, kept, s.sorted[stay - 1], stay, 0};
+            s.m = -1;
+          }
+          // By index, for the draw: order numbers with their halves exchanged,
+          // which places count what has a smaller index of.
+          for (int e = lane; e < stay; e += 64) {
+            const uint64_t x = s.sorted[e];
+            int place = 0;
+            for (int i = 0; i < stay; ++i) place += static_cast<uint32_t>(s.sorted[i]) > static_cast<uint32_t>(x);
+            args.kept[row * kTokens + place] = x << 32 | x >> 32;
+          }
+        }
+      }
+      __syncthreads();
+      if (s.m < 0) return;
+    }
+  }
+  // All candidates, by the block.
+  if (whole && n <= kTokens) {
+    const int size = padded(n);
+    for (int i = n + tid; i < size; i += kRow) s.list[i] = 0;
+    sort_down(s.list, size);
+    constexpr int kPer = kTokens / kRow;
+    uint64_t o[kPer];
+    double w[kPer], c[kPer], sum = 0.0, listed;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int at = kPer * tid + i;
+      o[i] = at < n ? s.list[at] : 0;
+      w[i] = at < n ? weigh(logit_of(o[i] >> 32)) : 0.0;
+      sum += w[i];
+      c[i] = sum;
+    }
+    const double before = row_scan(sum, s.sums.d, &listed) - sum;
+    const bool ends = bound <= cut || hard || lim.k <= n;
+    const int nk = min(lim.k, n);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      c[i] += before;
+      if (kPer * tid + i == nk - 1) s.weight = c[i];
+    }
+    __syncthreads();
+    const double of_k = ends ? s.weight : all;
+    const bool known = lim.p >= 1.0 || ends || lim.k == V;               // the sum that top-p is a share of
+    int np = kTokens + 1, nm = kTokens + 1;
+#pragma unroll
+    for (int i = kPer - 1; i >= 0; --i) {
+      const int at = kPer * tid + i;
+      if (lim.p < 1.0 && at < nk && c[i] >= lim.p * of_k) np = at + 1;
+      if (lim.m > 0.0 && at < n && w[i] < lim.m) nm = at;
+    }
+    np = row_min(np, s.sums.i);
+    nm = row_min(nm, s.sums.i);
+    if (known && (ends || np <= n || nm < n)) {
       const int stay = min(nk, min(np, nm));
       __syncthreads();
-      if (tid == stay - 1) *out = RowInfo{top, c, mine, stay, 0};
-      // By index, for the draw: order numbers with their halves exchanged.
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+        if (kPer * tid + i == stay - 1) *out = RowInfo{top, c[i], o[i], stay, 0};
+      // By index, for the draw.
       const int pad = padded(stay);
-      if (tid < pad)
-        s.list[tid] = tid < stay ? static_cast<uint64_t>(static_cast<uint32_t>(mine)) << 32 | static_cast<uint32_t>(mine >> 32) : 0;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const int at = kPer * tid + i;
+        if (at < pad) s.list[at] = at < stay ? o[i] << 32 | o[i] >> 32 : 0;
+      }
       sort_down(s.list, pad);
-      if (tid < stay) args.kept[row * kRow + tid] = s.list[tid];
+      for (int i = tid; i < stay; i += kRow) args.kept[row * kTokens + i] = s.list[i];
       return;
     }
   }
-  // The row itself. Weights as whole numbers: at most 2^62 over all of it.
+  // The row itself.
   const T* const logits = static_cast<const T*>(args.logits) + row * V;
+  // Beside the largest weight, min-p is a key: near the logit where the weight
+  // is equal, and there by trying.
+  uint32_t key_m = kLeastKey;
+  if (lim.m > 0.0) {
+    key_m = max(key_of(static_cast<float>(static_cast<double>(top) + static_cast<double>(lim.tau) * log(lim.m))), kLeastKey);
+    key_m = min(key_m, top_key);
+    for (int i = 0; i < 4 && key_m > kLeastKey && weigh(logit_of(key_m - 1)) >= lim.m; ++i) --key_m;
+    for (int i = 0; i < 8 && key_m < top_key && !(weigh(logit_of(key_m)) >= lim.m); ++i) ++key_m;
+  }
+  if constexpr (sizeof(T) == 2) {
+    // A bf16 row has few values: they are counted one by one, from the largest
+    // down to the cut if there is room, and every limit is a number of tokens
+    // that follows from the counts, with sums in 64 bits. Ties at the border go
+    // by index.
+    if (!hard) {
+      const uint32_t first = top_key >> 16;
+      const int down = static_cast<int>(first - (cut >> 16)) + 1, values = min(kValues, down);
+      const bool ends = values == down;          // nothing behind the values has a weight
+      auto value_key = [&](int at) {
+        const uint32_t v = first - at;
+        return v << 16 | (v < 0x8000u ? 0xFFFFu : 0u);
+      };
+      __syncthreads();
+      for (int i = tid; i < values; i += kRow) s.count[i] = 0;
+      __syncthreads();
+      each_slice(logits, V, [&](int, const float* z) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const uint32_t at = first - (key_of(z[i]) >> 16);
+          if (at < static_cast<uint32_t>(values)) atomicAdd(&s.count[at], 1u);
+        }
+      });
+      __syncthreads();
+      // A run of values a thread, in order.
+      constexpr int kRun = kValues / kRow;
+      const int at0 = tid * kRun, at1 = min(values, at0 + kRun);
+      uint64_t tokens = 0, all_tokens;
+      double weight = 0.0, all_weight;
+      for (int at = at0; at < at1; ++at) {
+        const uint32_t c = s.count[at];
+        tokens += c;
+        if (c) weight += c * weigh(logit_of(value_key(at)));
+      }
+      const uint64_t upto = row_scan(tokens, s.sums.u, &all_tokens);
+      const double mass = row_scan(weight, s.sums.d, &all_weight);
+      // Of the thread whose run holds the n-th token: its value, its number
+      // among those of this value, and the sum with it.
+      struct Place {
+        int at;
+        uint64_t nth;
+        double sum;
+        bool last;
+      };
+      auto place_of = [&](uint64_t n) {
+        uint64_t run = upto - tokens;
+        double x = mass - weight;
+        for (int at = at0; at < at1; ++at) {
+          const uint64_t c = s.count[at];
+          if (c == 0) continue;
+          const uint64_t take = min(c, n - run);
+          x += take * weigh(logit_of(value_key(at)));
+          run += take;
+          if (run == n) return Place{at, take, x, take == c};
+        }
+        return Place{at1 - 1, 1, x, true};
+      };
+      auto holds = [&](uint64_t n) { return upto >= n && upto - tokens < n; };
+      const bool has_k = lim.k < V && static_cast<uint64_t>(lim.k) <= all_tokens;
+      if (has_k && holds(lim.k)) s.weight = place_of(lim.k).sum;
+      __syncthreads();
+      const bool known = lim.p >= 1.0 || has_k || lim.k == V || ends;
+      const double share = lim.p * (has_k ? s.weight : ends ? all_weight : all);
+      uint64_t n = has_k ? static_cast<uint64_t>(lim.k) : ~uint64_t{0};
+      if (lim.p < 1.0) {
+        const int owner = row_min(tokens > 0 && mass >= share ? tid : kRow, s.sums.i);
+        if (tid == owner) {
+          uint64_t run = upto - tokens, reached = 0;
+          double x = mass - weight;
+          for (int at = at0; at < at1 && reached == 0; ++at) {
+            const uint64_t c = s.count[at];
+            if (c == 0) continue;
+            const double w = weigh(logit_of(value_key(at)));
+            if (x + c * w >= share)
+              reached = run + (x < share ? min(c, static_cast<uint64_t>(fmax(ceil((share - x) / w), 1.0))) : 1);
+            x += c * w;
+            run += c;
+          }
+          s.found = reached ? reached : run;     // (the run's own sum may round below the share)
+        }
+        __syncthreads();
+        if (owner < kRow) n = min(n, s.found);
+        __syncthreads();
+      }
+      if (lim.m > 0.0) {
+        // Values from key_m on, and how many tokens have them.
+        const uint32_t v = (key_m >> 16) + (key_m >= 0x80000000u && (key_m & 0xFFFFu) ? 1 : 0);
+        const int stay = static_cast<int>(first - v) + 1;
+        if (stay < values) {
+          if (stay >= at0 && stay < at0 + kRun) {
+            uint64_t run = upto - tokens;
+            for (int at = at0; at < stay; ++at) run += s.count[at];
+            s.above = run;
+          }
+          __syncthreads();
+          n = min(n, s.above);
+          __syncthreads();
+        }
+      }
+      if (known && (n <= all_tokens || ends)) {
+        if (n > all_tokens) {
+          if (tid == 0) *out = RowInfo{top, all_weight, order_of(cut, 0x7FFFFFFF), -1, 0};
+          return;
+        }
+        if (holds(n)) {
+          const Place p = place_of(n);
+          s.found = p.at;
+          s.above = p.last ? 0 : p.nth;
+          s.weight = p.sum;
+        }
+        __syncthreads();
+        const uint32_t key = value_key(static_cast<int>(s.found));
+        const uint64_t nth = s.above;
+        const double sum = s.weight;
+        __syncthreads();
+        const int index = nth ? nth_of_key(logits, V, key, nth, s) : 0x7FFFFFFF;
+        if (tid == 0) *out = RowInfo{top, sum, order_of(key, index), -1, 0};
+        return;
+      }
+    }
+  }
+  // Weights as whole numbers: at most 2^62 over all of the row.
   const int shift = min(50, __builtin_clz(V - 1) + 30);
   const WholeWeigher amount(top, lim.tau, shift);
-  const float least = fmaxf(low, static_cast<float>(static_cast<double>(top) - kCut * static_cast<double>(lim.tau)));
-  uint64_t border = order_of(1, 0x7FFFFFFF);             // everything that has a weight
+  const float least = hard ? top : logit_of(cut);
+  uint64_t border = order_of(kLeastKey, 0x7FFFFFFF);     // everything that can have a weight
+  uint64_t stay = 0;
+  bool summed = false;
   if (lim.k < V) {
-    const uint64_t b = select_border(
-        logits, V, top, low, static_cast<uint64_t>(lim.k), [](uint32_t k, int) { return k > 0; },
-        [](float z) { return z > -__builtin_inff() ? uint64_t{1} : uint64_t{0}; }, s);
-    border = max(border, b);
+    const Border b = select_border(
+        logits, V, top, least, -1.0, static_cast<uint64_t>(lim.k), [](uint32_t k, int) { return k >= kLeastKey; },
+        [&](float z) { return z >= least ? uint64_t{1} : uint64_t{0}; }, s);
+    border = max(border, b.order);
   }
   auto stays = [&](uint32_t k, int i) { return order_of(k, i) >= border; };
-  auto sum_of = [&]() {
-    uint64_t x = 0, total;
+  if (lim.p < 1.0) {
+    const Border b = select_border(logits, V, top, least, lim.p, 0, stays, amount, s);
+    border = max(border, b.order);
+    stay = b.sum;
+    summed = true;
+  }
+  if (lim.m > 0.0 && order_of(key_m, 0x7FFFFFFF) > border) {
+    border = order_of(key_m, 0x7FFFFFFF);
+    summed = false;
+  }
+  if (!summed) {
+    uint64_t x = 0;
     each_slice(logits, V, [&](int e, const float* z) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) x += stays(key_of(z[i]), e + i) ? amount(z[i]) : 0;
     });
-    row_scan(x, s.sums.u, &total);
-    return total;
-  };
-  if (lim.p < 1.0) {
-    const uint64_t of_k = sum_of();
-    const uint64_t target = max(uint64_t{1}, static_cast<uint64_t>(ceil(lim.p * static_cast<double>(of_k))));
-    const uint64_t b = select_border(logits, V, top, least, target, stays, amount, s);
-    border = max(border, b);
+    row_scan(x, s.sums.u, &stay);
   }
-  if (lim.m > 0.0) {
-    // The smallest key whose weight is large enough: near the logit where it is
-    // equal, and there by trying.
-    uint32_t k = max(key_of(static_cast<float>(static_cast<double>(top) + static_cast<double>(lim.tau) * log(lim.m))), 1u);
-    k = min(k, key_of(top));
-    for (int i = 0; i < 4 && k > 1 && weigh(logit_of(k - 1)) >= lim.m; ++i) --k;
-    for (int i = 0; i < 8 && k < key_of(top) && !(weigh(logit_of(k)) >= lim.m); ++i) ++k;
-    border = max(border, order_of(k, 0x7FFFFFFF));
-  }
-  const uint64_t stay = sum_of();
   if (tid == 0) *out = RowInfo{top, ldexp(static_cast<double>(stay), -shift), border, -1, 0};
 }
 
@@ -618,13 +1031,13 @@ __device__ __forceinline__ int draw_listed(const FilterArgs& a, const NodeInfo& 
   const float tau = temperature_of(a, r);
   const int64_t row = static_cast<int64_t>(r) * a.n_pos + info.node;
   const Weigher weigh(ri.top, tau);
-  constexpr int kPer = kRow / kThreads;
+  constexpr int kPer = kTokens / kThreads;
   double plain[kPer], x[kPer], sum = 0.0, whole = 0.0;
   int token[kPer];
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     const int at = threadIdx.x * kPer + i;
-    const uint64_t e = at < ri.n ? a.kept[row * kRow + at] : 0;
+    const uint64_t e = at < ri.n ? a.kept[row * kTokens + at] : 0;
     token[i] = static_cast<int>(~static_cast<uint32_t>(e >> 32));
     plain[i] = at < ri.n ? weigh(logit_of(static_cast<uint32_t>(e))) : 0.0;
     x[i] = plain[i];
@@ -802,7 +1215,7 @@ size_t filter_layout(const hrs_sample_desc* d, FilterArgs* args, char* ws) {
   char* const p0 = place(rows * chunks * sizeof(ChunkInfo));
   char* const p1 = place(rows * chunks * kList * sizeof(uint64_t));
   char* const p2 = place(rows * sizeof(RowInfo));
-  char* const p3 = place(rows * kRow * sizeof(uint64_t));
+  char* const p3 = place(rows * kTokens * sizeof(uint64_t));
   char* const p4 = place(d->n_req * pieces * sizeof(double2));
   char* const p5 = place(d->n_req * sizeof(NodeInfo));
   if (args) {
