@@ -358,7 +358,7 @@ template <typename T> struct Slice {
       z[i] = sizeof(T) == 4 ? __uint_as_float(w[i / 4 * (sizeof(T) / 4)][i % 4]) : i % 2 ? bf16_hi(w[0][i / 2]) : bf16_lo(w[0][i / 2]);
   }
 };
-template <typename T, typename F> __device__ __forceinline__ void each_slice(const T* row, int V, F f) {
+template <typename T, typename F> __device__ __forceinline__ void each_raw(const T* row, int V, F f) {
   constexpr int kAhead = 16 / sizeof(T);
   constexpr int64_t kStep = static_cast<int64_t>(kAhead) * 8 * kRow;
   Slice<T> x[2][kAhead];
@@ -369,11 +369,8 @@ template <typename T, typename F> __device__ __forceinline__ void each_slice(con
   };
   auto use = [&](const Slice<T>(&y)[kAhead], int64_t e) {
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      float z[8];
-      y[u].widen(z);
-      if (e + u * 8 * kRow < V) f(static_cast<int>(e + u * 8 * kRow), z);
-    }
+    for (int u = 0; u < kAhead; ++u)
+      if (e + u * 8 * kRow < V) f(static_cast<int>(e + u * 8 * kRow), y[u]);
   };
   load(x[0], e0);
   for (int64_t e = e0; e < V; e += 2 * kStep) {
@@ -382,6 +379,14 @@ template <typename T, typename F> __device__ __forceinline__ void each_slice(con
     load(x[0], e + 2 * kStep);
     use(x[1], e + kStep);
   }
+}
+
+template <typename T, typename F> __device__ __forceinline__ void each_slice(const T* row, int V, F f) {
+  each_raw(row, V, [&](int e, const Slice<T>& x) {
+    float z[8];
+    x.widen(z);
+    f(e, z);
+  });
 }
 
 // A weight as a whole number of 2^-shift.
@@ -399,35 +404,39 @@ struct WholeWeigher {
 // count their slices of 64 rounds at a time; the slice where the count is
 // reached is looked through again.
 template <typename T> __device__ int nth_of_key(const T* row, int V, uint32_t key, uint64_t nth, RowLds& s) {
-  constexpr int kRounds = 64;
+  constexpr int kWaves = kRow / 64, kRounds = 64, kPart = kRounds * 8 * kRow;
+  static_assert(kRounds * kWaves == kRow, "a count a thread");
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   uint32_t* const counts = reinterpret_cast<uint32_t*>(s.list);          // [rounds][waves]
-  uint64_t left = nth;
-  for (int64_t base = 0; base < V; base += static_cast<int64_t>(kRounds) * 8 * kRow) {
-    auto hits_of = [&](int64_t e) {
-      uint32_t hits = 0;
-      if (e < V) {
-        float z[8];
-        load8<T>(row + e, z);
+  auto hits_of = [&](const float* z) {
+    uint32_t hits = 0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) hits |= key_of(z[i]) == key ? 1u << i : 0;
-      }
-      return hits;
-    };
+    for (int i = 0; i < 8; ++i) hits |= key_of(z[i]) == key ? 1u << i : 0;
+    return hits;
+  };
+  const bool zero = key == 0x80000000u;                // two patterns
+  const uint32_t pattern = (__float_as_uint(logit_of(key)) >> 16) * 0x00010001u;
+  uint64_t left = nth;
+  for (int64_t base = 0; base < V; base += kPart) {
     __syncthreads();
-#pragma unroll 4
-    for (int it = 0; it < kRounds; ++it) {
-      const int64_t e = base + (static_cast<int64_t>(it) * kRow + tid) * 8;
-      if (base + static_cast<int64_t>(it) * kRow * 8 >= V) {
-        if (lane == 0) counts[it * (kRow / 64) + wave] = 0;
-        continue;
+    counts[tid] = 0;
+    __syncthreads();
+    each_raw(row + base, static_cast<int>(min(static_cast<int64_t>(kPart), V - base)), [&](int e, const Slice<T>& x) {
+      int n = 8;
+      if (sizeof(T) == 2 && !zero) {
+        // Halves of words that differ from the value's have their upper bit set.
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t y = x.w[0][i] ^ pattern;
+          n -= __popc((((y & 0x7FFF7FFFu) + 0x7FFF7FFFu) | y) & 0x80008000u);
+        }
+      } else {
+        float z[8];
+        x.widen(z);
+        n = __popc(hits_of(z));
       }
-      int n = __popc(hits_of(e));
-      n = static_cast<int>(group_sum<16>(static_cast<float>(n)));        // at most 128
-      n = __builtin_amdgcn_readlane(n, 0) + __builtin_amdgcn_readlane(n, 16) + __builtin_amdgcn_readlane(n, 32) +
-          __builtin_amdgcn_readlane(n, 48);
-      if (lane == 0) counts[it * (kRow / 64) + wave] = n;
-    }
+      if (n) atomicAdd(&counts[e / (8 * kRow) * kWaves + wave], static_cast<uint32_t>(n));
+    });
     __syncthreads();
     uint64_t all;
     const uint32_t mine = counts[tid];
@@ -442,8 +451,13 @@ template <typename T> __device__ int nth_of_key(const T* row, int V, uint32_t ke
       left -= s.above;
       __syncthreads();
       if (wave == 0) {
-        const int64_t e = base + (static_cast<int64_t>(slice / (kRow / 64)) * kRow + slice % (kRow / 64) * 64 + lane) * 8;
-        uint32_t hits = hits_of(e);
+        const int64_t e = base + (static_cast<int64_t>(slice / kWaves) * kRow + slice % kWaves * 64 + lane) * 8;
+        uint32_t hits = 0;
+        if (e < V) {
+          float z[8];
+          load8<T>(row + e, z);
+          hits = hits_of(z);
+        }
         int c = __popc(hits);
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) {
@@ -767,8 +781,20 @@ template <typename T> __global__ __launch_bounds__(kRow, 4) void border_kernel(c
       if (s.m < 0) return;
     }
   }
-  // All candidates, by the block.
-  if (whole && n <= kTokens) {
+  // All candidates, by the block, where they can settle it: not if their
+  // weights fall short of top-p's share (by more than the sum may be off).
+  bool worth = whole && n <= kTokens;
+  if (worth && lim.p < 1.0 && lim.k > n && bound > cut && !hard) {
+    if (lim.k < V) {
+      worth = false;                     // the sum of the first k is not known
+    } else if (!(lim.m > 0.0 && weigh(low) < lim.m * (1.0 + 1e-9))) {
+      double x = 0.0, listed;
+      for (int i = tid; i < n; i += kRow) x += weigh(logit_of(s.list[i] >> 32));
+      row_scan(x, s.sums.d, &listed);
+      worth = listed >= lim.p * all * (1.0 - 1e-9);
+    }
+  }
+  if (worth) {
     const int size = padded(n);
     for (int i = n + tid; i < size; i += kRow) s.list[i] = 0;
     sort_down(s.list, size);
@@ -848,17 +874,34 @@ template <typename T> __global__ __launch_bounds__(kRow, 4) void border_kernel(c
       __syncthreads();
       for (int i = tid; i < values; i += kRow) s.count[i] = 0;
       __syncthreads();
-      each_slice(logits, V, [&](int, const float* z) {
+      each_raw(logits, V, [&](int, const Slice<T>& x) {
+        // Two patterns a word: keys as key_of's, but for the negative zero's,
+        // which is one below the other's.
+        typedef int16_t i16x2 __attribute__((ext_vector_type(2)));
+        typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const uint32_t at = first - (key_of(z[i]) >> 16);
-          if (at < static_cast<uint32_t>(values)) atomicAdd(&s.count[at], 1u);
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t w = x.w[0][i];
+          const uint32_t sign = __builtin_bit_cast(uint32_t, __builtin_bit_cast(i16x2, w) >> i16x2{15, 15});
+          const u16x2 key = __builtin_bit_cast(u16x2, w ^ (sign | 0x80008000u));
+          const uint32_t at = __builtin_bit_cast(uint32_t, u16x2{static_cast<uint16_t>(first), static_cast<uint16_t>(first)} - key);
+          if ((at & 0xFFFFu) < static_cast<uint32_t>(values)) atomicAdd(&s.count[at & 0xFFFFu], 1u);
+          if (at >> 16 < static_cast<uint32_t>(values)) atomicAdd(&s.count[at >> 16], 1u);
         }
       });
       __syncthreads();
-      // A run of values a thread, in order.
-      constexpr int kRun = kValues / kRow;
-      const int at0 = tid * kRun, at1 = min(values, at0 + kRun);
+      const int zero = static_cast<int>(first - 0x8000u);
+      if (tid == 0 && zero >= 0 && zero + 1 < values) {
+        s.count[zero] += s.count[zero + 1];
+        s.count[zero + 1] = 0;
+      }
+      __syncthreads();
+      // A run of values a thread, in order, up to the last that there is.
+      int end = 0;
+      for (int i = tid; i < values; i += kRow) end = s.count[i] ? i + 1 : end;
+      end = -row_min(-end, s.sums.i);
+      const int run_len = (end + kRow - 1) / kRow;
+      const int at0 = min(end, tid * run_len), at1 = min(end, at0 + run_len);
       uint64_t tokens = 0, all_tokens;
       double weight = 0.0, all_weight;
       for (int at = at0; at < at1; ++at) {
@@ -921,7 +964,9 @@ template <typename T> __global__ __launch_bounds__(kRow, 4) void border_kernel(c
         const uint32_t v = (key_m >> 16) + (key_m >= 0x80000000u && (key_m & 0xFFFFu) ? 1 : 0);
         const int stay = static_cast<int>(first - v) + 1;
         if (stay < values) {
-          if (stay >= at0 && stay < at0 + kRun) {
+          if (tid == 0) s.above = all_tokens;
+          __syncthreads();
+          if (stay >= at0 && stay < at1) {
             uint64_t run = upto - tokens;
             for (int at = at0; at < stay; ++at) run += s.count[at];
             s.above = run;
