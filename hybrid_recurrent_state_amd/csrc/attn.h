@@ -161,6 +161,26 @@ struct AttnHole {
   int prefix;        // slots of the prefix, -1: not a length
 };
 
+__device__ __forceinline__ AttnHole attn_hole(const AttnLens& a, const AttnShared& args, const int (&len)[kAttnReqs / 64]) {
+  const int32_t given = *args.prefix_len;
+  const bool ok = given >= 0 && given <= args.prefix_pages << args.page_shift;
+  int lo = 0, hi = ok ? given : 0;
+#pragma unroll
+  for (int k = 0; k < kAttnReqs / 64; ++k) {
+    if (len[k] < 0 || len[k] > a.most) continue;
+    hi = min(hi, len[k]);
+    if (a.window > 0) lo = max(lo, len[k] + a.n_pos - a.window);
+  }
+#pragma unroll
+  for (int d = 32; d; d >>= 1) {
+    lo = max(lo, __shfl_xor(lo, d));
+    hi = min(hi, __shfl_xor(hi, d));
+  }
+  lo = __builtin_amdgcn_readfirstlane((lo + kHoleStep - 1) & ~(kHoleStep - 1));
+  hi = __builtin_amdgcn_readfirstlane(hi & ~(kHoleStep - 1));
+  return AttnHole{lo < hi ? lo : 0, lo < hi ? hi : 0, ok ? given : -1};
+}
+
 // Units of a request that leaves out the hole: its own tiles of the prefix
 // (`before` of them), then those of its own pages. The tile that the prefix
 // ends in is of both kinds.
@@ -202,6 +222,19 @@ template <int KIND> AttnShape attn_shape(int d, int cls);
 template <int KIND> void attn_launch(const AttnTree& args, const AttnLens& lens, int d, int cls, hipStream_t s);
 // Launches of attn_verify_shared: the requests' own part, the prefix.
 template <int KIND> void attn_own_launch(const AttnSharedTree& args, const AttnLens& lens, int d, int cls, hipStream_t s);
+// How the prefix launch for large batches is built (attn_prefix.h).
+template <int KIND, int D> struct PrefixCfg {
+  static constexpr int RT = D >= 128 ? 3 : 4;   // tiles of 16 rows a wave
+  static constexpr int NW = 4;
+  static constexpr bool NEXT = D == 256;                       // the next tile's scores under this one's weights
+  static constexpr int PER_CU = NEXT ? 1 : 2;                  // blocks
+  static constexpr int ROWS = 16 * RT * NW;
+  static constexpr int TS = 32;                                // slots of a tile
+  static constexpr int STAGE = 2 * TS * D * 2;                 // bytes of its keys and values
+  static constexpr int NST = KIND == kF8 ? 3 : 4;              // tiles of the ring
+  static constexpr int LDS = NST * STAGE;
+};
+template <int KIND> void attn_prefix_wide(const AttnShared& args, const AttnLens& lens, int runs, int d, hipStream_t s);
 template <int KIND> void attn_prefix_launch(const AttnShared& args, const AttnLens& lens, int d, int cls, hipStream_t s);
 
 inline bool sizes_ok(const hrs_attn_desc* d) {

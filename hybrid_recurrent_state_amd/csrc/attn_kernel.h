@@ -971,32 +971,11 @@ template <int MODE> struct AttnPlan {
     else return attn_units(a, n, ts);
   }
 
-  // The slots that all requests count at every position.
-  __device__ __forceinline__ void find_hole(const AttnLens& a, const AttnShared& args) {
-    const int32_t given = *args.prefix_len;
-    const bool ok = given >= 0 && given <= args.prefix_pages << args.page_shift;
-    int lo = 0, hi = ok ? given : 0;
-#pragma unroll
-    for (int k = 0; k < kAttnReqs / 64; ++k) {
-      if (len[k] < 0 || len[k] > a.most) continue;
-      hi = min(hi, len[k]);
-      if (a.window > 0) lo = max(lo, len[k] + a.n_pos - a.window);
-    }
-#pragma unroll
-    for (int d = 32; d; d >>= 1) {
-      lo = max(lo, __shfl_xor(lo, d));
-      hi = min(hi, __shfl_xor(hi, d));
-    }
-    lo = __builtin_amdgcn_readfirstlane((lo + kHoleStep - 1) & ~(kHoleStep - 1));
-    hi = __builtin_amdgcn_readfirstlane(hi & ~(kHoleStep - 1));
-    hole = AttnHole{lo < hi ? lo : 0, lo < hi ? hi : 0, ok ? given : -1};
-  }
-
   __device__ __forceinline__ AttnPlan(const AttnLens& a, const AttnBlockArgs<MODE>& args, int ts) {
     const int lane = fresh(threadIdx.x) & 63;
 #pragma unroll
     for (int k = 0; k < kAttnReqs / 64; ++k) len[k] = a.len[min(lane * (kAttnReqs / 64) + k, a.n - 1)];
-    if constexpr (MODE != kSpan) find_hole(a, args);
+    if constexpr (MODE != kSpan) hole = attn_hole(a, args, len);
     if constexpr (MODE == kPrefix) {     // one request of the rows of all, every head the hole's tiles
       const int tiles = (hole.end - hole.first) / ts;
 #pragma unroll

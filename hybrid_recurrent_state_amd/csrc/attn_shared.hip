@@ -23,11 +23,13 @@
 namespace hrs {
 namespace {
 
-// Parts of a launch: how its list of units was cut.
+// Parts of a launch: how its list of units was cut. runs > 0: attn_prefix.h's
+// launch, plan[0] of them for every (head, block of rows).
 struct Cut {
   const f32x4* part;
   const float2* ml;
   const int32_t* plan;   // units before every request, [n + 1]; prefix: [2]
+  int32_t runs;
   int32_t n;             // requests (prefix: 1)
   int32_t heads;         // segments of a request
   int32_t row_blocks;
@@ -39,8 +41,18 @@ struct Cut {
 struct Parts {
   int b0, count;         // blocks that worked on it
   int64_t slot0;         // first part
+  int step;              // from one part to the next
   int tile, n16;         // row's place in a part
   __device__ __forceinline__ Parts(const Cut& c, int i, int h, int row) {
+    tile = row % c.rows / 16;
+    n16 = row % 16;
+    if (c.runs > 0) {
+      b0 = 0;
+      count = c.plan[0];
+      slot0 = static_cast<int64_t>(h) * c.runs * c.row_blocks + row / c.rows;
+      step = c.row_blocks;
+      return;
+    }
     const int first = c.plan[i], units = (c.plan[i + 1] - first) / c.heads, total = c.plan[c.n];
     const int seg = h * c.row_blocks + row / c.rows;
     const int s0 = first + seg * units, s1 = s0 + units;
@@ -51,8 +63,7 @@ struct Parts {
     b0 = units > 0 ? block_of(s0) : 0;
     count = units > 0 ? block_of(s1 - 1) - b0 + 1 : 0;
     slot0 = static_cast<int64_t>(i) * c.heads + seg + b0;
-    tile = row % c.rows / 16;
-    n16 = row % 16;
+    step = 1;
   }
 };
 
@@ -85,7 +96,7 @@ __global__ __launch_bounds__(NS > 1 ? 64 * NS : 256) void shared_join_kernel(con
       f32x4 x[kAtOnce][2];
 #pragma unroll
       for (int j = 0; j < kAtOnce; ++j) {
-        const int64_t slot = p.slot0 + max(min(b + j * NS, p.count - 1), 0);
+        const int64_t slot = p.slot0 + static_cast<int64_t>(max(min(b + j * NS, p.count - 1), 0)) * p.step;
         w[j] = c.ml[slot * c.rows + p.tile * 16 + p.n16];
         const f32x4* from = c.part + (slot * (c.rows / 16) + p.tile) * (DT * 64) + g * 16 + p.n16;
         x[j][0] = from[(2 * dp) * 64];
@@ -178,6 +189,12 @@ template <bool F32> void launch_join(const Cut& own, const Cut& pre, const AttnB
   else launch_join<F32, 256>(own, pre, args, s);
 }
 
+// More rows of a key head than this go to attn_prefix.h's launch. Whole calls
+// there and here, 4 key heads of 256 in bf16: 192 rows over 2,048 slots 46 and
+// 38 us, over 16,384 slots 59 and 62; 384 rows 51 and 45, 74 and 83; 768 rows 61
+// and 62, 107 and 138. (8 heads of 128, e4m3, 768 rows: 63 and 63, 106 and 121.)
+constexpr int64_t kWideRows = 256;
+
 // How a launch's parts are laid out in the workspace.
 struct PartSizes {
   AttnShape shape;
@@ -191,6 +208,39 @@ PartSizes part_sizes(int kind, int d, int64_t n, int64_t kvheads, int64_t rows) 
   p.row_blocks = static_cast<int>((rows + p.shape.rows - 1) / p.shape.rows);
   p.segs = n * kvheads * p.row_blocks;
   p.parts = p.segs + p.shape.blocks;
+  p.ml_bytes = (p.parts * p.shape.rows * sizeof(float2) + 255) / 256 * 256;
+  p.bytes = p.ml_bytes + static_cast<size_t>(p.parts) * p.shape.rows * d * sizeof(float);
+  return p;
+}
+
+// The prefix launch for large batches: rows of a block, and the runs that a
+// head's slots are cut into, as many as let all blocks run at once or, where
+// there are more (head, block of rows) than that, leave the last round of
+// blocks nearly full.
+bool prefix_wide(int kind, int64_t rows) { return kind != kF32 && rows > kWideRows; }
+int prefix_rows(int d) { return d == 256 ? PrefixCfg<kB16, 256>::ROWS : d == 128 ? PrefixCfg<kB16, 128>::ROWS : PrefixCfg<kB16, 64>::ROWS; }
+int prefix_runs(int64_t segs, int d) {
+  const int64_t room = kAttnCus * static_cast<int64_t>(d == 256 ? PrefixCfg<kB16, 256>::PER_CU : PrefixCfg<kB16, 128>::PER_CU);
+  const int64_t most = std::max<int64_t>(1, room / segs);
+  if (segs * most * 10 >= room * 8 || segs > 8 * room) return static_cast<int>(most);
+  int best = static_cast<int>(most);
+  double least = 1.0 / best;
+  for (int r = best + 1; r <= 4 * most; ++r) {
+    const double t = static_cast<double>((segs * r + room - 1) / room) / r * (1.0 + 0.02 * (r - most) / most);
+    if (t < least) {
+      least = t;
+      best = r;
+    }
+  }
+  return best;
+}
+PartSizes wide_sizes(int d, int64_t kvheads, int64_t rows, int* runs) {
+  PartSizes p;
+  p.shape = {prefix_rows(d), 0, 0};
+  p.row_blocks = static_cast<int>((rows + p.shape.rows - 1) / p.shape.rows);
+  *runs = prefix_runs(kvheads * p.row_blocks, d);
+  p.segs = kvheads * p.row_blocks;
+  p.parts = p.segs * *runs;
   p.ml_bytes = (p.parts * p.shape.rows * sizeof(float2) + 255) / 256 * 256;
   p.bytes = p.ml_bytes + static_cast<size_t>(p.parts) * p.shape.rows * d * sizeof(float);
   return p;
@@ -214,9 +264,14 @@ extern "C" size_t attn_verify_shared_workspace_bytes(const hrs_attn_desc* d) {
   const int n = std::min(d->n_req, kAttnReqs);
   const int64_t rows = static_cast<int64_t>(d->n_pos) * (d->n_heads / d->n_kvheads);
   size_t most = 0;
-  for (const int kind : {kF32, kB16, kF8})
-    most = std::max(most, part_sizes(kind, d->d, n, d->n_kvheads, rows).bytes +
-                              part_sizes(kind, d->d, 1, d->n_kvheads, n * rows).bytes);
+  for (const int kind : {kF32, kB16, kF8}) {
+    const size_t own = part_sizes(kind, d->d, n, d->n_kvheads, rows).bytes;
+    most = std::max(most, own + part_sizes(kind, d->d, 1, d->n_kvheads, n * rows).bytes);
+    int runs;
+    // (Smaller batches may be cut into more runs.)
+    for (int m = n; prefix_wide(kind, m * rows); --m)
+      most = std::max(most, own + wide_sizes(d->d, d->n_kvheads, m * rows, &runs).bytes);
+  }
   return 2 * kPlanBytes + most;
 }
 
@@ -278,7 +333,9 @@ extern "C" int attn_verify_shared(const hrs_attn_desc* d, int32_t prefix_pages, 
   for (int r0 = 0; r0 < d->n_req; r0 += per_launch) {
     const int n = std::min(per_launch, d->n_req - r0);
     const PartSizes po = part_sizes(kind, d->d, n, args.kvheads, rows);
-    const PartSizes pp = part_sizes(kind, d->d, 1, args.kvheads, n * rows);
+    int runs = 0;
+    const PartSizes pp = prefix_wide(kind, n * rows) ? wide_sizes(d->d, args.kvheads, n * rows, &runs)
+                                                     : part_sizes(kind, d->d, 1, args.kvheads, n * rows);
     char* const own_at = ws + 2 * kPlanBytes;
     char* const pre_at = own_at + po.bytes;
     auto blocks_of = [](const AttnShape& sh, int64_t units) {
@@ -288,9 +345,11 @@ extern "C" int attn_verify_shared(const hrs_attn_desc* d, int32_t prefix_pages, 
     };
     AttnLens lens{seq_len + r0, n, args.kvheads * pp.row_blocks, args.table_len << args.page_shift, d->window, d->n_pos, 0};
     const int64_t pre_slots = static_cast<int64_t>(prefix_pages) << args.page_shift;
-    const int64_t pre_units = static_cast<int64_t>(lens.heads) * (pre_slots / pp.shape.ts + kExtraUnits);
-    if (pre_units > INT32_MAX) return HRS_EINVAL;
-    lens.log_blocks = blocks_of(pp.shape, pre_units);
+    if (runs == 0) {
+      const int64_t pre_units = static_cast<int64_t>(lens.heads) * (pre_slots / pp.shape.ts + kExtraUnits);
+      if (pre_units > INT32_MAX) return HRS_EINVAL;
+      lens.log_blocks = blocks_of(pp.shape, pre_units);
+    }
     // The prefix: the rows of all requests as one's.
     AttnShared pre = args;
     pre.q = static_cast<const char*>(q) + static_cast<int64_t>(r0) * d->n_pos * args.q_stride * (d->dtype == HRS_F32 ? 4 : 2);
@@ -301,10 +360,12 @@ extern "C" int attn_verify_shared(const hrs_attn_desc* d, int32_t prefix_pages, 
     pre.plan = reinterpret_cast<int32_t*>(ws + kPlanBytes);
     pre.part_ml = reinterpret_cast<float2*>(pre_at);
     pre.part = reinterpret_cast<float*>(pre_at + pp.ml_bytes);
-    const Cut pre_cut{reinterpret_cast<const f32x4*>(pre.part), pre.part_ml, pre.plan, 1, lens.heads, pp.row_blocks,
-                      lens.log_blocks, pp.shape.rows};
+    const Cut pre_cut{reinterpret_cast<const f32x4*>(pre.part), pre.part_ml, pre.plan, runs, 1, lens.heads,
+                      pp.row_blocks, lens.log_blocks, pp.shape.rows};
     const int pre_cls = rows_class(kind, d->d, n * rows);
-    if (kind == kF32) attn_prefix_launch<kF32>(pre, lens, d->d, pre_cls, s);
+    if (runs > 0 && kind == kB16) attn_prefix_wide<kB16>(pre, lens, runs, d->d, s);
+    else if (runs > 0) attn_prefix_wide<kF8>(pre, lens, runs, d->d, s);
+    else if (kind == kF32) attn_prefix_launch<kF32>(pre, lens, d->d, pre_cls, s);
     else if (kind == kB16) attn_prefix_launch<kB16>(pre, lens, d->d, pre_cls, s);
     else attn_prefix_launch<kF8>(pre, lens, d->d, pre_cls, s);
     if (launch_error() != hipSuccess) return HRS_EDEVICE;
@@ -319,7 +380,7 @@ extern "C" int attn_verify_shared(const hrs_attn_desc* d, int32_t prefix_pages, 
     args.part = reinterpret_cast<float*>(own_at + po.ml_bytes);
     lens.heads = args.kvheads * po.row_blocks;
     lens.log_blocks = blocks_of(po.shape, n * own_most);
-    const Cut own_cut{reinterpret_cast<const f32x4*>(args.part), args.part_ml, args.plan, n, lens.heads, po.row_blocks,
+    const Cut own_cut{reinterpret_cast<const f32x4*>(args.part), args.part_ml, args.plan, 0, n, lens.heads, po.row_blocks,
                       lens.log_blocks, po.shape.rows};
     if (args.tree)
       for (int i = 0; i < n * d->n_pos; ++i)

@@ -698,7 +698,11 @@ size_t attn_verify_shared_workspace_bytes(const hrs_attn_desc* desc);
  * What is computed for all requests at once are the slots that every one of
  * them counts at every position: from the latest window's start to the shortest
  * context's end within the prefix, in whole groups of 128. Batches of up to 256
- * requests (trees: 3072 positions) are one unit, larger ones several.
+ * requests are one unit (trees: fewer where their positions fill the launch's
+ * arguments), larger ones several. In a unit with more than 256 rows (positions
+ * times query heads) of a key head, a bf16 span's weights over those slots are
+ * rounded once, to bf16 (beside e4m3 values to float16), and it is the rounded
+ * weights that are summed.
  *
  * prefix_table [prefix_pages] int32, prefix_len [1] int32, device;
  * prefix_pages >= 1. A prefix_len outside [0, prefix_pages * page_size] refuses

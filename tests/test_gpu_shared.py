@@ -304,3 +304,79 @@ def test_shared_pages_behind_2_31_elements(hrs):
     t.update(k_cache=big[0], v_cache=big[1], prefix_table=dev(far[a.ptable]), page_table=dev(far[a.pages]))
     hrs.attn_verify_shared(**t)
     a.check(t["out"], [0, 39], what="far pages")
+
+
+# Batches with more than 256 rows of a key head, whose weights over the prefix
+# are rounded once, and the rounded ones summed: out = sum w (1 + e) v /
+# sum w (1 + e) is off by sum w e (v - out) / sum w, |e| <= 2^-8, which is at
+# most 2^-8 (sum w |v| + |out|).
+class Large(Shared):
+    def tolerance(self, ref, absv, reach, n):
+        return super().tolerance(ref, absv, reach, n) + 2.0 ** -8 * np.abs(ref)
+
+
+WIDE = [("bf16", "bf16"), ("bf16", "f8")]
+
+
+@pytest.mark.parametrize("dtype,cache", WIDE)
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("gain,scale", [(1e-3, None), (8.0, None), (700.0, None), (1.0, -0.3), (1.0, 0.0)])
+def test_shared_large_scores(hrs, dtype, cache, d, gain, scale):
+    a = Large(9, 9, 8, 2, d, 16, 900, [901 + 3 * r for r in range(9)], dtype, cache, gain=gain if cache != "f8" else 1.0,
+              scale=scale if scale is not None or cache != "f8" else min(gain, 20.0))
+    a.check(a.run(hrs), [0, 8], what=f"large, gain {gain} scale {scale}")
+
+
+@pytest.mark.parametrize("dtype,cache", WIDE)
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("rows", [257, 385, 576, 577])
+def test_shared_large_rows(hrs, dtype, cache, d, rows):
+    """Blocks that end inside a tile of rows and waves without any."""
+    a = Large(rows, 1, 2, 2, d, 32, 700, [700 + r % 90 for r in range(rows)], dtype, cache)
+    a.check(a.run(hrs), [0, 191, 192, 255, 256, rows - 1], what=f"large, {rows} rows")
+
+
+@pytest.mark.parametrize("dtype,cache", WIDE)
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_shared_large_prefixes(hrs, dtype, cache, d):
+    """A captured call on prefixes of every number of tiles a run may have, with eager calls in between."""
+    import torch
+    a = Large(40, 2, 16, 2, d, 16, 2000, [2000 + r for r in range(40)], dtype, cache)
+    t = a.tensors(hrs)
+    call = hrs.attn_verify_shared_call(**t)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        call()
+    torch.cuda.current_stream().wait_stream(side)
+    for prefix in (0, 1, 127, 128, 129, 384, 640, 1999, 2000):
+        a.prefix, a.lens = prefix, [prefix + r for r in range(40)]
+        a.ptable[5] = -1 if prefix == 1999 else abs(int(a.ptable[5]))
+        t["prefix_table"].copy_(dev(a.ptable))
+        t["prefix_len"].copy_(dev(np.array([prefix], np.int32)))
+        t["seq_len"].copy_(dev(np.array(a.lens, np.int32)))
+        t["out"].zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(t["out"], a.run(hrs)), prefix
+        a.check(t["out"], [39], what=f"large, prefix {prefix}")
+
+
+def test_shared_large_two_streams_at_once(hrs):
+    import torch
+    cases = [Large(20, 17, 8, 2, 128, 16, 3000, [3001 + r for r in range(20)], cache=c, seed=1) for c in ("bf16", "f8")]
+    cases.append(Large(20, 17, 12, 2, 256, 32, 2000, [2100 + r for r in range(20)], seed=2))
+    want = [c.run(hrs) for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    outs = [torch.zeros_like(w) for w in want]
+    calls = [hrs.attn_verify_shared_call(**c.tensors(hrs, out=o)) for c, o in zip(cases, outs)]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for o in outs:
+            o.zero_()
+        torch.cuda.synchronize()
+        for call, st in zip(calls, streams):
+            call(st)
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, w) for o, w in zip(outs, want))
