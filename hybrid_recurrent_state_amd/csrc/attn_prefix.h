@@ -97,7 +97,7 @@ template <int KIND, int D> struct PrefixBlock {
     for (int i = 0; i < TS / 16; ++i) {
       const bool ok = static_cast<uint32_t>(pg[i]) < static_cast<uint32_t>(a.n_pages);
       there |= ok ? 1u << i : 0u;
-      const uint32_t group = __builtin_amdgcn_readfirstlane(((ok ? pg[i] : 0) * a.kvheads + h) * per_page +
+      const uint32_t group = __builtin_amdgcn_readfirstlane((static_cast<uint32_t>(ok ? pg[i] : 0) * a.kvheads + h) * per_page +
                                                             ((tile * (TS / 16) + i) & (per_page - 1)));
       at[i] = static_cast<int64_t>(group) * (16 * D * CSZ);
     }

@@ -10,25 +10,34 @@
 // its complemented index, one number that compares in the order), its largest
 // logit and the sum of the weights that stay.
 //
-// MI355X design: four dependent launches, no host round trip.
+// MI355X design: three dependent launches, no host round trip.
 //  1. Candidates: every 32 KB chunk of every row is read once into registers. A
 //     wave's j-th largest of its lanes' maxima bounds from below what can be
 //     among the chunk's 4 j largest, so one comparison a logit leaves a short
-//     list that holds everything above the bound. Bound by the read: rows with
-//     a small top-k need no exponential here, others ten operations a logit.
+//     list that holds everything above the bound. Bound by the read (272 rows of
+//     151,936 bf16 logits, 83 MB: 21.7 us): rows with a small top-k need no
+//     exponential here, others ten operations a logit.
 //  2. Borders, a block a row: the chunks' largest bound T; everything above T is
-//     in their lists. They are sorted in LDS with 64-bit weights and sums, which
-//     settles top-k, and top-p and min-p where their border lies above T
-//     (language models' rows). What stays is left behind as a list.
+//     in their lists. Of that the few dozen largest (a histogram of the logits
+//     names them) are put in order by counting, and one wave with their weights
+//     and sums in 64 bits settles top-k, and top-p and min-p where their border
+//     lies among them (language models' rows: 9 us for 272); if not, and all
+//     candidates' weights reach top-p's share, the block sorts and sums all of
+//     them. What stays is left behind as a list.
 //     Rows that this does not settle (even distributions, hundreds of tokens)
-//     read their logits again: a histogram of weights over 2048 bins, in whole
-//     numbers of 2^-44 and less so that the order of the additions does not
-//     matter, names the border's bin, whose members are sorted as above; bins
-//     of too many members are divided by their keys until one number is left,
-//     whose ties go by index.
+//     are read again, by the one block: 18 bytes a nanosecond, 17 us for
+//     151,936 bf16 logits. A bf16 row has few values, which are counted one by
+//     one, and a second read finds the border among equal ones (72 rows: 51 us).
+//     A float32 row has a histogram of weights over 2048 bins, in whole numbers
+//     of 2^-44 and less so that the order of the additions does not matter, that
+//     names the border's bin, whose members are sorted; bins of too many members
+//     are divided by their keys until one number is left, whose ties go by
+//     index.
 //  3. Walk and draw: as accept_sample's, with the rows' descriptions; where the
-//     node's row is a list the token is drawn from it at once.
-//  4. Otherwise pieces' sums from 3 name the token's piece.
+//     node's row is a list the token is drawn from it at once (5 us). Otherwise
+//     the row's pieces are summed by many blocks, and the last of them to be
+//     done finds the token's piece and the token: 22 us, where a launch of its
+//     own for that took 8 and 7 but also 4 for rows that need nothing of it.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -47,6 +56,7 @@ constexpr int kPool = 2048;            // candidates that a block sorts at most
 constexpr int kFew = 256;              // candidates that one wave settles
 constexpr int kBins = 2048;
 constexpr int kValues = 15360;         // values of a bf16 row that are counted one by one
+constexpr int kGroup = 4;              // pieces of a row that a block sums
 constexpr int kSmallK = 64;            // a top-k up to this needs no row sums
 constexpr double kCut = 48.0;          // e^-48 of the largest weight: no weight
 constexpr uint32_t kLeastKey = 0x00800000u;   // of the lowest finite logit
@@ -74,6 +84,7 @@ struct FilterArgs : SampleArgs {
   uint64_t* lists;     // workspace [rows][n_chunks][kList]: order numbers
   RowInfo* rows;       // workspace [rows]
   uint64_t* kept;      // workspace [rows][kTokens]: complemented index above key, by index
+  int32_t* done;       // workspace [R]: pieces that are summed
 };
 using FilterTree = WithTree<FilterArgs>;
 
@@ -618,7 +629,10 @@ template <typename T> __global__ __launch_bounds__(kRow, 4) void border_kernel(c
   const ChunkInfo mine = chunks[min(lane, args.n_chunks - 1)];
   const Limits lim(args, r);
   if (tid < kFew) s.bins[tid] = 0;
-  if (tid == 0) s.n = s.m = 0;
+  if (tid == 0) {
+    s.n = s.m = 0;
+    if (row == static_cast<int64_t>(r) * args.n_pos) args.done[r] = 0;
+  }
   // The chunks' maxima and the largest bound, by every wave for itself.
   uint32_t top_key = key_of(mine.top), bound = max(mine.bound, kLeastKey);
   for (int c = lane + 64; c < args.n_chunks; c += 64) {
@@ -1160,70 +1174,69 @@ __device__ __forceinline__ double filtered_weights(const FilterArgs& a, const No
   return sum;
 }
 
-// 3. Grid: (piece, request).
+// 3. Grid: (group of pieces, request). The request's last block to have summed its piece
+// goes on to the draw (counted in memory; sums are added in the pieces' order
+// whoever it is).
 template <typename T, typename Args>
 __global__ __launch_bounds__(kThreads) void filter_node_kernel(const Args args) {
   __shared__ WalkLds w;
   __shared__ double lds[kThreads / 64];
   __shared__ int32_t ilds[kThreads / 64];
-  const int piece = blockIdx.x, rl = blockIdx.y, r = args.req0 + rl;
-  if (piece == 0 && r == 0 && args.status) {
+  __shared__ int32_t pick;
+  const int group = blockIdx.x, rl = blockIdx.y, r = args.req0 + rl;
+  if (group == 0 && r == 0 && args.status) {
     int bad = 0;
     for (int i = threadIdx.x; i < args.n_req; i += kThreads) bad += bad_temperature(temperature_of(args, i));
     const double all = block_reduce(bad, add, lds);
     if (threadIdx.x == 0) *args.status = static_cast<int32_t>(all);
   }
-  walk<T>(args, rl, piece == 0, w);
-  if (piece == 0) {
-    const int32_t* src = reinterpret_cast<const int32_t*>(&w.info);
-    int32_t* dst = reinterpret_cast<int32_t*>(args.info + r);
-    for (int i = threadIdx.x; i < static_cast<int>(sizeof(NodeInfo) / 4); i += kThreads) dst[i] = src[i];
-  }
+  walk<T>(args, rl, group == 0, w);
   if (w.info.bad) return;
   const RowInfo ri = args.rows[static_cast<int64_t>(r) * args.n_pos + w.info.node];
+  const double u = args.uniforms[static_cast<int64_t>(r) * args.n_pos];
   if (ri.n >= 0) {
-    if (piece != 0) return;
-    const double u = args.uniforms[static_cast<int64_t>(r) * args.n_pos];
-    const int pick = draw_listed(args, w.info, ri, r, u, lds, ilds);
-    if (threadIdx.x == 0) args.bonus[r] = pick;
+    if (group != 0) return;
+    const int token = draw_listed(args, w.info, ri, r, u, lds, ilds);
+    if (threadIdx.x == 0) args.bonus[r] = token;
     return;
   }
-  double x[8], plain;
-  double sum = filtered_weights<T>(args, w.info, ri, w.info.mode, r, piece, x, &plain);
-  sum = block_reduce(sum, add, lds);
-  plain = block_reduce(plain, add, lds);
-  if (threadIdx.x == 0) args.part[static_cast<int64_t>(r) * args.n_pieces + piece] = double2{sum, plain};
-}
-
-// 4. Grid: request.
-template <typename T> __global__ __launch_bounds__(kThreads) void filter_draw_kernel(const FilterArgs args) {
-  __shared__ double lds[kThreads / 64];
-  __shared__ int32_t ilds[kThreads / 64];
-  __shared__ int32_t pick;
-  const int r = args.req0 + blockIdx.x;
-  const NodeInfo& info = args.info[r];
-  if (info.bad) return;
-  const RowInfo ri = args.rows[static_cast<int64_t>(r) * args.n_pos + info.node];
-  if (ri.n >= 0) return;
-  const double u = args.uniforms[static_cast<int64_t>(r) * args.n_pos];
+  double x[8], plain[kGroup], sum[kGroup];
+#pragma unroll
+  for (int i = 0; i < kGroup; ++i)
+    sum[i] = filtered_weights<T>(args, w.info, ri, w.info.mode, r, min(group * kGroup + i, args.n_pieces - 1), x, &plain[i]);
+#pragma unroll
+  for (int i = 0; i < kGroup; ++i) {
+    sum[i] = block_reduce(sum[i], add, lds);
+    plain[i] = block_reduce(plain[i], add, lds);
+  }
+  if (threadIdx.x == 0) {
+#pragma unroll
+    for (int i = 0; i < kGroup; ++i)
+      if (group * kGroup + i < args.n_pieces)
+        args.part[static_cast<int64_t>(r) * args.n_pieces + group * kGroup + i] = double2{sum[i], plain[i]};
+    pick = __hip_atomic_fetch_add(&args.done[r], 1, __ATOMIC_RELEASE, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  __syncthreads();
+  if (pick != static_cast<int>(gridDim.x) - 1) return;
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
   const Pieces<double2> part(args.part + static_cast<int64_t>(r) * args.n_pieces, args.n_pieces);
-  int mode = info.mode;
-  Found f = find_piece(part, [](double2 x) { return x.x; }, u);
+  int mode = w.info.mode;
+  Found f = find_piece(part, [](double2 y) { return y.x; }, u);
   if (f.piece < 0 && mode != kPlain) {   // nothing is left over: the row itself
     mode = kPlain;
-    f = find_piece(part, [](double2 x) { return x.y; }, u);
+    f = find_piece(part, [](double2 y) { return y.y; }, u);
   }
+  __syncthreads();
   if (threadIdx.x == 0) pick = 0;
   if (f.piece >= 0) {
-    double x[8], plain;
-    const double sum = filtered_weights<T>(args, info, ri, mode, r, f.piece, x, &plain);
-    const double c = f.before + block_scan(sum, lds);
+    const double mine = filtered_weights<T>(args, w.info, ri, mode, r, f.piece, x, plain);
+    const double c = f.before + block_scan(mine, lds);
     const double target = u * f.total;
-    int owner = first_hit(sum > 0.0 && c > target, ilds);
+    int owner = first_hit(mine > 0.0 && c > target, ilds);
     const bool passes = owner < kThreads;
-    if (!passes) owner = last_hit(sum > 0.0, ilds);
+    if (!passes) owner = last_hit(mine > 0.0, ilds);
     if (static_cast<int>(threadIdx.x) == owner) {
-      double run = c - sum;
+      double run = c - mine;
       bool done = false;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -1262,14 +1275,14 @@ size_t filter_layout(const hrs_sample_desc* d, FilterArgs* args, char* ws) {
   char* const p2 = place(rows * sizeof(RowInfo));
   char* const p3 = place(rows * kTokens * sizeof(uint64_t));
   char* const p4 = place(d->n_req * pieces * sizeof(double2));
-  char* const p5 = place(d->n_req * sizeof(NodeInfo));
+  char* const p5 = place(d->n_req * sizeof(int32_t));
   if (args) {
     args->chunks = reinterpret_cast<ChunkInfo*>(p0);
     args->lists = reinterpret_cast<uint64_t*>(p1);
     args->rows = reinterpret_cast<RowInfo*>(p2);
     args->kept = reinterpret_cast<uint64_t*>(p3);
     args->part = reinterpret_cast<double2*>(p4);
-    args->info = reinterpret_cast<NodeInfo*>(p5);
+    args->done = reinterpret_cast<int32_t*>(p5);
   }
   return at;
 }
@@ -1291,11 +1304,9 @@ template <typename T> int filter_launch(const hrs_sample_desc* d, FilterTree& tr
     hipLaunchKernelGGL(border_kernel<T>, dim3(n * args.n_pos), dim3(kRow), 0, s, args);
     if (launch_error() != hipSuccess) return HRS_EDEVICE;
     if (tree)
-      hipLaunchKernelGGL((filter_node_kernel<T, FilterTree>), dim3(args.n_pieces, n), dim3(kThreads), 0, s, tree_args);
+      hipLaunchKernelGGL((filter_node_kernel<T, FilterTree>), dim3((args.n_pieces + kGroup - 1) / kGroup, n), dim3(kThreads), 0, s, tree_args);
     else
-      hipLaunchKernelGGL((filter_node_kernel<T, FilterArgs>), dim3(args.n_pieces, n), dim3(kThreads), 0, s, args);
-    if (launch_error() != hipSuccess) return HRS_EDEVICE;
-    hipLaunchKernelGGL(filter_draw_kernel<T>, dim3(n), dim3(kThreads), 0, s, args);
+      hipLaunchKernelGGL((filter_node_kernel<T, FilterArgs>), dim3((args.n_pieces + kGroup - 1) / kGroup, n), dim3(kThreads), 0, s, args);
     if (launch_error() != hipSuccess) return HRS_EDEVICE;
   }
   return HRS_OK;
@@ -1335,7 +1346,7 @@ extern "C" int accept_sample_filtered(const hrs_sample_desc* d, const void* logi
   args.logits = logits; args.tokens = tokens; args.uniforms = uniforms; args.draft = draft_probs;
   args.temperature = temperature; args.token_prob = token_prob; args.accept_node = accept_node;
   args.accept_len = accept_len; args.path = path; args.bonus = bonus; args.status = status;
-  args.stats = nullptr; args.rest = nullptr;
+  args.stats = nullptr; args.rest = nullptr; args.info = nullptr;
   args.top_k = top_k; args.top_p = top_p; args.min_p = min_p;
   args.n_req = d->n_req; args.n_pos = d->n_pos; args.vocab = d->vocab;
   const int chunk = d->logit_dtype == HRS_F32 ? kChunk<float> : kChunk<uint16_t>;
