@@ -14,10 +14,13 @@
 // (e4m3, 23,552 rows of 128 over 8,191 slots: 131 us; 80 rows a wave and one
 // block 167, 96 rows 229). 48 rows of 256 elements take all registers, and the
 // wave does that for itself: the scores of the next tile are formed under this
-// tile's exponentials (6,528 rows of 256 over 26,752 slots: 245 us; without that
-// 298). The order of a tile's instructions is written down and kept, vector
-// operations one or two behind each product (274 and 145 us where the compiler
-// orders within steps of RT products, 285 and 165 where it orders everything).
+// tile's exponentials (6,528 rows of 256 over 26,752 slots: 216 us; without that
+// 298). A product lets two vector operations of its wave pass (17 cycles without
+// any, 18 with two, five more for each further one), so the order of a tile's
+// instructions is written down and kept, one or two behind each product (274 and
+// 145 us where the compiler orders within steps of RT products, 285 and 165
+// where it orders everything), the next loads are among them, and scores leave
+// the matrix units' registers once (245 us without these two).
 // The path for smaller batches (attn_kernel.h) takes 376 and 156 us here.
 //
 // Weights are rounded to 16 bits once, at most 2^-8 of a bf16 weight (2^-11 of a
@@ -29,8 +32,8 @@
 // The slots are cut into as many equal runs for each (head, block of rows) as
 // fill the card, and blocks that read the same run sit on one XCD and read it at
 // the same time, so that it comes from its L2. What bounds it: matrix
-// instructions are busy 38% of the time, 760 TFLOP/s, the rest being what does
-// not fit under them (maxima, rescaling, barriers, widening).
+// instructions are busy 43% of the time, 830 TFLOP/s, the rest being what does
+// not fit under them (permutations, maxima, barriers; e4m3: widening).
 #pragma once
 
 #include "attn_kernel.h"
@@ -56,6 +59,7 @@ template <int KIND, int D> struct PrefixBlock {
   f32x4 o[RT][DT];
   f32x4 l[RT];
   float m[RT];
+  float off[RT];               // taken_off, where there are registers to keep it
   float c, vs;
   int held, pg[TS / 16];             // pages of the next tile to load
   uint32_t v_at[4];            // a lane's places in a tile's values
@@ -104,21 +108,20 @@ template <int KIND, int D> struct PrefixBlock {
     ring = __builtin_amdgcn_readfirstlane((ring & ~(3u << (2 * stage))) | there << (2 * stage));
   }
 
-  // bf16: the tile straight into its place of the ring, pieces of a row
-  // permuted as in attn_kernel.h.
+  // bf16: a wave's i-th load of a tile, or all of them, straight into the
+  // tile's place of the ring, pieces of a row permuted as in attn_kernel.h.
+  __device__ __forceinline__ void issue(const int64_t (&at)[TS / 16], int stage, int i) {
+    const int p0 = (i * NW + wave) * 64;
+    const uint32_t row = static_cast<uint32_t>(p0 + lane) / PIECES % 16;
+    const uint32_t off = row * ROW + ((static_cast<uint32_t>(lane) % PIECES) ^ swizzle<PIECES>(row)) * 16;
+    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(source<PIECES>(i, at) + off),
+                                     (__attribute__((address_space(3))) void*)(lds + stage * C::STAGE + p0 * 16), 16, 0, 0);
+  }
   __device__ __forceinline__ void issue(int tile, int stage) {
     int64_t at[TS / 16];
     places(tile, stage, at);
-    char* const dst = lds + stage * C::STAGE;
 #pragma unroll
-    for (int i = 0; i < LPS; ++i) {
-      const int p0 = (i * NW + wave) * 64;
-      const uint32_t row = (p0 + lane) / PIECES;
-      const char* const base = source<PIECES>(i, at);
-      const uint32_t piece = (static_cast<uint32_t>(lane) % PIECES) ^ swizzle<PIECES>(row);
-      __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(base + (row & 15) * ROW + piece * 16),
-                                       (__attribute__((address_space(3))) void*)(dst + p0 * 16), 16, 0, 0);
-    }
+    for (int i = 0; i < LPS; ++i) issue(at, stage, i);
   }
   // Which 16 rows a wave's i-th load belongs to, a row being kPieces pieces.
   template <int kPieces> __device__ __forceinline__ const char* source(int i, const int64_t (&at)[TS / 16]) const {
@@ -177,6 +180,7 @@ template <int KIND, int D> struct PrefixBlock {
         if (on) q[rt][x] = *reinterpret_cast<const u32x4*>(src + (4 * x + g) * 16);
       }
       m[rt] = -__builtin_inff();
+      if constexpr (C::NEXT) off[rt] = -kLift;
       l[rt] = f32x4{};
 #pragma unroll
       for (int dt = 0; dt < DT; ++dt) o[rt][dt] = f32x4{};
@@ -214,17 +218,28 @@ template <int KIND, int D> struct PrefixBlock {
 
   static constexpr int kAhead = QC * SB < 4 ? QC * SB : 4;       // reads of LDS before their products
 
-  __device__ __forceinline__ void scores(const char* kt, Scores& s) const {
-    const uint32_t ka = lds_address(kt) + n16 * ROW + ((g ^ swizzle<PIECES>(n16)) << 4);
-    auto read_k = [&](int i) { return *lds_at<u32x4>((ka ^ ((i / SB) << 6)) + (i % SB) * 16 * ROW); };
-    u32x4 k[kAhead];
+  __device__ __forceinline__ uint32_t k_place(const char* kt) const {
+    return lds_address(kt) + n16 * ROW + ((g ^ swizzle<PIECES>(n16)) << 4);
+  }
+  // Step i's keys, and the first steps'.
+  static __device__ __forceinline__ u32x4 read_k(uint32_t ka, int i) {
+    return *lds_at<u32x4>((ka ^ ((i / SB) << 6)) + (i % SB) * 16 * ROW);
+  }
+  __device__ __forceinline__ void first_k(const char* kt, u32x4 (&k)[kAhead]) const {
+    const uint32_t ka = k_place(kt);
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) k[i] = read_k(i);
+    for (int i = 0; i < kAhead; ++i) k[i] = read_k(ka, i);
+  }
+
+  __device__ __forceinline__ void scores(const char* kt, Scores& s) const {
+    const uint32_t ka = k_place(kt);
+    u32x4 k[kAhead];
+    first_k(kt, k);
 #pragma unroll
     for (int i = 0; i < QC * SB; ++i) {
       __builtin_amdgcn_sched_barrier(0);
       const u32x4 now = k[i % kAhead];
-      if (i + kAhead < QC * SB) k[i % kAhead] = read_k(i + kAhead);
+      if (i + kAhead < QC * SB) k[i % kAhead] = read_k(ka, i + kAhead);
       const int x = i / SB, sb = i % SB;
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt) s[rt][sb] = product(now, q[rt][x], x == 0 ? f32x4{} : s[rt][sb]);
@@ -232,6 +247,13 @@ template <int KIND, int D> struct PrefixBlock {
     __builtin_amdgcn_sched_barrier(0);
   }
 
+  // Scores out of the matrix units' registers, once for all that follows.
+  static __device__ __forceinline__ void fetch(f32x4 (&s)[SB]) {
+    if constexpr (C::NEXT) {
+#pragma unroll
+      for (int sb = 0; sb < SB; ++sb) asm volatile("" : "+v"(s[sb]));
+    }
+  }
   static __device__ __forceinline__ float highest(const f32x4 (&s)[SB]) {
     float x = -__builtin_inff();
 #pragma unroll
@@ -240,6 +262,9 @@ template <int KIND, int D> struct PrefixBlock {
       for (int i = 0; i < 4; ++i) x = fmaxf(x, s[sb][i]);
     return x;
   }
+
+  // What is taken off a row's scores: m, but for rows without any yet.
+  __device__ __forceinline__ float taken_off(int rt) const { return (m[rt] == -__builtin_inff() ? 0.0f : m[rt]) - kLift; }
 
   // Everything about a tile's scores that is rare (top: their highest, a lane's): a scale that is negative or
   // no number, absent pages, a reference that moves, scores far out. f: what the
@@ -287,16 +312,16 @@ template <int KIND, int D> struct PrefixBlock {
         scale(l[rt]);
 #pragma unroll
         for (int dt = 0; dt < DT; ++dt) scale(o[rt][dt]);
+        if constexpr (C::NEXT) off[rt] = taken_off(rt);
       }
     }
-    bool far = false;
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-      mb[rt] = m[rt] == -__builtin_inff() ? 0.0f : m[rt];
-      far = far || fabsf(mb[rt]) >= 0x1p22f;
-      mb[rt] -= kLift;
-    }
-    if (__any(far)) {
+    for (int rt = 0; rt < RT; ++rt) mb[rt] = C::NEXT ? off[rt] : taken_off(rt);
+    // References so large that differences to them round.
+    float most = 0.0f;
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) most = fmaxf(most, fabsf(mb[rt]));
+    if (__any(most >= 0x1p22f - 8.0f)) {
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt) {
         const bool own = fabsf(m[rt]) >= 0x1p22f && m[rt] != -__builtin_inff();
@@ -319,18 +344,18 @@ template <int KIND, int D> struct PrefixBlock {
   // products, and the vector operations stand one or two behind each product,
   // whose 16 cycles they take. Values: a lane's rows turned into columns by byte
   // permutations, as attn_kernel.h's Values.
+  // load(i): the i-th of kLoads loads.
+  template <int kLoads, typename Load>
   __device__ __forceinline__ void tile(const Scores& s, float f, const float (&mb)[RT], const char* vt, const char* kt,
-                                       Scores& then, float (&top)[RT]) {
+                                       u32x4 (&k)[kAhead], Scores& then, float (&top)[RT], Load load) {
     constexpr int kSteps = QC * SB, kValues = RT * SB * 4, kSlots = kSteps * RT;
     constexpr int kCols = D >= 128 ? 8 : 4, kHalves = D / (16 * kCols), kWords = kCols / 2, kReads = SB * 4;
-    const uint32_t ka = lds_address(kt) + n16 * ROW + ((g ^ swizzle<PIECES>(n16)) << 4);
+    const uint32_t ka = k_place(kt);
     uint32_t va[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) va[j] = lds_address(vt) + v_at[j];
-    u32x4 k[kAhead];
     uint32_t w[kHalves][kReads][kWords];
     u32x4 p[RT];
-    auto read_k = [&](int i) { return *lds_at<u32x4>((ka ^ ((i / SB) << 6)) + (i % SB) * 16 * ROW); };
     auto read_v = [&](int half, int i) {
       const uint32_t at = va[i % 4] + half * (32 * kCols) + (i / 4) * 16 * ROW;
       if constexpr (kWords == 4) {
@@ -361,11 +386,9 @@ template <int KIND, int D> struct PrefixBlock {
       static_assert(kSlots % kValues == 0 && kSteps >= kReads + 2, "each value in its slots");
       constexpr int kEach = kSlots / kValues;
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i) k[i] = read_k(i);
-#pragma unroll
       for (int i = 0; i < kSteps; ++i) {
         const u32x4 now = k[i % kAhead];
-        if (i + kAhead < kSteps) k[i % kAhead] = read_k(i + kAhead);
+        if (i + kAhead < kSteps) k[i % kAhead] = read_k(ka, i + kAhead);
         const int first = i - (kSteps - 2 - kReads);
         if (first >= 0 && first < kReads) read_v(0, first);
         const int x = i / SB, sb = i % SB;
@@ -414,13 +437,17 @@ template <int KIND, int D> struct PrefixBlock {
 #pragma unroll
           for (int i = rt * 4 / (RT - 1); i < (rt + 1) * 4 / (RT - 1) && i < 4; ++i) turn(col + 1, i);
         }
-        if (C::NEXT && rt == 0 && col < RT) top[col] = highest(then[col]);
+        if (C::NEXT && rt == 0 && col < RT) {
+          fetch(then[col]);
+          top[col] = highest(then[col]);
+        }
+        if (rt == RT - 1 && col >= DT - kLoads) load(col - (DT - kLoads));
         __builtin_amdgcn_sched_barrier(0);
       }
     }
   }
 
-  __device__ __forceinline__ char* stage_of(int i) const { return lds + (i % C::NST) * C::STAGE; }
+  __device__ __forceinline__ char* stage_of(int i) const { return lds + (static_cast<uint32_t>(i) % C::NST) * C::STAGE; }
 
   // Values of absent pages, which weights of 0 multiply: no numbers may be there.
   __device__ __forceinline__ void clear(char* vt, uint32_t there) {
@@ -431,21 +458,28 @@ template <int KIND, int D> struct PrefixBlock {
   // Tiles [t0, t1). The next tile's scores are formed while this one's become
   // weights: the matrix units work under the vector units' longest stretch.
   __device__ __forceinline__ void run(int t0, int t1) {
+    // bf16 tiles that the wave's own work hides are loaded among its products,
+    // the last tile again where there are no more.
+    constexpr bool kAmong = C::NEXT && KIND != kF8;
     ring = 0;
     fetch_pages(t0, 0);
     int next = t0;               // next tile to load
     u32x4 x[KIND == kF8 ? LP8 : 1];
-    auto start = [&]() {
-      if (next >= t1) return;
-      if constexpr (KIND == kF8) load8(next, (next - t0) % C::NST, x);
-      else issue(next, (next - t0) % C::NST);
+    auto step = [&]() {
       ++next;
       if (next < t1) fetch_pages(next, next - t0);
+    };
+    auto start = [&]() {
+      const int stage = static_cast<uint32_t>(next - t0) % C::NST;
+      if (!kAmong && next >= t1) return;
+      if constexpr (KIND == kF8) load8(next, stage, x);
+      else issue(min(next, t1 - 1), stage);
+      step();
     };
     // e4m3: what was loaded last, into its place.
     auto store = [&](int before) {
       if constexpr (KIND == kF8)
-        if (next > before) store8(x, (next - 1 - t0) % C::NST);
+        if (next > before) store8(x, static_cast<uint32_t>(next - 1 - t0) % C::NST);
     };
     if constexpr (KIND == kF8) {
       start();
@@ -461,18 +495,31 @@ template <int KIND, int D> struct PrefixBlock {
     Scores s;
     float top[RT];
     for (int u = t0; u < t1; ++u) {
-      // Tile u (with NEXT also the next) is there for everybody, and everybody is done with tile u - 1.
-      if constexpr (KIND != kF8) {
-        const int later = next - 1 - u - (C::NEXT ? 1 : 0);        // tiles that may be on their way
+      // Tile u (with NEXT also the next) is there for everybody, and everybody is
+      // done with tile u - 1.
+      if constexpr (kAmong) {
+        wait_vm<(C::NST - 3) * LPS>();
+      } else if constexpr (KIND != kF8) {
+        const int later = next - 1 - u;          // tiles that may be on their way
         if (later > 1) wait_vm<2 * LPS>();
         else if (later == 1) wait_vm<LPS>();
         else wait_vm<0>();
       }
       block_barrier();
+      // (The first keys of tile u + 1 come under the next loads' addresses.)
+      u32x4 k[kAhead];
+      if constexpr (C::NEXT) first_k(stage_of(u + 1 - t0), k);
       const int before = next;
-      start();
+      const int stage = static_cast<uint32_t>(next - t0) % C::NST;
+      int64_t at[TS / 16];
+      if constexpr (kAmong) {
+        places(min(next, t1 - 1), stage, at);
+        step();
+      } else {
+        start();
+      }
       mem_fence();
-      const uint32_t there = (ring >> (2 * ((u - t0) % C::NST))) & 3;
+      const uint32_t there = (ring >> (2 * (static_cast<uint32_t>(u - t0) % C::NST))) & 3;
       if (there != 3) {          // (the whole block's)
         clear(stage_of(u - t0) + TS * ROW, there);
         block_barrier();
@@ -481,24 +528,32 @@ template <int KIND, int D> struct PrefixBlock {
         if (!C::NEXT || u == t0) {
           scores(stage_of(u - t0), s);
 #pragma unroll
-          for (int rt = 0; rt < RT; ++rt) top[rt] = highest(s[rt]);
+          for (int rt = 0; rt < RT; ++rt) {
+            fetch(s[rt]);
+            top[rt] = highest(s[rt]);
+          }
         }
         float f, mb[RT];
         settle_scores(s, top, there, f, mb);
         // (Behind the last tile: scores of what the ring holds, for nobody. A
         // branch would part the products.)
         Scores then;
-        tile(s, f, mb, stage_of(u - t0) + TS * ROW, stage_of(u + 1 - t0), then, top);
+        tile<kAmong ? LPS : 0>(s, f, mb, stage_of(u - t0) + TS * ROW, stage_of(u + 1 - t0), k, then, top,
+                               [&](int i) { issue(at, stage, i); });
         if constexpr (C::NEXT) {
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt)
+          for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
-          for (int sb = 0; sb < SB; ++sb) s[rt][sb] = then[rt][sb];
+            for (int sb = 0; sb < SB; ++sb) s[rt][sb] = then[rt][sb];
         }
+      } else if constexpr (kAmong) {
+#pragma unroll
+        for (int i = 0; i < LPS; ++i) issue(at, stage, i);
       }
       mem_fence();
       store(before);
     }
+    if constexpr (kAmong) wait_vm<0>();          // nothing is on its way into LDS when the block ends
   }
 
   __device__ __forceinline__ void finish(int64_t slot) {
