@@ -191,8 +191,9 @@ template <bool F32> void launch_join(const Cut& own, const Cut& pre, const AttnB
 
 // More rows of a key head than this go to attn_prefix.h's launch. Whole calls
 // there and here, 4 key heads of 256 in bf16: 192 rows over 2,048 slots 46 and
-// 38 us, over 16,384 slots 59 and 62; 384 rows 51 and 45, 74 and 83; 768 rows 61
-// and 62, 107 and 138. (8 heads of 128, e4m3, 768 rows: 63 and 63, 106 and 121.)
+// 37 us, over 16,384 slots 58 and 61; 288 rows 48 and 44, 65 and 81; 768 rows 61
+// and 60, 99 and 139. (8 heads of 128, e4m3, 288 rows: 43 and 40, 65 and 68; 768
+// rows 64 and 62, 106 and 120.)
 constexpr int64_t kWideRows = 256;
 
 // How a launch's parts are laid out in the workspace.
@@ -269,8 +270,12 @@ extern "C" size_t attn_verify_shared_workspace_bytes(const hrs_attn_desc* d) {
     most = std::max(most, own + part_sizes(kind, d->d, 1, d->n_kvheads, n * rows).bytes);
     int runs;
     // (Smaller batches may be cut into more runs.)
-    for (int m = n; prefix_wide(kind, m * rows); --m)
-      most = std::max(most, own + wide_sizes(d->d, d->n_kvheads, m * rows, &runs).bytes);
+    int64_t last = 0;
+    for (int m = n; prefix_wide(kind, m * rows); --m) {
+      const int64_t blocks = (m * rows + prefix_rows(d->d) - 1) / prefix_rows(d->d);
+      if (blocks != last) most = std::max(most, own + wide_sizes(d->d, d->n_kvheads, m * rows, &runs).bytes);
+      last = blocks;
+    }
   }
   return 2 * kPlanBytes + most;
 }

@@ -680,8 +680,9 @@ int attn_verify_span(const hrs_attn_desc* desc, const void* q, const void* k, co
 
 /* Bytes of device workspace attn_verify_shared needs for these sizes (0 for a
  * NULL descriptor or sizes out of range). It does not depend on lengths, nor on
- * the cache. About twice the bytes of R * T * Hq results in float32, and those
- * of the parts of up to 512 blocks. */
+ * the cache. About twice the bytes of R * T * Hq results in float32 (up to five
+ * times those where hundreds of rows a key head leave the card's last round of
+ * blocks less than full), and those of the parts of up to 512 blocks. */
 size_t attn_verify_shared_workspace_bytes(const hrs_attn_desc* desc);
 
 /*
