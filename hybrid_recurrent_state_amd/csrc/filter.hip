@@ -36,7 +36,7 @@
 //  3. Walk and draw: as accept_sample's, with the rows' descriptions; where the
 //     node's row is a list the token is drawn from it at once (5 us). Otherwise
 //     the row's pieces are summed by many blocks, and the last of them to be
-//     done finds the token's piece and the token: 22 us, where a launch of its
+//     done finds the token's piece and the token: 23 us, where a launch of its
 //     own for that took 8 and 7 but also 4 for rows that need nothing of it.
 #include <hip/hip_runtime.h>
 
