@@ -249,3 +249,30 @@ def test_repeat_guard_and_graph(hrs, head):
         eager = c.run(hrs)
         assert all(np.array_equal(x, y) for x, y in zip(got, eager))
         c.check(got, what=f"replay {seed}")
+
+
+def test_even_rows_of_many_requests_on_two_streams(hrs):
+    """Rows without a list, whose last block draws: many requests, two calls at once, every call as when alone."""
+    import torch
+    cases = [Filtered(40, 3, 30000, "bf16", draft="f32", seed=1, p=[0.9, 0.6]),
+             Filtered(300, 1, 16392, "f32", seed=2, k=[0, 3000], p=[0.95])]
+    want = [c.run(hrs) for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    calls, keep = [], []
+    for c in cases:
+        a = c.args()
+        ws = torch.full((hrs.accept_sample_filtered_workspace_bytes(*c.logits.shape),), 0xFF, dtype=torch.uint8, device="cuda")
+        d = lambda x: None if x is None else dev(x)
+        more = dict(top_k=d(c.k), top_p=d(c.p), draft_probs=d(c.draft), temperature=d(c.temp))
+        calls.append(hrs.accept_sample_filtered_call(*a, ws, **more))
+        keep.append((a, ws, more))
+    for _ in range(4):
+        for c in cases:
+            for o in c.outs:
+                o.fill_(-7)
+        torch.cuda.synchronize()
+        for call, st in zip(calls, streams):
+            call(st)
+        torch.cuda.synchronize()
+        for c, w in zip(cases, want):
+            assert all(np.array_equal(host(x), y) for x, y in zip(c.outs, w))

@@ -380,3 +380,12 @@ def test_shared_large_two_streams_at_once(hrs):
             call(st)
         torch.cuda.synchronize()
         assert all(torch.equal(o, w) for o, w in zip(outs, want))
+
+
+@pytest.mark.parametrize("dtype,cache", WIDE)
+@pytest.mark.parametrize("d,S,tree,window", [(64, 16, True, 700), (128, 64, False, 500), (256, 128, False, 333)])
+def test_shared_large_windows(hrs, dtype, cache, d, S, tree, window):
+    """Windows that start in the prefix: the shared slots begin behind its start."""
+    a = Large(20, 17, 4, 2, d, S, 1000, [1000 + 9 * r for r in range(20)], dtype, cache, tree=tree, window=window)
+    a.ptable[len(a.ptable) // 2] = -1
+    a.check(a.run(hrs), [0, 10, 19], what=f"large, window {window}")
