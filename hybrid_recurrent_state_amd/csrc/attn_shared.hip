@@ -16,7 +16,7 @@
 // worked on it.
 //
 // 16 single positions behind 4,096 slots (24/4 heads of 256): prefix 13.3 us, own
-// slots 14.8, join 13.9, all latency; 16 chains of 17 behind 26,758: 216, 37 and
+// slots 14.8, join 15.0, all latency; 16 chains of 17 behind 26,758: 216, 37 and
 // 21 (60 MB of parts, 2.9 TB/s); 32 trees of 23 behind 8,191 e4m3 slots (32/8
 // heads of 128): 131, 46 and 21.
 #include <hip/hip_runtime.h>
@@ -95,45 +95,49 @@ __global__ __launch_bounds__(NS > 1 ? 64 * NS : 256) void shared_join_kernel(con
   float M = -__builtin_inff(), ls = 0.0f;
   f32x4 sum[2] = {};
   constexpr int kAtOnce = NS > 1 ? 8 : 4;
-  auto add = [&](const Cut& c, const Parts& p, int most) {
-    for (int b = ns; b < most; b += NS * kAtOnce) {
-      float2 w[kAtOnce];
-      f32x4 x[kAtOnce][2];
-#pragma unroll
-      for (int j = 0; j < kAtOnce; ++j) {
-        const int64_t slot = p.slot0 + static_cast<int64_t>(max(min(b + j * NS, p.count - 1), 0)) * p.step;
-        w[j] = c.ml[slot * c.rows + p.tile * 16 + p.n16];
-        const f32x4* from = c.part + (slot * (c.rows / 16) + p.tile) * (DT * 64) + g * 16 + p.n16;
-        x[j][0] = from[(2 * dp) * 64];
-        x[j][1] = from[(2 * dp + 1) * 64];
-      }
-      float top = M;
-#pragma unroll
-      for (int j = 0; j < kAtOnce; ++j)
-        if (b + j * NS < p.count) top = fmaxf(top, w[j].x);
-      const float keep = M == top ? 1.0f : __builtin_amdgcn_exp2f(M - top);
-      M = top;
-      ls *= keep;
-      sum[0] *= keep;
-      sum[1] *= keep;
-#pragma unroll
-      for (int j = 0; j < kAtOnce; ++j) {
-        // Parts that no slot counted in weigh nothing.
-        if (b + j * NS >= p.count || (w[j].x == -__builtin_inff() && w[j].y == 0.0f)) continue;
-        const float f = w[j].x == M ? 1.0f : __builtin_amdgcn_exp2f(w[j].x - M);
-        ls += w[j].y * f;
-        sum[0] += x[j][0] * f;
-        sum[1] += x[j][1] * f;
-      }
-    }
-  };
-  // (A tile's rows may lie in two of the prefix's segments: lanes differ in
-  // their number of parts.)
-  int most = pp.count;
+  // The prefix's parts and then the request's own, as one list (one after the
+  // other the small float32 case took 7.8 instead of 6.2 us, 16 chains 22.2
+  // instead of 21.2, 16 single positions of 256 13.8 instead of 15.0). A tile's
+  // rows may lie in two of the prefix's segments: lanes differ in their number
+  // of parts.
+  const int count = pp.count + po.count;
+  int most = count;
 #pragma unroll
   for (int d = 32; d; d >>= 1) most = max(most, __shfl_xor(most, d));
-  if (most > 0) add(pre, pp, most);
-  add(own, po, po.count);
+  for (int b = ns; b < most; b += NS * kAtOnce) {
+    float2 w[kAtOnce];
+    f32x4 x[kAtOnce][2];
+#pragma unroll
+    for (int j = 0; j < kAtOnce; ++j) {
+      const int k = min(b + j * NS, count - 1);
+      const bool shared = k < pp.count;
+      const int64_t slot = shared ? pp.slot0 + static_cast<int64_t>(k) * pp.step : po.slot0 + (k - pp.count);
+      const int rows = shared ? pre.rows : own.rows;
+      const int t = shared ? pp.tile : po.tile, n = shared ? pp.n16 : po.n16;
+      w[j] = (shared ? pre.ml : own.ml)[slot * rows + t * 16 + n];
+      const f32x4* from = (shared ? pre.part : own.part) + (slot * (rows / 16) + t) * (DT * 64) + g * 16 + n;
+      x[j][0] = from[(2 * dp) * 64];
+      x[j][1] = from[(2 * dp + 1) * 64];
+    }
+    float top = M;
+#pragma unroll
+    for (int j = 0; j < kAtOnce; ++j)
+      if (b + j * NS < count) top = fmaxf(top, w[j].x);
+    const float keep = M == top ? 1.0f : __builtin_amdgcn_exp2f(M - top);
+    M = top;
+    ls *= keep;
+    sum[0] *= keep;
+    sum[1] *= keep;
+#pragma unroll
+    for (int j = 0; j < kAtOnce; ++j) {
+      // Parts that no slot counted in weigh nothing.
+      if (b + j * NS >= count || (w[j].x == -__builtin_inff() && w[j].y == 0.0f)) continue;
+      const float f = w[j].x == M ? 1.0f : __builtin_amdgcn_exp2f(w[j].x - M);
+      ls += w[j].y * f;
+      sum[0] += x[j][0] * f;
+      sum[1] += x[j][1] * f;
+    }
+  }
   if constexpr (NS > 1) {
     __shared__ f32x4 sums[NS][2][64];
     __shared__ float2 ml[NS][64];
