@@ -334,7 +334,7 @@ struct RowLds {
   alignas(16) uint64_t list[kPool];
   union {
     uint64_t hist[kBins];                // of whole-number weights
-    uint32_t count[kValues];             // of values
+    uint32_t count[kValues + 1];         // of values, and of a negative zero behind the last
     struct {
       alignas(16) uint64_t few[kFew];    // the largest candidates
       alignas(16) uint64_t sorted[kFew];
@@ -885,8 +885,12 @@ template <typename T> __global__ __launch_bounds__(kRow, 4) void border_kernel(c
         const uint32_t v = first - at;
         return v << 16 | (v < 0x8000u ? 0xFFFFu : 0u);
       };
+      // A negative zero stands one place behind the other and counts there, also
+      // where zero is the last of the values.
+      const int zero = static_cast<int>(first - 0x8000u);
+      const int places = values + (zero == values - 1);
       __syncthreads();
-      for (int i = tid; i < values; i += kRow) s.count[i] = 0;
+      for (int i = tid; i < places; i += kRow) s.count[i] = 0;
       __syncthreads();
       each_raw(logits, V, [&](int, const Slice<T>& x) {
         // Two patterns a word: keys as key_of's, but for the negative zero's,
@@ -899,13 +903,12 @@ template <typename T> __global__ __launch_bounds__(kRow, 4) void border_kernel(c
           const uint32_t sign = __builtin_bit_cast(uint32_t, __builtin_bit_cast(i16x2, w) >> i16x2{15, 15});
           const u16x2 key = __builtin_bit_cast(u16x2, w ^ (sign | 0x80008000u));
           const uint32_t at = __builtin_bit_cast(uint32_t, u16x2{static_cast<uint16_t>(first), static_cast<uint16_t>(first)} - key);
-          if ((at & 0xFFFFu) < static_cast<uint32_t>(values)) atomicAdd(&s.count[at & 0xFFFFu], 1u);
-          if (at >> 16 < static_cast<uint32_t>(values)) atomicAdd(&s.count[at >> 16], 1u);
+          if ((at & 0xFFFFu) < static_cast<uint32_t>(places)) atomicAdd(&s.count[at & 0xFFFFu], 1u);
+          if (at >> 16 < static_cast<uint32_t>(places)) atomicAdd(&s.count[at >> 16], 1u);
         }
       });
       __syncthreads();
-      const int zero = static_cast<int>(first - 0x8000u);
-      if (tid == 0 && zero >= 0 && zero + 1 < values) {
+      if (tid == 0 && zero >= 0 && zero + 1 < places) {
         s.count[zero] += s.count[zero + 1];
         s.count[zero + 1] = 0;
       }
