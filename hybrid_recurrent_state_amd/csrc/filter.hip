@@ -126,23 +126,22 @@ __device__ __forceinline__ uint32_t cut_key(float top, float tau) {
   return max(key_of(static_cast<float>(static_cast<double>(top) - kCut * fmax(static_cast<double>(tau), 0.0))), kLeastKey);
 }
 
-// e^((z - top) / tau) in float32 with the argument good to 2^-40 or so: its
-// rounding error, which would be the same sign for all of a row's logits, goes
-// back in as a factor.
+// e^((z - top) / tau) as a float32 good to 3 u, u = 2^-24: the argument is formed
+// in 64 bits, where neither differences nor temperatures at the ends of float32
+// leave the range, and what its rounding for the exponential loses (the same
+// sign for all of a row's logits, if they are alike) goes back in as a factor.
 struct FastWeigher {
-  float top, hi, lo;
+  double top, c;
   bool hard;
   __device__ FastWeigher(float top_, float tau) : top(top_) {
-    hard = tau == 0.0f || top == __builtin_inff();
-    const double c = hard ? 1.0 : 1.4426950408889634074 / static_cast<double>(tau);
-    hi = static_cast<float>(fmin(fmax(c, 1.2e-38), 3.4e38));
-    lo = c < 1e30 ? static_cast<float>(c - hi) : 0.0f;
+    hard = tau == 0.0f || top_ == __builtin_inff();
+    c = hard ? 1.0 : 1.4426950408889634074 / static_cast<double>(tau);
   }
   __device__ __forceinline__ float operator()(float z) const {
     if (hard) return z == top ? 1.0f : 0.0f;
-    const float d = z - top;
-    const float y = d * hi;
-    const float rest = fmaf(d, lo, fmaf(d, hi, -y));
+    const double x = (static_cast<double>(z) - top) * c;
+    const float y = static_cast<float>(x);
+    const float rest = static_cast<float>(x - static_cast<double>(y));
     const float w = __builtin_amdgcn_exp2f(y);
     return z > -__builtin_inff() && y > -200.0f ? fmaf(w, rest * 0.69314718f, w) : 0.0f;   // (NaN has none)
   }
