@@ -88,13 +88,19 @@ __global__ __launch_bounds__(kThreads) void row_stats_kernel(const Args args) {
       for (int i = 0; i < 8; ++i)
         if (begin + (it * kThreads + threadIdx.x) * 8 < end) sum += v[it][i] == m ? 1.0f : 0.0f;
   } else if (m > -__builtin_inff()) {
-    const float c = fminf(fmaxf(1.4426950408889634f / tau, 1.2e-38f), 3.4e38f);
+    // Differences times 1 / (tau ln 2), either scaled by a power of two where
+    // one of them would leave float32's range and their product not: logits far
+    // apart at a large temperature, logits near zero at a very small one (others
+    // that differ are too far apart there).
+    const float by = tau >= 0x1p60f ? 0x1p-64f : tau < 0x1p-100f && fabsf(m) < 0x1p-40f ? 0x1p64f : 1.0f;
+    const float c = fminf(1.4426950408889634f / (tau * by), 3.4e38f);
+    const float mb = m * by;
 #pragma unroll
     for (int it = 0; it < kIter; ++it) {
       float s8 = 0.0f;
 #pragma unroll
       for (int i = 0; i < 8; ++i)       // a NaN becomes -inf, of weight zero
-        s8 += __builtin_amdgcn_exp2f(fmaxf((v[it][i] - m) * c, -__builtin_inff()));
+        s8 += __builtin_amdgcn_exp2f(fmaxf(fmaf(v[it][i], by, -mb) * c, -__builtin_inff()));
       if (begin + (it * kThreads + threadIdx.x) * 8 < end) sum += s8;
     }
   }
