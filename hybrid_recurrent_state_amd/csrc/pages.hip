@@ -51,6 +51,7 @@ struct PagesArgs {
   int32_t page_shift;
   int32_t table_len;
   int32_t n_prefix;
+  int32_t clip;
 };
 
 // What the second launch needs to know of a request.
@@ -125,9 +126,12 @@ template <bool ALL> __global__ __launch_bounds__(kThreads) void reserve_kernel(c
   }
 #pragma unroll
   for (int k = 0; k < kPer; ++k) {
+    const bool in_range = p[k].len >= 0 && p[k].n_new >= 0 && p[k].n_new <= a.n_pos;
+    if (a.clip && in_range)
+      p[k].n_new = static_cast<int32_t>(
+          min(static_cast<int64_t>(p[k].n_new), max(int64_t{0}, (static_cast<int64_t>(a.table_len) << a.page_shift) - p[k].len)));
     const int64_t want = (static_cast<int64_t>(p[k].len) + p[k].n_new + (1 << a.page_shift) - 1) >> a.page_shift;
-    const bool ok = p[k].len >= 0 && p[k].n_new >= 0 && p[k].n_new <= a.n_pos && want <= a.table_len && p[k].held >= 0 &&
-                    p[k].held <= a.table_len;
+    const bool ok = in_range && want <= a.table_len && p[k].held >= 0 && p[k].held <= a.table_len;
     if (!ok) p[k].len = -1;
     p[k].have = max(p[k].held, a.n_prefix);
     need[k] = ok && tid * kPer + k < a.n_req ? max(want - p[k].have, int64_t{0}) : 0;
@@ -351,7 +355,7 @@ bool pages_desc_ok(const hrs_pages_desc* d) {
   return d && d->n_req >= 1 && d->n_req <= kReqs && d->n_pos >= 1 && d->n_pos <= HRS_MAX_CHUNKED_POS &&
          d->page_size >= 16 && d->page_size <= 1024 && (d->page_size & (d->page_size - 1)) == 0 && d->n_pages >= 1 &&
          d->table_len >= 1 && static_cast<int64_t>(d->table_len) * d->page_size <= INT32_MAX - HRS_MAX_CHUNKED_POS &&
-         d->n_prefix >= 0 && d->n_prefix <= d->table_len;
+         d->n_prefix >= 0 && d->n_prefix <= d->table_len && (d->clip == 0 || d->clip == 1);
 }
 
 PagesArgs pages_args(const hrs_pages_desc* d, const int32_t* len, int32_t* page_table, int32_t* n_held,
@@ -360,6 +364,7 @@ PagesArgs pages_args(const hrs_pages_desc* d, const int32_t* len, int32_t* page_
   a.len = len; a.page_table = page_table; a.n_held = n_held; a.free_pages = free_pages; a.n_free = n_free;
   a.status = status; a.plan = static_cast<Plan*>(workspace);
   a.n_req = d->n_req; a.n_pos = d->n_pos; a.n_pages = d->n_pages; a.table_len = d->table_len; a.n_prefix = d->n_prefix;
+  a.clip = d->clip;
   a.page_shift = __builtin_ctz(static_cast<unsigned>(d->page_size));
   return a;
 }

@@ -627,7 +627,7 @@ class HybridVerifyStep(FusedVerifyStep):
             lists = (b.page_table, b.n_held, b.free_pages, b.n_free, b.workspace)
             whole = 0 if b.whole_prefix is None else b.whole_prefix.shape[0]
             self.reserve_call = kv_pages_reserve_call(b.seq_len, *lists, page_size=s.page_size, n_pos=bufs.shape.n_pos,
-                                                      prefix_table=b.whole_prefix, status=b.page_status[0])
+                                                      prefix_table=b.whole_prefix, status=b.page_status[0], clip=True)
             self.release_call = kv_pages_release_call(b.seq_len, *lists, page_size=s.page_size, n_prefix=whole,
                                                       status=b.page_status[1])
 

@@ -89,7 +89,7 @@
 extern "C" {
 #endif
 
-#define HRS_ABI_VERSION 1
+#define HRS_ABI_VERSION 2
 
 /* Largest span (root + drafts) a call accepts. */
 #define HRS_MAX_POS 64
@@ -925,6 +925,10 @@ typedef struct {
   int32_t n_prefix;  /* leading entries of every table that hold the pages
                         of a prefix shared by all requests; 0 = none. Whole
                         pages of it: new positions are written behind them */
+  int32_t clip;      /* reserve: 1 = positions behind the last slot of a
+                        request's table are left out, 0 = a request that has
+                        such positions is refused (release: ignored but for
+                        these values)                                       */
 } hrs_pages_desc;
 
 /* Bytes of device workspace the two calls need for this descriptor (0 if it
@@ -936,7 +940,8 @@ size_t kv_pages_workspace_bytes(const hrs_pages_desc* desc);
  * free list on the device, and their slots ([P2] What Changed: the hybrid
  * state includes the KV cache; [P1] Changes: nothing through the host). The
  * list is a stack free_pages[0 .. n_free). With S = page_size,
- * m = n_new[r] (NULL: n_pos), request r needs
+ * m = n_new[r] (NULL: n_pos; with clip at most table_len * S - seq_len[r]),
+ * request r needs
  *     need_r = max(0, ceil((seq_len[r] + m) / S) - max(n_held[r], n_prefix))
  * pages beyond those it holds (table entries [0, n_held[r])) and the prefix's.
  * It is served where need_0 + ... + need_r <= n_free: in request order until

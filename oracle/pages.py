@@ -13,9 +13,13 @@ from __future__ import annotations
 import numpy as np
 
 
-def reserve(seq_len, n_new, table, held, free, n_free: int, page_size: int, n_pos: int, prefix=(), n_pages=None):
+def reserve(seq_len, n_new, table, held, free, n_free: int, page_size: int, n_pos: int, prefix=(), n_pages=None,
+            clip=False):
     """In place; returns (n_free, slot map [R, n_pos], requests that were refused or got nothing)."""
     R, P = table.shape
+    if clip:
+        n_new = [min(int(m), max(0, P * page_size - int(n))) if n >= 0 and 0 <= m <= n_pos else m
+                 for n, m in zip(seq_len, n_new)]
     n_pages = len(free) if n_pages is None else n_pages
     have0, needs, ok = [], [], []
     for r in range(R):
