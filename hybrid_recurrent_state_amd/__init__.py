@@ -126,7 +126,7 @@ class HoldDesc(ctypes.Structure):
 
 class PagesDesc(ctypes.Structure):
     _fields_ = [("n_req", _i32), ("n_pos", _i32), ("n_pages", _i32), ("page_size", _i32), ("table_len", _i32),
-                ("n_prefix", _i32), ("clip", _i32)]
+                ("n_prefix", _i32), ("clip", _i32), ("skip", _p)]
 
 
 # Exported symbols and their signatures (every function of include/hrs.h).
@@ -1103,7 +1103,7 @@ def _pages_checks(page_table, n_held, free_pages, n_free, workspace, status, **l
     R, P = page_table.shape
     chk = _SpanChecks()
     for name, t in lens.items():
-        chk(name, t, (R,), _i32t(), optional=name == "n_new")
+        chk(name, t, (R,), _i32t(), optional=name in ("n_new", "skip"))
     for name, t, shape in (("page_table", page_table, (R, P)), ("n_held", n_held, (R,)),
                            ("free_pages", free_pages, None), ("n_free", n_free, (1,))):
         chk(name, t, shape, _i32t())
@@ -1113,9 +1113,11 @@ def _pages_checks(page_table, n_held, free_pages, n_free, workspace, status, **l
 
 
 def kv_pages_reserve_call(seq_len, page_table, n_held, free_pages, n_free, workspace, page_size: int, n_pos: int = 0,
-                          n_new=None, prefix_table=None, slot_map=None, status=None, clip: bool = False) -> PreparedCall:
+                          n_new=None, prefix_table=None, slot_map=None, status=None, clip: bool = False,
+                          skip=None) -> PreparedCall:
     """The PreparedCall of kv_pages_reserve (same arguments, without the stream)."""
-    chk, R, P = _pages_checks(page_table, n_held, free_pages, n_free, workspace, status, seq_len=seq_len, n_new=n_new)
+    chk, R, P = _pages_checks(page_table, n_held, free_pages, n_free, workspace, status, seq_len=seq_len, n_new=n_new,
+                              skip=skip)
     if prefix_table is not None:
         _rank("prefix_table", prefix_table, 1)
     chk("prefix_table", prefix_table, None, _i32t(), optional=True)
@@ -1126,7 +1128,7 @@ def kv_pages_reserve_call(seq_len, page_table, n_held, free_pages, n_free, works
     chk.written("page_table", "n_held", "n_free", "slot_map", "workspace", "status")
     chk.on_gpu()
     d = PagesDesc(R, n_pos, free_pages.shape[0], page_size, P, 0 if prefix_table is None else prefix_table.shape[0],
-                  int(clip))
+                  int(clip), _data(skip))
     nbytes = workspace.numel() * workspace.element_size()
     return chk.call("kv_pages_reserve",
                     (ctypes.byref(d), _data(seq_len), _data(n_new), _data(prefix_table) if d.n_prefix else None,
@@ -1135,15 +1137,17 @@ def kv_pages_reserve_call(seq_len, page_table, n_held, free_pages, n_free, works
 
 
 def kv_pages_reserve(seq_len, page_table, n_held, free_pages, n_free, workspace, page_size: int, n_pos: int = 0,
-                     n_new=None, prefix_table=None, slot_map=None, status=None, stream=None, clip: bool = False):
+                     n_new=None, prefix_table=None, slot_map=None, status=None, stream=None, clip: bool = False,
+                     skip=None):
     """Pages for slots up to seq_len[r] + n_new[r] (None: n_pos) of every
     request, from the stack free_pages [n_pages], n_free [1] into page_table
     [R,P], n_held [R]; prefix_table: the shared leading entries of every table.
-    clip: only up to the end of a request's table, which is refused otherwise.
+    clip: only up to the end of a request's table, which is refused otherwise;
+    skip [R] int32: requests (any value but 0) that take nothing.
     slot_map [R,n_pos] int64: where the new positions lie. int32 device tensors
     but for slot_map; workspace of at least kv_pages_workspace_bytes."""
     kv_pages_reserve_call(seq_len, page_table, n_held, free_pages, n_free, workspace, page_size, n_pos, n_new,
-                          prefix_table, slot_map, status, clip)(stream)
+                          prefix_table, slot_map, status, clip, skip)(stream)
 
 
 def kv_pages_release_call(keep_len, page_table, n_held, free_pages, n_free, workspace, page_size: int,

@@ -37,6 +37,7 @@ constexpr int kFillSlots = 4096;       // positions of a request that one of its
 struct PagesArgs {
   const int32_t* len;        // seq_len or keep_len
   const int32_t* n_new;
+  const int32_t* skip;
   const int32_t* prefix_table;
   int32_t* page_table;
   int32_t* n_held;
@@ -56,7 +57,7 @@ struct PagesArgs {
 
 // What the second launch needs to know of a request.
 struct Plan {
-  int32_t len;       // reserve: seq_len; -1: refused
+  int32_t len;       // reserve: seq_len; -1: refused or passed over
   int32_t n_new;
   int32_t held;      // entries before the call
   int32_t have;      // reserve: entries with the prefix's; release: entries that stay
@@ -117,6 +118,7 @@ template <bool ALL> __global__ __launch_bounds__(kThreads) void reserve_kernel(c
   const int32_t in_list = clamp_free(*a.n_free, a.n_pages);
   Plan p[kPer];
   int64_t need[kPer], sum = 0;
+  int32_t skips[kPer] = {};
 #pragma unroll
   for (int k = 0; k < kPer; ++k) {
     const int r = tid * kPer + k, rr = min(r, a.n_req - 1);
@@ -124,14 +126,18 @@ template <bool ALL> __global__ __launch_bounds__(kThreads) void reserve_kernel(c
     p[k].n_new = a.n_new ? a.n_new[rr] : a.n_pos;
     p[k].held = a.n_held[rr];
   }
+  if (a.skip) {
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) skips[k] = a.skip[min(tid * kPer + k, a.n_req - 1)];
+  }
+  // Slots that new positions may take (without a clip longer requests are refused).
+  const int32_t room = a.clip ? a.table_len << a.page_shift : INT32_MAX;
 #pragma unroll
   for (int k = 0; k < kPer; ++k) {
     const bool in_range = p[k].len >= 0 && p[k].n_new >= 0 && p[k].n_new <= a.n_pos;
-    if (a.clip && in_range)
-      p[k].n_new = static_cast<int32_t>(
-          min(static_cast<int64_t>(p[k].n_new), max(int64_t{0}, (static_cast<int64_t>(a.table_len) << a.page_shift) - p[k].len)));
+    if (in_range) p[k].n_new = min(p[k].n_new, max(0, room - p[k].len));
     const int64_t want = (static_cast<int64_t>(p[k].len) + p[k].n_new + (1 << a.page_shift) - 1) >> a.page_shift;
-    const bool ok = in_range && want <= a.table_len && p[k].held >= 0 && p[k].held <= a.table_len;
+    const bool ok = in_range && want <= a.table_len && p[k].held >= 0 && p[k].held <= a.table_len && skips[k] == 0;
     if (!ok) p[k].len = -1;
     p[k].have = max(p[k].held, a.n_prefix);
     need[k] = ok && tid * kPer + k < a.n_req ? max(want - p[k].have, int64_t{0}) : 0;
@@ -148,7 +154,7 @@ template <bool ALL> __global__ __launch_bounds__(kThreads) void reserve_kernel(c
     upto += need[k];
     p[k].count = upto <= in_list ? static_cast<int32_t>(need[k]) : 0;
     taken += p[k].count;
-    bad += r < a.n_req && (p[k].len < 0 || p[k].count < need[k]);
+    bad += r < a.n_req && skips[k] == 0 && (p[k].len < 0 || p[k].count < need[k]);
   }
   int64_t all_taken, all_bad;
   block_sum(taken, lds, &all_taken);
@@ -388,10 +394,11 @@ extern "C" int kv_pages_reserve(const hrs_pages_desc* d, const int32_t* seq_len,
     return HRS_EINVAL;
   if (!workspace || workspace_bytes < kv_pages_workspace_bytes(d)) return HRS_EINVAL;
   if (!aligned16(seq_len) || !aligned16(n_new) || !aligned16(prefix_table) || !aligned16(page_table) || !aligned16(n_held) ||
-      !aligned16(free_pages) || !aligned16(n_free) || !aligned16(slot_map) || !aligned16(status) || !aligned16(workspace))
+      !aligned16(free_pages) || !aligned16(n_free) || !aligned16(slot_map) || !aligned16(status) || !aligned16(workspace) ||
+      !aligned16(d->skip))
     return HRS_EALIGN;
   PagesArgs a = pages_args(d, seq_len, page_table, n_held, const_cast<int32_t*>(free_pages), n_free, status, workspace);
-  a.n_new = n_new; a.prefix_table = prefix_table; a.slot_map = slot_map;
+  a.n_new = n_new; a.skip = d->skip; a.prefix_table = prefix_table; a.slot_map = slot_map;
   const hipStream_t s = static_cast<hipStream_t>(stream);
   (void)hipGetLastError();
   // One block where the slot map has few entries: it writes 1024 at a time.

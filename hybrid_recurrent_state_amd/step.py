@@ -573,10 +573,12 @@ class HybridVerifyStep(FusedVerifyStep):
     ``filtered`` samples after top-k, top-p and min-p (accept_sample_filtered:
     ``top_k``, ``top_p``, ``min_p`` of the AttnBuffers). A shape with a prefix
     reads its slots once for all requests (attn_verify_shared). With a page list
-    a step takes the pages of its span's slots before its layers and gives
-    those that the accepted rows leave empty back behind the append, so a
-    request is held for want of pages only where the list has none; a request
-    that ends gives its own back through kv_pages_release.
+    a step takes the pages of its span's slots, up to the table's end, before
+    its layers and gives those that the accepted rows leave empty back behind
+    the append. Requests are served in their order until one's pages are not all
+    there, so a request is held for want of pages where the list has too few for
+    the requests up to it; held ones take none. A request that ends gives its
+    own back through kv_pages_release.
     """
 
     def __init__(self, bufs: StepBuffers, attn: AttnBuffers, parent=None, runs: Optional[Sequence[tuple]] = None,
@@ -627,7 +629,8 @@ class HybridVerifyStep(FusedVerifyStep):
             lists = (b.page_table, b.n_held, b.free_pages, b.n_free, b.workspace)
             whole = 0 if b.whole_prefix is None else b.whole_prefix.shape[0]
             self.reserve_call = kv_pages_reserve_call(b.seq_len, *lists, page_size=s.page_size, n_pos=bufs.shape.n_pos,
-                                                      prefix_table=b.whole_prefix, status=b.page_status[0], clip=True)
+                                                      prefix_table=b.whole_prefix, status=b.page_status[0], clip=True,
+                                                      skip=b.held)
             self.release_call = kv_pages_release_call(b.seq_len, *lists, page_size=s.page_size, n_prefix=whole,
                                                       status=b.page_status[1])
 

@@ -929,6 +929,11 @@ typedef struct {
                         request's table are left out, 0 = a request that has
                         such positions is refused (release: ignored but for
                         these values)                                       */
+  const int32_t* skip; /* reserve: [R], device, or NULL: a request with any
+                        value but 0 takes nothing and is left as it is, with
+                        a slot map of -1; not counted in status (accept_hold's
+                        held: what it would take is for those behind it)
+                        (release: ignored)                                  */
 } hrs_pages_desc;
 
 /* Bytes of device workspace the two calls need for this descriptor (0 if it
@@ -966,7 +971,7 @@ size_t kv_pages_workspace_bytes(const hrs_pages_desc* desc);
  *          workspace: device scratch of at least kv_pages_workspace_bytes(desc)
  *          bytes, contents ignored.
  * page_table, n_held, n_free, slot_map, status and workspace overlap nothing
- * else of the call. Errors: HRS_EINVAL, HRS_EALIGN, HRS_EDEVICE.
+ * else of the call (skip among it). Errors: HRS_EINVAL, HRS_EALIGN, HRS_EDEVICE.
  */
 int kv_pages_reserve(const hrs_pages_desc* desc, const int32_t* seq_len, const int32_t* n_new,
                      const int32_t* prefix_table, int32_t* page_table, int32_t* n_held,

@@ -14,7 +14,7 @@ import numpy as np
 
 
 def reserve(seq_len, n_new, table, held, free, n_free: int, page_size: int, n_pos: int, prefix=(), n_pages=None,
-            clip=False):
+            clip=False, skip=None):
     """In place; returns (n_free, slot map [R, n_pos], requests that were refused or got nothing)."""
     R, P = table.shape
     if clip:
@@ -25,6 +25,7 @@ def reserve(seq_len, n_new, table, held, free, n_free: int, page_size: int, n_po
     for r in range(R):
         want = -(-(int(seq_len[r]) + int(n_new[r])) // page_size)
         good = seq_len[r] >= 0 and 0 <= n_new[r] <= n_pos and want <= P and 0 <= held[r] <= P
+        good = good and (skip is None or not skip[r])
         have = max(int(held[r]), len(prefix))
         have0.append(have)
         needs.append(max(0, want - have) if good else 0)
@@ -34,7 +35,7 @@ def reserve(seq_len, n_new, table, held, free, n_free: int, page_size: int, n_po
         left -= needs[r]
         served = needs[r] == 0 or left >= 0
         gets.append(needs[r] if served else 0)
-        missed += not ok[r] or not served
+        missed += (skip is None or not skip[r]) and (not ok[r] or not served)
     at = n_free - sum(gets)
     n_free = at
     slots = np.full((R, n_pos), -1, dtype=np.int64)

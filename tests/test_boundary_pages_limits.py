@@ -1,16 +1,18 @@
 """Refusals and hand-worked lists of kv_pages_reserve up to the end of a
-request's table, on the host as in test_boundary_pages.py."""
+request's table and without some of the requests, on the host as in
+test_boundary_pages.py."""
 import numpy as np
 import pytest
 
 from oracle import pages as op
-from tests.test_boundary_host import hrs
-from tests.test_boundary_pages import DESC, call, release, RESERVE
+from tests.test_boundary_attn import t
+from tests.test_boundary_host import FAKE, MIS, hrs
+from tests.test_boundary_pages import DESC, RESERVE, args, call
 from tests.test_oracle_pages import i32
 
 
 def reserve(**kw):
-    return call("kv_pages_reserve", hrs.PagesDesc, RESERVE, dict(DESC, clip=0), kw, extra=(1 << 20,))[0]
+    return call("kv_pages_reserve", hrs.PagesDesc, RESERVE, dict(DESC, clip=0, skip=None), kw, extra=(1 << 20,))[0]
 
 
 @pytest.mark.parametrize("clip,want", [(0, hrs.HRS_EDEVICE), (1, hrs.HRS_EDEVICE), (2, hrs.HRS_EINVAL), (-1, hrs.HRS_EINVAL)])
@@ -28,3 +30,27 @@ def test_hand_worked():
         assert have.tolist() == held and bad == missed
         assert [int(x) for x in got[:, 0]] == slots and (got[1, 1:] == -1).all() and n == (1 if clip else 2)
         assert not clip or ((got[0, :16] == 112 + np.arange(16)).all() and got[0, 16] == -1)
+
+
+def test_skip():
+    assert reserve(skip=FAKE) == hrs.HRS_EDEVICE and reserve(skip=MIS) == hrs.HRS_EALIGN
+    # The first request's three pages would leave one for the second, which needs two.
+    for skip, held, left in ((None, [3, 0], 1), ([1, 0], [0, 2], 2)):
+        table, have, free = np.full((2, 4), -1, np.int32), i32(0, 0), i32(3, 1, 0, 2)
+        n, slots, missed = op.reserve([0, 0], [40, 20], table, have, free, 4, 16, 40, skip=skip)
+        assert have.tolist() == held and n == left and missed == (skip is None)
+        assert skip is None or ((slots[0] == -1).all() and (table[0] == -1).all())
+
+
+def test_binding_refuses_wrong_tensors():
+    import torch
+    i32_ = torch.int32
+    ok = dict(args(), seq_len=t(4, dtype=i32_), skip=t(4, dtype=i32_), n_pos=3, clip=True)
+    with pytest.raises(ValueError, match="GPU"):
+        hrs.kv_pages_reserve(**ok)
+    with pytest.raises(TypeError):
+        hrs.kv_pages_reserve(**{**ok, "skip": t(4, dtype=torch.bool)})
+    with pytest.raises(ValueError):
+        hrs.kv_pages_reserve(**{**ok, "skip": t(3, dtype=i32_)})
+    with pytest.raises(ValueError, match="overlaps"):
+        hrs.kv_pages_reserve(**{**ok, "skip": ok["n_held"]})

@@ -1,5 +1,5 @@
 """Verify steps with a page list where a request runs to its table's last
-slot."""
+slot, or is held in front of others."""
 import numpy as np
 import pytest
 
@@ -42,3 +42,28 @@ def test_a_request_goes_on_to_its_tables_last_slot(w, graph):
         assert int(xa.page_status[0, 0]) == 0
         ended = R - len(on)
     assert ended >= 3 and max(xa.seq_len.tolist()) > 464
+
+
+@pytest.mark.parametrize("graph", [False, True])
+def test_a_held_request_takes_no_pages_from_those_behind_it(graph):
+    """Pages for exactly the requests that go on, a held one in front of them."""
+    w = WORKLOADS[0]
+    bufs, a, step, loaded = make(w)
+    if graph:
+        step.capture_graph()
+    go = step.replay if graph else step.run
+    a.temperature[0] = float("nan")
+    refill(bufs, a, 0, True, loaded.parent)
+    acc, _ = go()
+    assert acc[0] == -1 and min(acc[1:]) >= 0
+    taken = 0
+    for i in range(1, 5):
+        own = int(a.n_held[0])
+        need = sum(max(0, -(-(int(a.seq_len[r]) + w.n_pos) // S) - int(a.n_held[r])) for r in range(1, R))
+        a.n_free.fill_(need)                             # (the list below that stays as it is)
+        refill(bufs, a, i, True, loaded.parent)
+        acc, _ = go()
+        assert int(a.page_status[0, 0]) == 0 and int(a.n_held[0]) == own
+        assert acc[0] == -1 and min(acc[1:]) >= 0, i
+        taken += need
+    assert taken > 0 and a.held.tolist() == [1, 0, 0, 0]

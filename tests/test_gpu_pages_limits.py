@@ -1,5 +1,5 @@
-"""kv_pages_reserve up to the end of a request's table, against the oracle:
-whole numbers, equal."""
+"""kv_pages_reserve up to the end of a request's table and without some of the
+requests, against the oracle: whole numbers, equal."""
 import numpy as np
 import pytest
 
@@ -34,6 +34,22 @@ def test_up_to_the_tables_end(hrs, size):
         if step > 1:
             lens = np.where(x.rng.random(R) < 0.2, x.rng.choice([P * S, P * S - 1, P * S + 1, -1], R), lens).astype(np.int32)
         x.reserve(lens, None if step == 1 else x.rng.integers(-1, n_pos + 2, R).astype(np.int32), clip=True)
+        x.release(np.maximum(lens, 0))
+
+
+@pytest.mark.parametrize("clip", [False, True])
+@pytest.mark.parametrize("size", SIZES, ids=lambda s: "R{}P{}N{}S{}p{}T{}".format(*s))
+def test_without_some_of_the_requests(hrs, size, clip):
+    """What they would take is for those behind them; refused ones among them are not counted."""
+    R, P, N, S, prefix, n_pos = size
+    x = Limited(hrs, R, P, N, S, seed=R + P + 1, prefix=prefix, n_pos=n_pos)
+    for step in range(4):
+        skip = np.where(x.rng.random(R) < 0.3, x.rng.choice([1, -1, 256, 1 << 31 - 1], R), 0).astype(np.int32)
+        lens = np.minimum(x.held.astype(np.int64) * S, x.rng.integers(0, P * S + 1, R)).astype(np.int32)
+        lens[x.rng.random(R) < 0.1] = -1
+        before = x.held.copy()
+        x.reserve(lens, x.rng.integers(0, n_pos + 1, R).astype(np.int32), clip=clip, skip=skip)
+        assert np.array_equal(x.held[skip != 0], before[skip != 0])
         x.release(np.maximum(lens, 0))
 
 
