@@ -121,7 +121,8 @@ class SampleDesc(ctypes.Structure):
 
 
 class HoldDesc(ctypes.Structure):
-    _fields_ = [("n_req", _i32), ("n_pos", _i32), ("n_pages", _i32), ("page_size", _i32), ("table_len", _i32)]
+    _fields_ = [("n_req", _i32), ("n_pos", _i32), ("n_pages", _i32), ("page_size", _i32), ("table_len", _i32),
+                ("min_len", _i32)]
 
 
 class PagesDesc(ctypes.Structure):
@@ -1058,7 +1059,7 @@ def accept_sample_filtered(logits, tokens, uniforms, token_prob, accept_node, ac
 
 
 def accept_hold_call(page_table, seq_len, accept_node, accept_len, path, bonus, held, last_node, n_pages: int,
-                     page_size: int, held_node=None, temperature=None) -> PreparedCall:
+                     page_size: int, held_node=None, temperature=None, min_len: int = 0) -> PreparedCall:
     """The PreparedCall of accept_hold (same arguments, without the stream)."""
     _rank("path", path, 2)
     _rank("page_table", page_table, 2)
@@ -1073,21 +1074,22 @@ def accept_hold_call(page_table, seq_len, accept_node, accept_len, path, bonus, 
     chk("temperature", temperature, (R,), _f32(), optional=True)
     chk.written("accept_node", "accept_len", "path", "bonus", "held", "last_node", "held_node")
     chk.on_gpu()
-    d = HoldDesc(R, T, n_pages, page_size, page_table.shape[1])
+    d = HoldDesc(R, T, n_pages, page_size, page_table.shape[1], min_len)
     return chk.call("accept_hold",
                     (ctypes.byref(d), _data(page_table), _data(seq_len), _data(temperature), _data(accept_node),
                      _data(accept_len), _data(path), _data(bonus), _data(held), _data(last_node), _data(held_node)), d)
 
 
 def accept_hold(page_table, seq_len, accept_node, accept_len, path, bonus, held, last_node, n_pages: int,
-                page_size: int, held_node=None, temperature=None, stream=None):
+                page_size: int, held_node=None, temperature=None, stream=None, min_len: int = 0):
     """Requests that cannot go on taken out of an acceptance (accept_node,
     accept_len, bonus [R] and path [R,T] become -1, held [R] 1): pages of
-    page_table [R,P] missing or full behind seq_len [R], a temperature [R]
-    that is negative or NaN, or held before. The others' accept_node goes to
+    page_table [R,P] missing or full behind seq_len [R], a seq_len below
+    min_len (slots that others read too), a temperature [R] that is negative or
+    NaN, or held before. The others' accept_node goes to
     last_node [R]; a newly held request's last_node to held_node [R]."""
     accept_hold_call(page_table, seq_len, accept_node, accept_len, path, bonus, held, last_node, n_pages, page_size,
-                     held_node, temperature)(stream)
+                     held_node, temperature, min_len)(stream)
 
 
 # --- page lists -----------------------------------------------------------------

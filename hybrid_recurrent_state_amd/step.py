@@ -486,6 +486,7 @@ class AttnBuffers:
 
     With a prefix, prefix_table names its pages, the last one possibly in part:
     that one is of no request's table, each has a page of its own in its place.
+    seq_len starts at the prefix's length; a request with less is held.
     With a page list, free_pages [n_pages] and n_free [1] start with every page
     behind the prefix's, which are pages 0, 1, ... then, and n_held [R] with
     none: the step fills and cuts page_table itself."""
@@ -517,7 +518,7 @@ class AttnBuffers:
             self.k_cache, self.v_cache = z(*pages, dtype=dt), z(*pages, dtype=dt)
             self.k_scale = self.v_scale = None
         self.page_table = z(R, s.table_len)
-        self.seq_len = z(R)
+        self.seq_len = torch.full((R,), s.prefix_len, dtype=torch.int32, device=device)
         whole, pages = s.prefix_len // s.page_size, -(-s.prefix_len // s.page_size)
         self.prefix_table = torch.arange(pages, dtype=torch.int32, device=device) if s.prefix_len else None
         self.prefix_len = torch.full((1,), s.prefix_len, dtype=torch.int32, device=device) if s.prefix_len else None
@@ -562,10 +563,11 @@ class HybridVerifyStep(FusedVerifyStep):
     advances, so replays of the captured step carry on by themselves.
 
     A request that cannot go on is held (accept_hold): its accepted rows do not
-    fit in its page table, a page for them is not there, or its temperature is
-    negative or NaN. The step then reports -1 as its accepted length and bonus
-    token and leaves its pages, length, conv and recurrent state as they were;
-    so do all later steps. The other requests go on. To take it up again:
+    fit in its page table, a page for them is not there, they would begin inside
+    a prefix that all requests read, or its temperature is negative or NaN. The
+    step then reports -1 as its accepted length and bonus token and leaves its
+    pages, length, conv and recurrent state as they were; so do all later steps.
+    The other requests go on. To take it up again:
     ``materialize()`` (which writes every request's recurrent state, a held
     one's from in front of the step that held it), give it what it lacks, and
     start a new speculation with a new HybridVerifyStep.
@@ -620,7 +622,7 @@ class HybridVerifyStep(FusedVerifyStep):
         self.hold_calls = {c: accept_hold_call(
             b.page_table, b.seq_len, bufs.accept_node, bufs.accept_len, bufs.path, bufs.bonus, b.held, b.last_node,
             s.n_pages, s.page_size, held_node=None if c is None else b.held_node[c],
-            temperature=b.temperature if sample else None) for c in (None, 0, 1)}
+            temperature=b.temperature if sample else None, min_len=s.prefix_len) for c in (None, 0, 1)}
         self.append_call = kv_cache_append_call(
             b.k_out, b.v, b.k_cache, b.v_cache, b.page_table, b.seq_len, bufs.accept_len, b.seq_len, bufs.path,
             b.k_scale, b.v_scale, b.status[-1])

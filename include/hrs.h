@@ -880,6 +880,8 @@ typedef struct {
   int32_t n_pages;   /* pages, slots of a page and entries of a request's  */
   int32_t page_size; /* table, as hrs_cache_desc                           */
   int32_t table_len;
+  int32_t min_len;   /* slots below this are not a request's to write (those
+                        of a prefix that others read); 0: none             */
 } hrs_hold_desc;
 
 /*
@@ -888,8 +890,8 @@ typedef struct {
  * ([P3] Safety boundary: rejected before execution). A request goes on if
  * held[r] is 0, its temperature is not negative or NaN, accept_len[r] and
  * accept_node[r] are in [0, T), path[r][0..accept_len[r]] too, and slots
- * seq_len[r] .. seq_len[r] + accept_len[r] lie inside its page table, in
- * pages that are there. Then last_node[r] = accept_node[r]. Otherwise
+ * seq_len[r] .. seq_len[r] + accept_len[r] lie inside its page table, not
+ * below min_len, in pages that are there. Then last_node[r] = accept_node[r]. Otherwise
  *     accept_node[r] = accept_len[r] = bonus[r] = -1,  path[r][:] = -1
  * and, where held[r] was 0, held[r] = 1 and held_node[r] = last_node[r].
  * rollback_restore, conv_state_advance, kv_cache_append and the next
@@ -903,8 +905,8 @@ typedef struct {
  *           last_node [R] and path [R][T] int32, read and written; held_node
  *           [R] int32 or NULL (spans that started from `state`); all device.
  *           No two of them overlap.
- * Errors: HRS_EINVAL (R > 65535; sizes as hrs_cache_desc), HRS_EALIGN,
- * HRS_EDEVICE.
+ * Errors: HRS_EINVAL (R > 65535; sizes as hrs_cache_desc; min_len < 0),
+ * HRS_EALIGN, HRS_EDEVICE.
  */
 int accept_hold(const hrs_hold_desc* desc, const int32_t* page_table, const int32_t* seq_len,
                 const float* temperature, int32_t* accept_node, int32_t* accept_len, int32_t* path,

@@ -1,11 +1,12 @@
-"""Verify steps with a page list where a request runs to its table's last
-slot, or is held in front of others."""
+"""Verify steps with a page list where requests end, wait or start over: one
+that runs to its table's last slot, a held one in front of others, one whose
+slots do not reach behind the shared prefix."""
 import numpy as np
 import pytest
 
 from tests.test_gpu_attn import dev, host
 from tests.test_gpu_hybrid import refill
-from tests.test_gpu_hybrid_pages import R, S, WORKLOADS, make
+from tests.test_gpu_hybrid_pages import P, R, S, WORKLOADS, make
 
 pytestmark = pytest.mark.gpu
 
@@ -67,3 +68,35 @@ def test_a_held_request_takes_no_pages_from_those_behind_it(graph):
         assert acc[0] == -1 and min(acc[1:]) >= 0, i
         taken += need
     assert taken > 0 and a.held.tolist() == [1, 0, 0, 0]
+
+
+@pytest.mark.parametrize("listed", [True, False])
+@pytest.mark.parametrize("short", [0, 160, P - 1])
+def test_a_request_that_ends_inside_the_prefix_leaves_it_alone(listed, short):
+    """Its rows would go into pages that all requests read, or behind slots that are read through the prefix."""
+    w = WORKLOADS[0]
+    x_bufs, xa, x, loaded = make(w, listed=listed)
+    y_bufs, ya, y, _ = make(w, listed=listed)
+    if not listed:
+        for a in (xa, ya):
+            a.page_table.copy_(dev(np.concatenate([np.tile(np.arange(18), (R, 1)), 19 + np.arange(R * 10).reshape(R, 10),
+                                                   np.full((R, 2), -1)], 1).astype(np.int32)))
+    before = [host(c[:, :19]).copy() for c in (xa.k_cache, xa.v_cache)]
+    xa.seq_len[2] = short
+    for i in range(3):
+        refill(x_bufs, xa, i, True, loaded.parent)
+        refill(y_bufs, ya, i, True, loaded.parent)
+        p, q = x.run(), y.run()
+        assert p[0][2] == p[1][2] == -1 and int(xa.seq_len[2]) == short
+        for r in (0, 1, 3):
+            assert (p[0][r], p[1][r]) == (q[0][r], q[1][r]), (i, r)
+        for c, b in zip((xa.k_cache, xa.v_cache), before):
+            assert np.array_equal(host(c[:, :19]), b)
+
+
+def test_lengths_start_behind_the_prefix():
+    w = WORKLOADS[0]
+    _, a, _, _ = make(w)
+    from hybrid_recurrent_state_amd.step import AttnBuffers
+    from synth.device import step_shape
+    assert AttnBuffers(a.shape, step_shape(w)).seq_len.tolist() == [P] * R
