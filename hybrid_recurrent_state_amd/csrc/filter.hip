@@ -29,7 +29,7 @@
 //     151,936 bf16 logits. A bf16 row has few values, which are counted one by
 //     one, and a second read finds the border among equal ones (72 rows: 51 us).
 //     A float32 row has a histogram of weights over 2048 bins, in whole numbers
-//     of 2^-44 and less so that the order of the additions does not matter, that
+//     of 2^-50 or so that the order of the additions does not matter, that
 //     names the border's bin, whose members are sorted; bins of too many members
 //     are divided by their keys until one number is left, whose ties go by
 //     index.
@@ -1014,8 +1014,10 @@ template <typename T> __global__ __launch_bounds__(kRow, 4) void border_kernel(c
       }
     }
   }
-  // Weights as whole numbers: at most 2^62 over all of the row.
-  const int shift = min(50, __builtin_clz(V - 1) + 30);
+  // Weights as whole numbers: at most 2^62 over all that can stay, whose sum is
+  // `all` or below kSmallK. They are off by half each, V 2^-51 of the sum at
+  // most.
+  const int shift = small ? 50 : min(50, 61 - ilogb(fmax(all, 1.0)));
   const WholeWeigher amount(top, lim.tau, shift);
   const float least = hard ? top : logit_of(cut);
   uint64_t border = order_of(kLeastKey, 0x7FFFFFFF);     // everything that can have a weight

@@ -83,3 +83,16 @@ def test_weights_that_are_off_the_same_way(hrs):
     prob = b.run(hrs)[0][0, 1]
     want = filtered(b.logits[0, 0], 1.25, V - 1)[0][1000]
     assert abs(prob - want) <= 5 * U * want, (prob - want) / want / U
+
+
+def test_weights_as_whole_numbers_in_a_very_long_row(hrs):
+    """2^24 logits that weigh e^-16.1 each beside one: half a unit of 2^-38 each, for sums that could hold 2^24 of the largest,
+    was 272 u of them; the sum says how many fit (2^-50: 0.1 u). Else as above."""
+    V = 1 << 24
+    b = Filtered(1, 2, 64, "f32", temp=False, k=V - 1)
+    b.logits = np.zeros((1, 2, V), np.float32)
+    b.logits[:, :, 1000] = 16.109375
+    b.tokens[:, 1] = 1000
+    prob = b.run(hrs)[0][0, 1]
+    want = 1 / (1 + (V - 2) * np.exp(-16.109375))
+    assert abs(prob - want) <= 5 * U * want, (prob - want) / want / U
