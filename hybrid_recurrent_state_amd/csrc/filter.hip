@@ -62,7 +62,7 @@ constexpr double kCut = 48.0;          // e^-48 of the largest weight: no weight
 constexpr uint32_t kLeastKey = 0x00800000u;   // of the lowest finite logit
 
 struct ChunkInfo {
-  double sum;        // of the weights beside the chunk's own maximum (not for a small top-k)
+  double sum;        // of the weights beside the chunk's own maximum (not for a small top-k), good to 18 u
   float top;         // largest logit
   uint32_t bound;    // everything with a key from here on is in the list
   int32_t n;         // how many that are; more than kList: the list is not whole
@@ -795,7 +795,8 @@ template <typename T> __global__ __launch_bounds__(kRow, 4) void border_kernel(c
     }
   }
   // All candidates, by the block, where they can settle it: not if their
-  // weights fall short of top-p's share (by more than the sum may be off).
+  // weights fall short of top-p's share of the same total (by more than another
+  // order of the additions makes).
   bool worth = whole && n <= kTokens;
   if (worth && lim.p < 1.0 && lim.k > n && bound > cut && !hard) {
     if (lim.k < V) {

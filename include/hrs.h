@@ -858,8 +858,11 @@ size_t accept_sample_filtered_workspace_bytes(const hrs_sample_desc* desc);
  * else as accept_sample, whose results it gives without limits; n_pos = 1 is
  * plain sampling (bonus). Weights below e^-48 of the largest count as none.
  * Borders are decided on 64-bit sums of weights in 64 bits where a row is
- * settled by its largest few hundred logits, otherwise of weights good to a
- * few units of 2^-24; the draw is in 64 bits.
+ * settled by its largest few hundred logits or a bf16 row by how often each
+ * value is there; the total that a top-p without a top-k is a share of, where
+ * such a row has weights behind those, is good to 18 units of 2^-24, and so is
+ * the sum of a row without limits. Other rows' weights are good to 3 units, and
+ * their sum, of whole numbers, to V 2^-51 more. The draw is in 64 bits.
  *
  * Layouts: as accept_sample; top_k [R] int32, top_p, min_p [R] float32, device,
  *          each or NULL; workspace of at least

@@ -1,6 +1,7 @@
 """accept_sample_filtered where its counts, sums and arguments end: zeros of
 both signs at the last value that is counted, temperatures and logits at the
-ends of float32, weights that are all off the same way.
+ends of float32, weights that are all off the same way, borders a rounding away
+from top-p or below zero, and rows of more than a million logits.
 
 Tolerances of test_gpu_filter.py but where a test derives its own.
 """
@@ -96,3 +97,54 @@ def test_weights_as_whole_numbers_in_a_very_long_row(hrs):
     prob = b.run(hrs)[0][0, 1]
     want = 1 / (1 + (V - 2) * np.exp(-16.109375))
     assert abs(prob - want) <= 5 * U * want, (prob - want) / want / U
+
+
+@pytest.mark.parametrize("dtype,V", [("bf16", 4096), ("f32", 4096), ("f32", 40000), ("bf16", 40000)])
+def test_borders_a_rounding_away_from_top_p(hrs, dtype, V):
+    """top-p is the cumulative share of a token rounded to float32, so whether that token reaches it is decided 2^-25 or so
+    from the border: by the 64-bit sums of a row that top-k leaves to its list. A 64-bit weight over such a sum is rounded
+    once; 2 u."""
+    R = 64
+    rng = np.random.default_rng(V)
+    b = Filtered(R, 2, V, dtype, temp=True, k=rng.integers(3, 120, R))
+    b.p = np.ones(R, np.float32)
+    for r in range(R):
+        p, n = filtered(b.logits[r, 0], float(b.temp[r]), int(b.k[r]))
+        z = widen(b.logits[r, 0])
+        order = np.lexsort((np.arange(V), -z))[:n]
+        c = np.cumsum(p[order])
+        j = int(rng.integers(0, n - 1))
+        b.p[r] = np.float32(c[j] / c[-1])
+        if abs(float(b.p[r]) * c[-1] - c[j]) < 1e-11:
+            b.p[r] = np.nextafter(b.p[r], np.float32(1))
+        b.tokens[r, 1] = order[j + 1]                  # stays only if the j-th does not reach the share
+    prob = b.run(hrs)[0]
+    for r in range(R):
+        want = filtered(b.logits[r, 0], float(b.temp[r]), int(b.k[r]), float(b.p[r]))[0][b.tokens[r, 1]]
+        assert abs(prob[r, 1] - want) <= 2 * U * want + 2.0 ** -126, (r, prob[r, 1], want)
+
+
+LONG = [("f32", 600008, dict(p=0.9)), ("f32", 600008, dict(k=300000, m=1e-4)), ("bf16", 1100008, dict(p=0.9)),
+        ("bf16", 1100008, dict(k=700000, p=0.97))]
+
+
+@pytest.mark.parametrize("dtype,V,limits", LONG, ids=str)
+def test_rows_of_a_million_logits(hrs, dtype, V, limits):
+    b = Filtered(1, 2, V, dtype, **limits)
+    b.check(b.run(hrs), what="long")
+
+
+@pytest.mark.parametrize("dtype,V", [("f32", 600008), ("bf16", 1100008)])
+def test_ties_far_into_a_long_row(hrs, dtype, V):
+    b = Filtered(3, 1, V, dtype, temp=False, k=[500001, 0, 262145], p=[1.0, 0.75, 1.0])
+    b.logits = cast(np.full((3, 1, V), 1.5, np.float32), dtype)
+    b.u[:, 0] = [0.99999, 0.6, 0.5]
+    b.check(b.run(hrs), what="far ties", margins=False)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("shift", [-4.0, -8.0])
+def test_even_rows_with_their_border_below_zero(hrs, dtype, shift):
+    b = Filtered(4, 3, 30000, dtype, draft="f32", temp=False, k=[0, 12000, 0, 0], p=[0.9, 1.0, 0.97, 1.0], m=[0, 0, 0, 0.01])
+    b.logits = cast(widen(b.logits) + shift, dtype)
+    b.check(b.run(hrs), what=f"shifted by {shift}")
