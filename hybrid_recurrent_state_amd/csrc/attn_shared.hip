@@ -16,7 +16,9 @@
 // worked on it.
 //
 // 16 single positions behind 4,096 slots (24/4 heads of 256): prefix 13.3 us, own
-// slots 14.8, join 15.0, all latency; 16 chains of 17 behind 26,758: 216, 37 and
+// slots 14.8, join 15.0: latency, and 25 MB of the prefix's parts (256 runs of two
+// tiles, each of which reads 64 KB and leaves 98), written and read beside its 17
+// MB; 16 chains of 17 behind 26,758: 216, 37 and
 // 21 (60 MB of parts, 2.9 TB/s); 32 trees of 23 behind 8,191 e4m3 slots (32/8
 // heads of 128): 131, 46 and 21.
 #include <hip/hip_runtime.h>
@@ -202,7 +204,10 @@ template <bool F32> void launch_join(const Cut& own, const Cut& pre, const AttnB
 // there and here, 4 key heads of 256 in bf16: 192 rows over 2,048 slots 46 and
 // 37 us, over 16,384 slots 58 and 61; 288 rows 48 and 44, 65 and 81; 768 rows 61
 // and 60, 99 and 139. (8 heads of 128, e4m3, 288 rows: 43 and 40, 65 and 68; 768
-// rows 64 and 62, 106 and 120.)
+// rows 64 and 62, 106 and 120.) So behind short prefixes the kernels for
+// smaller batches take up to 8% less at 288 and 768 rows too, and behind long ones
+// up to 40% more. The rule goes by rows alone: the host knows the prefix's table,
+// not its length.
 constexpr int64_t kWideRows = 256;
 
 // How a launch's parts are laid out in the workspace.

@@ -14,10 +14,14 @@
 // MI355X design. A verify step's lists are a few entries a request: one block
 // of 1024 threads sums in LDS and then takes the entries of all requests as one
 // flat list (a binary search names an entry's request), so neither many short
-// nor a few long requests leave threads idle; the launch bounds it (reserve 5.6
+// nor a few long requests leave threads idle; the launch bounds it (reserve 6.0
 // us, release 4.7 for 16 requests). Prompts (reserve) and long tables (release)
 // take a second launch of many blocks behind the sums, bound by the slot map's
-// writes (67 MB for 256 prompts: 15.0 us, 4.5 TB/s).
+// writes (67 MB for 256 prompts: 15.1 us, 4.5 TB/s). Reserve chooses by the slot
+// map: few new positions whose requests get all entries of long tables at once
+// are one block's work (calls: 256 requests that start behind 1672 pages of a
+// prefix 71 us, that get 1673 pages each 368). Release's second launch sums what
+// is before each request again (4096 requests of 2 pages: 17 us).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
