@@ -121,13 +121,12 @@ class SampleDesc(ctypes.Structure):
 
 
 class HoldDesc(ctypes.Structure):
-    _fields_ = [("n_req", _i32), ("n_pos", _i32), ("n_pages", _i32), ("page_size", _i32), ("table_len", _i32),
-                ("min_len", _i32)]
+    _fields_ = [("n_req", _i32), ("n_pos", _i32), ("n_pages", _i32), ("page_size", _i32), ("table_len", _i32)]
 
 
 class PagesDesc(ctypes.Structure):
     _fields_ = [("n_req", _i32), ("n_pos", _i32), ("n_pages", _i32), ("page_size", _i32), ("table_len", _i32),
-                ("n_prefix", _i32), ("clip", _i32), ("skip", _p)]
+                ("n_prefix", _i32)]
 
 
 # Exported symbols and their signatures (every function of include/hrs.h).
@@ -163,8 +162,10 @@ _SIGNATURES = {
     "accept_sample_filtered_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(SampleDesc)]),
     "accept_sample_filtered": (_i32, [ctypes.POINTER(SampleDesc)] + [_p] * 15 + [ctypes.c_size_t, _p]),
     "accept_hold": (_i32, [ctypes.POINTER(HoldDesc)] + [_p] * 11),
+    "accept_hold_behind": (_i32, [ctypes.POINTER(HoldDesc), _i32] + [_p] * 11),
     "kv_pages_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(PagesDesc)]),
     "kv_pages_reserve": (_i32, [ctypes.POINTER(PagesDesc)] + [_p] * 10 + [ctypes.c_size_t, _p]),
+    "kv_pages_reserve_step": (_i32, [ctypes.POINTER(PagesDesc)] + [_p] * 11 + [ctypes.c_size_t, _p]),
     "kv_pages_release": (_i32, [ctypes.POINTER(PagesDesc)] + [_p] * 7 + [ctypes.c_size_t, _p]),
     "hrs_strerror": (ctypes.c_char_p, [_i32]),
     "hrs_abi_version": (_i32, []),
@@ -1058,9 +1059,9 @@ def accept_sample_filtered(logits, tokens, uniforms, token_prob, accept_node, ac
                                 top_k, top_p, min_p, draft_probs, temperature, parent, status)(stream)
 
 
-def accept_hold_call(page_table, seq_len, accept_node, accept_len, path, bonus, held, last_node, n_pages: int,
-                     page_size: int, held_node=None, temperature=None, min_len: int = 0) -> PreparedCall:
-    """The PreparedCall of accept_hold (same arguments, without the stream)."""
+def _hold_checks(page_table, seq_len, accept_node, accept_len, path, bonus, held, last_node, n_pages, page_size, held_node,
+                 temperature):
+    """Checks, descriptor and pointers of the accept_hold calls."""
     _rank("path", path, 2)
     _rank("page_table", page_table, 2)
     R, T = path.shape
@@ -1074,22 +1075,44 @@ def accept_hold_call(page_table, seq_len, accept_node, accept_len, path, bonus, 
     chk("temperature", temperature, (R,), _f32(), optional=True)
     chk.written("accept_node", "accept_len", "path", "bonus", "held", "last_node", "held_node")
     chk.on_gpu()
-    d = HoldDesc(R, T, n_pages, page_size, page_table.shape[1], min_len)
-    return chk.call("accept_hold",
-                    (ctypes.byref(d), _data(page_table), _data(seq_len), _data(temperature), _data(accept_node),
-                     _data(accept_len), _data(path), _data(bonus), _data(held), _data(last_node), _data(held_node)), d)
+    d = HoldDesc(R, T, n_pages, page_size, page_table.shape[1])
+    return chk, d, (_data(page_table), _data(seq_len), _data(temperature), _data(accept_node), _data(accept_len),
+                    _data(path), _data(bonus), _data(held), _data(last_node), _data(held_node))
+
+
+def accept_hold_call(page_table, seq_len, accept_node, accept_len, path, bonus, held, last_node, n_pages: int,
+                     page_size: int, held_node=None, temperature=None) -> PreparedCall:
+    """The PreparedCall of accept_hold (same arguments, without the stream)."""
+    chk, d, ptrs = _hold_checks(page_table, seq_len, accept_node, accept_len, path, bonus, held, last_node, n_pages,
+                                page_size, held_node, temperature)
+    return chk.call("accept_hold", (ctypes.byref(d), *ptrs), d)
 
 
 def accept_hold(page_table, seq_len, accept_node, accept_len, path, bonus, held, last_node, n_pages: int,
-                page_size: int, held_node=None, temperature=None, stream=None, min_len: int = 0):
+                page_size: int, held_node=None, temperature=None, stream=None):
     """Requests that cannot go on taken out of an acceptance (accept_node,
     accept_len, bonus [R] and path [R,T] become -1, held [R] 1): pages of
-    page_table [R,P] missing or full behind seq_len [R], a seq_len below
-    min_len (slots that others read too), a temperature [R] that is negative or
-    NaN, or held before. The others' accept_node goes to
+    page_table [R,P] missing or full behind seq_len [R], a temperature [R]
+    that is negative or NaN, or held before. The others' accept_node goes to
     last_node [R]; a newly held request's last_node to held_node [R]."""
     accept_hold_call(page_table, seq_len, accept_node, accept_len, path, bonus, held, last_node, n_pages, page_size,
-                     held_node, temperature, min_len)(stream)
+                     held_node, temperature)(stream)
+
+
+def accept_hold_behind_call(page_table, seq_len, accept_node, accept_len, path, bonus, held, last_node, n_pages: int,
+                            page_size: int, prefix_len: int, held_node=None, temperature=None) -> PreparedCall:
+    """The PreparedCall of accept_hold_behind (same arguments, without the stream)."""
+    chk, d, ptrs = _hold_checks(page_table, seq_len, accept_node, accept_len, path, bonus, held, last_node, n_pages,
+                                page_size, held_node, temperature)
+    return chk.call("accept_hold_behind", (ctypes.byref(d), prefix_len, *ptrs), d)
+
+
+def accept_hold_behind(page_table, seq_len, accept_node, accept_len, path, bonus, held, last_node, n_pages: int,
+                       page_size: int, prefix_len: int, held_node=None, temperature=None, stream=None):
+    """accept_hold of requests behind a prefix that all of them read: those
+    with a seq_len below prefix_len are held as well."""
+    accept_hold_behind_call(page_table, seq_len, accept_node, accept_len, path, bonus, held, last_node, n_pages, page_size,
+                            prefix_len, held_node, temperature)(stream)
 
 
 # --- page lists -----------------------------------------------------------------
@@ -1114,10 +1137,8 @@ def _pages_checks(page_table, n_held, free_pages, n_free, workspace, status, **l
     return chk, R, P
 
 
-def kv_pages_reserve_call(seq_len, page_table, n_held, free_pages, n_free, workspace, page_size: int, n_pos: int = 0,
-                          n_new=None, prefix_table=None, slot_map=None, status=None, clip: bool = False,
-                          skip=None) -> PreparedCall:
-    """The PreparedCall of kv_pages_reserve (same arguments, without the stream)."""
+def _reserve_call(fn, seq_len, page_table, n_held, free_pages, n_free, workspace, page_size, n_pos, n_new, prefix_table,
+                  slot_map, status, skip=None) -> PreparedCall:
     chk, R, P = _pages_checks(page_table, n_held, free_pages, n_free, workspace, status, seq_len=seq_len, n_new=n_new,
                               skip=skip)
     if prefix_table is not None:
@@ -1129,27 +1150,47 @@ def kv_pages_reserve_call(seq_len, page_table, n_held, free_pages, n_free, works
     chk("slot_map", slot_map, (R, n_pos), (_torch().int64,), optional=True)
     chk.written("page_table", "n_held", "n_free", "slot_map", "workspace", "status")
     chk.on_gpu()
-    d = PagesDesc(R, n_pos, free_pages.shape[0], page_size, P, 0 if prefix_table is None else prefix_table.shape[0],
-                  int(clip), _data(skip))
+    d = PagesDesc(R, n_pos, free_pages.shape[0], page_size, P, 0 if prefix_table is None else prefix_table.shape[0])
     nbytes = workspace.numel() * workspace.element_size()
-    return chk.call("kv_pages_reserve",
-                    (ctypes.byref(d), _data(seq_len), _data(n_new), _data(prefix_table) if d.n_prefix else None,
-                     _data(page_table), _data(n_held), _data(free_pages), _data(n_free), _data(slot_map), _data(status),
-                     _data(workspace), nbytes), d)
+    first = (_data(seq_len), _data(n_new)) + ((_data(skip),) if fn == "kv_pages_reserve_step" else ())
+    return chk.call(fn,
+                    (ctypes.byref(d), *first, _data(prefix_table) if d.n_prefix else None, _data(page_table),
+                     _data(n_held), _data(free_pages), _data(n_free), _data(slot_map), _data(status), _data(workspace),
+                     nbytes), d)
+
+
+def kv_pages_reserve_call(seq_len, page_table, n_held, free_pages, n_free, workspace, page_size: int, n_pos: int = 0,
+                          n_new=None, prefix_table=None, slot_map=None, status=None) -> PreparedCall:
+    """The PreparedCall of kv_pages_reserve (same arguments, without the stream)."""
+    return _reserve_call("kv_pages_reserve", seq_len, page_table, n_held, free_pages, n_free, workspace, page_size, n_pos,
+                         n_new, prefix_table, slot_map, status)
 
 
 def kv_pages_reserve(seq_len, page_table, n_held, free_pages, n_free, workspace, page_size: int, n_pos: int = 0,
-                     n_new=None, prefix_table=None, slot_map=None, status=None, stream=None, clip: bool = False,
-                     skip=None):
+                     n_new=None, prefix_table=None, slot_map=None, status=None, stream=None):
     """Pages for slots up to seq_len[r] + n_new[r] (None: n_pos) of every
     request, from the stack free_pages [n_pages], n_free [1] into page_table
     [R,P], n_held [R]; prefix_table: the shared leading entries of every table.
-    clip: only up to the end of a request's table, which is refused otherwise;
-    skip [R] int32: requests (any value but 0) that take nothing.
     slot_map [R,n_pos] int64: where the new positions lie. int32 device tensors
     but for slot_map; workspace of at least kv_pages_workspace_bytes."""
     kv_pages_reserve_call(seq_len, page_table, n_held, free_pages, n_free, workspace, page_size, n_pos, n_new,
-                          prefix_table, slot_map, status, clip, skip)(stream)
+                          prefix_table, slot_map, status)(stream)
+
+
+def kv_pages_reserve_step_call(seq_len, page_table, n_held, free_pages, n_free, workspace, page_size: int, n_pos: int = 0,
+                               n_new=None, prefix_table=None, slot_map=None, status=None, skip=None) -> PreparedCall:
+    """The PreparedCall of kv_pages_reserve_step (same arguments, without the stream)."""
+    return _reserve_call("kv_pages_reserve_step", seq_len, page_table, n_held, free_pages, n_free, workspace, page_size,
+                         n_pos, n_new, prefix_table, slot_map, status, skip)
+
+
+def kv_pages_reserve_step(seq_len, page_table, n_held, free_pages, n_free, workspace, page_size: int, n_pos: int = 0,
+                          n_new=None, prefix_table=None, slot_map=None, status=None, skip=None, stream=None):
+    """kv_pages_reserve up to the end of a request's table, where that refuses
+    the request, and without the requests that skip [R] int32 names (any value
+    but 0)."""
+    kv_pages_reserve_step_call(seq_len, page_table, n_held, free_pages, n_free, workspace, page_size, n_pos, n_new,
+                               prefix_table, slot_map, status, skip)(stream)
 
 
 def kv_pages_release_call(keep_len, page_table, n_held, free_pages, n_free, workspace, page_size: int,

@@ -35,7 +35,7 @@ struct HoldArgs {
   int32_t n_pages;
   int32_t page_shift;
   int32_t table_len;
-  int32_t min_len;
+  int32_t prefix_len;
 };
 
 __global__ __launch_bounds__(kThreads) void hold_kernel(const HoldArgs a) {
@@ -47,7 +47,7 @@ __global__ __launch_bounds__(kThreads) void hold_kernel(const HoldArgs a) {
   const int len = a.seq_len[r], n = a.accept_len[r], node = a.accept_node[r], before = a.held[r];
   const float tau = a.temperature ? a.temperature[r] : 1.0f;
   const int64_t slots = static_cast<int64_t>(a.table_len) << a.page_shift;
-  bool ok = before == 0 && n >= 0 && n < a.n_pos && node >= 0 && node < a.n_pos && tau >= 0.0f && len >= a.min_len &&
+  bool ok = before == 0 && n >= 0 && n < a.n_pos && node >= 0 && node < a.n_pos && tau >= 0.0f && len >= a.prefix_len &&
             static_cast<int64_t>(len) + n + 1 <= slots;
   if (ok) {
     bool fits = true;
@@ -78,14 +78,14 @@ __global__ __launch_bounds__(kThreads) void hold_kernel(const HoldArgs a) {
 
 using namespace hrs;
 
-extern "C" int accept_hold(const hrs_hold_desc* d, const int32_t* page_table, const int32_t* seq_len,
-                           const float* temperature, int32_t* accept_node, int32_t* accept_len, int32_t* path,
-                           int32_t* bonus, int32_t* held, int32_t* last_node, int32_t* held_node, void* stream) {
+extern "C" int accept_hold_behind(const hrs_hold_desc* d, int32_t prefix_len, const int32_t* page_table, const int32_t* seq_len,
+                                  const float* temperature, int32_t* accept_node, int32_t* accept_len, int32_t* path,
+                                  int32_t* bonus, int32_t* held, int32_t* last_node, int32_t* held_node, void* stream) {
   if (d == nullptr) return HRS_EINVAL;
   const bool pages_ok = d->page_size >= 16 && d->page_size <= 1024 && (d->page_size & (d->page_size - 1)) == 0 &&
                         d->n_pages >= 1 && d->table_len >= 1 &&
                         static_cast<int64_t>(d->table_len) * d->page_size <= INT32_MAX - HRS_MAX_CHUNKED_POS;
-  if (d->n_req < 1 || d->n_req > 65535 || d->n_pos < 1 || d->n_pos > HRS_MAX_POS || d->min_len < 0 || !pages_ok)
+  if (d->n_req < 1 || d->n_req > 65535 || d->n_pos < 1 || d->n_pos > HRS_MAX_POS || prefix_len < 0 || !pages_ok)
     return HRS_EINVAL;
   if (!page_table || !seq_len || !accept_node || !accept_len || !path || !bonus || !held || !last_node)
     return HRS_EINVAL;
@@ -95,9 +95,16 @@ extern "C" int accept_hold(const hrs_hold_desc* d, const int32_t* page_table, co
     return HRS_EALIGN;
   const HoldArgs args{page_table, seq_len, temperature, accept_node, accept_len, path, bonus, held, last_node, held_node,
                       d->n_req, d->n_pos, d->n_pages, __builtin_ctz(static_cast<unsigned>(d->page_size)), d->table_len,
-                      d->min_len};
+                      prefix_len};
   (void)hipGetLastError();
   hipLaunchKernelGGL(hold_kernel, dim3((d->n_req + kThreads / 64 - 1) / (kThreads / 64)), dim3(kThreads), 0,
                      static_cast<hipStream_t>(stream), args);
   return launch_error() == hipSuccess ? HRS_OK : HRS_EDEVICE;
+}
+
+extern "C" int accept_hold(const hrs_hold_desc* d, const int32_t* page_table, const int32_t* seq_len,
+                           const float* temperature, int32_t* accept_node, int32_t* accept_len, int32_t* path,
+                           int32_t* bonus, int32_t* held, int32_t* last_node, int32_t* held_node, void* stream) {
+  return accept_hold_behind(d, 0, page_table, seq_len, temperature, accept_node, accept_len, path, bonus, held, last_node,
+                            held_node, stream);
 }

@@ -1,4 +1,4 @@
-// kv_pages_reserve, kv_pages_release: page tables that grow from a free list
+// kv_pages_reserve(_step), kv_pages_release: page tables that grow from a free list
 // and shrink back into it on the device, and the slots of new positions.
 //
 // openinfer PR #626 ("feat(qwen35): add opt-in DFlash speculative decoding"),
@@ -134,7 +134,7 @@ template <bool ALL> __global__ __launch_bounds__(kThreads) void reserve_kernel(c
 #pragma unroll
     for (int k = 0; k < kPer; ++k) skips[k] = a.skip[min(tid * kPer + k, a.n_req - 1)];
   }
-  // Slots that new positions may take (without a clip longer requests are refused).
+  // Slots that new positions may take (kv_pages_reserve refuses longer requests).
   const int32_t room = a.clip ? a.table_len << a.page_shift : INT32_MAX;
 #pragma unroll
   for (int k = 0; k < kPer; ++k) {
@@ -365,7 +365,7 @@ bool pages_desc_ok(const hrs_pages_desc* d) {
   return d && d->n_req >= 1 && d->n_req <= kReqs && d->n_pos >= 1 && d->n_pos <= HRS_MAX_CHUNKED_POS &&
          d->page_size >= 16 && d->page_size <= 1024 && (d->page_size & (d->page_size - 1)) == 0 && d->n_pages >= 1 &&
          d->table_len >= 1 && static_cast<int64_t>(d->table_len) * d->page_size <= INT32_MAX - HRS_MAX_CHUNKED_POS &&
-         d->n_prefix >= 0 && d->n_prefix <= d->table_len && (d->clip == 0 || d->clip == 1);
+         d->n_prefix >= 0 && d->n_prefix <= d->table_len;
 }
 
 PagesArgs pages_args(const hrs_pages_desc* d, const int32_t* len, int32_t* page_table, int32_t* n_held,
@@ -374,7 +374,6 @@ PagesArgs pages_args(const hrs_pages_desc* d, const int32_t* len, int32_t* page_
   a.len = len; a.page_table = page_table; a.n_held = n_held; a.free_pages = free_pages; a.n_free = n_free;
   a.status = status; a.plan = static_cast<Plan*>(workspace);
   a.n_req = d->n_req; a.n_pos = d->n_pos; a.n_pages = d->n_pages; a.table_len = d->table_len; a.n_prefix = d->n_prefix;
-  a.clip = d->clip;
   a.page_shift = __builtin_ctz(static_cast<unsigned>(d->page_size));
   return a;
 }
@@ -389,20 +388,20 @@ extern "C" size_t kv_pages_workspace_bytes(const hrs_pages_desc* d) {
   return (static_cast<size_t>(d->n_req) + 1) * sizeof(Plan);
 }
 
-extern "C" int kv_pages_reserve(const hrs_pages_desc* d, const int32_t* seq_len, const int32_t* n_new,
-                                const int32_t* prefix_table, int32_t* page_table, int32_t* n_held,
-                                const int32_t* free_pages, int32_t* n_free, int64_t* slot_map, int32_t* status,
-                                void* workspace, size_t workspace_bytes, void* stream) {
+static int reserve(const hrs_pages_desc* d, bool clip, const int32_t* seq_len, const int32_t* n_new, const int32_t* skip,
+                   const int32_t* prefix_table, int32_t* page_table, int32_t* n_held, const int32_t* free_pages,
+                   int32_t* n_free, int64_t* slot_map, int32_t* status, void* workspace, size_t workspace_bytes,
+                   void* stream) {
   if (!pages_desc_ok(d)) return HRS_EINVAL;
   if (!seq_len || !page_table || !n_held || !free_pages || !n_free || (d->n_prefix > 0) != (prefix_table != nullptr))
     return HRS_EINVAL;
   if (!workspace || workspace_bytes < kv_pages_workspace_bytes(d)) return HRS_EINVAL;
   if (!aligned16(seq_len) || !aligned16(n_new) || !aligned16(prefix_table) || !aligned16(page_table) || !aligned16(n_held) ||
       !aligned16(free_pages) || !aligned16(n_free) || !aligned16(slot_map) || !aligned16(status) || !aligned16(workspace) ||
-      !aligned16(d->skip))
+      !aligned16(skip))
     return HRS_EALIGN;
   PagesArgs a = pages_args(d, seq_len, page_table, n_held, const_cast<int32_t*>(free_pages), n_free, status, workspace);
-  a.n_new = n_new; a.skip = d->skip; a.prefix_table = prefix_table; a.slot_map = slot_map;
+  a.n_new = n_new; a.skip = skip; a.clip = clip; a.prefix_table = prefix_table; a.slot_map = slot_map;
   const hipStream_t s = static_cast<hipStream_t>(stream);
   (void)hipGetLastError();
   // One block where the slot map has few entries: it writes 1024 at a time.
@@ -414,6 +413,22 @@ extern "C" int kv_pages_reserve(const hrs_pages_desc* d, const int32_t* seq_len,
   if (launch_error() != hipSuccess) return HRS_EDEVICE;
   hipLaunchKernelGGL(reserve_fill_kernel, dim3(d->n_req, (d->n_pos + kFillSlots - 1) / kFillSlots), dim3(kFill), 0, s, a);
   return launch_error() == hipSuccess ? HRS_OK : HRS_EDEVICE;
+}
+
+extern "C" int kv_pages_reserve(const hrs_pages_desc* d, const int32_t* seq_len, const int32_t* n_new,
+                                const int32_t* prefix_table, int32_t* page_table, int32_t* n_held,
+                                const int32_t* free_pages, int32_t* n_free, int64_t* slot_map, int32_t* status,
+                                void* workspace, size_t workspace_bytes, void* stream) {
+  return reserve(d, false, seq_len, n_new, nullptr, prefix_table, page_table, n_held, free_pages, n_free, slot_map, status,
+                 workspace, workspace_bytes, stream);
+}
+
+extern "C" int kv_pages_reserve_step(const hrs_pages_desc* d, const int32_t* seq_len, const int32_t* n_new,
+                                     const int32_t* skip, const int32_t* prefix_table, int32_t* page_table, int32_t* n_held,
+                                     const int32_t* free_pages, int32_t* n_free, int64_t* slot_map, int32_t* status,
+                                     void* workspace, size_t workspace_bytes, void* stream) {
+  return reserve(d, true, seq_len, n_new, skip, prefix_table, page_table, n_held, free_pages, n_free, slot_map, status,
+                 workspace, workspace_bytes, stream);
 }
 
 extern "C" int kv_pages_release(const hrs_pages_desc* d, const int32_t* keep_len, int32_t* page_table, int32_t* n_held,

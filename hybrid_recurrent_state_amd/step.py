@@ -34,11 +34,11 @@ from typing import List, Optional, Sequence
 import numpy as np
 
 from . import (AcceptDesc, ConvAdvanceDesc, ConvDesc, GdnDesc, GdnLayerDesc, HRS_BF16, HRS_CHAIN, HRS_F32, HRS_TREE,
-               HrsError, RingDesc, RingRun, RollbackDesc, SpanSource, accept_greedy_workspace_bytes, accept_hold_call,
+               HrsError, RingDesc, RingRun, RollbackDesc, SpanSource, accept_greedy_workspace_bytes, accept_hold_behind_call,
                accept_sample_call, accept_sample_filtered_call, accept_sample_filtered_workspace_bytes,
                accept_sample_workspace_bytes, attn_verify_shared_call, attn_verify_shared_workspace_bytes,
                attn_verify_span_call, attn_verify_span_workspace_bytes, kv_cache_append_call, kv_pages_release_call,
-               kv_pages_reserve_call, kv_pages_workspace_bytes, lib, qk_norm_rope_call)
+               kv_pages_reserve_step_call, kv_pages_workspace_bytes, lib, qk_norm_rope_call)
 
 
 @dataclasses.dataclass(frozen=True)
@@ -562,7 +562,7 @@ class HybridVerifyStep(FusedVerifyStep):
     accepted rows of all attention layers go into their pages and ``seq_len``
     advances, so replays of the captured step carry on by themselves.
 
-    A request that cannot go on is held (accept_hold): its accepted rows do not
+    A request that cannot go on is held (accept_hold_behind): its accepted rows do not
     fit in its page table, a page for them is not there, they would begin inside
     a prefix that all requests read, or its temperature is negative or NaN. The
     step then reports -1 as its accepted length and bonus token and leaves its
@@ -619,10 +619,10 @@ class HybridVerifyStep(FusedVerifyStep):
             self.sample_call = accept_sample_call(*sample_args, **more)
         sample = sample or filtered
         # By the checkpoint buffer that a step's spans start from; None: from ``state``.
-        self.hold_calls = {c: accept_hold_call(
+        self.hold_calls = {c: accept_hold_behind_call(
             b.page_table, b.seq_len, bufs.accept_node, bufs.accept_len, bufs.path, bufs.bonus, b.held, b.last_node,
-            s.n_pages, s.page_size, held_node=None if c is None else b.held_node[c],
-            temperature=b.temperature if sample else None, min_len=s.prefix_len) for c in (None, 0, 1)}
+            s.n_pages, s.page_size, s.prefix_len, held_node=None if c is None else b.held_node[c],
+            temperature=b.temperature if sample else None) for c in (None, 0, 1)}
         self.append_call = kv_cache_append_call(
             b.k_out, b.v, b.k_cache, b.v_cache, b.page_table, b.seq_len, bufs.accept_len, b.seq_len, bufs.path,
             b.k_scale, b.v_scale, b.status[-1])
@@ -630,9 +630,9 @@ class HybridVerifyStep(FusedVerifyStep):
         if s.page_list:
             lists = (b.page_table, b.n_held, b.free_pages, b.n_free, b.workspace)
             whole = 0 if b.whole_prefix is None else b.whole_prefix.shape[0]
-            self.reserve_call = kv_pages_reserve_call(b.seq_len, *lists, page_size=s.page_size, n_pos=bufs.shape.n_pos,
-                                                      prefix_table=b.whole_prefix, status=b.page_status[0], clip=True,
-                                                      skip=b.held)
+            self.reserve_call = kv_pages_reserve_step_call(
+                b.seq_len, *lists, page_size=s.page_size, n_pos=bufs.shape.n_pos, prefix_table=b.whole_prefix,
+                status=b.page_status[0], skip=b.held)
             self.release_call = kv_pages_release_call(b.seq_len, *lists, page_size=s.page_size, n_prefix=whole,
                                                       status=b.page_status[1])
 

@@ -37,8 +37,9 @@
  *   accept_sample_filtered
  *                       the same after top-k, top-p and min-p
  *   accept_hold         requests that cannot go on (pages full or missing, no
- *                       valid temperature) taken out before the commit
- *   kv_pages_reserve / kv_pages_release
+ *                       valid temperature) taken out before the commit;
+ *                       accept_hold_behind: of requests that share a prefix
+ *   kv_pages_reserve / kv_pages_reserve_step / kv_pages_release
  *                       page tables that grow from a free list and shrink back
  *                       into it, and the slots of new positions
  *
@@ -89,7 +90,7 @@
 extern "C" {
 #endif
 
-#define HRS_ABI_VERSION 2
+#define HRS_ABI_VERSION 1
 
 /* Largest span (root + drafts) a call accepts. */
 #define HRS_MAX_POS 64
@@ -886,8 +887,6 @@ typedef struct {
   int32_t n_pages;   /* pages, slots of a page and entries of a request's  */
   int32_t page_size; /* table, as hrs_cache_desc                           */
   int32_t table_len;
-  int32_t min_len;   /* slots below this are not a request's to write (those
-                        of a prefix that others read); 0: none             */
 } hrs_hold_desc;
 
 /*
@@ -896,8 +895,8 @@ typedef struct {
  * ([P3] Safety boundary: rejected before execution). A request goes on if
  * held[r] is 0, its temperature is not negative or NaN, accept_len[r] and
  * accept_node[r] are in [0, T), path[r][0..accept_len[r]] too, and slots
- * seq_len[r] .. seq_len[r] + accept_len[r] lie inside its page table, not
- * below min_len, in pages that are there. Then last_node[r] = accept_node[r]. Otherwise
+ * seq_len[r] .. seq_len[r] + accept_len[r] lie inside its page table, in
+ * pages that are there. Then last_node[r] = accept_node[r]. Otherwise
  *     accept_node[r] = accept_len[r] = bonus[r] = -1,  path[r][:] = -1
  * and, where held[r] was 0, held[r] = 1 and held_node[r] = last_node[r].
  * rollback_restore, conv_state_advance, kv_cache_append and the next
@@ -911,12 +910,23 @@ typedef struct {
  *           last_node [R] and path [R][T] int32, read and written; held_node
  *           [R] int32 or NULL (spans that started from `state`); all device.
  *           No two of them overlap.
- * Errors: HRS_EINVAL (R > 65535; sizes as hrs_cache_desc; min_len < 0),
- * HRS_EALIGN, HRS_EDEVICE.
+ * Errors: HRS_EINVAL (R > 65535; sizes as hrs_cache_desc), HRS_EALIGN,
+ * HRS_EDEVICE.
  */
 int accept_hold(const hrs_hold_desc* desc, const int32_t* page_table, const int32_t* seq_len,
                 const float* temperature, int32_t* accept_node, int32_t* accept_len, int32_t* path,
                 int32_t* bonus, int32_t* held, int32_t* last_node, int32_t* held_node, void* stream);
+
+/*
+ * accept_hold_behind - accept_hold of requests behind a prefix that all of them
+ * read: a request whose seq_len[r] is below prefix_len is held too, since its
+ * rows would go into the prefix's pages, or into slots that are read there.
+ * Errors as accept_hold; HRS_EINVAL also for prefix_len < 0.
+ */
+int accept_hold_behind(const hrs_hold_desc* desc, int32_t prefix_len, const int32_t* page_table,
+                       const int32_t* seq_len, const float* temperature, int32_t* accept_node,
+                       int32_t* accept_len, int32_t* path, int32_t* bonus, int32_t* held,
+                       int32_t* last_node, int32_t* held_node, void* stream);
 
 /* ------------------------------------------------------------------------ */
 /* Page lists                                                               */
@@ -933,15 +943,6 @@ typedef struct {
   int32_t n_prefix;  /* leading entries of every table that hold the pages
                         of a prefix shared by all requests; 0 = none. Whole
                         pages of it: new positions are written behind them */
-  int32_t clip;      /* reserve: 1 = positions behind the last slot of a
-                        request's table are left out, 0 = a request that has
-                        such positions is refused (release: ignored but for
-                        these values)                                       */
-  const int32_t* skip; /* reserve: [R], device, or NULL: a request with any
-                        value but 0 takes nothing and is left as it is, with
-                        a slot map of -1; not counted in status (accept_hold's
-                        held: what it would take is for those behind it)
-                        (release: ignored)                                  */
 } hrs_pages_desc;
 
 /* Bytes of device workspace the two calls need for this descriptor (0 if it
@@ -953,8 +954,7 @@ size_t kv_pages_workspace_bytes(const hrs_pages_desc* desc);
  * free list on the device, and their slots ([P2] What Changed: the hybrid
  * state includes the KV cache; [P1] Changes: nothing through the host). The
  * list is a stack free_pages[0 .. n_free). With S = page_size,
- * m = n_new[r] (NULL: n_pos; with clip at most table_len * S - seq_len[r]),
- * request r needs
+ * m = n_new[r] (NULL: n_pos), request r needs
  *     need_r = max(0, ceil((seq_len[r] + m) / S) - max(n_held[r], n_prefix))
  * pages beyond those it holds (table entries [0, n_held[r])) and the prefix's.
  * It is served where need_0 + ... + need_r <= n_free: in request order until
@@ -979,12 +979,28 @@ size_t kv_pages_workspace_bytes(const hrs_pages_desc* desc);
  *          workspace: device scratch of at least kv_pages_workspace_bytes(desc)
  *          bytes, contents ignored.
  * page_table, n_held, n_free, slot_map, status and workspace overlap nothing
- * else of the call (skip among it). Errors: HRS_EINVAL, HRS_EALIGN, HRS_EDEVICE.
+ * else of the call. Errors: HRS_EINVAL, HRS_EALIGN, HRS_EDEVICE.
  */
 int kv_pages_reserve(const hrs_pages_desc* desc, const int32_t* seq_len, const int32_t* n_new,
                      const int32_t* prefix_table, int32_t* page_table, int32_t* n_held,
                      const int32_t* free_pages, int32_t* n_free, int64_t* slot_map, int32_t* status,
                      void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * kv_pages_reserve_step - kv_pages_reserve for the spans of a verify step, of
+ * which a part is accepted: positions behind the last slot of a request's table
+ * are left out (m is at most table_len * S - seq_len[r]; -1 in the slot map)
+ * where kv_pages_reserve refuses the request, and a request with
+ * skip[r] != 0 (accept_hold's held; [R] int32, device, or NULL) takes nothing
+ * and is left as it is, with a slot map of -1 and without being counted in
+ * status: what it would take is for those behind it. Layouts, overlaps and
+ * errors as kv_pages_reserve.
+ */
+int kv_pages_reserve_step(const hrs_pages_desc* desc, const int32_t* seq_len, const int32_t* n_new,
+                          const int32_t* skip, const int32_t* prefix_table, int32_t* page_table,
+                          int32_t* n_held, const int32_t* free_pages, int32_t* n_free,
+                          int64_t* slot_map, int32_t* status, void* workspace,
+                          size_t workspace_bytes, void* stream);
 
 /*
  * kv_pages_release - the counterpart: every request keeps the pages of its

@@ -1,5 +1,5 @@
-"""Refusals and hand-worked lists of kv_pages_reserve up to the end of a
-request's table and without some of the requests, on the host as in
+"""Refusals and hand-worked lists of kv_pages_reserve_step (up to the end of a
+request's table, without some of the requests), on the host as in
 test_boundary_pages.py."""
 import numpy as np
 import pytest
@@ -11,15 +11,25 @@ from tests.test_boundary_pages import DESC, RESERVE, args, call
 from tests.test_oracle_pages import i32
 
 
-def reserve(**kw):
-    return call("kv_pages_reserve", hrs.PagesDesc, RESERVE, dict(DESC, clip=0, skip=None), kw, extra=(1 << 20,))[0]
+NAMES = RESERVE[:2] + ["skip"] + RESERVE[2:]
 
 
-@pytest.mark.parametrize("clip,want", [(0, hrs.HRS_EDEVICE), (1, hrs.HRS_EDEVICE), (2, hrs.HRS_EINVAL), (-1, hrs.HRS_EINVAL)])
-def test_clip_is_one_of_two(clip, want):
-    assert reserve(clip=clip) == want
-    assert call("kv_pages_release", hrs.PagesDesc, ["keep_len", "page_table", "n_held", "free_pages", "n_free", "status",
-                                                    "workspace"], dict(DESC, clip=clip), {}, extra=(1 << 20,))[0] == want
+def reserve(nbytes=1 << 20, **kw):
+    return call("kv_pages_reserve_step", hrs.PagesDesc, NAMES, DESC, kw, extra=(nbytes,))[0]
+
+
+def test_rejections():
+    optional = ("n_new", "skip", "slot_map", "status")
+    assert reserve() == hrs.HRS_EDEVICE
+    assert reserve(**{n: None for n in optional}) == hrs.HRS_EDEVICE
+    for bad in (dict(n_req=0), dict(n_req=4097), dict(n_pos=0), dict(n_pages=0), dict(page_size=48), dict(table_len=0),
+                dict(n_prefix=5), dict(n_prefix=0), dict(nbytes=24)):
+        assert reserve(**bad) == hrs.HRS_EINVAL, bad
+    for name in NAMES:
+        if name not in optional:
+            assert reserve(**{name: None}) == hrs.HRS_EINVAL, name
+        assert reserve(**{name: MIS}) == hrs.HRS_EALIGN, name
+    assert hrs.lib.kv_pages_reserve_step(None, *[FAKE] * 11, 1 << 20, None) == hrs.HRS_EINVAL
 
 
 def test_hand_worked():
@@ -33,7 +43,6 @@ def test_hand_worked():
 
 
 def test_skip():
-    assert reserve(skip=FAKE) == hrs.HRS_EDEVICE and reserve(skip=MIS) == hrs.HRS_EALIGN
     # The first request's three pages would leave one for the second, which needs two.
     for skip, held, left in ((None, [3, 0], 1), ([1, 0], [0, 2], 2)):
         table, have, free = np.full((2, 4), -1, np.int32), i32(0, 0), i32(3, 1, 0, 2)
@@ -45,12 +54,13 @@ def test_skip():
 def test_binding_refuses_wrong_tensors():
     import torch
     i32_ = torch.int32
-    ok = dict(args(), seq_len=t(4, dtype=i32_), skip=t(4, dtype=i32_), n_pos=3, clip=True)
-    with pytest.raises(ValueError, match="GPU"):
-        hrs.kv_pages_reserve(**ok)
+    ok = dict(args(), seq_len=t(4, dtype=i32_), skip=t(4, dtype=i32_), n_pos=3)
+    for more in (dict(), dict(skip=None)):
+        with pytest.raises(ValueError, match="GPU"):
+            hrs.kv_pages_reserve_step(**{**ok, **more})
     with pytest.raises(TypeError):
-        hrs.kv_pages_reserve(**{**ok, "skip": t(4, dtype=torch.bool)})
+        hrs.kv_pages_reserve_step(**{**ok, "skip": t(4, dtype=torch.bool)})
     with pytest.raises(ValueError):
-        hrs.kv_pages_reserve(**{**ok, "skip": t(3, dtype=i32_)})
+        hrs.kv_pages_reserve_step(**{**ok, "skip": t(3, dtype=i32_)})
     with pytest.raises(ValueError, match="overlaps"):
-        hrs.kv_pages_reserve(**{**ok, "skip": ok["n_held"]})
+        hrs.kv_pages_reserve_step(**{**ok, "skip": ok["n_held"]})

@@ -1,5 +1,5 @@
-"""kv_pages_reserve up to the end of a request's table and without some of the
-requests, against the oracle: whole numbers, equal."""
+"""kv_pages_reserve_step (up to the end of a request's table, without some of
+the requests) against the oracle: whole numbers, equal."""
 import numpy as np
 import pytest
 
@@ -11,16 +11,15 @@ pytestmark = pytest.mark.gpu
 
 
 class Limited(Lists):
-    def reserve(self, lens, new, **more):
+    def reserve(self, lens, new, skip=None):
         import torch
         out = torch.full((len(lens), self.n_pos), -5, dtype=torch.int64, device="cuda")
-        on_device = {k: dev(np.asarray(v, np.int32)) if isinstance(v, np.ndarray) else v for k, v in more.items()}
-        self.hrs.kv_pages_reserve(dev(np.asarray(lens, np.int32)), *self.d, self.ws, page_size=self.S, n_pos=self.n_pos,
-                                  n_new=None if new is None else dev(np.asarray(new, np.int32)),
-                                  prefix_table=dev(self.prefix) if self.pre else None, slot_map=out, status=self.status,
-                                  **on_device)
+        d = lambda x: None if x is None else dev(np.asarray(x, np.int32))
+        self.hrs.kv_pages_reserve_step(d(lens), *self.d, self.ws, page_size=self.S, n_pos=self.n_pos, n_new=d(new),
+                                       prefix_table=dev(self.prefix) if self.pre else None, slot_map=out, status=self.status,
+                                       skip=d(skip))
         self.n, want, missed = op.reserve(lens, np.full(len(lens), self.n_pos) if new is None else new, self.table, self.held,
-                                          self.free, self.n, self.S, self.n_pos, self.prefix, **more)
+                                          self.free, self.n, self.S, self.n_pos, self.prefix, clip=True, skip=skip)
         self.same(missed)
         assert np.array_equal(host(out), want)
 
@@ -33,13 +32,12 @@ def test_up_to_the_tables_end(hrs, size):
         lens = np.minimum(x.held.astype(np.int64) * S, x.rng.integers(0, P * S + 1, R)).astype(np.int32)
         if step > 1:
             lens = np.where(x.rng.random(R) < 0.2, x.rng.choice([P * S, P * S - 1, P * S + 1, -1], R), lens).astype(np.int32)
-        x.reserve(lens, None if step == 1 else x.rng.integers(-1, n_pos + 2, R).astype(np.int32), clip=True)
+        x.reserve(lens, None if step == 1 else x.rng.integers(-1, n_pos + 2, R).astype(np.int32))
         x.release(np.maximum(lens, 0))
 
 
-@pytest.mark.parametrize("clip", [False, True])
 @pytest.mark.parametrize("size", SIZES, ids=lambda s: "R{}P{}N{}S{}p{}T{}".format(*s))
-def test_without_some_of_the_requests(hrs, size, clip):
+def test_without_some_of_the_requests(hrs, size):
     """What they would take is for those behind them; refused ones among them are not counted."""
     R, P, N, S, prefix, n_pos = size
     x = Limited(hrs, R, P, N, S, seed=R + P + 1, prefix=prefix, n_pos=n_pos)
@@ -48,12 +46,12 @@ def test_without_some_of_the_requests(hrs, size, clip):
         lens = np.minimum(x.held.astype(np.int64) * S, x.rng.integers(0, P * S + 1, R)).astype(np.int32)
         lens[x.rng.random(R) < 0.1] = -1
         before = x.held.copy()
-        x.reserve(lens, x.rng.integers(0, n_pos + 1, R).astype(np.int32), clip=clip, skip=skip)
+        x.reserve(lens, x.rng.integers(0, n_pos + 1, R).astype(np.int32), skip)
         assert np.array_equal(x.held[skip != 0], before[skip != 0])
         x.release(np.maximum(lens, 0))
 
 
 def test_large_lengths(hrs):
     x = Limited(hrs, 3, 4, 12, 16, seed=2, n_pos=20)
-    x.reserve(np.array([2 ** 31 - 1, 63, 50], np.int32), None, clip=True)
+    x.reserve(np.array([2 ** 31 - 1, 63, 50], np.int32), None)
     assert x.held.tolist() == [0, 4, 4] and x.n == 4
